@@ -317,6 +317,122 @@ int gla_spatial_swiglu(const void* a, const void* u, const float* weight,
                        const float* bias, void* h, int B, int grid_h,
                        int grid_w, int F, int dtype, void* stream);
 
+/* ---- gradients, single tokens and the norm before a mixer ------------------
+ *
+ * The calls below follow the same rules as the forward: caller-owned,
+ * contiguous device memory, 16-byte aligned (workspaces 256, slots 4); every
+ * argument is checked on the host before any HIP call; kernels are enqueued on
+ * `stream` without allocating or synchronising, so every call can be captured
+ * in a graph. Workspaces may hold anything on entry and nothing is kept in
+ * them between calls; calls that may overlap in time (two streams, two graphs
+ * replayed at once) need a workspace each. Values are not checked: a NaN or
+ * Inf makes the outputs that depend on it non-finite, and in the gradients may
+ * reach every token of its 64-token chunk. Results do not change from run to
+ * run. An empty problem (no row, token or head) returns GLA_OK and writes
+ * nothing. */
+
+/* Bytes of workspace gla_bwd needs (0 for an empty or unsupported problem):
+ * two float states and a decay row per (batch, head, 64-token chunk). */
+size_t gla_bwd_workspace_bytes(int B, int H, int grid_h, int grid_w, int dk,
+                               int dv);
+
+/* Gradient of gla_fwd_state. With go = dL/do and gs_final = dL/dS_T (NULL for
+ * zero), the gradient of the state runs the recurrence from the end,
+ *   E_t = D_t + q_t^T go_t,  D_{t-1} = diag(exp(gk_t)) E_t,  D_T = gs_final,
+ *   gq_t = S_t go_t,  gkey_t = E_t v_t,  gv_t = E_t^T k_t,
+ *   ggk_t[d] = sum_e exp(gk_t[d]) S_{t-1}[d][e] E_t[d][e],  gs0 = D_0,
+ * along the same scan order. Nothing of the forward has to be kept: the
+ * states are computed again from k, v, gk and s0.
+ *   go, gv: [B][T][H][dv]; gq, gkey, ggk: [B][T][H][dk], in the input dtype;
+ *   s0, gs_final, gs0: float [B][H][dk][dv], each may be NULL (gs0 NULL: not
+ *   returned). gs0 may be gs_final; no other output may overlap an input,
+ *   another output or the workspace (GLA_E_ARG).
+ * Sums and states are float. Products run on the matrix cores over operands
+ * split into bf16 terms: 16 bits for GLA_F16, 24 for GLA_F32 (whose q, k, v
+ * are not rounded to half here; they and go must not exceed 65504 in
+ * magnitude). gk <= 0; a token's decay below 2^-160 counts as 2^-160. */
+int gla_bwd(const void* q, const void* k, const void* v, const void* gk,
+            const void* go, void* gq, void* gkey, void* gv, void* ggk, int B,
+            int H, int grid_h, int grid_w, int dk, int dv, const int32_t* dir,
+            int dtype, const float* s0, const float* gs_final, float* gs0,
+            void* workspace, size_t workspace_bytes, void* stream);
+
+/* One new token per row on a pool of states:
+ *   S <- diag(exp(gk)) S + k^T v,   o = q S,   S = state[slot of the row].
+ *   q, k, gk: [B][H][dk], v, o: [B][H][dv] in the input dtype;
+ *   state: float [n_slots][H][dk][dv], updated in place (what gla_fwd_state
+ *   hands back as s_final for a batch element is one slot);
+ *   slots: int32 [B] device memory, or NULL (row b uses slot b, n_slots >= B).
+ * A row whose slot is negative or not below n_slots is padding: it is skipped
+ * and its o is left as it was. Rows that name the same slot are consecutive
+ * tokens of one sequence and are applied in row order. B <= 65535. o and state
+ * must not overlap each other or an input. */
+int gla_step(const void* q, const void* k, const void* v, const void* gk,
+             void* o, int B, int H, int dk, int dv, int dtype, float* state,
+             int64_t n_slots, const int32_t* slots, void* stream);
+
+/* gla_step with the output gate of gla_fwd_gated on each row:
+ *   y = o / sqrt(mean_e(o_e^2) + eps) * norm_weight * silu(gate),
+ * gate [B][H][dv] in the input dtype, norm_weight float [dv], eps >= 0. */
+int gla_step_gated(const void* q, const void* k, const void* v, const void* gk,
+                   const void* gate, const float* norm_weight, float eps,
+                   void* y, int B, int H, int dk, int dv, int dtype,
+                   float* state, int64_t n_slots, const int32_t* slots,
+                   void* stream);
+
+/* Residual addition and root-mean-square norm, the step before each mixer of a
+ * block, for `rows` rows of F values (F a multiple of 8, at most 16384):
+ *   sum = x + residual   (rounded to the input dtype; x if residual is NULL),
+ *   y   = sum / sqrt(mean(sum^2) + eps) * weight.
+ * x, residual, sum, y: [rows][F] GLA_F16 or GLA_F32; weight: float [F];
+ * eps >= 0. sum may be NULL. sum and y may each be x or residual themselves
+ * (not both the same one) but must not overlap anything otherwise. A row of
+ * zeros with eps 0 gives NaN. */
+int gla_add_rmsnorm(const void* x, const void* residual, const float* weight,
+                    float eps, void* sum, void* y, int64_t rows, int F,
+                    int dtype, void* stream);
+
+/* The same with y in 8 bits (OCP e4m3, one byte per value) and a float scale
+ * per row, for products in 8 bits: scale = max|y| / 448 (at least 2^-126; 1
+ * for a row of zeros), y8 = e4m3(y / scale), to nearest even. y8 and scales
+ * must not overlap any other argument. */
+int gla_add_rmsnorm_q8(const void* x, const void* residual,
+                       const float* weight, float eps, void* sum, void* y8,
+                       float* scales, int64_t rows, int F, int dtype,
+                       void* stream);
+
+/* Bytes of workspace gla_add_rmsnorm_bwd needs (0 for an empty or unsupported
+ * problem). */
+size_t gla_add_rmsnorm_bwd_workspace_bytes(int64_t rows, int F);
+
+/* Gradient of gla_add_rmsnorm from its `sum`: with n = sum / sqrt(mean(sum^2)
+ * + eps), gy = dL/dy and gsum = what reaches the sum itself from the blocks
+ * behind (NULL for none),
+ *   gx = (gy w - n mean(gy w n)) / sqrt(mean(sum^2) + eps) + gsum,
+ *   gweight = sum over rows of gy n   (float [F], 16-byte aligned).
+ * gx is the gradient of x and of residual alike. It may be sum, gy or gsum
+ * itself; nothing else may overlap. */
+int gla_add_rmsnorm_bwd(const void* sum, const float* weight, float eps,
+                        const void* gy, const void* gsum, void* gx,
+                        float* gweight, int64_t rows, int F, int dtype,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gla_gate_bwd needs (0 for an empty or unsupported
+ * problem). */
+size_t gla_gate_bwd_workspace_bytes(int64_t rows, int dv);
+
+/* Gradient of the output gate y = n * w * silu(gate), n = o / sqrt(mean(o^2) +
+ * eps), for `rows` rows of dv values (B T H rows of gla_fwd_gated; o is what
+ * gla_fwd_state gives for the same inputs):
+ *   go    = (gn - n mean(gn n)) / sqrt(mean(o^2) + eps), gn = gy w silu(gate),
+ *   ggate = gy n w silu'(gate),   gnorm_weight = sum over rows of gy n silu(gate)
+ * (float [dv], 16-byte aligned). o, gate, gy, go, ggate: [rows][dv] in the
+ * input dtype. No output may overlap an input or another output. */
+int gla_gate_bwd(const void* o, const void* gate, const float* norm_weight,
+                 float eps, const void* gy, void* go, void* ggate,
+                 float* gnorm_weight, int64_t rows, int dv, int dtype,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static text for a status code; never NULL. */
 const char* gla_status_string(int status);
 

@@ -1,0 +1,801 @@
+// Backward pass of the chunkwise key-only gated linear recurrence.
+//
+// Forward: S_t = diag(2^g_t) S_{t-1} + k_t^T v_t, o_t = q_t S_t (g the decay in
+// log2). With go_t = dL/do_t and the gradient of the state after the last
+// token, the gradient of the state runs the same recurrence from the end:
+//   E_t = D_t + q_t^T go_t,   D_{t-1} = diag(2^g_t) E_t,
+//   gq_t = S_t go_t,  gk_t = E_t v_t,  gv_t = E_t^T k_t,
+//   gg_t[d] = sum_e 2^g_t[d] S_{t-1}[d][e] E_t[d][e].
+// In chunks of 64 tokens, with b the in-chunk inclusive cumulative decay (log2)
+// and B its last value:
+//   U_n = sum_j (k_j 2^(B-b_j))^T v_j,   S_{n+1} = 2^B S_n + U_n   (forward)
+//   R_n = sum_i (q_i 2^b_i)^T go_i,      D_{n-1} = 2^B D_n + R_n   (from the end)
+//   P_ij = go_i . v_j,  A_ij = sum_d q_i k_j 2^(b_i-b_j)           (j <= i)
+//   gq_i = 2^b_i S_n go_i + sum_{j<=i} P_ij k_j 2^(b_i-b_j)
+//   gk_j = 2^(B-b_j) D_n v_j + sum_{i>=j} P_ij q_i 2^(b_i-b_j)
+//   gv_j = D_n^T (k_j 2^(B-b_j)) + sum_{i>=j} A_ij go_i
+// The decay's gradient at token t collects every path that crosses t: from the
+// state before the chunk to the state behind it, from that state to the
+// outputs at t and later, from the inputs before t to the state behind the
+// chunk, and the pairs i >= t > j inside the chunk:
+//   gg_t = 2^B <S_n, D_n> + sum_{i>=t} q_i gq_i^state + sum_{j<t} k_j gk_j^state
+//          + sum_{i>=t} (q_i gq_i^pairs - k_i gk_i^pairs),
+// rows of the inner product over e. In the last sum a token's pair with itself
+// (no decay) is left out of both terms, where it would only cancel, so that
+// what is left of a strongly decaying channel is not lost in its rounding.
+//
+// Products run on the matrix cores over operands split into bf16 terms
+// (x = t0 + t1 [+ t2], each the rounding of what is left): bf16 has float's
+// range, so no operand needs a scale, two terms hold 16 bits (half inputs are
+// exact in them) and three hold float's 24. The products of two operands'
+// terms are added in float, the smallest ones left out. States between chunks
+// are float.
+#include "gla_bwd.h"
+#include "gla_tile.h"
+
+namespace gla {
+namespace bwd {
+
+using tile::fexp2;
+using tile::row_scan16;
+using tile::token_row;
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+
+constexpr int C = kBwdChunk, NB = C / 16;
+// A token's decay is taken as at least 2^-160: float rounds anything beyond
+// 2^-149 to zero, and the cumulative sums stay small enough that their
+// differences keep their low bits.
+constexpr float kMinLog2 = -160.f;
+__device__ __forceinline__ float log2_decay(float gk) {
+  const float x = gk * kLog2e;
+  return x < kMinLog2 ? kMinLog2 : x;  // NaN stays
+}
+
+__device__ __forceinline__ floatx4 mma(bf8 a, bf8 b, floatx4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Eight or four floats as NT bf16 terms.
+template <int NT> struct Split8 { bf8 t[NT]; };
+template <int NT> struct Split4 { bf4 t[NT]; };
+template <int NT>
+__device__ __forceinline__ Split8<NT> split8(const float* x) {
+  typedef float f8 __attribute__((ext_vector_type(8)));
+  Split8<NT> s;
+  f8 r = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    s.t[t] = __builtin_convertvector(r, bf8);
+    if (t + 1 < NT) r -= __builtin_convertvector(s.t[t], f8);
+  }
+  return s;
+}
+template <int NT>
+__device__ __forceinline__ Split4<NT> split4(floatx4 r) {
+  Split4<NT> s;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    s.t[t] = __builtin_convertvector(r, bf4);
+    if (t + 1 < NT) r -= __builtin_convertvector(s.t[t], floatx4);
+  }
+  return s;
+}
+
+// c += a b over 32 contracted elements: the products of terms i + j < NT, and
+// with three terms the middle ones' product.
+template <int NT>
+__device__ __forceinline__ floatx4 mm(const Split8<NT>& a, const Split8<NT>& b, floatx4 c) {
+  if constexpr (NT == 3) {
+    c = mma(a.t[2], b.t[0], c);
+    c = mma(a.t[0], b.t[2], c);
+    c = mma(a.t[1], b.t[1], c);
+  }
+  c = mma(a.t[1], b.t[0], c);
+  c = mma(a.t[0], b.t[1], c);
+  return mma(a.t[0], b.t[0], c);
+}
+
+__device__ __forceinline__ bf8 join(bf4 a, bf4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+// c += x p over 16 contracted elements, four per lane: the 32 places of one
+// matrix product hold two terms of x against the same term of p.
+template <int NT>
+__device__ __forceinline__ floatx4 mm16(const Split4<NT>& x, const Split4<NT>& p, floatx4 c) {
+  const bf8 x01 = join(x.t[0], x.t[1]);
+  if constexpr (NT == 3) c = mma(join(x.t[2], x.t[0]), join(p.t[0], p.t[2]), c);
+  c = mma(x01, join(p.t[1], p.t[1]), c);
+  return mma(x01, join(p.t[0], p.t[0]), c);
+}
+
+// Four rows of one column of a row-major 16-bit tile in LDS, through the
+// transposing read: lane (i = lane % 16, q = lane / 16) receives rows
+// GSTEP*q + 0..3 of column i of a 16-column block whose columns 4g..4g+3 lie
+// at blk + CSTEP*g.
+template <int STR, int GSTEP, int CSTEP>
+__device__ __forceinline__ bf4 tr4(const __bf16* blk) {
+  const int s = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
+  const __bf16* p = blk + (GSTEP * q + (s >> 2)) * STR + CSTEP * (s & 3);
+  return __builtin_bit_cast(bf4, __builtin_amdgcn_ds_read_tr16_b64_v4f16((tile::lds_fp16x4_t*)p));
+}
+
+// Orders a wave's LDS writes before its own later LDS reads (the LDS unit
+// keeps a wave's accesses in order; this keeps the compiler from moving them).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__device__ __forceinline__ void load4(const half_t* p, float* x) {
+  const half4 h = *reinterpret_cast<const half4*>(p);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) x[c] = (float)h[c];
+}
+__device__ __forceinline__ void load4(const float* p, float* x) {
+  const floatx4 f = *reinterpret_cast<const floatx4*>(p);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) x[c] = f[c];
+}
+__device__ __forceinline__ void store4(half_t* p, const float* x) {
+  *reinterpret_cast<half4*>(p) = half4{(half_t)x[0], (half_t)x[1], (half_t)x[2], (half_t)x[3]};
+}
+__device__ __forceinline__ void store4(float* p, const float* x) {
+  *reinterpret_cast<floatx4*>(p) = floatx4{x[0], x[1], x[2], x[3]};
+}
+
+// Inclusive suffix sum over the 16 lanes of a DPP row, and the sum of the
+// lanes before each one.
+__device__ __forceinline__ float row_suffix16(float x) {
+  x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x101, 0xf, 0xf, true));
+  x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x102, 0xf, 0xf, true));
+  x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x104, 0xf, 0xf, true));
+  x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x108, 0xf, 0xf, true));
+  return x;
+}
+__device__ __forceinline__ float row_before16(float scan) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(scan), 0x111, 0xf, 0xf, true));
+}
+
+// ===========================================================================
+// Chunk summaries: one workgroup per (chunk, head, batch) and direction of
+// time: U_n and the decay a_n from (k, v) with factors 2^(B-b), or R_n from
+// (q, go) with factors 2^b. Both contract over tokens: the operands go to LDS
+// as token rows and come back through the transposing read.
+// ===========================================================================
+template <int DK, int DV, typename InT, int NT>
+__global__ __launch_bounds__(kThreads) void bwd_summary_kernel(
+    const InT* __restrict__ kp, const InT* __restrict__ vp, const InT* __restrict__ qp,
+    const InT* __restrict__ dop, const InT* __restrict__ gp, float* __restrict__ Uws,
+    float* __restrict__ Rws, float* __restrict__ Aws, int T, int H, int N, int gh, int gw,
+    DirPack dirs) {
+  constexpr int NKS = DK / 32, NEL = 8 * NKS, ND = DK / 16, NE = DV / 16;
+  constexpr int XSTR = DK + 16, YSTR = DV + 16;
+  __shared__ __attribute__((aligned(16))) __bf16 sX[NT][C][XSTR];
+  __shared__ __attribute__((aligned(16))) __bf16 sY[NT][C][YSTR];
+  __shared__ __attribute__((aligned(16))) float sTot[NB][DK];
+  const bool rev = blockIdx.z & 1;
+  const int n = blockIdx.x, h = blockIdx.y, b = blockIdx.z >> 1;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lr = lane & 15, lq = lane >> 4, lk = 8 * lq;
+  const int dir = dirs.get(b), t = 16 * wave + lr;
+  const InT* xp = rev ? qp : kp;
+  const InT* yp = rev ? dop : vp;
+
+  const int rr = token_row(n * C + t, T, gh, gw, dir);
+  const bool pad = rr < 0;
+  const long row = ((long)b * T + (pad ? 0 : rr)) * H + h;
+  float x[NEL], g[NEL], y[DV / 4];
+#pragma unroll
+  for (int ks = 0; ks < NKS; ++ks) {
+    load8(xp + row * DK + 32 * ks + lk, reinterpret_cast<float(&)[8]>(x[8 * ks]));
+    load8(gp + row * DK + 32 * ks + lk, reinterpret_cast<float(&)[8]>(g[8 * ks]));
+  }
+#pragma unroll
+  for (int ks = 0; ks < DV / 32; ++ks)
+    load8(yp + row * DV + 32 * ks + lk, reinterpret_cast<float(&)[8]>(y[8 * ks]));
+#pragma unroll
+  for (int e = 0; e < NEL; ++e) {
+    x[e] = pad ? 0.f : x[e];
+    g[e] = row_scan16(pad ? 0.f : log2_decay(g[e]));
+  }
+  if (lr == 15) {
+#pragma unroll
+    for (int e = 0; e < NEL; ++e) sTot[wave][32 * (e / 8) + lk + e % 8] = g[e];
+  }
+#pragma unroll
+  for (int ks = 0; ks < DV / 32; ++ks) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) y[8 * ks + c] = pad ? 0.f : y[8 * ks + c];
+    const Split8<NT> s = split8<NT>(y + 8 * ks);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) *reinterpret_cast<bf8*>(&sY[i][t][32 * ks + lk]) = s.t[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int ks = 0; ks < NKS; ++ks) {
+    float o[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = rev ? 0.f : -g[8 * ks + c];
+#pragma unroll
+    for (int J = 0; J < NB; ++J) {
+      const bool in = rev ? J < wave : J >= wave;
+      float tt[8];
+      tile::lds8(&sTot[J][32 * ks + lk], tt);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) o[c] += in ? tt[c] : 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = x[8 * ks + c] * fexp2(rev ? o[c] + g[8 * ks + c] : o[c]);
+    const Split8<NT> s = split8<NT>(o);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) *reinterpret_cast<bf8*>(&sX[i][t][32 * ks + lk]) = s.t[i];
+  }
+  __syncthreads();
+
+  const long bhn = ((long)b * H + h) * N + n;
+  if (!rev && tid < DK) {
+    float B = 0.f;
+#pragma unroll
+    for (int J = 0; J < NB; ++J) B += sTot[J][tid];
+    Aws[bhn * DK + tid] = fexp2(B);
+  }
+  // the transposed product Y^T X in 16x16 blocks: a lane ends up with four
+  // consecutive value columns of one key dim
+  float* out = (rev ? Rws : Uws) + bhn * (long)(DK * DV);
+  auto frag = [&](const __bf16* base, int str, auto read) {
+    Split8<NT> s;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s.t[i] = join(read(base + i * C * str), read(base + i * C * str + 4 * str));
+    return s;
+  };
+  constexpr int NBLK = ND * NE, BPW = NBLK / 4;
+#pragma unroll
+  for (int i = 0; i < BPW; ++i) {
+    const int blk = wave * BPW + i, D = blk / NE, E = blk % NE;
+    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < C / 32; ++j) {
+      const Split8<NT> xa = frag(&sX[0][32 * j][16 * D], XSTR, [](const __bf16* p) { return tr4<XSTR, 8, 4>(p); });
+      const Split8<NT> ya = frag(&sY[0][32 * j][16 * E], YSTR, [](const __bf16* p) { return tr4<YSTR, 8, 4>(p); });
+      acc = mm<NT>(ya, xa, acc);
+    }
+    *reinterpret_cast<floatx4*>(out + (16 * D + lr) * DV + 16 * E + 4 * lq) = acc;
+  }
+}
+
+// ===========================================================================
+// State scans, in place: S_n over U_n in forward order, D_n over R_n from the
+// end. Every state element is its own first-order recurrence over the chunks;
+// one thread walks four of them with the next W chunks' loads in flight.
+// ===========================================================================
+template <int W>
+__global__ __launch_bounds__(kThreads) void bwd_scan_kernel(float* __restrict__ Uws,
+                                                            float* __restrict__ Rws,
+                                                            const float* __restrict__ Aws,
+                                                            const float* s0, const float* gsf,
+                                                            float* gs0, int N, int DK, int DV,
+                                                            long groups) {
+  const long gid = (long)blockIdx.x * kThreads + threadIdx.x;
+  if (gid >= groups) return;
+  const bool rev = blockIdx.y;
+  const long DKDV = (long)DK * DV, per = DKDV / 4;
+  const long bh = gid / per;
+  const int x4 = 4 * (int)(gid - bh * per), d = x4 / DV;
+  float* X = (rev ? Rws : Uws) + bh * N * DKDV + x4;
+  const float* A = Aws + bh * N * DK + d;
+  const float* init = rev ? gsf : s0;
+  floatx4 s = {0.f, 0.f, 0.f, 0.f};
+  if (init) s = *reinterpret_cast<const floatx4*>(init + bh * DKDV + x4);
+  floatx4 u[W];
+  float a[W];
+  auto at = [&](int i) { return (long)(rev ? N - 1 - i : i); };
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const long m = at(i < N ? i : N - 1);
+    u[i] = *reinterpret_cast<const floatx4*>(X + m * DKDV);
+    a[i] = A[m * DK];
+  }
+  for (int n0 = 0; n0 < N; n0 += W) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const int n = n0 + i;
+      if (n < N) {
+        *reinterpret_cast<floatx4*>(X + at(n) * DKDV) = s;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[c] = fmaf(a[i], s[c], u[i][c]);
+        // a chunk W ahead: not yet overwritten, this thread alone writes it
+        const long m = at(n + W < N ? n + W : N - 1);
+        if (n + W < N) {
+          u[i] = *reinterpret_cast<const floatx4*>(X + m * DKDV);
+          a[i] = A[m * DK];
+        }
+      }
+    }
+  }
+  if (rev && gs0) *reinterpret_cast<floatx4*>(gs0 + bh * DKDV + x4) = s;
+}
+
+// ===========================================================================
+// Gradients: one workgroup per (chunk, head, batch), four waves; wave w owns
+// the 16 tokens of sub-block w as queries (gq) and as keys (gk, gv). A lane
+// holds token lr = lane % 16 of it and the dims d = 32 ks + 16 h + 4 lq + r
+// (lq = lane / 16): as an operand these are eight contracted places per ks,
+// and a product written transposed (rows = dims, columns = tokens) leaves
+// exactly the same token and dims in the lane, so inputs, factors and results
+// meet in registers. LDS rows hold dim d at place 32 ks + 8 lq + 4 h + r, so
+// that a lane's eight values are 16 contiguous bytes.
+//
+// With s the cumulative decay inside a sub-block and tot its last value,
+//   q~ = q 2^s,  k~ = k 2^(tot-s),  2^(b_i-b_j) = 2^s_i 2^(tot_J-s_j) prod 2^tot
+// over the sub-blocks between: all factors <= 1. The products over earlier
+// (gq) and later (gk) sub-blocks are accumulated farthest first and decayed
+// from one sub-block to the next. Inside a sub-block one reference at its 8th
+// token, q' = q 2^(s-s7) and k' = k 2^(s7-s), spans decays up to 2^88; a
+// sub-block that decays more sums its pairs directly in float.
+// ===========================================================================
+constexpr float kMaxSpan = 88.f;
+
+template <int DK, int DV, typename InT, int NT>
+__global__ __launch_bounds__(kThreads) void bwd_grad_kernel(
+    const InT* __restrict__ qp, const InT* __restrict__ kp, const InT* __restrict__ vp,
+    const InT* __restrict__ gp, const InT* __restrict__ dop, const float* __restrict__ Sws,
+    const float* __restrict__ Dws, InT* __restrict__ gqp, InT* __restrict__ gkp,
+    InT* __restrict__ gvp, InT* __restrict__ ggp, int T, int H, int N, int gh, int gw,
+    DirPack dirs) {
+  constexpr int NKS = DK / 32, NES = DV / 32, ND = DK / 16, NE = DV / 16;
+  constexpr int NEL = 4 * ND, NVL = 4 * NE;  // a lane's dims of q/k/g and of v/go
+  constexpr int KSTR = DK + 8, VSTR = DV + 8;
+  __shared__ __attribute__((aligned(16))) __bf16 sQ[NT][C][KSTR];
+  __shared__ __attribute__((aligned(16))) __bf16 sK[NT][C][KSTR];
+  __shared__ __attribute__((aligned(16))) __bf16 sO[NT][C][VSTR];   // go
+  __shared__ __attribute__((aligned(16))) __bf16 sV[NT][C][VSTR];
+  __shared__ __attribute__((aligned(16))) __bf16 sX[NT][DK][VSTR];  // S_n, then D_n
+  __shared__ __attribute__((aligned(16))) float sTot[NB][DK];  // a sub-block's decay, log2
+  __shared__ __attribute__((aligned(16))) float sRef[NB][DK];  // s at its 8th token
+  __shared__ __attribute__((aligned(16))) float sZ[NB][DK];    // its sum of q gq - k gk^pairs
+  __shared__ __attribute__((aligned(16))) float sW[NB][DK];    // its sum of k gk^state
+  __shared__ __attribute__((aligned(16))) float sAD[DK];       // <S_n, D_n> by rows
+  __shared__ float sSelf[C];                                   // P_tt
+  __shared__ float sPd[NB][16][17], sAd[NB][16][17];           // direct sub-blocks only
+  const int n = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lr = lane & 15, lq = lane >> 4;
+  const int dir = dirs.get(b), t = 16 * wave + lr;
+  const long bhn = ((long)b * H + h) * N + n;
+  // place of a lane's dims 4D + r in memory rows, and of its eight per ks in LDS rows
+  auto dim = [&](int D) { return 16 * D + 4 * lq; };
+  auto place = [&](int ks) { return 32 * ks + 8 * lq; };
+
+  // -- this lane's token row
+  const int rr = token_row(n * C + t, T, gh, gw, dir);
+  const bool pad = rr < 0;
+  const long row = ((long)b * T + (pad ? 0 : rr)) * H + h;
+  float q[NEL], k[NEL], s[NEL], v[NVL], go[NVL];
+#pragma unroll
+  for (int D = 0; D < ND; ++D) {
+    load4(qp + row * DK + dim(D), q + 4 * D);
+    load4(kp + row * DK + dim(D), k + 4 * D);
+    load4(gp + row * DK + dim(D), s + 4 * D);
+  }
+#pragma unroll
+  for (int E = 0; E < NE; ++E) {
+    load4(vp + row * DV + dim(E), v + 4 * E);
+    load4(dop + row * DV + dim(E), go + 4 * E);
+  }
+  // -- the states at the chunk's ends: S_n to LDS, D_n kept for later, their
+  // rows' inner products
+  constexpr int NG = DK * DV / 4 / kThreads, LPR = DV / 4;  // groups of four per thread, per row
+  floatx4 dn[NG];
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    const int u = tid + kThreads * i, d = u / LPR, e = 4 * (u % LPR);
+    const floatx4 sn = *reinterpret_cast<const floatx4*>(Sws + bhn * (DK * DV) + 4 * u);
+    dn[i] = *reinterpret_cast<const floatx4*>(Dws + bhn * (DK * DV) + 4 * u);
+    const Split4<NT> sp = split4<NT>(sn);
+    const int p = 32 * (e / 32) + 8 * ((e / 4) % 4) + 4 * ((e / 16) % 2);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) *reinterpret_cast<bf4*>(&sX[j][d][p]) = sp.t[j];
+    float dot = sn[0] * dn[i][0] + sn[1] * dn[i][1] + sn[2] * dn[i][2] + sn[3] * dn[i][3];
+#pragma unroll
+    for (int m = 1; m < LPR; m <<= 1) dot += __shfl_xor(dot, m);
+    if (e == 0) sAD[d] = dot;
+  }
+#pragma unroll
+  for (int e = 0; e < NEL; ++e) {
+    q[e] = pad ? 0.f : q[e];
+    k[e] = pad ? 0.f : k[e];
+    s[e] = row_scan16(pad ? 0.f : log2_decay(s[e]));
+  }
+#pragma unroll
+  for (int e = 0; e < NVL; ++e) {
+    v[e] = pad ? 0.f : v[e];
+    go[e] = pad ? 0.f : go[e];
+  }
+  if (lr == 15 || lr == 7) {
+    float(*dst)[DK] = lr == 15 ? sTot : sRef;
+#pragma unroll
+    for (int D = 0; D < ND; ++D)
+      *reinterpret_cast<floatx4*>(&dst[wave][dim(D)]) = floatx4{s[4 * D], s[4 * D + 1], s[4 * D + 2], s[4 * D + 3]};
+  }
+  Split8<NT> vs[NES], os[NES];  // this token's v and go as operands
+#pragma unroll
+  for (int ks = 0; ks < NES; ++ks) {
+    vs[ks] = split8<NT>(v + 8 * ks);
+    os[ks] = split8<NT>(go + 8 * ks);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      *reinterpret_cast<bf8*>(&sV[i][t][place(ks)]) = vs[ks].t[i];
+      *reinterpret_cast<bf8*>(&sO[i][t][place(ks)]) = os[ks].t[i];
+    }
+  }
+  __syncthreads();
+
+  auto table = [&](const float(*tab)[DK], int J, float* x) {
+#pragma unroll
+    for (int D = 0; D < ND; ++D) {
+      const floatx4 f = *reinterpret_cast<const floatx4*>(&tab[J][dim(D)]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[4 * D + r] = f[r];
+    }
+  };
+  auto put_row = [&](__bf16(*tl)[C][KSTR], const float* x) {
+#pragma unroll
+    for (int ks = 0; ks < NKS; ++ks) {
+      const Split8<NT> sp = split8<NT>(x + 8 * ks);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) *reinterpret_cast<bf8*>(&tl[i][t][place(ks)]) = sp.t[i];
+    }
+  };
+  // operand of 16 rows of a tile contracted along the row, and of 16 of its
+  // columns (block D) contracted along 16 rows
+  auto rows8 = [&](const __bf16* tl, int plane, int str, int ks) {
+    Split8<NT> sp;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      sp.t[i] = *reinterpret_cast<const bf8*>(tl + i * plane + lr * str + place(ks));
+    return sp;
+  };
+  auto cols4 = [&](const __bf16* tl, int plane, auto read) {
+    Split4<NT> sp;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sp.t[i] = read(tl + i * plane);
+    return sp;
+  };
+  auto rdK = [](const __bf16* p) { return tr4<KSTR, 4, 8>(p); };
+  auto rdV = [](const __bf16* p) { return tr4<VSTR, 4, 8>(p); };
+  constexpr int KPL = C * KSTR, VPL = C * VSTR, XPL = DK * VSTR;
+  auto colblk = [](int D) { return 32 * (D / 2) + 4 * (D % 2); };  // place of column block D
+
+  // -- the sub-block's own pairs. P transposed (rows j) for gq; P and A (rows
+  // i) for gk and gv.
+  float tot[NEL], ref[NEL];
+  table(sTot, wave, tot);
+  table(sRef, wave, ref);
+  floatx4 pt = {0.f, 0.f, 0.f, 0.f}, pn = pt;
+#pragma unroll
+  for (int ks = 0; ks < NES; ++ks) {
+    pt = mm<NT>(vs[ks], os[ks], pt);
+    pn = mm<NT>(os[ks], vs[ks], pn);
+  }
+  float span = 0.f, big = 0.f, bigp = 0.f;
+  float qx[NEL], kx[NEL];
+#pragma unroll
+  for (int e = 0; e < NEL; ++e) {
+    span = fmaxf(span, fmaxf(fabsf(ref[e]), fabsf(tot[e] - ref[e])));
+    qx[e] = q[e] * fexp2(s[e] - ref[e]);
+    kx[e] = k[e] * fexp2(ref[e] - s[e]);
+    big = fmaxf(big, fmaxf(fabsf(qx[e]), fabsf(kx[e])));
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    bigp = fmaxf(bigp, fabsf(pn[r]));
+    if (4 * lq + r == lr) sSelf[t] = pn[r];
+  }
+  big = tile::group_max<64>(big);
+  bigp = tile::group_max<64>(bigp);
+  floatx4 gqd[ND], gkd[ND], gva[NE];
+#pragma unroll
+  for (int D = 0; D < ND; ++D) gqd[D] = gkd[D] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int E = 0; E < NE; ++E) gva[E] = floatx4{0.f, 0.f, 0.f, 0.f};
+  floatx4 an = {0.f, 0.f, 0.f, 0.f};
+  if (__all(span <= kMaxSpan && big * fmaxf(fmaxf(bigp, big), 1.f) < 0x1p118f)) {
+    put_row(sQ, qx);
+    put_row(sK, kx);
+#pragma unroll
+    for (int ks = 0; ks < NKS; ++ks)
+      an = mm<NT>(split8<NT>(qx + 8 * ks), split8<NT>(kx + 8 * ks), an);
+    floatx4 ps = pn;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int x = 4 * lq + r;
+      pt[r] = x < lr ? pt[r] : 0.f;
+      ps[r] = x > lr ? pn[r] : 0.f;
+    }
+    const Split4<NT> pts = split4<NT>(pt), pns = split4<NT>(ps);
+    wave_sync();
+#pragma unroll
+    for (int D = 0; D < ND; ++D) {
+      gqd[D] = mm16<NT>(cols4(&sK[0][16 * wave][colblk(D)], KPL, rdK), pts, gqd[D]);
+      gkd[D] = mm16<NT>(cols4(&sQ[0][16 * wave][colblk(D)], KPL, rdK), pns, gkd[D]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        gqd[D][r] *= fexp2(s[4 * D + r] - ref[4 * D + r]);
+        gkd[D][r] *= fexp2(ref[4 * D + r] - s[4 * D + r]);
+      }
+    }
+    wave_sync();  // these rows are written again below
+  } else {
+    // every pair on its own: 2^(s_i - s_j) <= 1 for j <= i
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sPd[wave][4 * lq + r][lr] = pn[r];
+    wave_sync();
+    for (int j = 0; j < 16; ++j) {
+      const int src = (lane & 48) | j;
+      const float pij = sPd[wave][lr][j], pji = sPd[wave][j][lr];
+      float aij = 0.f;
+#pragma unroll
+      for (int e = 0; e < NEL; ++e) {
+        const float sj = __shfl(s[e], src), kj = __shfl(k[e], src), qj = __shfl(q[e], src);
+        // token j as the key of this lane's query, and as the query of its key
+        const float fq = j <= lr ? fexp2(s[e] - sj) : 0.f;
+        const float fk = j > lr ? fexp2(sj - s[e]) : 0.f;
+        aij = fmaf(q[e] * kj, fq, aij);
+        if (j < lr) gqd[e / 4][e % 4] = fmaf(pij * kj, fq, gqd[e / 4][e % 4]);
+        if (j > lr) gkd[e / 4][e % 4] = fmaf(pji * qj, fk, gkd[e / 4][e % 4]);
+      }
+      aij += __shfl_xor(aij, 16);
+      aij += __shfl_xor(aij, 32);
+      if (lq == 0) sAd[wave][lr][j] = aij;
+    }
+    wave_sync();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) an[r] = sAd[wave][4 * lq + r][lr];
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) an[r] = 4 * lq + r >= lr ? an[r] : 0.f;
+  {
+    const Split4<NT> as = split4<NT>(an);
+#pragma unroll
+    for (int E = 0; E < NE; ++E)
+      gva[E] = mm16<NT>(cols4(&sO[0][16 * wave][colblk(E)], VPL, rdV), as, gva[E]);
+  }
+  // -- q~ and k~ for the other sub-blocks
+#pragma unroll
+  for (int e = 0; e < NEL; ++e) {
+    qx[e] = q[e] * fexp2(s[e]);
+    kx[e] = k[e] * fexp2(tot[e] - s[e]);
+  }
+  put_row(sQ, qx);
+  put_row(sK, kx);
+  // -- gq from the entering state, S_n go
+  floatx4 gqa[ND];
+#pragma unroll
+  for (int D = 0; D < ND; ++D) {
+    gqa[D] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < NES; ++ks)
+      gqa[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), os[ks], gqa[D]);
+  }
+  __syncthreads();  // S_n is read, q~ and k~ are written
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    const int u = tid + kThreads * i, d = u / LPR, e = 4 * (u % LPR);
+    const Split4<NT> sp = split4<NT>(dn[i]);
+    const int p = 32 * (e / 32) + 8 * ((e / 4) % 4) + 4 * ((e / 16) % 2);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) *reinterpret_cast<bf4*>(&sX[j][d][p]) = sp.t[j];
+  }
+  // -- gq from the earlier sub-blocks
+  for (int J = 0; J < wave; ++J) {
+    floatx4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < NES; ++ks)
+      p = mm<NT>(rows8(&sV[0][16 * J][0], VPL, VSTR, ks), os[ks], p);
+    const Split4<NT> ps = split4<NT>(p);
+    float tj[NEL];
+    table(sTot, J, tj);
+#pragma unroll
+    for (int D = 0; D < ND; ++D) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) gqa[D][r] *= fexp2(tj[4 * D + r]);
+      gqa[D] = mm16<NT>(cols4(&sK[0][16 * J][colblk(D)], KPL, rdK), ps, gqa[D]);
+    }
+  }
+  // -- gk and gv from the later sub-blocks; `m` is the decay (log2) of the
+  // sub-blocks strictly between
+  floatx4 gka[ND];
+#pragma unroll
+  for (int D = 0; D < ND; ++D) gka[D] = floatx4{0.f, 0.f, 0.f, 0.f};
+  float after[NEL];  // decay of all later sub-blocks
+#pragma unroll
+  for (int e = 0; e < NEL; ++e) after[e] = 0.f;
+  for (int I = wave + 1; I < NB; ++I) {
+    float ti[NEL];
+    table(sTot, I, ti);
+#pragma unroll
+    for (int e = 0; e < NEL; ++e) after[e] += ti[e];
+  }
+  float m[NEL];
+#pragma unroll
+  for (int e = 0; e < NEL; ++e) m[e] = after[e];
+  for (int I = NB - 1; I > wave; --I) {
+    floatx4 p = {0.f, 0.f, 0.f, 0.f}, a = p;
+#pragma unroll
+    for (int ks = 0; ks < NES; ++ks)
+      p = mm<NT>(rows8(&sO[0][16 * I][0], VPL, VSTR, ks), vs[ks], p);
+    float ti[NEL];
+    table(sTot, I, ti);
+#pragma unroll
+    for (int ks = 0; ks < NKS; ++ks) {
+      float x[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        m[8 * ks + c] -= ti[8 * ks + c];
+        x[c] = kx[8 * ks + c] * fexp2(m[8 * ks + c]);
+      }
+      a = mm<NT>(rows8(&sQ[0][16 * I][0], KPL, KSTR, ks), split8<NT>(x), a);
+    }
+    const Split4<NT> ps = split4<NT>(p), as = split4<NT>(a);
+#pragma unroll
+    for (int D = 0; D < ND; ++D) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) gka[D][r] *= fexp2(ti[4 * D + r]);
+      gka[D] = mm16<NT>(cols4(&sQ[0][16 * I][colblk(D)], KPL, rdK), ps, gka[D]);
+    }
+#pragma unroll
+    for (int E = 0; E < NE; ++E)
+      gva[E] = mm16<NT>(cols4(&sO[0][16 * I][colblk(E)], VPL, rdV), as, gva[E]);
+  }
+  __syncthreads();  // D_n is written
+  // -- gk and gv from the state behind the chunk
+  floatx4 gks[ND];
+#pragma unroll
+  for (int D = 0; D < ND; ++D) {
+    gks[D] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < NES; ++ks)
+      gks[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), vs[ks], gks[D]);
+  }
+#pragma unroll
+  for (int ks = 0; ks < NKS; ++ks) {
+    float x[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = kx[8 * ks + c] * fexp2(after[8 * ks + c]);
+    const Split8<NT> xs = split8<NT>(x);
+#pragma unroll
+    for (int E = 0; E < NE; ++E) {
+      Split8<NT> dt;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        dt.t[i] = join(rdV(&sX[i][32 * ks][colblk(E)]), rdV(&sX[i][32 * ks + 16][colblk(E)]));
+      gva[E] = mm<NT>(dt, xs, gva[E]);
+    }
+  }
+  // -- the decay's gradient: suffix sums of q gq - k gk^pairs, sums of
+  // k gk^state over the tokens before
+  float z[NEL], w[NEL], g2[NEL];
+#pragma unroll
+  for (int D = 0; D < ND; ++D) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int e = 4 * D + r;
+      const float fq = fexp2(s[e]), fk = fexp2(tot[e] - s[e]);
+      gqd[D][r] = fmaf(gqa[D][r], fq, gqd[D][r]);
+      gkd[D][r] = fmaf(gka[D][r], fk, gkd[D][r]);
+      gks[D][r] *= fexp2(tot[e] - s[e] + after[e]);
+      z[e] = row_suffix16(fmaf(q[e], gqd[D][r], -k[e] * gkd[D][r]));
+      w[e] = row_scan16(k[e] * gks[D][r]);
+      g2[e] = z[e] + row_before16(w[e]);
+    }
+    if (lr == 0) *reinterpret_cast<floatx4*>(&sZ[wave][dim(D)]) = floatx4{z[4 * D], z[4 * D + 1], z[4 * D + 2], z[4 * D + 3]};
+    if (lr == 15) *reinterpret_cast<floatx4*>(&sW[wave][dim(D)]) = floatx4{w[4 * D], w[4 * D + 1], w[4 * D + 2], w[4 * D + 3]};
+  }
+  __syncthreads();
+  const float self = sSelf[t];
+  float before[NEL];  // decay of the earlier sub-blocks
+#pragma unroll
+  for (int e = 0; e < NEL; ++e) before[e] = 0.f;
+  for (int J = 0; J < NB; ++J) {
+    if (J == wave) continue;
+    float x[NEL], tj[NEL];
+    table(J < wave ? sW : sZ, J, x);
+    table(sTot, J, tj);
+#pragma unroll
+    for (int e = 0; e < NEL; ++e) {
+      g2[e] += x[e];
+      before[e] += J < wave ? tj[e] : 0.f;
+    }
+  }
+#pragma unroll
+  for (int D = 0; D < ND; ++D) {
+    const floatx4 ad = *reinterpret_cast<const floatx4*>(&sAD[dim(D)]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int e = 4 * D + r;
+      g2[e] = fmaf(fexp2(before[e] + tot[e] + after[e]), ad[r], g2[e]);
+      gqd[D][r] = fmaf(self, k[e], gqd[D][r]);
+      gkd[D][r] = fmaf(self, q[e], gkd[D][r] + gks[D][r]);
+    }
+  }
+  if (!pad) {
+#pragma unroll
+    for (int D = 0; D < ND; ++D) {
+      const float x[4] = {gqd[D][0], gqd[D][1], gqd[D][2], gqd[D][3]};
+      const float y[4] = {gkd[D][0], gkd[D][1], gkd[D][2], gkd[D][3]};
+      store4(gqp + row * DK + dim(D), x);
+      store4(gkp + row * DK + dim(D), y);
+      store4(ggp + row * DK + dim(D), g2 + 4 * D);
+    }
+#pragma unroll
+    for (int E = 0; E < NE; ++E) {
+      const float x[4] = {gva[E][0], gva[E][1], gva[E][2], gva[E][3]};
+      store4(gvp + row * DV + dim(E), x);
+    }
+  }
+}
+
+template <int DK, int DV, typename InT>
+hipError_t bwd_t(const Problem& p, int b0, int nb, const DirPack& dirs, const BwdArgs& a, char* ws,
+                 hipStream_t s) {
+  constexpr int NT = sizeof(InT) == 2 ? 2 : 3;
+  const BwdLayout w = bwd_layout(p);
+  const long rows = (long)b0 * p.T * p.H, bh0 = (long)b0 * p.H, bhn = bh0 * p.N;
+  const InT* q = static_cast<const InT*>(a.q) + rows * DK;
+  const InT* k = static_cast<const InT*>(a.k) + rows * DK;
+  const InT* v = static_cast<const InT*>(a.v) + rows * DV;
+  const InT* g = static_cast<const InT*>(a.gk) + rows * DK;
+  const InT* go = static_cast<const InT*>(a.go) + rows * DV;
+  float* S = reinterpret_cast<float*>(ws + w.off_S) + bhn * DK * DV;
+  float* D = reinterpret_cast<float*>(ws + w.off_D) + bhn * DK * DV;
+  float* A = reinterpret_cast<float*>(ws + w.off_a) + bhn * DK;
+  hipLaunchKernelGGL((bwd_summary_kernel<DK, DV, InT, NT>), dim3(p.N, p.H, 2 * nb), dim3(kThreads),
+                     0, s, k, v, q, go, g, S, D, A, p.T, p.H, p.N, p.gh, p.gw, dirs);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const long groups = (long)nb * p.H * (DK * DV / 4);
+  hipLaunchKernelGGL((bwd_scan_kernel<8>), dim3((unsigned)((groups + kThreads - 1) / kThreads), 2),
+                     dim3(kThreads), 0, s, S, D, A, a.s0 ? a.s0 + bh0 * DK * DV : nullptr,
+                     a.gs_final ? a.gs_final + bh0 * DK * DV : nullptr,
+                     a.gs0 ? a.gs0 + bh0 * DK * DV : nullptr, p.N, DK, DV, groups);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((bwd_grad_kernel<DK, DV, InT, NT>), dim3(p.N, p.H, nb), dim3(kThreads), 0, s,
+                     q, k, v, g, go, S, D, static_cast<InT*>(a.gq) + rows * DK,
+                     static_cast<InT*>(a.gkey) + rows * DK, static_cast<InT*>(a.gv) + rows * DV,
+                     static_cast<InT*>(a.ggk) + rows * DK, p.T, p.H, p.N, p.gh, p.gw, dirs);
+  return hipGetLastError();
+}
+
+}  // namespace bwd
+
+BwdLayout bwd_layout(const Problem& p) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  const size_t units = (size_t)p.B * p.H * p.N;
+  BwdLayout w;
+  w.off_S = 0;
+  w.off_D = up(units * p.dk * p.dv * sizeof(float));
+  w.off_a = 2 * w.off_D;
+  w.total = w.off_a + up(units * p.dk * sizeof(float));
+  return w;
+}
+
+hipError_t launch_bwd(const Problem& p, int b0, int nb, const DirPack& dirs, const BwdArgs& a,
+                      char* ws, hipStream_t s) {
+  const bool f16 = p.dtype == 0;
+#define GLA_BWD_CASE(DK, DV)                                                                   \
+  if (p.dk == DK && p.dv == DV)                                                                \
+    return f16 ? bwd::bwd_t<DK, DV, half_t>(p, b0, nb, dirs, a, ws, s)                         \
+               : bwd::bwd_t<DK, DV, float>(p, b0, nb, dirs, a, ws, s);
+  GLA_BWD_CASE(32, 32)
+  GLA_BWD_CASE(32, 64)
+  GLA_BWD_CASE(64, 32)
+  GLA_BWD_CASE(64, 64)
+#undef GLA_BWD_CASE
+  return hipErrorInvalidValue;
+}
+
+}  // namespace gla

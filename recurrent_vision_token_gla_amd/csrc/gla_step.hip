@@ -1,0 +1,129 @@
+// One new token per sequence: S <- diag(exp(gk)) S + k^T v, o = q S, on states
+// held in a pool (float [slot][H][dk][dv]), optionally with the block's output
+// gate on o. The serving form of the recurrence: the state is read and written
+// once, 8 dk dv bytes per (row, head) against 5 dk dv flops, so the memory
+// bounds it (and the launch, for a few rows).
+//
+// One workgroup per (row, head). A thread holds four neighbouring value
+// columns of every (256 / (dv/4))-th key dim, so a wave's accesses are
+// contiguous, and all of them are in flight before the first is used. The sum
+// over key dims goes through lane permutations and then LDS, in a fixed order.
+//
+// Rows of one call that name the same slot are consecutive tokens of one
+// sequence: the workgroup of the first such row applies all of them in row
+// order with the state in registers, and those of the others leave. Every wave
+// finds them by comparing the call's slots, 64 at a time.
+#include "gla_step.h"
+#include "gla_tile.h"
+
+namespace gla {
+namespace step {
+
+template <int DK, int DV, typename InT, bool kGate>
+__global__ __launch_bounds__(kThreads) void step_kernel(
+    const InT* __restrict__ qp, const InT* __restrict__ kp, const InT* __restrict__ vp,
+    const InT* __restrict__ gp, const InT* __restrict__ zp, const float* __restrict__ nw, float eps,
+    InT* __restrict__ op, float* __restrict__ state, long n_slots, const int32_t* __restrict__ slots,
+    int B, int H) {
+  constexpr int LPR = DV / 4, RPP = kThreads / LPR, NG = DK / RPP;
+  static_assert(DK % RPP == 0, "whole passes over the key dims");
+  __shared__ float sPart[kThreads / 64][DV];
+  const int h = blockIdx.x, b = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int e4 = 4 * (tid % LPR), d0 = tid / LPR;
+  const long slot = slots ? (long)slots[b] : (long)b;
+  if (slot < 0 || slot >= n_slots) return;  // a padding row
+  float* S = state + (slot * H + h) * (long)(DK * DV) + d0 * DV + e4;
+  floatx4 s[NG];
+#pragma unroll
+  for (int i = 0; i < NG; ++i) s[i] = *reinterpret_cast<const floatx4*>(S + i * RPP * DV);
+  if (slots) {
+    for (int j0 = 0; j0 < b; j0 += 64) {
+      const int j = j0 + lane;
+      if (__any(j < b && slots[j < b ? j : b] == (int32_t)slot)) return;  // the first such row does this one
+    }
+  }
+  for (int r = b;;) {
+    const long row = (long)r * H + h;
+    float x[4], o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = (float)vp[row * DV + e4 + c];
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const long at = row * DK + d0 + i * RPP;
+      const float a = tile::fexp2((float)gp[at] * kLog2e), kd = (float)kp[at], qd = (float)qp[at];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        s[i][c] = fmaf(a, s[i][c], kd * x[c]);
+        o[c] = fmaf(qd, s[i][c], o[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+      for (int m = LPR; m < 64; m <<= 1) o[c] += __shfl_xor(o[c], m);
+    }
+    if (lane < LPR) *reinterpret_cast<floatx4*>(&sPart[wave][e4]) = floatx4{o[0], o[1], o[2], o[3]};
+    __syncthreads();
+    if (tid < DV) {
+      float y = 0.f;
+#pragma unroll
+      for (int w = 0; w < kThreads / 64; ++w) y += sPart[w][tid];
+      if constexpr (kGate) {
+        const float z = (float)zp[row * DV + tid];
+        float ss = y * y;
+#pragma unroll
+        for (int m = 1; m < DV; m <<= 1) ss += __shfl_xor(ss, m);
+        const float sig = __builtin_amdgcn_rcpf(1.f + tile::fexp2(-z * kLog2e));
+        y *= __builtin_amdgcn_rsqf(ss * (1.f / DV) + eps) * nw[tid] * z * sig;
+      }
+      op[row * DV + tid] = (InT)y;
+    }
+    // the next row of the same sequence
+    int next = B;
+    if (slots) {
+      for (int j0 = (r + 1) & ~63; j0 < B; j0 += 64) {
+        const int j = j0 + lane;
+        const unsigned long long hit =
+            __ballot(j > r && j < B && slots[j < B ? j : B - 1] == (int32_t)slot);
+        if (hit) {
+          next = j0 + __builtin_ctzll(hit);
+          break;
+        }
+      }
+    }
+    if (next >= B) break;
+    r = next;
+    __syncthreads();  // sPart is read
+  }
+#pragma unroll
+  for (int i = 0; i < NG; ++i) *reinterpret_cast<floatx4*>(S + i * RPP * DV) = s[i];
+}
+
+template <int DK, int DV, typename InT>
+hipError_t step_t(const StepArgs& a, hipStream_t s) {
+  auto kernel = a.epi.gate ? step_kernel<DK, DV, InT, true> : step_kernel<DK, DV, InT, false>;
+  hipLaunchKernelGGL(kernel, dim3(a.H, a.B), dim3(kThreads), 0, s, static_cast<const InT*>(a.q),
+                     static_cast<const InT*>(a.k), static_cast<const InT*>(a.v),
+                     static_cast<const InT*>(a.gk), static_cast<const InT*>(a.epi.gate),
+                     a.epi.weight, a.epi.eps, static_cast<InT*>(a.out), a.state, a.n_slots, a.slots,
+                     a.B, a.H);
+  return hipGetLastError();
+}
+
+}  // namespace step
+
+hipError_t launch_step(const StepArgs& a, hipStream_t s) {
+  const bool f16 = a.dtype == 0;
+#define GLA_STEP_CASE(DK, DV)              \
+  if (a.dk == DK && a.dv == DV)            \
+    return f16 ? step::step_t<DK, DV, half_t>(a, s) : step::step_t<DK, DV, float>(a, s);
+  GLA_STEP_CASE(32, 32)
+  GLA_STEP_CASE(32, 64)
+  GLA_STEP_CASE(64, 32)
+  GLA_STEP_CASE(64, 64)
+#undef GLA_STEP_CASE
+  return hipErrorInvalidValue;
+}
+
+}  // namespace gla

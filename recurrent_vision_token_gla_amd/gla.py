@@ -6,6 +6,7 @@ no fallback: if the library is not built, or a call fails, this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import weakref
@@ -28,7 +29,10 @@ EXPORTS = ["gla_abi_version", "gla_fwd_workspace_bytes", "gla_workspace_layout",
            "gla_fwd_state", "gla_fwd_gated", "gla_fwd_schedule", "gla_auto_schedule", "gla_workspace_init",
            "gla_workspace_release", "gla_workspace_is_prepared", "gla_workspace_status",
            "gla_chunk_summaries", "gla_spatial_swiglu", "gla_state_scan", "gla_chunk_outputs", "gla_scan_perm",
-           "gla_status_string", "gla_last_error_detail", "gla_fwd_noalloc"]
+           "gla_status_string", "gla_last_error_detail", "gla_fwd_noalloc",
+           "gla_bwd_workspace_bytes", "gla_bwd", "gla_step", "gla_step_gated", "gla_add_rmsnorm",
+           "gla_add_rmsnorm_q8", "gla_add_rmsnorm_bwd_workspace_bytes", "gla_add_rmsnorm_bwd",
+           "gla_gate_bwd_workspace_bytes", "gla_gate_bwd"]
 
 # With check_errors(True), every forward call made through this module waits
 # for its stream and raises if the workspace's sticky error word is set
@@ -44,6 +48,7 @@ def check_errors(on: bool) -> None:
 _lib = None
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _i32p = ctypes.POINTER(ctypes.c_int32)
+_i64, _f32 = ctypes.c_int64, ctypes.c_float
 
 
 class GLAError(RuntimeError):
@@ -102,6 +107,27 @@ def load():
     lib.gla_scan_perm.argtypes = [_vp, _i32, _i32, _i32, _vp]
     lib.gla_spatial_swiglu.restype = _i32
     lib.gla_spatial_swiglu.argtypes = [_vp] * 5 + [_i32] * 5 + [_vp]
+    lib.gla_bwd_workspace_bytes.restype = _sz
+    lib.gla_bwd_workspace_bytes.argtypes = [_i32] * 6
+    lib.gla_bwd.restype = _i32
+    lib.gla_bwd.argtypes = [_vp] * 9 + [_i32] * 6 + [_i32p, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.gla_step.restype = _i32
+    lib.gla_step.argtypes = [_vp] * 5 + [_i32] * 5 + [_vp, _i64, _vp, _vp]
+    lib.gla_step_gated.restype = _i32
+    lib.gla_step_gated.argtypes = [_vp] * 6 + [_f32, _vp] + [_i32] * 5 + [_vp, _i64, _vp, _vp]
+    lib.gla_add_rmsnorm.restype = _i32
+    lib.gla_add_rmsnorm.argtypes = [_vp] * 3 + [_f32, _vp, _vp, _i64, _i32, _i32, _vp]
+    lib.gla_add_rmsnorm_q8.restype = _i32
+    lib.gla_add_rmsnorm_q8.argtypes = [_vp] * 3 + [_f32, _vp, _vp, _vp, _i64, _i32, _i32, _vp]
+    lib.gla_add_rmsnorm_bwd_workspace_bytes.restype = _sz
+    lib.gla_add_rmsnorm_bwd_workspace_bytes.argtypes = [_i64, _i32]
+    lib.gla_add_rmsnorm_bwd.restype = _i32
+    lib.gla_add_rmsnorm_bwd.argtypes = ([_vp, _vp, _f32] + [_vp] * 4 + [_i64, _i32, _i32, _vp, _sz,
+                                                                        _vp])
+    lib.gla_gate_bwd_workspace_bytes.restype = _sz
+    lib.gla_gate_bwd_workspace_bytes.argtypes = [_i64, _i32]
+    lib.gla_gate_bwd.restype = _i32
+    lib.gla_gate_bwd.argtypes = [_vp, _vp, _vp, _f32] + [_vp] * 4 + [_i64, _i32, _i32, _vp, _sz, _vp]
     lib.gla_status_string.restype = ctypes.c_char_p
     lib.gla_status_string.argtypes = [_i32]
     lib.gla_last_error_detail.restype = ctypes.c_char_p
@@ -480,3 +506,232 @@ def spatial_swiglu(a: torch.Tensor, u: torch.Tensor, weight: torch.Tensor,
                                        B, grid_h, grid_w, Fc, _dtype_code(u), _stream_ptr(stream))
     _check(st, "gla_spatial_swiglu")
     return out
+
+
+# ---- gradients, single tokens and the norm before a mixer ---------------------
+
+@contextlib.contextmanager
+def _launching(device, stream, *inputs):
+    """Device and stream of a call, as the raw stream pointer. On a stream
+    other than the current one, what the call allocates belongs to that stream
+    and the caller's tensors are not reused before its work is done (the
+    caller orders the streams themselves)."""
+    with _on_device(device):
+        if stream is None:
+            yield _stream_ptr(None)
+            return
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            if not torch.cuda.is_current_stream_capturing():
+                for t in inputs:
+                    if t is not None:
+                        t.record_stream(stream)
+            yield _stream_ptr(stream)
+
+
+def _like(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
+    if not t.is_cuda or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+    """The caller's workspace or a new one (inside _launching)."""
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    return workspace
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def bwd_workspace_bytes(B, H, grid_h, grid_w, dk, dv) -> int:
+    return int(load().gla_bwd_workspace_bytes(B, H, grid_h, grid_w, dk, dv))
+
+
+def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gk: torch.Tensor, go: torch.Tensor,
+        grid_h: int, grid_w: int, direction: Union[int, Sequence[int]] = L2R,
+        s0: Optional[torch.Tensor] = None, gs_final: Optional[torch.Tensor] = None,
+        return_gs0: bool = False, gs0: Optional[torch.Tensor] = None,
+        out: Optional[Sequence[torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
+        stream: Optional[torch.cuda.Stream] = None):
+    """Gradients (gq, gkey, gv, ggk) of the forward's q, k, v, gk from go =
+    dL/do, along the same direction and from the same s0 (None for zero);
+    gs_final [B, H, dk, dv] float32 is the gradient of the final state (None
+    for zero). With return_gs0 the gradient of s0 follows (in gs0 if given,
+    which may be gs_final). out: four tensors to write the gradients to."""
+    B, T, H, dk, dv = _shapes(q, k, v, gk, grid_h, grid_w)
+    _like(go, (B, T, H, dv), q.dtype, q.device, "go")
+    p0 = _state_ptr(s0, B, H, dk, dv, "s0", q.device)
+    pf = _state_ptr(gs_final, B, H, dk, dv, "gs_final", q.device)
+    if gs0 is not None and not return_gs0:
+        raise ValueError("gs0 is written with return_gs0 only")
+    if out is not None and len(out) != 4:
+        raise ValueError("out must be four tensors (gq, gkey, gv, ggk)")
+    with _launching(q.device, stream, q, k, v, gk, go, s0, gs_final, gs0, workspace, *(out or ())) as st_ptr:
+        outs = tuple(_out(None if out is None else out[i], t.shape, q.dtype, q.device)
+                     for i, t in enumerate((q, k, v, gk)))
+        if return_gs0 and gs0 is None:
+            gs0 = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        pg = _state_ptr(gs0, B, H, dk, dv, "gs0", q.device)
+        if return_gs0 and T == 0 and gs0 is not gs_final:  # no token: the state passes through
+            gs0.zero_() if gs_final is None else gs0.copy_(gs_final)
+        workspace = _scratch(workspace, bwd_workspace_bytes(B, H, grid_h, grid_w, dk, dv), q.device)
+        ws, nws = _ws(workspace, q.device)
+        st = load().gla_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), gk.data_ptr(), go.data_ptr(),
+                            *[t.data_ptr() for t in outs], B, H, grid_h, grid_w, dk, dv,
+                            _dirs(direction, B), _dtype_code(q), p0, pf, pg, ws, nws, st_ptr)
+    _check(st, "gla_bwd")
+    return outs + (gs0,) if return_gs0 else outs
+
+
+def _step(q, k, v, gk, state, slots, out, stream, gate=None, norm_weight=None, eps=0.0):
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, gk must be [B, H, dk] and v [B, H, dv]")
+    B, H, dk = q.shape
+    dv, dev = v.shape[-1], q.device
+    for name, t, d in (("q", q, dk), ("k", k, dk), ("v", v, dv), ("gk", gk, dk)):
+        _like(t, (B, H, d), q.dtype, dev, name)
+    if state.dim() != 4:
+        raise ValueError("state must be [n_slots, H, dk, dv]")
+    _like(state, (state.shape[0], H, dk, dv), torch.float32, dev, "state")
+    if slots is not None:
+        _like(slots, (B,), torch.int32, dev, "slots")
+    elif state.shape[0] < B:
+        raise ValueError(f"{B} rows without slots need as many states, got {state.shape[0]}")
+    if gate is not None:
+        _like(gate, (B, H, dv), q.dtype, dev, "gate")
+        _like(norm_weight, (dv,), torch.float32, dev, "norm_weight")
+    with _launching(dev, stream, q, k, v, gk, state, slots, out, gate, norm_weight) as st_ptr:
+        out = _out(out, (B, H, dv), q.dtype, dev)
+        tail = (out.data_ptr(), B, H, dk, dv, _dtype_code(q), state.data_ptr(), state.shape[0],
+                _ptr(slots), st_ptr)
+        if gate is None:
+            st = load().gla_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), gk.data_ptr(), *tail)
+        else:
+            st = load().gla_step_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), gk.data_ptr(),
+                                       gate.data_ptr(), norm_weight.data_ptr(), float(eps), *tail)
+    _check(st, "gla_step" if gate is None else "gla_step_gated")
+    return out
+
+
+def step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gk: torch.Tensor, state: torch.Tensor,
+         slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One new token per row: state[slot] <- diag(exp(gk)) state[slot] + k^T v
+    in place, o = q state[slot]; q, k, gk [B, H, dk], v [B, H, dv], state
+    [n_slots, H, dk, dv] float32, slots [B] int32 (None: row b uses slot b).
+    A slot outside the pool marks a padding row: its row of `out` is left as
+    it was (unset in a new one). Rows of one slot are applied in row order."""
+    return _step(q, k, v, gk, state, slots, out, stream)
+
+
+def step_gated(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gk: torch.Tensor,
+               gate: torch.Tensor, norm_weight: torch.Tensor, eps: float, state: torch.Tensor,
+               slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """step with the output gate, y = RMSNorm(o) * norm_weight * silu(gate);
+    gate [B, H, dv] in q's dtype, norm_weight [dv] float32."""
+    return _step(q, k, v, gk, state, slots, out, stream, gate, norm_weight, eps)
+
+
+def _norm_args(x, residual, weight):
+    if not x.is_cuda or not x.is_contiguous() or x.dim() < 1:
+        raise ValueError("x must be a contiguous device tensor [..., F]")
+    if residual is not None:
+        _like(residual, x.shape, x.dtype, x.device, "residual")
+    F = x.shape[-1]
+    _like(weight, (F,), torch.float32, x.device, "weight")
+    return (x.numel() // F if F else 0), F
+
+
+def add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor, eps: float,
+                out: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None):
+    """(y, s): s = x + residual (x if None) rounded to x's dtype, y =
+    RMSNorm(s) * weight; x [..., F] float16 or float32, weight [F] float32, F
+    a multiple of 8. out and sum_out may be x or residual (not the same one)."""
+    rows, F = _norm_args(x, residual, weight)
+    with _launching(x.device, stream, x, residual, weight, out, sum_out) as st_ptr:
+        y = _out(out, x.shape, x.dtype, x.device)
+        s = _out(sum_out, x.shape, x.dtype, x.device)
+        st = load().gla_add_rmsnorm(x.data_ptr(), _ptr(residual), weight.data_ptr(), float(eps),
+                                    s.data_ptr(), y.data_ptr(), rows, F, _dtype_code(x), st_ptr)
+    _check(st, "gla_add_rmsnorm")
+    return y, s
+
+
+def add_rmsnorm_q8(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor,
+                   eps: float, out: Optional[torch.Tensor] = None,
+                   scales: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None):
+    """(y8, scales, s): add_rmsnorm with y in float8_e4m3fn and a float32
+    scale per row (shape x.shape[:-1]): y8 * scale stands for y, the row's
+    largest |y| for 448."""
+    rows, F = _norm_args(x, residual, weight)
+    with _launching(x.device, stream, x, residual, weight, out, scales, sum_out) as st_ptr:
+        y8 = _out(out, x.shape, torch.float8_e4m3fn, x.device)
+        sc = _out(scales, x.shape[:-1], torch.float32, x.device)
+        s = _out(sum_out, x.shape, x.dtype, x.device)
+        st = load().gla_add_rmsnorm_q8(x.data_ptr(), _ptr(residual), weight.data_ptr(), float(eps),
+                                       s.data_ptr(), y8.data_ptr(), sc.data_ptr(), rows, F,
+                                       _dtype_code(x), st_ptr)
+    _check(st, "gla_add_rmsnorm_q8")
+    return y8, sc, s
+
+
+def add_rmsnorm_bwd(s: torch.Tensor, weight: torch.Tensor, eps: float, gy: torch.Tensor,
+                    gsum: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    gweight: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None):
+    """(gx, gweight) of add_rmsnorm from its s and gy = dL/dy; gsum is the
+    gradient that reaches s itself (None for none). gx is the gradient of x
+    and of residual; out may be s, gy or gsum. gweight [F] float32."""
+    rows, F = _norm_args(s, gsum, weight)
+    _like(gy, s.shape, s.dtype, s.device, "gy")
+    if rows == 0 and F > 0:  # no rows: a sum of nothing
+        gw = _out(gweight, (F,), torch.float32, s.device).zero_()
+        return _out(out, s.shape, s.dtype, s.device), gw
+    with _launching(s.device, stream, s, weight, gy, gsum, out, gweight, workspace) as st_ptr:
+        gx = _out(out, s.shape, s.dtype, s.device)
+        gw = _out(gweight, (F,), torch.float32, s.device)
+        workspace = _scratch(workspace, int(load().gla_add_rmsnorm_bwd_workspace_bytes(rows, F)), s.device)
+        ws, nws = _ws(workspace, s.device)
+        st = load().gla_add_rmsnorm_bwd(s.data_ptr(), weight.data_ptr(), float(eps), gy.data_ptr(),
+                                        _ptr(gsum), gx.data_ptr(), gw.data_ptr(), rows, F,
+                                        _dtype_code(s), ws, nws, st_ptr)
+    _check(st, "gla_add_rmsnorm_bwd")
+    return gx, gw
+
+
+def gate_bwd(o: torch.Tensor, gate: torch.Tensor, norm_weight: torch.Tensor, eps: float,
+             gy: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None,
+             gnorm_weight: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """(go, ggate, gnorm_weight) of the output gate y = RMSNorm(o) *
+    norm_weight * silu(gate) (fwd_gated's, with o what fwd gives); o, gate, gy
+    [..., dv]; norm_weight and its gradient [dv] float32. out: two tensors to
+    write go and ggate to."""
+    rows, dv = _norm_args(o, gate, norm_weight)
+    _like(gy, o.shape, o.dtype, o.device, "gy")
+    if out is not None and len(out) != 2:
+        raise ValueError("out must be two tensors (go, ggate)")
+    if rows == 0 and dv > 0:
+        gw = _out(gnorm_weight, (dv,), torch.float32, o.device).zero_()
+        return (_out(out[0] if out else None, o.shape, o.dtype, o.device),
+                _out(out[1] if out else None, o.shape, o.dtype, o.device), gw)
+    with _launching(o.device, stream, o, gate, norm_weight, gy, gnorm_weight, workspace,
+                    *(out or ())) as st_ptr:
+        go = _out(out[0] if out else None, o.shape, o.dtype, o.device)
+        gz = _out(out[1] if out else None, o.shape, o.dtype, o.device)
+        gw = _out(gnorm_weight, (dv,), torch.float32, o.device)
+        workspace = _scratch(workspace, int(load().gla_gate_bwd_workspace_bytes(rows, dv)), o.device)
+        ws, nws = _ws(workspace, o.device)
+        st = load().gla_gate_bwd(o.data_ptr(), gate.data_ptr(), norm_weight.data_ptr(), float(eps),
+                                 gy.data_ptr(), go.data_ptr(), gz.data_ptr(), gw.data_ptr(), rows, dv,
+                                 _dtype_code(o), ws, nws, st_ptr)
+    _check(st, "gla_gate_bwd")
+    return go, gz, gw
