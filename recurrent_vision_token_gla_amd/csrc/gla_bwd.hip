@@ -129,16 +129,31 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-__device__ __forceinline__ void load4(const half_t* p, float* x) {
-  const half4 h = *reinterpret_cast<const half4*>(p);
+// A lane's values of a token row as loaded (half inputs stay packed, and are
+// converted where a product uses them).
+template <typename InT, int NEL> struct Raw {
+  typedef InT V4 __attribute__((ext_vector_type(4)));
+  V4 v[NEL / 4];
+  __device__ __forceinline__ void load(const InT* p) {  // dims 16 D + 0..3 from p
 #pragma unroll
-  for (int c = 0; c < 4; ++c) x[c] = (float)h[c];
-}
-__device__ __forceinline__ void load4(const float* p, float* x) {
-  const floatx4 f = *reinterpret_cast<const floatx4*>(p);
+    for (int D = 0; D < NEL / 4; ++D) v[D] = *reinterpret_cast<const V4*>(p + 16 * D);
+  }
+  __device__ __forceinline__ void zero_if(bool pad) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) x[c] = f[c];
-}
+    for (int D = 0; D < NEL / 4; ++D) v[D] = pad ? V4{} : v[D];
+  }
+  __device__ __forceinline__ float operator[](int e) const { return (float)v[e / 4][e % 4]; }
+  // the eight values of dims 32 ks + ..: packed, or in bf16 terms
+  __device__ __forceinline__ auto pack8(int ks) const {
+    return __builtin_shufflevector(v[2 * ks], v[2 * ks + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  template <int NT> __device__ __forceinline__ Split8<NT> terms(int ks) const {
+    float x[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = (*this)[8 * ks + c];
+    return split8<NT>(x);
+  }
+};
 __device__ __forceinline__ void store4(half_t* p, const float* x) {
   *reinterpret_cast<half4*>(p) = half4{(half_t)x[0], (half_t)x[1], (half_t)x[2], (half_t)x[3]};
 }
@@ -328,38 +343,43 @@ __global__ __launch_bounds__(kThreads) void bwd_scan_kernel(float* __restrict__ 
 // meet in registers. LDS rows hold dim d at place 32 ks + 8 lq + 4 h + r, so
 // that a lane's eight values are 16 contiguous bytes.
 //
-// With s the cumulative decay inside a sub-block and tot its last value,
-//   q~ = q 2^s,  k~ = k 2^(tot-s),  2^(b_i-b_j) = 2^s_i 2^(tot_J-s_j) prod 2^tot
-// over the sub-blocks between: all factors <= 1. The products over earlier
-// (gq) and later (gk) sub-blocks are accumulated farthest first and decayed
-// from one sub-block to the next. Inside a sub-block one reference at its 8th
-// token, q' = q 2^(s-s7) and k' = k 2^(s7-s), spans decays up to 2^88; a
-// sub-block that decays more sums its pairs directly in float.
+// With s the cumulative decay inside a sub-block (log2), tot its last value
+// and ref its value at the 8th token, the rows kept in LDS are
+//   qx = q 2^(s-ref),  kx = k 2^(ref-s),
+// so the pairs inside the sub-block need no other factor, and pairs of two
+// sub-blocks I > J only factors by dim, all <= 1 (tables in LDS):
+//   2^(b_i-b_j) = 2^(s_i-ref_I) [2^ref_I prod_{J<M<I} 2^tot_M 2^(tot_J-ref_J)] 2^(ref_J-s_j).
+// Every product stays finite while qx and kx are below 2^84 (P is at most 64
+// products of two values up to 65504). A sub-block that decays more keeps
+// q 2^s and k 2^(tot-s) instead (its bracket then holds 1 for the two outer
+// factors) and sums its own pairs directly in float.
 // ===========================================================================
-constexpr float kMaxSpan = 88.f;
+constexpr float kMaxSpan = 84.f;
 
 template <int DK, int DV, typename InT, int NT>
-__global__ __launch_bounds__(kThreads) void bwd_grad_kernel(
+__global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_kernel(
     const InT* __restrict__ qp, const InT* __restrict__ kp, const InT* __restrict__ vp,
     const InT* __restrict__ gp, const InT* __restrict__ dop, const float* __restrict__ Sws,
     const float* __restrict__ Dws, InT* __restrict__ gqp, InT* __restrict__ gkp,
     InT* __restrict__ gvp, InT* __restrict__ ggp, int T, int H, int N, int gh, int gw,
     DirPack dirs) {
+  constexpr bool kHalf = sizeof(InT) == 2;
   constexpr int NKS = DK / 32, NES = DV / 32, ND = DK / 16, NE = DV / 16;
   constexpr int NEL = 4 * ND, NVL = 4 * NE;  // a lane's dims of q/k/g and of v/go
-  constexpr int KSTR = DK + 8, VSTR = DV + 8;
-  __shared__ __attribute__((aligned(16))) __bf16 sQ[NT][C][KSTR];
-  __shared__ __attribute__((aligned(16))) __bf16 sK[NT][C][KSTR];
-  __shared__ __attribute__((aligned(16))) __bf16 sO[NT][C][VSTR];   // go
-  __shared__ __attribute__((aligned(16))) __bf16 sV[NT][C][VSTR];
+  constexpr int KSTR = DK + 8, VSTR = DV + 8, NV = kHalf ? 1 : NT;
+  __shared__ __attribute__((aligned(16))) __bf16 sQ[NT][C][KSTR];   // qx
+  __shared__ __attribute__((aligned(16))) __bf16 sK[NT][C][KSTR];   // kx
+  __shared__ __attribute__((aligned(16))) __bf16 sO[NV][C][VSTR];   // go (half inputs: half bits)
+  __shared__ __attribute__((aligned(16))) __bf16 sV[NV][C][VSTR];   // v
   __shared__ __attribute__((aligned(16))) __bf16 sX[NT][DK][VSTR];  // S_n, then D_n
-  __shared__ __attribute__((aligned(16))) float sTot[NB][DK];  // a sub-block's decay, log2
-  __shared__ __attribute__((aligned(16))) float sRef[NB][DK];  // s at its 8th token
-  __shared__ __attribute__((aligned(16))) float sZ[NB][DK];    // its sum of q gq - k gk^pairs
-  __shared__ __attribute__((aligned(16))) float sW[NB][DK];    // its sum of k gk^state
-  __shared__ __attribute__((aligned(16))) float sAD[DK];       // <S_n, D_n> by rows
-  __shared__ float sSelf[C];                                   // P_tt
-  __shared__ float sPd[NB][16][17], sAd[NB][16][17];           // direct sub-blocks only
+  __shared__ __attribute__((aligned(16))) float sA[NB][DK];   // tot, later sums of q gq - k gk^pairs
+  __shared__ __attribute__((aligned(16))) float sB[NB][DK];   // ref, later sums of k gk^state
+  __shared__ __attribute__((aligned(16))) float sE[NB][DK];   // 2^tot
+  __shared__ __attribute__((aligned(16))) float sEQ[NB][DK];  // 2^ref (1 in a direct sub-block)
+  __shared__ __attribute__((aligned(16))) float sEK[NB][DK];  // 2^(tot-ref) (likewise)
+  __shared__ __attribute__((aligned(16))) float sAD[DK];      // <S_n, D_n> by rows
+  __shared__ float sSelf[C];                                  // P_tt
+  __shared__ int sDirect[NB];
   const int n = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lq = lane >> 4;
@@ -369,70 +389,37 @@ __global__ __launch_bounds__(kThreads) void bwd_grad_kernel(
   auto dim = [&](int D) { return 16 * D + 4 * lq; };
   auto place = [&](int ks) { return 32 * ks + 8 * lq; };
 
-  // -- this lane's token row
+  // -- this lane's token row, and the states at the chunk's ends
   const int rr = token_row(n * C + t, T, gh, gw, dir);
   const bool pad = rr < 0;
   const long row = ((long)b * T + (pad ? 0 : rr)) * H + h;
-  float q[NEL], k[NEL], s[NEL], v[NVL], go[NVL];
-#pragma unroll
-  for (int D = 0; D < ND; ++D) {
-    load4(qp + row * DK + dim(D), q + 4 * D);
-    load4(kp + row * DK + dim(D), k + 4 * D);
-    load4(gp + row * DK + dim(D), s + 4 * D);
-  }
-#pragma unroll
-  for (int E = 0; E < NE; ++E) {
-    load4(vp + row * DV + dim(E), v + 4 * E);
-    load4(dop + row * DV + dim(E), go + 4 * E);
-  }
-  // -- the states at the chunk's ends: S_n to LDS, D_n kept for later, their
-  // rows' inner products
+  Raw<InT, NEL> q, k, g;
+  Raw<InT, NVL> v, go;
+  g.load(gp + row * DK + dim(0));
+  q.load(qp + row * DK + dim(0));
+  k.load(kp + row * DK + dim(0));
+  v.load(vp + row * DV + dim(0));
+  go.load(dop + row * DV + dim(0));
   constexpr int NG = DK * DV / 4 / kThreads, LPR = DV / 4;  // groups of four per thread, per row
-  floatx4 dn[NG];
+  auto load_state = [&](const float* p, floatx4* x) {
 #pragma unroll
-  for (int i = 0; i < NG; ++i) {
-    const int u = tid + kThreads * i, d = u / LPR, e = 4 * (u % LPR);
-    const floatx4 sn = *reinterpret_cast<const floatx4*>(Sws + bhn * (DK * DV) + 4 * u);
-    dn[i] = *reinterpret_cast<const floatx4*>(Dws + bhn * (DK * DV) + 4 * u);
-    const Split4<NT> sp = split4<NT>(sn);
-    const int p = 32 * (e / 32) + 8 * ((e / 4) % 4) + 4 * ((e / 16) % 2);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) *reinterpret_cast<bf4*>(&sX[j][d][p]) = sp.t[j];
-    float dot = sn[0] * dn[i][0] + sn[1] * dn[i][1] + sn[2] * dn[i][2] + sn[3] * dn[i][3];
-#pragma unroll
-    for (int m = 1; m < LPR; m <<= 1) dot += __shfl_xor(dot, m);
-    if (e == 0) sAD[d] = dot;
+    for (int i = 0; i < NG; ++i)
+      x[i] = *reinterpret_cast<const floatx4*>(p + bhn * (DK * DV) + 4 * (tid + kThreads * i));
+  };
+  floatx4 sn[NG], dn[NG];
+  load_state(Sws, sn);
+  load_state(Dws, dn);
+  if ((n + 1) * C > T) {  // the chain's last chunk: padding rows are zeros without decay
+    g.zero_if(pad);
+    q.zero_if(pad);
+    k.zero_if(pad);
+    v.zero_if(pad);
+    go.zero_if(pad);
   }
+  float s[NEL];
 #pragma unroll
-  for (int e = 0; e < NEL; ++e) {
-    q[e] = pad ? 0.f : q[e];
-    k[e] = pad ? 0.f : k[e];
-    s[e] = row_scan16(pad ? 0.f : log2_decay(s[e]));
-  }
-#pragma unroll
-  for (int e = 0; e < NVL; ++e) {
-    v[e] = pad ? 0.f : v[e];
-    go[e] = pad ? 0.f : go[e];
-  }
-  if (lr == 15 || lr == 7) {
-    float(*dst)[DK] = lr == 15 ? sTot : sRef;
-#pragma unroll
-    for (int D = 0; D < ND; ++D)
-      *reinterpret_cast<floatx4*>(&dst[wave][dim(D)]) = floatx4{s[4 * D], s[4 * D + 1], s[4 * D + 2], s[4 * D + 3]};
-  }
-  Split8<NT> vs[NES], os[NES];  // this token's v and go as operands
-#pragma unroll
-  for (int ks = 0; ks < NES; ++ks) {
-    vs[ks] = split8<NT>(v + 8 * ks);
-    os[ks] = split8<NT>(go + 8 * ks);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      *reinterpret_cast<bf8*>(&sV[i][t][place(ks)]) = vs[ks].t[i];
-      *reinterpret_cast<bf8*>(&sO[i][t][place(ks)]) = os[ks].t[i];
-    }
-  }
-  __syncthreads();
-
+  for (int e = 0; e < NEL; ++e) s[e] = row_scan16(log2_decay(g[e]));
+  auto row4 = [&](const float* x, int D) { return floatx4{x[4 * D], x[4 * D + 1], x[4 * D + 2], x[4 * D + 3]}; };
   auto table = [&](const float(*tab)[DK], int J, float* x) {
 #pragma unroll
     for (int D = 0; D < ND; ++D) {
@@ -441,16 +428,73 @@ __global__ __launch_bounds__(kThreads) void bwd_grad_kernel(
       for (int r = 0; r < 4; ++r) x[4 * D + r] = f[r];
     }
   };
-  auto put_row = [&](__bf16(*tl)[C][KSTR], const float* x) {
+  if ((lr | 8) == 15) {
+    float(*dst)[DK] = lr == 15 ? sA : sB;
 #pragma unroll
-    for (int ks = 0; ks < NKS; ++ks) {
-      const Split8<NT> sp = split8<NT>(x + 8 * ks);
+    for (int D = 0; D < ND; ++D) *reinterpret_cast<floatx4*>(&dst[wave][dim(D)]) = row4(s, D);
+  }
+  // -- S_n to LDS, and the states' inner products by rows
+  auto put_state = [&](const floatx4* x) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) *reinterpret_cast<bf8*>(&tl[i][t][place(ks)]) = sp.t[i];
+    for (int i = 0; i < NG; ++i) {
+      const int u = tid + kThreads * i, d = u / LPR, e = 4 * (u % LPR);
+      const Split4<NT> sp = split4<NT>(x[i]);
+      const int p = 32 * (e / 32) + 8 * ((e / 4) % 4) + 4 * ((e / 16) % 2);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) *reinterpret_cast<bf4*>(&sX[j][d][p]) = sp.t[j];
     }
   };
-  // operand of 16 rows of a tile contracted along the row, and of 16 of its
-  // columns (block D) contracted along 16 rows
+  put_state(sn);
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    const int u = tid + kThreads * i;
+    float dot = sn[i][0] * dn[i][0] + sn[i][1] * dn[i][1] + sn[i][2] * dn[i][2] + sn[i][3] * dn[i][3];
+#pragma unroll
+    for (int m = 1; m < LPR; m <<= 1) dot += __shfl_xor(dot, m);
+    if (u % LPR == 0) sAD[u / LPR] = dot;
+  }
+  // -- v and go to LDS; P inside the sub-block: transposed (rows j) for gq,
+  // and rows i for gk
+  constexpr int KPL = C * KSTR, VPL = C * VSTR, XPL = DK * VSTR;
+  floatx4 pt = {0.f, 0.f, 0.f, 0.f}, pn = pt;
+#pragma unroll
+  for (int ks = 0; ks < NES; ++ks) {
+    if constexpr (kHalf) {
+      *reinterpret_cast<half8*>(&sV[0][t][place(ks)]) = v.pack8(ks);
+      *reinterpret_cast<half8*>(&sO[0][t][place(ks)]) = go.pack8(ks);
+      pt = mfma16x16x32(v.pack8(ks), go.pack8(ks), pt);
+      pn = mfma16x16x32(go.pack8(ks), v.pack8(ks), pn);
+    } else {
+      const Split8<NT> vs = v.template terms<NT>(ks), os = go.template terms<NT>(ks);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        *reinterpret_cast<bf8*>(&sV[i][t][place(ks)]) = vs.t[i];
+        *reinterpret_cast<bf8*>(&sO[i][t][place(ks)]) = os.t[i];
+      }
+      pt = mm<NT>(vs, os, pt);
+      pn = mm<NT>(os, vs, pn);
+    }
+  }
+  // P of this wave's queries with the keys of block J, transposed; and of the
+  // queries of block I with this wave's keys
+  auto p_with = [&](const __bf16(*tl)[C][VSTR], int I, const Raw<InT, NVL>& own) {
+    floatx4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < NES; ++ks) {
+      const __bf16* at = &tl[0][16 * I + lr][place(ks)];
+      if constexpr (kHalf) {
+        p = mfma16x16x32(*reinterpret_cast<const half8*>(at), own.pack8(ks), p);
+      } else {
+        Split8<NT> x;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) x.t[i] = *reinterpret_cast<const bf8*>(at + i * VPL);
+        p = mm<NT>(x, own.template terms<NT>(ks), p);
+      }
+    }
+    return p;
+  };
+  // operands from LDS: 16 rows of S or D, or of qx, contracted along the row;
+  // 16 columns (block D of the places) contracted along 16 rows
   auto rows8 = [&](const __bf16* tl, int plane, int str, int ks) {
     Split8<NT> sp;
 #pragma unroll
@@ -458,84 +502,77 @@ __global__ __launch_bounds__(kThreads) void bwd_grad_kernel(
       sp.t[i] = *reinterpret_cast<const bf8*>(tl + i * plane + lr * str + place(ks));
     return sp;
   };
-  auto cols4 = [&](const __bf16* tl, int plane, auto read) {
+  auto colblk = [](int D) { return 32 * (D / 2) + 4 * (D % 2); };
+  auto cols_k = [&](const __bf16(*tl)[C][KSTR], int I, int D) {
     Split4<NT> sp;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) sp.t[i] = read(tl + i * plane);
+    for (int i = 0; i < NT; ++i) sp.t[i] = tr4<KSTR, 4, 8>(&tl[i][16 * I][colblk(D)]);
     return sp;
   };
-  auto rdK = [](const __bf16* p) { return tr4<KSTR, 4, 8>(p); };
-  auto rdV = [](const __bf16* p) { return tr4<VSTR, 4, 8>(p); };
-  constexpr int KPL = C * KSTR, VPL = C * VSTR, XPL = DK * VSTR;
-  auto colblk = [](int D) { return 32 * (D / 2) + 4 * (D % 2); };  // place of column block D
+  auto cols_o = [&](int I, int E) {
+    if constexpr (kHalf) {
+      const half4 x = __builtin_bit_cast(half4, tr4<VSTR, 4, 8>(&sO[0][16 * I][colblk(E)]));
+      return split4<NT>(__builtin_convertvector(x, floatx4));
+    } else {
+      Split4<NT> sp;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) sp.t[i] = tr4<VSTR, 4, 8>(&sO[i][16 * I][colblk(E)]);
+      return sp;
+    }
+  };
 
-  // -- the sub-block's own pairs. P transposed (rows j) for gq; P and A (rows
-  // i) for gk and gv.
-  float tot[NEL], ref[NEL];
-  table(sTot, wave, tot);
-  table(sRef, wave, ref);
-  floatx4 pt = {0.f, 0.f, 0.f, 0.f}, pn = pt;
+  wave_sync();  // tot and ref
+  float cq[NEL], ck[NEL];  // the factors of qx and kx, which their gradients take too
+  {
+    float tot[NEL], ref[NEL], span = 0.f, big = 0.f;
+    table(sA, wave, tot);
+    table(sB, wave, ref);
 #pragma unroll
-  for (int ks = 0; ks < NES; ++ks) {
-    pt = mm<NT>(vs[ks], os[ks], pt);
-    pn = mm<NT>(os[ks], vs[ks], pn);
-  }
-  float span = 0.f, big = 0.f, bigp = 0.f;
-  float qx[NEL], kx[NEL];
+    for (int e = 0; e < NEL; ++e) {
+      span = fmaxf(span, fmaxf(fabsf(ref[e]), fabsf(tot[e] - ref[e])));
+      cq[e] = fexp2(s[e] - ref[e]);
+      ck[e] = fexp2(ref[e] - s[e]);
+      big = fmaxf(big, fmaxf(fabsf(q[e] * cq[e]), fabsf(k[e] * ck[e])));
+    }
 #pragma unroll
-  for (int e = 0; e < NEL; ++e) {
-    span = fmaxf(span, fmaxf(fabsf(ref[e]), fabsf(tot[e] - ref[e])));
-    qx[e] = q[e] * fexp2(s[e] - ref[e]);
-    kx[e] = k[e] * fexp2(ref[e] - s[e]);
-    big = fmaxf(big, fmaxf(fabsf(qx[e]), fabsf(kx[e])));
-  }
+    for (int r = 0; r < 4; ++r)
+      if (4 * lq + r == lr) sSelf[t] = pn[r];
+    const bool direct = !__all(span <= kMaxSpan && big < 0x1p84f);
+    if (lane == 0) sDirect[wave] = direct;
+    for (int d = lane; d < DK; d += 64) {
+      const float td = sA[wave][d], rd = sB[wave][d];
+      sE[wave][d] = fexp2(td);
+      sEQ[wave][d] = direct ? 1.f : fexp2(rd);
+      sEK[wave][d] = direct ? 1.f : fexp2(td - rd);
+    }
+    if (direct) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    bigp = fmaxf(bigp, fabsf(pn[r]));
-    if (4 * lq + r == lr) sSelf[t] = pn[r];
+      for (int e = 0; e < NEL; ++e) {
+        cq[e] = fexp2(s[e]);
+        ck[e] = fexp2(tot[e] - s[e]);
+      }
+    }
   }
-  big = tile::group_max<64>(big);
-  bigp = tile::group_max<64>(bigp);
   floatx4 gqd[ND], gkd[ND], gva[NE];
 #pragma unroll
   for (int D = 0; D < ND; ++D) gqd[D] = gkd[D] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int E = 0; E < NE; ++E) gva[E] = floatx4{0.f, 0.f, 0.f, 0.f};
+  wave_sync();
+  const bool direct = sDirect[wave] != 0;
   floatx4 an = {0.f, 0.f, 0.f, 0.f};
-  if (__all(span <= kMaxSpan && big * fmaxf(fmaxf(bigp, big), 1.f) < 0x1p118f)) {
-    put_row(sQ, qx);
-    put_row(sK, kx);
+  if (direct) {
+    // every pair on its own: 2^(s_i - s_j) <= 1 for j <= i. The wave's own
+    // rows of qx and kx, not yet written, pass P and A between lanes.
+    float(*sP)[17] = reinterpret_cast<float(*)[17]>(&sQ[0][16 * wave][0]);
+    float(*sC)[17] = reinterpret_cast<float(*)[17]>(&sK[0][16 * wave][0]);
+    static_assert(16 * 17 * 4 <= 16 * KSTR * 2, "P fits the wave's rows");
 #pragma unroll
-    for (int ks = 0; ks < NKS; ++ks)
-      an = mm<NT>(split8<NT>(qx + 8 * ks), split8<NT>(kx + 8 * ks), an);
-    floatx4 ps = pn;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int x = 4 * lq + r;
-      pt[r] = x < lr ? pt[r] : 0.f;
-      ps[r] = x > lr ? pn[r] : 0.f;
-    }
-    const Split4<NT> pts = split4<NT>(pt), pns = split4<NT>(ps);
-    wave_sync();
-#pragma unroll
-    for (int D = 0; D < ND; ++D) {
-      gqd[D] = mm16<NT>(cols4(&sK[0][16 * wave][colblk(D)], KPL, rdK), pts, gqd[D]);
-      gkd[D] = mm16<NT>(cols4(&sQ[0][16 * wave][colblk(D)], KPL, rdK), pns, gkd[D]);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        gqd[D][r] *= fexp2(s[4 * D + r] - ref[4 * D + r]);
-        gkd[D][r] *= fexp2(ref[4 * D + r] - s[4 * D + r]);
-      }
-    }
-    wave_sync();  // these rows are written again below
-  } else {
-    // every pair on its own: 2^(s_i - s_j) <= 1 for j <= i
-#pragma unroll
-    for (int r = 0; r < 4; ++r) sPd[wave][4 * lq + r][lr] = pn[r];
+    for (int r = 0; r < 4; ++r) sP[4 * lq + r][lr] = pn[r];
     wave_sync();
     for (int j = 0; j < 16; ++j) {
       const int src = (lane & 48) | j;
-      const float pij = sPd[wave][lr][j], pji = sPd[wave][j][lr];
+      const float pij = sP[lr][j], pji = sP[j][lr];
       float aij = 0.f;
 #pragma unroll
       for (int e = 0; e < NEL; ++e) {
@@ -549,174 +586,208 @@ __global__ __launch_bounds__(kThreads) void bwd_grad_kernel(
       }
       aij += __shfl_xor(aij, 16);
       aij += __shfl_xor(aij, 32);
-      if (lq == 0) sAd[wave][lr][j] = aij;
+      if (lq == 0) sC[lr][j] = aij;
     }
     wave_sync();
 #pragma unroll
-    for (int r = 0; r < 4; ++r) an[r] = sAd[wave][4 * lq + r][lr];
+    for (int r = 0; r < 4; ++r) an[r] = sC[4 * lq + r][lr];
+    wave_sync();
+  }
+  float kx[NEL];
+#pragma unroll
+  for (int e = 0; e < NEL; ++e) kx[e] = k[e] * ck[e];
+  {
+    float qx[NEL];
+#pragma unroll
+    for (int e = 0; e < NEL; ++e) qx[e] = q[e] * cq[e];
+#pragma unroll
+    for (int ks = 0; ks < NKS; ++ks) {
+      const Split8<NT> a = split8<NT>(qx + 8 * ks), c = split8<NT>(kx + 8 * ks);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        *reinterpret_cast<bf8*>(&sQ[i][t][place(ks)]) = a.t[i];
+        *reinterpret_cast<bf8*>(&sK[i][t][place(ks)]) = c.t[i];
+      }
+      if (!direct) an = mm<NT>(a, c, an);
+    }
+  }
+  wave_sync();
+  if (!direct) {
+    floatx4 ps;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int x = 4 * lq + r;
+      pt[r] = x < lr ? pt[r] : 0.f;
+      ps[r] = x > lr ? pn[r] : 0.f;
+    }
+    const Split4<NT> pts = split4<NT>(pt), pns = split4<NT>(ps);
+#pragma unroll
+    for (int D = 0; D < ND; ++D) {
+      gqd[D] = mm16<NT>(cols_k(sK, wave, D), pts, gqd[D]);
+      gkd[D] = mm16<NT>(cols_k(sQ, wave, D), pns, gkd[D]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        gqd[D][r] *= cq[4 * D + r];
+        gkd[D][r] *= ck[4 * D + r];
+      }
+    }
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) an[r] = 4 * lq + r >= lr ? an[r] : 0.f;
   {
     const Split4<NT> as = split4<NT>(an);
 #pragma unroll
-    for (int E = 0; E < NE; ++E)
-      gva[E] = mm16<NT>(cols4(&sO[0][16 * wave][colblk(E)], VPL, rdV), as, gva[E]);
+    for (int E = 0; E < NE; ++E) gva[E] = mm16<NT>(cols_o(wave, E), as, gva[E]);
   }
-  // -- q~ and k~ for the other sub-blocks
-#pragma unroll
-  for (int e = 0; e < NEL; ++e) {
-    qx[e] = q[e] * fexp2(s[e]);
-    kx[e] = k[e] * fexp2(tot[e] - s[e]);
-  }
-  put_row(sQ, qx);
-  put_row(sK, kx);
+  __syncthreads();
+  load_state(Dws, dn);  // again (from the cache): kept from above, it would spill
   // -- gq from the entering state, S_n go
   floatx4 gqa[ND];
 #pragma unroll
-  for (int D = 0; D < ND; ++D) {
-    gqa[D] = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (int D = 0; D < ND; ++D) gqa[D] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int ks = 0; ks < NES; ++ks)
-      gqa[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), os[ks], gqa[D]);
+  for (int ks = 0; ks < NES; ++ks) {
+    const Split8<NT> x = go.template terms<NT>(ks);
+#pragma unroll
+    for (int D = 0; D < ND; ++D) gqa[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), x, gqa[D]);
   }
-  __syncthreads();  // S_n is read, q~ and k~ are written
+  __syncthreads();  // S_n is read
+  put_state(dn);
+  // -- and from the earlier sub-blocks, farthest first: what is accumulated is
+  // decayed from one sub-block's reference to the next one's
+  float f[NEL];
 #pragma unroll
-  for (int i = 0; i < NG; ++i) {
-    const int u = tid + kThreads * i, d = u / LPR, e = 4 * (u % LPR);
-    const Split4<NT> sp = split4<NT>(dn[i]);
-    const int p = 32 * (e / 32) + 8 * ((e / 4) % 4) + 4 * ((e / 16) % 2);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) *reinterpret_cast<bf4*>(&sX[j][d][p]) = sp.t[j];
-  }
-  // -- gq from the earlier sub-blocks
+  for (int e = 0; e < NEL; ++e) f[e] = 1.f;
   for (int J = 0; J < wave; ++J) {
-    floatx4 p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int ks = 0; ks < NES; ++ks)
-      p = mm<NT>(rows8(&sV[0][16 * J][0], VPL, VSTR, ks), os[ks], p);
-    const Split4<NT> ps = split4<NT>(p);
-    float tj[NEL];
-    table(sTot, J, tj);
+    const Split4<NT> ps = split4<NT>(p_with(sV, J, go));
+    float x[NEL];
+    table(sDirect[J] ? sE : sEQ, J, x);
 #pragma unroll
     for (int D = 0; D < ND; ++D) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) gqa[D][r] *= fexp2(tj[4 * D + r]);
-      gqa[D] = mm16<NT>(cols4(&sK[0][16 * J][colblk(D)], KPL, rdK), ps, gqa[D]);
+      for (int r = 0; r < 4; ++r) gqa[D][r] *= f[4 * D + r] * x[4 * D + r];
+      gqa[D] = mm16<NT>(cols_k(sK, J, D), ps, gqa[D]);
     }
+    table(sEK, J, f);
   }
-  // -- gk and gv from the later sub-blocks; `m` is the decay (log2) of the
-  // sub-blocks strictly between
+  {
+    float x[NEL];
+    table(sEQ, wave, x);
+#pragma unroll
+    for (int D = 0; D < ND; ++D)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        gqd[D][r] = fmaf(gqa[D][r], cq[4 * D + r] * f[4 * D + r] * x[4 * D + r], gqd[D][r]);
+  }
+  // -- gk and gv from the later sub-blocks, nearest first; f is the decay of
+  // the sub-blocks between
+  table(sEK, wave, f);
+#pragma unroll
+  for (int e = 0; e < NEL; ++e) kx[e] *= f[e];  // k 2^(tot-s)
   floatx4 gka[ND];
 #pragma unroll
   for (int D = 0; D < ND; ++D) gka[D] = floatx4{0.f, 0.f, 0.f, 0.f};
-  float after[NEL];  // decay of all later sub-blocks
 #pragma unroll
-  for (int e = 0; e < NEL; ++e) after[e] = 0.f;
+  for (int e = 0; e < NEL; ++e) f[e] = 1.f;
   for (int I = wave + 1; I < NB; ++I) {
-    float ti[NEL];
-    table(sTot, I, ti);
+    floatx4 a = {0.f, 0.f, 0.f, 0.f};
+    float x[NEL];
+    table(sEQ, I, x);
 #pragma unroll
-    for (int e = 0; e < NEL; ++e) after[e] += ti[e];
-  }
-  float m[NEL];
-#pragma unroll
-  for (int e = 0; e < NEL; ++e) m[e] = after[e];
-  for (int I = NB - 1; I > wave; --I) {
-    floatx4 p = {0.f, 0.f, 0.f, 0.f}, a = p;
-#pragma unroll
-    for (int ks = 0; ks < NES; ++ks)
-      p = mm<NT>(rows8(&sO[0][16 * I][0], VPL, VSTR, ks), vs[ks], p);
-    float ti[NEL];
-    table(sTot, I, ti);
+    for (int e = 0; e < NEL; ++e) x[e] *= f[e];
 #pragma unroll
     for (int ks = 0; ks < NKS; ++ks) {
-      float x[8];
+      float y[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        m[8 * ks + c] -= ti[8 * ks + c];
-        x[c] = kx[8 * ks + c] * fexp2(m[8 * ks + c]);
-      }
-      a = mm<NT>(rows8(&sQ[0][16 * I][0], KPL, KSTR, ks), split8<NT>(x), a);
+      for (int c = 0; c < 8; ++c) y[c] = kx[8 * ks + c] * x[8 * ks + c];
+      a = mm<NT>(rows8(&sQ[0][16 * I][0], KPL, KSTR, ks), split8<NT>(y), a);
     }
-    const Split4<NT> ps = split4<NT>(p), as = split4<NT>(a);
+    const Split4<NT> ps = split4<NT>(p_with(sO, I, v)), as = split4<NT>(a);
 #pragma unroll
     for (int D = 0; D < ND; ++D) {
+      const floatx4 y = mm16<NT>(cols_k(sQ, I, D), ps, floatx4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-      for (int r = 0; r < 4; ++r) gka[D][r] *= fexp2(ti[4 * D + r]);
-      gka[D] = mm16<NT>(cols4(&sQ[0][16 * I][colblk(D)], KPL, rdK), ps, gka[D]);
+      for (int r = 0; r < 4; ++r) gka[D][r] = fmaf(y[r], x[4 * D + r], gka[D][r]);
     }
 #pragma unroll
-    for (int E = 0; E < NE; ++E)
-      gva[E] = mm16<NT>(cols4(&sO[0][16 * I][colblk(E)], VPL, rdV), as, gva[E]);
+    for (int E = 0; E < NE; ++E) gva[E] = mm16<NT>(cols_o(I, E), as, gva[E]);
+    table(sE, I, x);
+#pragma unroll
+    for (int e = 0; e < NEL; ++e) f[e] *= x[e];
   }
-  __syncthreads();  // D_n is written
+  {
+    float x[NEL];
+    table(sEK, wave, x);
+#pragma unroll
+    for (int D = 0; D < ND; ++D)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        ck[4 * D + r] *= x[4 * D + r];  // 2^(tot - s)
+        gkd[D][r] = fmaf(gka[D][r], ck[4 * D + r], gkd[D][r]);
+        ck[4 * D + r] *= f[4 * D + r];  // 2^(B - b)
+      }
+  }
+  __syncthreads();  // D_n is written; tot and ref are read
   // -- gk and gv from the state behind the chunk
   floatx4 gks[ND];
 #pragma unroll
-  for (int D = 0; D < ND; ++D) {
-    gks[D] = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (int D = 0; D < ND; ++D) gks[D] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int ks = 0; ks < NES; ++ks)
-      gks[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), vs[ks], gks[D]);
+  for (int ks = 0; ks < NES; ++ks) {
+    const Split8<NT> x = v.template terms<NT>(ks);
+#pragma unroll
+    for (int D = 0; D < ND; ++D) gks[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), x, gks[D]);
   }
 #pragma unroll
   for (int ks = 0; ks < NKS; ++ks) {
     float x[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = kx[8 * ks + c] * fexp2(after[8 * ks + c]);
+    for (int c = 0; c < 8; ++c) x[c] = kx[8 * ks + c] * f[8 * ks + c];
     const Split8<NT> xs = split8<NT>(x);
 #pragma unroll
     for (int E = 0; E < NE; ++E) {
       Split8<NT> dt;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        dt.t[i] = join(rdV(&sX[i][32 * ks][colblk(E)]), rdV(&sX[i][32 * ks + 16][colblk(E)]));
+        dt.t[i] = join(tr4<VSTR, 4, 8>(&sX[i][32 * ks][colblk(E)]), tr4<VSTR, 4, 8>(&sX[i][32 * ks + 16][colblk(E)]));
       gva[E] = mm<NT>(dt, xs, gva[E]);
     }
   }
   // -- the decay's gradient: suffix sums of q gq - k gk^pairs, sums of
   // k gk^state over the tokens before
-  float z[NEL], w[NEL], g2[NEL];
+  float g2[NEL];
 #pragma unroll
   for (int D = 0; D < ND; ++D) {
+    float z[4], w[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int e = 4 * D + r;
-      const float fq = fexp2(s[e]), fk = fexp2(tot[e] - s[e]);
-      gqd[D][r] = fmaf(gqa[D][r], fq, gqd[D][r]);
-      gkd[D][r] = fmaf(gka[D][r], fk, gkd[D][r]);
-      gks[D][r] *= fexp2(tot[e] - s[e] + after[e]);
-      z[e] = row_suffix16(fmaf(q[e], gqd[D][r], -k[e] * gkd[D][r]));
-      w[e] = row_scan16(k[e] * gks[D][r]);
-      g2[e] = z[e] + row_before16(w[e]);
+      gks[D][r] *= ck[e];
+      z[r] = row_suffix16(fmaf(q[e], gqd[D][r], -k[e] * gkd[D][r]));
+      w[r] = row_scan16(k[e] * gks[D][r]);
+      g2[e] = z[r] + row_before16(w[r]);
     }
-    if (lr == 0) *reinterpret_cast<floatx4*>(&sZ[wave][dim(D)]) = floatx4{z[4 * D], z[4 * D + 1], z[4 * D + 2], z[4 * D + 3]};
-    if (lr == 15) *reinterpret_cast<floatx4*>(&sW[wave][dim(D)]) = floatx4{w[4 * D], w[4 * D + 1], w[4 * D + 2], w[4 * D + 3]};
+    if (lr == 0) *reinterpret_cast<floatx4*>(&sA[wave][dim(D)]) = floatx4{z[0], z[1], z[2], z[3]};
+    if (lr == 15) *reinterpret_cast<floatx4*>(&sB[wave][dim(D)]) = floatx4{w[0], w[1], w[2], w[3]};
   }
   __syncthreads();
   const float self = sSelf[t];
-  float before[NEL];  // decay of the earlier sub-blocks
-#pragma unroll
-  for (int e = 0; e < NEL; ++e) before[e] = 0.f;
   for (int J = 0; J < NB; ++J) {
     if (J == wave) continue;
-    float x[NEL], tj[NEL];
-    table(J < wave ? sW : sZ, J, x);
-    table(sTot, J, tj);
+    float x[NEL];
+    table(J < wave ? sB : sA, J, x);
 #pragma unroll
-    for (int e = 0; e < NEL; ++e) {
-      g2[e] += x[e];
-      before[e] += J < wave ? tj[e] : 0.f;
-    }
+    for (int e = 0; e < NEL; ++e) g2[e] += x[e];
   }
 #pragma unroll
   for (int D = 0; D < ND; ++D) {
-    const floatx4 ad = *reinterpret_cast<const floatx4*>(&sAD[dim(D)]);
+    floatx4 ad = *reinterpret_cast<const floatx4*>(&sAD[dim(D)]);
+#pragma unroll
+    for (int J = 0; J < NB; ++J) ad *= *reinterpret_cast<const floatx4*>(&sE[J][dim(D)]);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int e = 4 * D + r;
-      g2[e] = fmaf(fexp2(before[e] + tot[e] + after[e]), ad[r], g2[e]);
+      g2[e] += ad[r];
       gqd[D][r] = fmaf(self, k[e], gqd[D][r]);
       gkd[D][r] = fmaf(self, q[e], gkd[D][r] + gks[D][r]);
     }
