@@ -283,54 +283,157 @@ __global__ __launch_bounds__(kThreads) void bwd_summary_kernel(
 
 // ===========================================================================
 // State scans, in place: S_n over U_n in forward order, D_n over R_n from the
-// end. Every state element is its own first-order recurrence over the chunks;
-// one thread walks four of them with the next W chunks' loads in flight.
+// end; every state element is its own first-order recurrence over the chunks,
+//   x_0 given or 0,  x_{i+1} = a_i x_i + u_i,
+// held in float. What the gradients read back (x_i) is stored as float, or
+// for half inputs as the two bf16 terms their products take: 16 bytes per
+// four elements either way, {t0 of the four, t1 of the four}.
 // ===========================================================================
-template <int W>
-__global__ __launch_bounds__(kThreads) void bwd_scan_kernel(float* __restrict__ Uws,
-                                                            float* __restrict__ Rws,
-                                                            const float* __restrict__ Aws,
-                                                            const float* s0, const float* gsf,
-                                                            float* gs0, int N, int DK, int DV,
-                                                            long groups) {
+template <bool kTerms>
+__device__ __forceinline__ void put_state4(float* p, floatx4 s) {
+  if constexpr (kTerms) {
+    const Split4<2> t = split4<2>(s);
+    *reinterpret_cast<bf8*>(p) = join(t.t[0], t.t[1]);
+  } else {
+    *reinterpret_cast<floatx4*>(p) = s;
+  }
+}
+__device__ __forceinline__ floatx4 step4(float a, floatx4 s, floatx4 u) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) s[c] = fmaf(a, s[c], u[c]);
+  return s;
+}
+
+// Many chains: one thread walks four elements of a chain in order, the next
+// W/2 to W chunks' loads in flight (the window is refilled half by half, and
+// whole windows run without a condition, which would wait for every load).
+template <int W, bool kTerms>
+__global__ __launch_bounds__(kThreads) void bwd_scan_serial_kernel(
+    float* Uws, float* Rws, const float* __restrict__ Aws, const float* s0, const float* gsf,
+    float* gs0, int N, int DK, int DV, long groups) {
   const long gid = (long)blockIdx.x * kThreads + threadIdx.x;
   if (gid >= groups) return;
   const bool rev = blockIdx.y;
   const long DKDV = (long)DK * DV, per = DKDV / 4;
   const long bh = gid / per;
   const int x4 = 4 * (int)(gid - bh * per), d = x4 / DV;
-  float* X = (rev ? Rws : Uws) + bh * N * DKDV + x4;
-  const float* A = Aws + bh * N * DK + d;
+  // chunk i of the walk is chunk i, or N-1-i
+  const long first = rev ? N - 1 : 0, sx = rev ? -DKDV : DKDV, sa = rev ? -DK : DK;
+  float* X = (rev ? Rws : Uws) + (bh * N + first) * DKDV + x4;
+  const float* A = Aws + (bh * N + first) * DK + d;
   const float* init = rev ? gsf : s0;
   floatx4 s = {0.f, 0.f, 0.f, 0.f};
   if (init) s = *reinterpret_cast<const floatx4*>(init + bh * DKDV + x4);
   floatx4 u[W];
   float a[W];
-  auto at = [&](int i) { return (long)(rev ? N - 1 - i : i); };
+  constexpr int HW = W / 2;
+  auto refill = [&](int h, int i0) {  // half h of the window: chunks i0.. (clamped)
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const long m = at(i < N ? i : N - 1);
-    u[i] = *reinterpret_cast<const floatx4*>(X + m * DKDV);
-    a[i] = A[m * DK];
+    for (int j = 0; j < HW; ++j) {
+      const long m = i0 + j < N ? i0 + j : N - 1;
+      u[h * HW + j] = *reinterpret_cast<const floatx4*>(X + m * sx);
+      a[h * HW + j] = A[m * sa];
+    }
+  };
+  auto step = [&](int w, int i) {
+    put_state4<kTerms>(X + i * sx, s);
+    s = step4(a[w], s, u[w]);
+  };
+  refill(0, 0);
+  refill(1, HW);
+  int n0 = 0;
+  for (; n0 + W <= N; n0 += W) {
+#pragma unroll
+    for (int j = 0; j < HW; ++j) step(j, n0 + j);
+    __builtin_amdgcn_sched_barrier(0);
+    refill(0, n0 + W);
+#pragma unroll
+    for (int j = 0; j < HW; ++j) step(HW + j, n0 + HW + j);
+    __builtin_amdgcn_sched_barrier(0);
+    refill(1, n0 + W + HW);
   }
-  for (int n0 = 0; n0 < N; n0 += W) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const int n = n0 + i;
-      if (n < N) {
-        *reinterpret_cast<floatx4*>(X + at(n) * DKDV) = s;
+  for (int w = 0; w < W - 1; ++w)
+    if (n0 + w < N) step(w, n0 + w);
+  if (rev && gs0) *reinterpret_cast<floatx4*>(gs0 + bh * DKDV + x4) = s;
+}
+
+// Few chains: the chunk axis in 16 segments of L chunks, one per lane of a DPP
+// row. Each lane folds its segment into (a, u), a row scan composes them, and
+// the lane replays its segment from the state that enters it. R: chunks kept
+// in registers between the two passes.
+template <int R, bool kTerms>
+__global__ __launch_bounds__(kThreads) void bwd_scan_kernel(
+    float* Uws, float* Rws, const float* __restrict__ Aws, const float* s0, const float* gsf,
+    float* gs0, int N, int DK, int DV, int L, long groups) {
+  const long gid = (long)blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
+  if (gid >= groups) return;  // whole DPP rows
+  const int seg = threadIdx.x & 15;
+  const bool rev = blockIdx.y;
+  const long DKDV = (long)DK * DV, per = DKDV / 4;
+  const long bh = gid / per;
+  const int x4 = 4 * (int)(gid - bh * per), d = x4 / DV;
+  const long first = rev ? N - 1 : 0, sx = rev ? -DKDV : DKDV, sa = rev ? -DK : DK;
+  float* X = (rev ? Rws : Uws) + (bh * N + first) * DKDV + x4;
+  const float* A = Aws + (bh * N + first) * DK + d;
+  const float* init = rev ? gsf : s0;
+  floatx4 st0 = {0.f, 0.f, 0.f, 0.f};
+  if (init) st0 = *reinterpret_cast<const floatx4*>(init + bh * DKDV + x4);
+  const int n0 = min(seg * L, N), n1 = min(n0 + L, N);
+  float ag = 1.f;
+  floatx4 ug = {0.f, 0.f, 0.f, 0.f}, u[R];
+  float a[R];
+  for (int nb = n0; nb < n1; nb += R) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[c] = fmaf(a[i], s[c], u[i][c]);
-        // a chunk W ahead: not yet overwritten, this thread alone writes it
-        const long m = at(n + W < N ? n + W : N - 1);
-        if (n + W < N) {
-          u[i] = *reinterpret_cast<const floatx4*>(X + m * DKDV);
-          a[i] = A[m * DK];
-        }
+    for (int i = 0; i < R; ++i) {  // clamped, all in flight together
+      const long m = min(nb + i, n1 - 1);
+      u[i] = *reinterpret_cast<const floatx4*>(X + m * sx);
+      a[i] = A[m * sa];
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (nb + i < n1) {
+        ug = step4(a[i], ug, u[i]);
+        ag *= a[i];
       }
     }
   }
-  if (rev && gs0) *reinterpret_cast<floatx4*>(gs0 + bh * DKDV + x4) = s;
+  // inclusive composition over the row's segments, then shifted by one
+#define GLA_BWD_SCAN_STEP(CTRL)                                                                \
+  {                                                                                            \
+    const float ap = tile::dpp_row_shr<CTRL>(ag, 1.f);                                         \
+    _Pragma("unroll") for (int c = 0; c < 4; ++c) ug[c] =                                      \
+        fmaf(ag, tile::dpp_row_shr<CTRL>(ug[c], 0.f), ug[c]);                                  \
+    ag *= ap;                                                                                  \
+  }
+  GLA_BWD_SCAN_STEP(0x111)
+  GLA_BWD_SCAN_STEP(0x112)
+  GLA_BWD_SCAN_STEP(0x114)
+  GLA_BWD_SCAN_STEP(0x118)
+#undef GLA_BWD_SCAN_STEP
+  if (rev && gs0 && seg == 15) *reinterpret_cast<floatx4*>(gs0 + bh * DKDV + x4) = step4(ag, st0, ug);
+  const float ae = tile::dpp_row_shr<0x111>(ag, 1.f);
+  floatx4 s;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) s[c] = fmaf(ae, st0[c], tile::dpp_row_shr<0x111>(ug[c], 0.f));
+  const bool cached = n1 - n0 <= R;
+  for (int nb = n0; nb < n1; nb += R) {
+    if (!cached) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const long m = min(nb + i, n1 - 1);
+        u[i] = *reinterpret_cast<const floatx4*>(X + m * sx);
+        a[i] = A[m * sa];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (nb + i < n1) {
+        put_state4<kTerms>(X + (nb + i) * sx, s);
+        s = step4(a[i], s, u[i]);
+      }
+    }
+  }
 }
 
 // ===========================================================================
@@ -349,12 +452,19 @@ __global__ __launch_bounds__(kThreads) void bwd_scan_kernel(float* __restrict__ 
 // so the pairs inside the sub-block need no other factor, and pairs of two
 // sub-blocks I > J only factors by dim, all <= 1 (tables in LDS):
 //   2^(b_i-b_j) = 2^(s_i-ref_I) [2^ref_I prod_{J<M<I} 2^tot_M 2^(tot_J-ref_J)] 2^(ref_J-s_j).
-// Every product stays finite while qx and kx are below 2^84 (P is at most 64
-// products of two values up to 65504). A sub-block that decays more keeps
-// q 2^s and k 2^(tot-s) instead (its bracket then holds 1 for the two outer
-// factors) and sums its own pairs directly in float.
+// Where no s - ref exceeds 68 in magnitude, values up to 65504 keep qx and kx
+// below 2^84 and every product finite (P is at most 64 products of two such
+// values); a 2^ref that underflows has all of its sub-block's q 2^s do so. A sub-block that decays more keeps q 2^s and k 2^(tot-s)
+// instead (its bracket then holds 1 for the two outer factors) and sums its
+// own pairs directly in float.
 // ===========================================================================
-constexpr float kMaxSpan = 84.f;
+constexpr float kMaxSpan = 68.f;
+
+// Lane n of each row of 16, on all of the row's lanes.
+template <int LANE>
+__device__ __forceinline__ float row_lane(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + LANE, 0xf, 0xf, true));
+}
 
 template <int DK, int DV, typename InT, int NT>
 __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_kernel(
@@ -366,18 +476,20 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   constexpr bool kHalf = sizeof(InT) == 2;
   constexpr int NKS = DK / 32, NES = DV / 32, ND = DK / 16, NE = DV / 16;
   constexpr int NEL = 4 * ND, NVL = 4 * NE;  // a lane's dims of q/k/g and of v/go
+  constexpr int NP = NB * (NB - 1) / 2;      // pairs of sub-blocks
   constexpr int KSTR = DK + 8, VSTR = DV + 8, NV = kHalf ? 1 : NT;
   __shared__ __attribute__((aligned(16))) __bf16 sQ[NT][C][KSTR];   // qx
   __shared__ __attribute__((aligned(16))) __bf16 sK[NT][C][KSTR];   // kx
   __shared__ __attribute__((aligned(16))) __bf16 sO[NV][C][VSTR];   // go (half inputs: half bits)
   __shared__ __attribute__((aligned(16))) __bf16 sV[NV][C][VSTR];   // v
   __shared__ __attribute__((aligned(16))) __bf16 sX[NT][DK][VSTR];  // S_n, then D_n
-  __shared__ __attribute__((aligned(16))) float sA[NB][DK];   // tot, later sums of q gq - k gk^pairs
-  __shared__ __attribute__((aligned(16))) float sB[NB][DK];   // ref, later sums of k gk^state
+  __shared__ __attribute__((aligned(16))) float sF[NP][DK];   // factors between two sub-blocks
+  __shared__ __attribute__((aligned(16))) float sA[NB][DK];   // tot; factors to the chunk's end; sums
+  __shared__ __attribute__((aligned(16))) float sB[NB][DK];   // ref; sums of k gk^state
   __shared__ __attribute__((aligned(16))) float sE[NB][DK];   // 2^tot
   __shared__ __attribute__((aligned(16))) float sEQ[NB][DK];  // 2^ref (1 in a direct sub-block)
   __shared__ __attribute__((aligned(16))) float sEK[NB][DK];  // 2^(tot-ref) (likewise)
-  __shared__ __attribute__((aligned(16))) float sAD[DK];      // <S_n, D_n> by rows
+  __shared__ __attribute__((aligned(16))) float sAD[DK];      // 2^B <S_n, D_n> by rows
   __shared__ float sSelf[C];                                  // P_tt
   __shared__ int sDirect[NB];
   const int n = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
@@ -385,11 +497,13 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   const int lr = lane & 15, lq = lane >> 4;
   const int dir = dirs.get(b), t = 16 * wave + lr;
   const long bhn = ((long)b * H + h) * N + n;
-  // place of a lane's dims 4D + r in memory rows, and of its eight per ks in LDS rows
+  // place of a lane's dims 4D + r in memory rows, of its eight per ks in LDS
+  // rows, and of column block D there
   auto dim = [&](int D) { return 16 * D + 4 * lq; };
   auto place = [&](int ks) { return 32 * ks + 8 * lq; };
+  auto colblk = [](int D) { return 32 * (D / 2) + 4 * (D % 2); };
 
-  // -- this lane's token row, and the states at the chunk's ends
+  // -- this lane's token row
   const int rr = token_row(n * C + t, T, gh, gw, dir);
   const bool pad = rr < 0;
   const long row = ((long)b * T + (pad ? 0 : rr)) * H + h;
@@ -400,15 +514,31 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   k.load(kp + row * DK + dim(0));
   v.load(vp + row * DV + dim(0));
   go.load(dop + row * DV + dim(0));
-  constexpr int NG = DK * DV / 4 / kThreads, LPR = DV / 4;  // groups of four per thread, per row
-  auto load_state = [&](const float* p, floatx4* x) {
+  // -- a state of the chunk's ends: 16 bytes of it per thread and step
+  constexpr int NG = DK * DV / 4 / kThreads, LPR = DV / 4;
+  floatx4 st[NG];
+  auto load_state = [&](const float* p) {
 #pragma unroll
     for (int i = 0; i < NG; ++i)
-      x[i] = *reinterpret_cast<const floatx4*>(p + bhn * (DK * DV) + 4 * (tid + kThreads * i));
+      st[i] = *reinterpret_cast<const floatx4*>(p + bhn * (DK * DV) + 4 * (tid + kThreads * i));
   };
-  floatx4 sn[NG], dn[NG];
-  load_state(Sws, sn);
-  load_state(Dws, dn);
+  auto put_state = [&]() {
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const int u = tid + kThreads * i, d = u / LPR, e = 4 * (u % LPR);
+      const int p = 32 * (e / 32) + 8 * ((e / 4) % 4) + 4 * ((e / 16) % 2);
+      if constexpr (kHalf) {
+        const bf8 x = __builtin_bit_cast(bf8, st[i]);
+        *reinterpret_cast<bf4*>(&sX[0][d][p]) = __builtin_shufflevector(x, x, 0, 1, 2, 3);
+        *reinterpret_cast<bf4*>(&sX[1][d][p]) = __builtin_shufflevector(x, x, 4, 5, 6, 7);
+      } else {
+        const Split4<NT> sp = split4<NT>(st[i]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) *reinterpret_cast<bf4*>(&sX[j][d][p]) = sp.t[j];
+      }
+    }
+  };
+  load_state(Sws);
   if ((n + 1) * C > T) {  // the chain's last chunk: padding rows are zeros without decay
     g.zero_if(pad);
     q.zero_if(pad);
@@ -420,43 +550,62 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
 #pragma unroll
   for (int e = 0; e < NEL; ++e) s[e] = row_scan16(log2_decay(g[e]));
   auto row4 = [&](const float* x, int D) { return floatx4{x[4 * D], x[4 * D + 1], x[4 * D + 2], x[4 * D + 3]}; };
-  auto table = [&](const float(*tab)[DK], int J, float* x) {
-#pragma unroll
-    for (int D = 0; D < ND; ++D) {
-      const floatx4 f = *reinterpret_cast<const floatx4*>(&tab[J][dim(D)]);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[4 * D + r] = f[r];
-    }
-  };
   if ((lr | 8) == 15) {
     float(*dst)[DK] = lr == 15 ? sA : sB;
 #pragma unroll
     for (int D = 0; D < ND; ++D) *reinterpret_cast<floatx4*>(&dst[wave][dim(D)]) = row4(s, D);
   }
-  // -- S_n to LDS, and the states' inner products by rows
-  auto put_state = [&](const floatx4* x) {
+  // -- the sub-block's reference, its rows of qx and kx
+  float cq[NEL], ck[NEL], span = 0.f;  // the factors, which the gradients take too
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int u = tid + kThreads * i, d = u / LPR, e = 4 * (u % LPR);
-      const Split4<NT> sp = split4<NT>(x[i]);
-      const int p = 32 * (e / 32) + 8 * ((e / 4) % 4) + 4 * ((e / 16) % 2);
+  for (int e = 0; e < NEL; ++e) {
+    cq[e] = s[e] - row_lane<7>(s[e]);
+    span = fmaxf(span, fabsf(cq[e]));
+  }
+  const bool direct = !__all(span <= kMaxSpan);
+  if (!direct) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) *reinterpret_cast<bf4*>(&sX[j][d][p]) = sp.t[j];
+    for (int e = 0; e < NEL; ++e) {
+      ck[e] = fexp2(-cq[e]);
+      cq[e] = fexp2(cq[e]);
     }
-  };
-  put_state(sn);
+  } else {
 #pragma unroll
-  for (int i = 0; i < NG; ++i) {
-    const int u = tid + kThreads * i;
-    float dot = sn[i][0] * dn[i][0] + sn[i][1] * dn[i][1] + sn[i][2] * dn[i][2] + sn[i][3] * dn[i][3];
+    for (int e = 0; e < NEL; ++e) {
+      ck[e] = fexp2(row_lane<15>(s[e]) - s[e]);
+      cq[e] = fexp2(s[e]);
+    }
+  }
+  wave_sync();  // tot and ref
+  for (int d = lane; d < DK; d += 64) {
+    const float td = sA[wave][d], rd = sB[wave][d];
+    sE[wave][d] = fexp2(td);
+    sEQ[wave][d] = direct ? 1.f : fexp2(rd);
+    sEK[wave][d] = direct ? 1.f : fexp2(td - rd);
+  }
+  if (lane == 0) sDirect[wave] = direct;
+  constexpr int KPL = C * KSTR, VPL = C * VSTR, XPL = DK * VSTR;
+  const floatx4 zero4 = {0.f, 0.f, 0.f, 0.f};
+  floatx4 an = zero4;  // A inside the sub-block, rows i
 #pragma unroll
-    for (int m = 1; m < LPR; m <<= 1) dot += __shfl_xor(dot, m);
-    if (u % LPR == 0) sAD[u / LPR] = dot;
+  for (int ks = 0; ks < NKS; ++ks) {
+    float x[8], y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = tile::mulw(q[8 * ks + i], cq[8 * ks + i]);
+      y[i] = tile::mulw(k[8 * ks + i], ck[8 * ks + i]);
+    }
+    const Split8<NT> xs = split8<NT>(x), ys = split8<NT>(y);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      *reinterpret_cast<bf8*>(&sQ[i][t][place(ks)]) = xs.t[i];
+      *reinterpret_cast<bf8*>(&sK[i][t][place(ks)]) = ys.t[i];
+    }
+    an = mm<NT>(xs, ys, an);
   }
   // -- v and go to LDS; P inside the sub-block: transposed (rows j) for gq,
   // and rows i for gk
-  constexpr int KPL = C * KSTR, VPL = C * VSTR, XPL = DK * VSTR;
-  floatx4 pt = {0.f, 0.f, 0.f, 0.f}, pn = pt;
+  floatx4 pt = zero4, pn = zero4;
 #pragma unroll
   for (int ks = 0; ks < NES; ++ks) {
     if constexpr (kHalf) {
@@ -475,26 +624,9 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
       pn = mm<NT>(os, vs, pn);
     }
   }
-  // P of this wave's queries with the keys of block J, transposed; and of the
-  // queries of block I with this wave's keys
-  auto p_with = [&](const __bf16(*tl)[C][VSTR], int I, const Raw<InT, NVL>& own) {
-    floatx4 p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int ks = 0; ks < NES; ++ks) {
-      const __bf16* at = &tl[0][16 * I + lr][place(ks)];
-      if constexpr (kHalf) {
-        p = mfma16x16x32(*reinterpret_cast<const half8*>(at), own.pack8(ks), p);
-      } else {
-        Split8<NT> x;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) x.t[i] = *reinterpret_cast<const bf8*>(at + i * VPL);
-        p = mm<NT>(x, own.template terms<NT>(ks), p);
-      }
-    }
-    return p;
-  };
-  // operands from LDS: 16 rows of S or D, or of qx, contracted along the row;
-  // 16 columns (block D of the places) contracted along 16 rows
+  put_state();  // S_n
+  // operands from LDS: 16 rows of a tile contracted along the row; 16 columns
+  // (block D of the places) contracted along 16 rows
   auto rows8 = [&](const __bf16* tl, int plane, int str, int ks) {
     Split8<NT> sp;
 #pragma unroll
@@ -502,8 +634,7 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
       sp.t[i] = *reinterpret_cast<const bf8*>(tl + i * plane + lr * str + place(ks));
     return sp;
   };
-  auto colblk = [](int D) { return 32 * (D / 2) + 4 * (D % 2); };
-  auto cols_k = [&](const __bf16(*tl)[C][KSTR], int I, int D) {
+  auto cols_r = [&](const __bf16(*tl)[C][KSTR], int I, int D) {
     Split4<NT> sp;
 #pragma unroll
     for (int i = 0; i < NT; ++i) sp.t[i] = tr4<KSTR, 4, 8>(&tl[i][16 * I][colblk(D)]);
@@ -511,8 +642,8 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   };
   auto cols_o = [&](int I, int E) {
     if constexpr (kHalf) {
-      const half4 x = __builtin_bit_cast(half4, tr4<VSTR, 4, 8>(&sO[0][16 * I][colblk(E)]));
-      return split4<NT>(__builtin_convertvector(x, floatx4));
+      const half4 o = __builtin_bit_cast(half4, tr4<VSTR, 4, 8>(&sO[0][16 * I][colblk(E)]));
+      return split4<NT>(__builtin_convertvector(o, floatx4));
     } else {
       Split4<NT> sp;
 #pragma unroll
@@ -520,97 +651,29 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
       return sp;
     }
   };
-
-  wave_sync();  // tot and ref
-  float cq[NEL], ck[NEL];  // the factors of qx and kx, which their gradients take too
-  {
-    float tot[NEL], ref[NEL], span = 0.f, big = 0.f;
-    table(sA, wave, tot);
-    table(sB, wave, ref);
+  // 16 rows of v with this wave's own go: P transposed; or of go with its v
+  auto p_block = [&](const __bf16(*tl)[C][VSTR], int I, const Raw<InT, NVL>& own) {
+    floatx4 p = zero4;
 #pragma unroll
-    for (int e = 0; e < NEL; ++e) {
-      span = fmaxf(span, fmaxf(fabsf(ref[e]), fabsf(tot[e] - ref[e])));
-      cq[e] = fexp2(s[e] - ref[e]);
-      ck[e] = fexp2(ref[e] - s[e]);
-      big = fmaxf(big, fmaxf(fabsf(q[e] * cq[e]), fabsf(k[e] * ck[e])));
-    }
+    for (int ks = 0; ks < NES; ++ks) {
+      const __bf16* at = &tl[0][16 * I + lr][place(ks)];
+      if constexpr (kHalf) {
+        p = mfma16x16x32(*reinterpret_cast<const half8*>(at), own.pack8(ks), p);
+      } else {
+        Split8<NT> o;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (4 * lq + r == lr) sSelf[t] = pn[r];
-    const bool direct = !__all(span <= kMaxSpan && big < 0x1p84f);
-    if (lane == 0) sDirect[wave] = direct;
-    for (int d = lane; d < DK; d += 64) {
-      const float td = sA[wave][d], rd = sB[wave][d];
-      sE[wave][d] = fexp2(td);
-      sEQ[wave][d] = direct ? 1.f : fexp2(rd);
-      sEK[wave][d] = direct ? 1.f : fexp2(td - rd);
-    }
-    if (direct) {
-#pragma unroll
-      for (int e = 0; e < NEL; ++e) {
-        cq[e] = fexp2(s[e]);
-        ck[e] = fexp2(tot[e] - s[e]);
+        for (int i = 0; i < NT; ++i) o.t[i] = *reinterpret_cast<const bf8*>(at + i * VPL);
+        p = mm<NT>(o, own.template terms<NT>(ks), p);
       }
     }
-  }
-  floatx4 gqd[ND], gkd[ND], gva[NE];
+    return p;
+  };
+  // -- pairs inside the sub-block, a token's pair with itself left out of gq
+  // and gk (added at the end); the rows are this wave's own
+  floatx4 gq[ND], gk[ND], gv[NE];
 #pragma unroll
-  for (int D = 0; D < ND; ++D) gqd[D] = gkd[D] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int E = 0; E < NE; ++E) gva[E] = floatx4{0.f, 0.f, 0.f, 0.f};
-  wave_sync();
-  const bool direct = sDirect[wave] != 0;
-  floatx4 an = {0.f, 0.f, 0.f, 0.f};
-  if (direct) {
-    // every pair on its own: 2^(s_i - s_j) <= 1 for j <= i. The wave's own
-    // rows of qx and kx, not yet written, pass P and A between lanes.
-    float(*sP)[17] = reinterpret_cast<float(*)[17]>(&sQ[0][16 * wave][0]);
-    float(*sC)[17] = reinterpret_cast<float(*)[17]>(&sK[0][16 * wave][0]);
-    static_assert(16 * 17 * 4 <= 16 * KSTR * 2, "P fits the wave's rows");
-#pragma unroll
-    for (int r = 0; r < 4; ++r) sP[4 * lq + r][lr] = pn[r];
-    wave_sync();
-    for (int j = 0; j < 16; ++j) {
-      const int src = (lane & 48) | j;
-      const float pij = sP[lr][j], pji = sP[j][lr];
-      float aij = 0.f;
-#pragma unroll
-      for (int e = 0; e < NEL; ++e) {
-        const float sj = __shfl(s[e], src), kj = __shfl(k[e], src), qj = __shfl(q[e], src);
-        // token j as the key of this lane's query, and as the query of its key
-        const float fq = j <= lr ? fexp2(s[e] - sj) : 0.f;
-        const float fk = j > lr ? fexp2(sj - s[e]) : 0.f;
-        aij = fmaf(q[e] * kj, fq, aij);
-        if (j < lr) gqd[e / 4][e % 4] = fmaf(pij * kj, fq, gqd[e / 4][e % 4]);
-        if (j > lr) gkd[e / 4][e % 4] = fmaf(pji * qj, fk, gkd[e / 4][e % 4]);
-      }
-      aij += __shfl_xor(aij, 16);
-      aij += __shfl_xor(aij, 32);
-      if (lq == 0) sC[lr][j] = aij;
-    }
-    wave_sync();
-#pragma unroll
-    for (int r = 0; r < 4; ++r) an[r] = sC[4 * lq + r][lr];
-    wave_sync();
-  }
-  float kx[NEL];
-#pragma unroll
-  for (int e = 0; e < NEL; ++e) kx[e] = k[e] * ck[e];
-  {
-    float qx[NEL];
-#pragma unroll
-    for (int e = 0; e < NEL; ++e) qx[e] = q[e] * cq[e];
-#pragma unroll
-    for (int ks = 0; ks < NKS; ++ks) {
-      const Split8<NT> a = split8<NT>(qx + 8 * ks), c = split8<NT>(kx + 8 * ks);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        *reinterpret_cast<bf8*>(&sQ[i][t][place(ks)]) = a.t[i];
-        *reinterpret_cast<bf8*>(&sK[i][t][place(ks)]) = c.t[i];
-      }
-      if (!direct) an = mm<NT>(a, c, an);
-    }
-  }
+  for (int r = 0; r < 4; ++r)
+    if (4 * lq + r == lr) sSelf[t] = pn[r];
   wave_sync();
   if (!direct) {
     floatx4 ps;
@@ -623,13 +686,43 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
     const Split4<NT> pts = split4<NT>(pt), pns = split4<NT>(ps);
 #pragma unroll
     for (int D = 0; D < ND; ++D) {
-      gqd[D] = mm16<NT>(cols_k(sK, wave, D), pts, gqd[D]);
-      gkd[D] = mm16<NT>(cols_k(sQ, wave, D), pns, gkd[D]);
+      gq[D] = mm16<NT>(cols_r(sK, wave, D), pts, zero4);
+      gk[D] = mm16<NT>(cols_r(sQ, wave, D), pns, zero4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        gqd[D][r] *= cq[4 * D + r];
-        gkd[D][r] *= ck[4 * D + r];
+        gq[D][r] *= cq[4 * D + r];
+        gk[D][r] *= ck[4 * D + r];
       }
+    }
+  } else {
+    // every pair on its own: 2^(s_i - s_j) <= 1 for j <= i; component x of the
+    // 16 that P and A spread over the four lanes of a token
+#pragma unroll
+    for (int D = 0; D < ND; ++D) gq[D] = gk[D] = zero4;
+    auto component = [&](const floatx4& p, int x) {
+      const float a = (x & 1) ? p[1] : p[0], c = (x & 1) ? p[3] : p[2];
+      return __shfl((x & 2) ? c : a, 16 * (x / 4) + lr);
+    };
+    an = zero4;
+#pragma unroll 1
+    for (int j = 0; j < 16; ++j) {
+      const float pij = component(pt, j), pji = component(pn, j);  // P[lr][j], P[j][lr]
+      float aij = 0.f;
+#pragma unroll
+      for (int e = 0; e < NEL; ++e) {
+        const int src = (lane & 48) | j;
+        const float sj = __shfl(s[e], src), kj = __shfl(k[e], src), qj = __shfl(q[e], src);
+        // token j as the key of this lane's query, and as the query of its key
+        const float fq = j < lr ? fexp2(s[e] - sj) : 0.f;
+        const float fk = j >= lr ? fexp2(sj - s[e]) : 0.f;
+        gq[e / 4][e % 4] = fmaf(j < lr ? pij * kj : 0.f, fq, gq[e / 4][e % 4]);
+        gk[e / 4][e % 4] = fmaf(j > lr ? pji * qj : 0.f, fk, gk[e / 4][e % 4]);
+        aij = fmaf(qj * k[e], fk, aij);
+      }
+      aij += __shfl_xor(aij, 16);
+      aij += __shfl_xor(aij, 32);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) an[r] = 4 * lq + r == j ? aij : an[r];
     }
   }
 #pragma unroll
@@ -637,112 +730,101 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   {
     const Split4<NT> as = split4<NT>(an);
 #pragma unroll
-    for (int E = 0; E < NE; ++E) gva[E] = mm16<NT>(cols_o(wave, E), as, gva[E]);
+    for (int E = 0; E < NE; ++E) gv[E] = mm16<NT>(cols_o(wave, E), as, zero4);
   }
   __syncthreads();
-  load_state(Dws, dn);  // again (from the cache): kept from above, it would spill
-  // -- gq from the entering state, S_n go
-  floatx4 gqa[ND];
+  load_state(Dws);
+  // -- gq from the entering state, S_n go; the rows of S_n of column block
+  // `wave` are kept for <S_n, D_n>
+  floatx4 acc[ND];
+  Split8<NT> keep[NES];
 #pragma unroll
-  for (int D = 0; D < ND; ++D) gqa[D] = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (int D = 0; D < ND; ++D) acc[D] = zero4;
 #pragma unroll
   for (int ks = 0; ks < NES; ++ks) {
-    const Split8<NT> x = go.template terms<NT>(ks);
+    const Split8<NT> o = go.template terms<NT>(ks);
 #pragma unroll
-    for (int D = 0; D < ND; ++D) gqa[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), x, gqa[D]);
+    for (int D = 0; D < ND; ++D) acc[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), o, acc[D]);
+    keep[ks] = rows8(&sX[0][16 * (wave % ND)][0], XPL, VSTR, ks);
   }
-  __syncthreads();  // S_n is read
-  put_state(dn);
-  // -- and from the earlier sub-blocks, farthest first: what is accumulated is
-  // decayed from one sub-block's reference to the next one's
-  float f[NEL];
+  // -- the brackets of the pairs of sub-blocks, and 2^(tot_J - ref_J) prod
+  // 2^tot_M over all later sub-blocks M
+  for (int i = tid; i < (NP + NB) * DK; i += kThreads) {
+    const int pr = i / DK, d = i % DK;
+    int I = NB, J = pr - NP;
+    if (J < 0) {
+      I = pr < 1 ? 1 : pr < 3 ? 2 : 3;
+      J = pr - I * (I - 1) / 2;
+    }
+    float o = sEK[J][d];
 #pragma unroll
-  for (int e = 0; e < NEL; ++e) f[e] = 1.f;
-  for (int J = 0; J < wave; ++J) {
-    const Split4<NT> ps = split4<NT>(p_with(sV, J, go));
-    float x[NEL];
-    table(sDirect[J] ? sE : sEQ, J, x);
+    for (int M = 1; M < NB; ++M) o *= M > J && M < I ? sE[M][d] : 1.f;
+    if (I < NB) sF[pr][d] = o * sEQ[I][d];
+    else sA[J][d] = o;
+  }
+  __syncthreads();  // S_n is read, the factors are written
+  put_state();      // D_n
+  // -- gq from the earlier sub-blocks, farthest first: what is accumulated is
+  // decayed from one sub-block's reference to the next one's
+  auto decay = [&](int J, const float(*tab)[DK]) {  // from block J-1's end to tab's point in block J
 #pragma unroll
     for (int D = 0; D < ND; ++D) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) gqa[D][r] *= f[4 * D + r] * x[4 * D + r];
-      gqa[D] = mm16<NT>(cols_k(sK, J, D), ps, gqa[D]);
+      floatx4 f = *reinterpret_cast<const floatx4*>(&tab[J][dim(D)]);
+      if (J > 0) f *= *reinterpret_cast<const floatx4*>(&sEK[J - 1][dim(D)]);
+      acc[D] *= f;
     }
-    table(sEK, J, f);
+  };
+  for (int J = 0; J < wave; ++J) {
+    const Split4<NT> ps = split4<NT>(p_block(sV, J, go));
+    decay(J, sDirect[J] ? sE : sEQ);
+#pragma unroll
+    for (int D = 0; D < ND; ++D) acc[D] = mm16<NT>(cols_r(sK, J, D), ps, acc[D]);
   }
-  {
-    float x[NEL];
-    table(sEQ, wave, x);
+  decay(wave, sEQ);
 #pragma unroll
-    for (int D = 0; D < ND; ++D)
+  for (int D = 0; D < ND; ++D)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        gqd[D][r] = fmaf(gqa[D][r], cq[4 * D + r] * f[4 * D + r] * x[4 * D + r], gqd[D][r]);
-  }
-  // -- gk and gv from the later sub-blocks, nearest first; f is the decay of
-  // the sub-blocks between
-  table(sEK, wave, f);
+    for (int r = 0; r < 4; ++r) gq[D][r] = fmaf(acc[D][r], cq[4 * D + r], gq[D][r]);
+  // -- gk and gv from the later sub-blocks
 #pragma unroll
-  for (int e = 0; e < NEL; ++e) kx[e] *= f[e];  // k 2^(tot-s)
-  floatx4 gka[ND];
-#pragma unroll
-  for (int D = 0; D < ND; ++D) gka[D] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int e = 0; e < NEL; ++e) f[e] = 1.f;
+  for (int D = 0; D < ND; ++D) acc[D] = zero4;
   for (int I = wave + 1; I < NB; ++I) {
-    floatx4 a = {0.f, 0.f, 0.f, 0.f};
-    float x[NEL];
-    table(sEQ, I, x);
-#pragma unroll
-    for (int e = 0; e < NEL; ++e) x[e] *= f[e];
+    const float* f = &sF[I * (I - 1) / 2 + wave][4 * lq];
+    floatx4 a = zero4;
 #pragma unroll
     for (int ks = 0; ks < NKS; ++ks) {
-      float y[8];
+      float x[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) y[c] = kx[8 * ks + c] * x[8 * ks + c];
-      a = mm<NT>(rows8(&sQ[0][16 * I][0], KPL, KSTR, ks), split8<NT>(y), a);
+      for (int i = 0; i < 8; ++i)
+        x[i] = tile::mulw(k[8 * ks + i], ck[8 * ks + i] * f[32 * ks + 16 * (i / 4) + i % 4]);
+      a = mm<NT>(rows8(&sQ[0][16 * I][0], KPL, KSTR, ks), split8<NT>(x), a);
     }
-    const Split4<NT> ps = split4<NT>(p_with(sO, I, v)), as = split4<NT>(a);
+    const Split4<NT> ps = split4<NT>(p_block(sO, I, v)), as = split4<NT>(a);
 #pragma unroll
     for (int D = 0; D < ND; ++D) {
-      const floatx4 y = mm16<NT>(cols_k(sQ, I, D), ps, floatx4{0.f, 0.f, 0.f, 0.f});
+      const floatx4 o = mm16<NT>(cols_r(sQ, I, D), ps, zero4);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) gka[D][r] = fmaf(y[r], x[4 * D + r], gka[D][r]);
+      for (int r = 0; r < 4; ++r) acc[D][r] = fmaf(o[r], f[16 * D + r], acc[D][r]);
     }
 #pragma unroll
-    for (int E = 0; E < NE; ++E) gva[E] = mm16<NT>(cols_o(I, E), as, gva[E]);
-    table(sE, I, x);
-#pragma unroll
-    for (int e = 0; e < NEL; ++e) f[e] *= x[e];
+    for (int E = 0; E < NE; ++E) gv[E] = mm16<NT>(cols_o(I, E), as, gv[E]);
   }
-  {
-    float x[NEL];
-    table(sEK, wave, x);
 #pragma unroll
-    for (int D = 0; D < ND; ++D)
+  for (int D = 0; D < ND; ++D) {
+    const floatx4 f = *reinterpret_cast<const floatx4*>(&sA[wave][dim(D)]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        ck[4 * D + r] *= x[4 * D + r];  // 2^(tot - s)
-        gkd[D][r] = fmaf(gka[D][r], ck[4 * D + r], gkd[D][r]);
-        ck[4 * D + r] *= f[4 * D + r];  // 2^(B - b)
-      }
+    for (int r = 0; r < 4; ++r) {
+      gk[D][r] = fmaf(acc[D][r], ck[4 * D + r], gk[D][r]);
+      ck[4 * D + r] *= f[r];  // 2^(B - b)
+    }
   }
-  __syncthreads();  // D_n is written; tot and ref are read
+  __syncthreads();  // D_n is written
   // -- gk and gv from the state behind the chunk
-  floatx4 gks[ND];
-#pragma unroll
-  for (int D = 0; D < ND; ++D) gks[D] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int ks = 0; ks < NES; ++ks) {
-    const Split8<NT> x = v.template terms<NT>(ks);
-#pragma unroll
-    for (int D = 0; D < ND; ++D) gks[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), x, gks[D]);
-  }
 #pragma unroll
   for (int ks = 0; ks < NKS; ++ks) {
     float x[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = kx[8 * ks + c] * f[8 * ks + c];
+    for (int i = 0; i < 8; ++i) x[i] = tile::mulw(k[8 * ks + i], ck[8 * ks + i]);
     const Split8<NT> xs = split8<NT>(x);
 #pragma unroll
     for (int E = 0; E < NE; ++E) {
@@ -750,64 +832,81 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
 #pragma unroll
       for (int i = 0; i < NT; ++i)
         dt.t[i] = join(tr4<VSTR, 4, 8>(&sX[i][32 * ks][colblk(E)]), tr4<VSTR, 4, 8>(&sX[i][32 * ks + 16][colblk(E)]));
-      gva[E] = mm<NT>(dt, xs, gva[E]);
-    }
-  }
-  // -- the decay's gradient: suffix sums of q gq - k gk^pairs, sums of
-  // k gk^state over the tokens before
-  float g2[NEL];
-#pragma unroll
-  for (int D = 0; D < ND; ++D) {
-    float z[4], w[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int e = 4 * D + r;
-      gks[D][r] *= ck[e];
-      z[r] = row_suffix16(fmaf(q[e], gqd[D][r], -k[e] * gkd[D][r]));
-      w[r] = row_scan16(k[e] * gks[D][r]);
-      g2[e] = z[r] + row_before16(w[r]);
-    }
-    if (lr == 0) *reinterpret_cast<floatx4*>(&sA[wave][dim(D)]) = floatx4{z[0], z[1], z[2], z[3]};
-    if (lr == 15) *reinterpret_cast<floatx4*>(&sB[wave][dim(D)]) = floatx4{w[0], w[1], w[2], w[3]};
-  }
-  __syncthreads();
-  const float self = sSelf[t];
-  for (int J = 0; J < NB; ++J) {
-    if (J == wave) continue;
-    float x[NEL];
-    table(J < wave ? sB : sA, J, x);
-#pragma unroll
-    for (int e = 0; e < NEL; ++e) g2[e] += x[e];
-  }
-#pragma unroll
-  for (int D = 0; D < ND; ++D) {
-    floatx4 ad = *reinterpret_cast<const floatx4*>(&sAD[dim(D)]);
-#pragma unroll
-    for (int J = 0; J < NB; ++J) ad *= *reinterpret_cast<const floatx4*>(&sE[J][dim(D)]);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int e = 4 * D + r;
-      g2[e] += ad[r];
-      gqd[D][r] = fmaf(self, k[e], gqd[D][r]);
-      gkd[D][r] = fmaf(self, q[e], gkd[D][r] + gks[D][r]);
+      gv[E] = mm<NT>(dt, xs, gv[E]);
     }
   }
   if (!pad) {
 #pragma unroll
-    for (int D = 0; D < ND; ++D) {
-      const float x[4] = {gqd[D][0], gqd[D][1], gqd[D][2], gqd[D][3]};
-      const float y[4] = {gkd[D][0], gkd[D][1], gkd[D][2], gkd[D][3]};
-      store4(gqp + row * DK + dim(D), x);
-      store4(gkp + row * DK + dim(D), y);
-      store4(ggp + row * DK + dim(D), g2 + 4 * D);
-    }
-#pragma unroll
     for (int E = 0; E < NE; ++E) {
-      const float x[4] = {gva[E][0], gva[E][1], gva[E][2], gva[E][3]};
+      const float x[4] = {gv[E][0], gv[E][1], gv[E][2], gv[E][3]};
       store4(gvp + row * DV + dim(E), x);
     }
   }
+#pragma unroll
+  for (int D = 0; D < ND; ++D) acc[D] = zero4;
+  floatx4 sd = zero4;
+#pragma unroll
+  for (int ks = 0; ks < NES; ++ks) {
+    const Split8<NT> o = v.template terms<NT>(ks);
+#pragma unroll
+    for (int D = 0; D < ND; ++D) acc[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), o, acc[D]);
+    sd = mm<NT>(keep[ks], rows8(&sX[0][16 * (wave % ND)][0], XPL, VSTR, ks), sd);
+  }
+  // -- 2^B <S_n, D_n>: the diagonals of the blocks of S_n D_n^T
+  if (wave < ND) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (4 * lq + r == lr) {
+        float o = sd[r];
+#pragma unroll
+        for (int J = 0; J < NB; ++J) o *= sE[J][16 * wave + lr];
+        sAD[16 * wave + lr] = o;
+      }
+    }
+  }
+  // -- the decay's gradient: suffix sums of q gq - k gk^pairs, and sums of
+  // k gk^state over the tokens before
+  const float self = sSelf[t];
+  float g2[NEL];
+#pragma unroll
+  for (int D = 0; D < ND; ++D) {
+    floatx4 z, w;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int e = 4 * D + r;
+      acc[D][r] *= ck[e];
+      z[r] = row_suffix16(fmaf(-k[e], gk[D][r], tile::mulw(q[e], gq[D][r])));
+      w[r] = row_scan16(tile::mulw(k[e], acc[D][r]));
+      g2[e] = z[r] + row_before16(w[r]);
+      gq[D][r] = fmaf(self, k[e], gq[D][r]);
+      gk[D][r] = fmaf(self, q[e], gk[D][r] + acc[D][r]);
+    }
+    if (lr == 0) *reinterpret_cast<floatx4*>(&sB[wave][dim(D)]) = z;
+    if (lr == 15) *reinterpret_cast<floatx4*>(&sEQ[wave][dim(D)]) = w;
+    if (!pad) {
+      const float x[4] = {gq[D][0], gq[D][1], gq[D][2], gq[D][3]};
+      const float y[4] = {gk[D][0], gk[D][1], gk[D][2], gk[D][3]};
+      store4(gqp + row * DK + dim(D), x);
+      store4(gkp + row * DK + dim(D), y);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int D = 0; D < ND; ++D) {
+    floatx4 o = *reinterpret_cast<const floatx4*>(&sAD[dim(D)]);
+#pragma unroll
+    for (int J = 0; J < NB; ++J)  // the sums of the tokens behind, and of those before
+      if (J != wave) o += *reinterpret_cast<const floatx4*>(J < wave ? &sEQ[J][dim(D)] : &sB[J][dim(D)]);
+    if (!pad) {
+      const float x[4] = {g2[4 * D] + o[0], g2[4 * D + 1] + o[1], g2[4 * D + 2] + o[2], g2[4 * D + 3] + o[3]};
+      store4(ggp + row * DK + dim(D), x);
+    }
+  }
 }
+
+// The serial scan replaces the segmented one from this many groups of four
+// state elements per launch and direction.
+constexpr long kSerialGroups = 32768;
 
 template <int DK, int DV, typename InT>
 hipError_t bwd_t(const Problem& p, int b0, int nb, const DirPack& dirs, const BwdArgs& a, char* ws,
@@ -827,11 +926,21 @@ hipError_t bwd_t(const Problem& p, int b0, int nb, const DirPack& dirs, const Bw
                      0, s, k, v, q, go, g, S, D, A, p.T, p.H, p.N, p.gh, p.gw, dirs);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  constexpr bool kTerms = NT == 2;
   const long groups = (long)nb * p.H * (DK * DV / 4);
-  hipLaunchKernelGGL((bwd_scan_kernel<8>), dim3((unsigned)((groups + kThreads - 1) / kThreads), 2),
-                     dim3(kThreads), 0, s, S, D, A, a.s0 ? a.s0 + bh0 * DK * DV : nullptr,
-                     a.gs_final ? a.gs_final + bh0 * DK * DV : nullptr,
-                     a.gs0 ? a.gs0 + bh0 * DK * DV : nullptr, p.N, DK, DV, groups);
+  const float* s0 = a.s0 ? a.s0 + bh0 * DK * DV : nullptr;
+  const float* gsf = a.gs_final ? a.gs_final + bh0 * DK * DV : nullptr;
+  float* gs0 = a.gs0 ? a.gs0 + bh0 * DK * DV : nullptr;
+  if (groups >= kSerialGroups) {
+    const dim3 grid((unsigned)((groups + kThreads - 1) / kThreads), 2);
+    hipLaunchKernelGGL((bwd_scan_serial_kernel<8, kTerms>), grid, dim3(kThreads), 0, s, S, D, A, s0,
+                       gsf, gs0, p.N, DK, DV, groups);
+  } else {
+    const int L = (p.N + 15) / 16;
+    const dim3 grid((unsigned)((groups + kThreads / 16 - 1) / (kThreads / 16)), 2);
+    auto scan = L <= 2 ? bwd_scan_kernel<2, kTerms> : L <= 4 ? bwd_scan_kernel<4, kTerms> : bwd_scan_kernel<8, kTerms>;
+    hipLaunchKernelGGL(scan, grid, dim3(kThreads), 0, s, S, D, A, s0, gsf, gs0, p.N, DK, DV, L, groups);
+  }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((bwd_grad_kernel<DK, DV, InT, NT>), dim3(p.N, p.H, nb), dim3(kThreads), 0, s,
