@@ -60,25 +60,43 @@ __device__ __forceinline__ floatx4 mma(bf8 a, bf8 b, floatx4 c) {
 // Eight or four floats as NT bf16 terms.
 template <int NT> struct Split8 { bf8 t[NT]; };
 template <int NT> struct Split4 { bf4 t[NT]; };
+// Two floats' leading bf16 terms in one register, and what they leave: pairs,
+// written out, take one conversion and two subtractions per term (whole
+// vectors were converted element by element).
+__device__ __forceinline__ unsigned term2(float& a, float& b, bool rest) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  const unsigned u = __builtin_bit_cast(unsigned, __builtin_convertvector(f2{a, b}, bf2));
+  if (rest) {
+    a -= __uint_as_float(u << 16);
+    b -= __uint_as_float(u & 0xffff0000u);
+  }
+  return u;
+}
 template <int NT>
 __device__ __forceinline__ Split8<NT> split8(const float* x) {
-  typedef float f8 __attribute__((ext_vector_type(8)));
   Split8<NT> s;
-  f8 r = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+  float r[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) r[c] = x[c];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    s.t[t] = __builtin_convertvector(r, bf8);
-    if (t + 1 < NT) r -= __builtin_convertvector(s.t[t], f8);
+    tile::u32x4 u;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) u[c] = term2(r[2 * c], r[2 * c + 1], t + 1 < NT);
+    s.t[t] = __builtin_bit_cast(bf8, u);
   }
   return s;
 }
 template <int NT>
-__device__ __forceinline__ Split4<NT> split4(floatx4 r) {
+__device__ __forceinline__ Split4<NT> split4(floatx4 x) {
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
   Split4<NT> s;
+  float r[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    s.t[t] = __builtin_convertvector(r, bf4);
-    if (t + 1 < NT) r -= __builtin_convertvector(s.t[t], floatx4);
+    const u32x2 u = {term2(r[0], r[1], t + 1 < NT), term2(r[2], r[3], t + 1 < NT)};
+    s.t[t] = __builtin_bit_cast(bf4, u);
   }
   return s;
 }
@@ -444,7 +462,7 @@ __global__ __launch_bounds__(kThreads) void bwd_scan_kernel(
 // and a product written transposed (rows = dims, columns = tokens) leaves
 // exactly the same token and dims in the lane, so inputs, factors and results
 // meet in registers. LDS rows hold dim d at place 32 ks + 8 lq + 4 h + r, so
-// that a lane's eight values are 16 contiguous bytes.
+// that a lane's eight values are one 16-byte chunk.
 //
 // With s the cumulative decay inside a sub-block (log2), tot its last value
 // and ref its value at the 8th token, the rows kept in LDS are
@@ -459,6 +477,44 @@ __global__ __launch_bounds__(kThreads) void bwd_scan_kernel(
 // own pairs directly in float.
 // ===========================================================================
 constexpr float kMaxSpan = 68.f;
+
+// LDS tiles have rows of W 16-bit places without padding; the 16-byte chunk c
+// of a row lies at chunk c ^ swz<W>(row). Eight neighbouring rows' equal chunks
+// (an operand read along rows) and the four rows' 8-byte pieces of a
+// transposed read then fall on different banks.
+template <int W>
+__device__ __forceinline__ int swz(int row) {
+  return W == 64 ? ((row & 2) << 1) | ((row >> 1) & 2) | (row & 1) : (row >> 2) & 3;
+}
+template <int W>
+__device__ __forceinline__ int at_chunk(int row, int c) {
+  return row * W + 8 * (c ^ swz<W>(row));
+}
+// A lane's places in a tile, relative to a row that is a multiple of 16: its
+// eight contracted values of row lr, chunk 4 ks + lq; and its part of the
+// transposed read of column block D along rows 4 lq + 0..3.
+template <int W>
+struct Lane {
+  int row[W / 32], col[W / 32];
+  __device__ __forceinline__ Lane() {
+    const int lr = threadIdx.x & 15, lq = (threadIdx.x >> 4) & 3;
+#pragma unroll
+    for (int ks = 0; ks < W / 32; ++ks) {
+      row[ks] = at_chunk<W>(lr, 4 * ks + lq);
+      col[ks] = at_chunk<W>(4 * lq + (lr >> 2), 4 * ks + (lr & 3));
+    }
+  }
+  __device__ __forceinline__ bf8 rows(const __bf16* tl, int ks) const {
+    return *reinterpret_cast<const bf8*>(tl + row[ks]);
+  }
+  __device__ __forceinline__ void put(__bf16* tl, int ks, bf8 x) const {
+    *reinterpret_cast<bf8*>(tl + row[ks]) = x;
+  }
+  __device__ __forceinline__ bf4 cols(const __bf16* tl, int D) const {
+    return __builtin_bit_cast(
+        bf4, __builtin_amdgcn_ds_read_tr16_b64_v4f16((tile::lds_fp16x4_t*)(tl + col[D / 2] + 4 * (D % 2))));
+  }
+};
 
 // Lane n of each row of 16, on all of the row's lanes.
 template <int LANE>
@@ -477,12 +533,12 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   constexpr int NKS = DK / 32, NES = DV / 32, ND = DK / 16, NE = DV / 16;
   constexpr int NEL = 4 * ND, NVL = 4 * NE;  // a lane's dims of q/k/g and of v/go
   constexpr int NP = NB * (NB - 1) / 2;      // pairs of sub-blocks
-  constexpr int KSTR = DK + 8, VSTR = DV + 8, NV = kHalf ? 1 : NT;
-  __shared__ __attribute__((aligned(16))) __bf16 sQ[NT][C][KSTR];   // qx
-  __shared__ __attribute__((aligned(16))) __bf16 sK[NT][C][KSTR];   // kx
-  __shared__ __attribute__((aligned(16))) __bf16 sO[NV][C][VSTR];   // go (half inputs: half bits)
-  __shared__ __attribute__((aligned(16))) __bf16 sV[NV][C][VSTR];   // v
-  __shared__ __attribute__((aligned(16))) __bf16 sX[NT][DK][VSTR];  // S_n, then D_n
+  constexpr int KB = 16 * DK, VB = 16 * DV;  // 16 rows of a tile
+  __shared__ __attribute__((aligned(16))) __bf16 sQ[NT][C * DK];             // qx
+  __shared__ __attribute__((aligned(16))) __bf16 sK[NT][C * DK];             // kx
+  __shared__ __attribute__((aligned(16))) __bf16 sO[NT][C * DV];             // go
+  __shared__ __attribute__((aligned(16))) __bf16 sV[kHalf ? 1 : NT][C * DV];  // v (half inputs: as they are)
+  __shared__ __attribute__((aligned(16))) __bf16 sX[NT][DK * DV];            // S_n, then D_n
   __shared__ __attribute__((aligned(16))) float sF[NP][DK];   // factors between two sub-blocks
   __shared__ __attribute__((aligned(16))) float sA[NB][DK];   // tot; factors to the chunk's end; sums
   __shared__ __attribute__((aligned(16))) float sB[NB][DK];   // ref; sums of k gk^state
@@ -497,11 +553,9 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   const int lr = lane & 15, lq = lane >> 4;
   const int dir = dirs.get(b), t = 16 * wave + lr;
   const long bhn = ((long)b * H + h) * N + n;
-  // place of a lane's dims 4D + r in memory rows, of its eight per ks in LDS
-  // rows, and of column block D there
-  auto dim = [&](int D) { return 16 * D + 4 * lq; };
-  auto place = [&](int ks) { return 32 * ks + 8 * lq; };
-  auto colblk = [](int D) { return 32 * (D / 2) + 4 * (D % 2); };
+  auto dim = [&](int D) { return 16 * D + 4 * lq; };  // of a lane's dims 4 D + r in memory rows
+  const Lane<DK> lk;
+  const Lane<DV> lv;
 
   // -- this lane's token row
   const int rr = token_row(n * C + t, T, gh, gw, dir);
@@ -526,15 +580,15 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       const int u = tid + kThreads * i, d = u / LPR, e = 4 * (u % LPR);
-      const int p = 32 * (e / 32) + 8 * ((e / 4) % 4) + 4 * ((e / 16) % 2);
+      const int p = at_chunk<DV>(d, 4 * (e / 32) + (e / 4) % 4) + 4 * ((e / 16) % 2);
       if constexpr (kHalf) {
         const bf8 x = __builtin_bit_cast(bf8, st[i]);
-        *reinterpret_cast<bf4*>(&sX[0][d][p]) = __builtin_shufflevector(x, x, 0, 1, 2, 3);
-        *reinterpret_cast<bf4*>(&sX[1][d][p]) = __builtin_shufflevector(x, x, 4, 5, 6, 7);
+        *reinterpret_cast<bf4*>(&sX[0][p]) = __builtin_shufflevector(x, x, 0, 1, 2, 3);
+        *reinterpret_cast<bf4*>(&sX[1][p]) = __builtin_shufflevector(x, x, 4, 5, 6, 7);
       } else {
         const Split4<NT> sp = split4<NT>(st[i]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) *reinterpret_cast<bf4*>(&sX[j][d][p]) = sp.t[j];
+        for (int j = 0; j < NT; ++j) *reinterpret_cast<bf4*>(&sX[j][p]) = sp.t[j];
       }
     }
   };
@@ -584,7 +638,6 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
     sEK[wave][d] = direct ? 1.f : fexp2(td - rd);
   }
   if (lane == 0) sDirect[wave] = direct;
-  constexpr int KPL = C * KSTR, VPL = C * VSTR, XPL = DK * VSTR;
   const floatx4 zero4 = {0.f, 0.f, 0.f, 0.f};
   floatx4 an = zero4;  // A inside the sub-block, rows i
 #pragma unroll
@@ -598,8 +651,8 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
     const Split8<NT> xs = split8<NT>(x), ys = split8<NT>(y);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      *reinterpret_cast<bf8*>(&sQ[i][t][place(ks)]) = xs.t[i];
-      *reinterpret_cast<bf8*>(&sK[i][t][place(ks)]) = ys.t[i];
+      lk.put(&sQ[i][wave * KB], ks, xs.t[i]);
+      lk.put(&sK[i][wave * KB], ks, ys.t[i]);
     }
     an = mm<NT>(xs, ys, an);
   }
@@ -608,63 +661,58 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   floatx4 pt = zero4, pn = zero4;
 #pragma unroll
   for (int ks = 0; ks < NES; ++ks) {
+    const Split8<NT> os = go.template terms<NT>(ks);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) lv.put(&sO[i][wave * VB], ks, os.t[i]);
     if constexpr (kHalf) {
-      *reinterpret_cast<half8*>(&sV[0][t][place(ks)]) = v.pack8(ks);
-      *reinterpret_cast<half8*>(&sO[0][t][place(ks)]) = go.pack8(ks);
+      lv.put(&sV[0][wave * VB], ks, __builtin_bit_cast(bf8, v.pack8(ks)));
       pt = mfma16x16x32(v.pack8(ks), go.pack8(ks), pt);
       pn = mfma16x16x32(go.pack8(ks), v.pack8(ks), pn);
     } else {
-      const Split8<NT> vs = v.template terms<NT>(ks), os = go.template terms<NT>(ks);
+      const Split8<NT> vs = v.template terms<NT>(ks);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        *reinterpret_cast<bf8*>(&sV[i][t][place(ks)]) = vs.t[i];
-        *reinterpret_cast<bf8*>(&sO[i][t][place(ks)]) = os.t[i];
-      }
+      for (int i = 0; i < NT; ++i) lv.put(&sV[i][wave * VB], ks, vs.t[i]);
       pt = mm<NT>(vs, os, pt);
       pn = mm<NT>(os, vs, pn);
     }
   }
   put_state();  // S_n
-  // operands from LDS: 16 rows of a tile contracted along the row; 16 columns
-  // (block D of the places) contracted along 16 rows
-  auto rows8 = [&](const __bf16* tl, int plane, int str, int ks) {
+  // operands from LDS: 16 rows of a tile (from element `at` of its planes)
+  // contracted along the row; 16 columns (block D) contracted along 16 rows
+  auto rows8 = [&](const auto& ln, const auto& tl, int at, int ks) {
     Split8<NT> sp;
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-      sp.t[i] = *reinterpret_cast<const bf8*>(tl + i * plane + lr * str + place(ks));
+    for (int i = 0; i < NT; ++i) sp.t[i] = ln.rows(&tl[i][at], ks);
     return sp;
   };
-  auto cols_r = [&](const __bf16(*tl)[C][KSTR], int I, int D) {
+  auto cols4 = [&](const auto& ln, const auto& tl, int at, int D) {
     Split4<NT> sp;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) sp.t[i] = tr4<KSTR, 4, 8>(&tl[i][16 * I][colblk(D)]);
+    for (int i = 0; i < NT; ++i) sp.t[i] = ln.cols(&tl[i][at], D);
     return sp;
   };
-  auto cols_o = [&](int I, int E) {
-    if constexpr (kHalf) {
-      const half4 o = __builtin_bit_cast(half4, tr4<VSTR, 4, 8>(&sO[0][16 * I][colblk(E)]));
-      return split4<NT>(__builtin_convertvector(o, floatx4));
-    } else {
-      Split4<NT> sp;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) sp.t[i] = tr4<VSTR, 4, 8>(&sO[i][16 * I][colblk(E)]);
-      return sp;
-    }
-  };
-  // 16 rows of v with this wave's own go: P transposed; or of go with its v
-  auto p_block = [&](const __bf16(*tl)[C][VSTR], int I, const Raw<InT, NVL>& own) {
+  // P of block J's keys with this wave's queries, transposed; and of block I's
+  // queries with this wave's keys (half inputs: exact, four products of terms)
+  auto p_keys = [&](int J) {
     floatx4 p = zero4;
 #pragma unroll
     for (int ks = 0; ks < NES; ++ks) {
-      const __bf16* at = &tl[0][16 * I + lr][place(ks)];
       if constexpr (kHalf) {
-        p = mfma16x16x32(*reinterpret_cast<const half8*>(at), own.pack8(ks), p);
+        p = mfma16x16x32(__builtin_bit_cast(half8, lv.rows(&sV[0][J * VB], ks)), go.pack8(ks), p);
       } else {
-        Split8<NT> o;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) o.t[i] = *reinterpret_cast<const bf8*>(at + i * VPL);
-        p = mm<NT>(o, own.template terms<NT>(ks), p);
+        p = mm<NT>(rows8(lv, sV, J * VB, ks), go.template terms<NT>(ks), p);
       }
+    }
+    return p;
+  };
+  Split8<NT> vs[NES];
+  auto p_queries = [&](int I) {
+    floatx4 p = zero4;
+#pragma unroll
+    for (int ks = 0; ks < NES; ++ks) {
+      const Split8<NT> o = rows8(lv, sO, I * VB, ks);
+      if constexpr (kHalf) p = mma(o.t[1], vs[ks].t[1], p);
+      p = mm<NT>(o, vs[ks], p);
     }
     return p;
   };
@@ -686,8 +734,8 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
     const Split4<NT> pts = split4<NT>(pt), pns = split4<NT>(ps);
 #pragma unroll
     for (int D = 0; D < ND; ++D) {
-      gq[D] = mm16<NT>(cols_r(sK, wave, D), pts, zero4);
-      gk[D] = mm16<NT>(cols_r(sQ, wave, D), pns, zero4);
+      gq[D] = mm16<NT>(cols4(lk, sK, wave * KB, D), pts, zero4);
+      gk[D] = mm16<NT>(cols4(lk, sQ, wave * KB, D), pns, zero4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         gq[D][r] *= cq[4 * D + r];
@@ -730,7 +778,7 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   {
     const Split4<NT> as = split4<NT>(an);
 #pragma unroll
-    for (int E = 0; E < NE; ++E) gv[E] = mm16<NT>(cols_o(wave, E), as, zero4);
+    for (int E = 0; E < NE; ++E) gv[E] = mm16<NT>(cols4(lv, sO, wave * VB, E), as, zero4);
   }
   __syncthreads();
   load_state(Dws);
@@ -742,10 +790,10 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   for (int D = 0; D < ND; ++D) acc[D] = zero4;
 #pragma unroll
   for (int ks = 0; ks < NES; ++ks) {
-    const Split8<NT> o = go.template terms<NT>(ks);
+    const Split8<NT> o = rows8(lv, sO, wave * VB, ks);
 #pragma unroll
-    for (int D = 0; D < ND; ++D) acc[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), o, acc[D]);
-    keep[ks] = rows8(&sX[0][16 * (wave % ND)][0], XPL, VSTR, ks);
+    for (int D = 0; D < ND; ++D) acc[D] = mm<NT>(rows8(lv, sX, D * VB, ks), o, acc[D]);
+    keep[ks] = rows8(lv, sX, (wave % ND) * VB, ks);
   }
   // -- the brackets of the pairs of sub-blocks, and 2^(tot_J - ref_J) prod
   // 2^tot_M over all later sub-blocks M
@@ -775,10 +823,10 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
     }
   };
   for (int J = 0; J < wave; ++J) {
-    const Split4<NT> ps = split4<NT>(p_block(sV, J, go));
+    const Split4<NT> ps = split4<NT>(p_keys(J));
     decay(J, sDirect[J] ? sE : sEQ);
 #pragma unroll
-    for (int D = 0; D < ND; ++D) acc[D] = mm16<NT>(cols_r(sK, J, D), ps, acc[D]);
+    for (int D = 0; D < ND; ++D) acc[D] = mm16<NT>(cols4(lk, sK, J * KB, D), ps, acc[D]);
   }
   decay(wave, sEQ);
 #pragma unroll
@@ -786,6 +834,8 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
 #pragma unroll
     for (int r = 0; r < 4; ++r) gq[D][r] = fmaf(acc[D][r], cq[4 * D + r], gq[D][r]);
   // -- gk and gv from the later sub-blocks
+#pragma unroll
+  for (int ks = 0; ks < NES; ++ks) vs[ks] = v.template terms<NT>(ks);
 #pragma unroll
   for (int D = 0; D < ND; ++D) acc[D] = zero4;
   for (int I = wave + 1; I < NB; ++I) {
@@ -797,17 +847,17 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         x[i] = tile::mulw(k[8 * ks + i], ck[8 * ks + i] * f[32 * ks + 16 * (i / 4) + i % 4]);
-      a = mm<NT>(rows8(&sQ[0][16 * I][0], KPL, KSTR, ks), split8<NT>(x), a);
+      a = mm<NT>(rows8(lk, sQ, I * KB, ks), split8<NT>(x), a);
     }
-    const Split4<NT> ps = split4<NT>(p_block(sO, I, v)), as = split4<NT>(a);
+    const Split4<NT> ps = split4<NT>(p_queries(I)), as = split4<NT>(a);
 #pragma unroll
     for (int D = 0; D < ND; ++D) {
-      const floatx4 o = mm16<NT>(cols_r(sQ, I, D), ps, zero4);
+      const floatx4 o = mm16<NT>(cols4(lk, sQ, I * KB, D), ps, zero4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[D][r] = fmaf(o[r], f[16 * D + r], acc[D][r]);
     }
 #pragma unroll
-    for (int E = 0; E < NE; ++E) gv[E] = mm16<NT>(cols_o(I, E), as, gv[E]);
+    for (int E = 0; E < NE; ++E) gv[E] = mm16<NT>(cols4(lv, sO, I * VB, E), as, gv[E]);
   }
 #pragma unroll
   for (int D = 0; D < ND; ++D) {
@@ -831,7 +881,7 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
       Split8<NT> dt;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        dt.t[i] = join(tr4<VSTR, 4, 8>(&sX[i][32 * ks][colblk(E)]), tr4<VSTR, 4, 8>(&sX[i][32 * ks + 16][colblk(E)]));
+        dt.t[i] = join(lv.cols(&sX[i][2 * ks * VB], E), lv.cols(&sX[i][(2 * ks + 1) * VB], E));
       gv[E] = mm<NT>(dt, xs, gv[E]);
     }
   }
@@ -847,10 +897,9 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   floatx4 sd = zero4;
 #pragma unroll
   for (int ks = 0; ks < NES; ++ks) {
-    const Split8<NT> o = v.template terms<NT>(ks);
 #pragma unroll
-    for (int D = 0; D < ND; ++D) acc[D] = mm<NT>(rows8(&sX[0][16 * D][0], XPL, VSTR, ks), o, acc[D]);
-    sd = mm<NT>(keep[ks], rows8(&sX[0][16 * (wave % ND)][0], XPL, VSTR, ks), sd);
+    for (int D = 0; D < ND; ++D) acc[D] = mm<NT>(rows8(lv, sX, D * VB, ks), vs[ks], acc[D]);
+    sd = mm<NT>(keep[ks], rows8(lv, sX, (wave % ND) * VB, ks), sd);
   }
   // -- 2^B <S_n, D_n>: the diagonals of the blocks of S_n D_n^T
   if (wave < ND) {
