@@ -147,24 +147,20 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// A lane's values of a token row as loaded (half inputs stay packed, and are
-// converted where a product uses them).
+// A lane's values of a token row as loaded, eight neighbours per ks (half
+// inputs stay packed, and are converted where a product uses them).
 template <typename InT, int NEL> struct Raw {
-  typedef InT V4 __attribute__((ext_vector_type(4)));
-  V4 v[NEL / 4];
-  __device__ __forceinline__ void load(const InT* p) {  // dims 16 D + 0..3 from p
+  typedef InT V8 __attribute__((ext_vector_type(8)));
+  V8 v[NEL / 8];
+  __device__ __forceinline__ void load(const InT* p) {  // dims 32 ks + 0..7 from p
 #pragma unroll
-    for (int D = 0; D < NEL / 4; ++D) v[D] = *reinterpret_cast<const V4*>(p + 16 * D);
+    for (int ks = 0; ks < NEL / 8; ++ks) v[ks] = *reinterpret_cast<const V8*>(p + 32 * ks);
   }
   __device__ __forceinline__ void zero_if(bool pad) {
 #pragma unroll
-    for (int D = 0; D < NEL / 4; ++D) v[D] = pad ? V4{} : v[D];
+    for (int ks = 0; ks < NEL / 8; ++ks) v[ks] = pad ? V8{} : v[ks];
   }
-  __device__ __forceinline__ float operator[](int e) const { return (float)v[e / 4][e % 4]; }
-  // the eight values of dims 32 ks + ..: packed, or in bf16 terms
-  __device__ __forceinline__ auto pack8(int ks) const {
-    return __builtin_shufflevector(v[2 * ks], v[2 * ks + 1], 0, 1, 2, 3, 4, 5, 6, 7);
-  }
+  __device__ __forceinline__ float operator[](int e) const { return (float)v[e / 8][e % 8]; }
   template <int NT> __device__ __forceinline__ Split8<NT> terms(int ks) const {
     float x[8];
 #pragma unroll
@@ -172,12 +168,6 @@ template <typename InT, int NEL> struct Raw {
     return split8<NT>(x);
   }
 };
-__device__ __forceinline__ void store4(half_t* p, const float* x) {
-  *reinterpret_cast<half4*>(p) = half4{(half_t)x[0], (half_t)x[1], (half_t)x[2], (half_t)x[3]};
-}
-__device__ __forceinline__ void store4(float* p, const float* x) {
-  *reinterpret_cast<floatx4*>(p) = floatx4{x[0], x[1], x[2], x[3]};
-}
 
 // Inclusive suffix sum over the 16 lanes of a DPP row, and the sum of the
 // lanes before each one.
@@ -457,12 +447,12 @@ __global__ __launch_bounds__(kThreads) void bwd_scan_kernel(
 // ===========================================================================
 // Gradients: one workgroup per (chunk, head, batch), four waves; wave w owns
 // the 16 tokens of sub-block w as queries (gq) and as keys (gk, gv). A lane
-// holds token lr = lane % 16 of it and the dims d = 32 ks + 16 h + 4 lq + r
-// (lq = lane / 16): as an operand these are eight contracted places per ks,
-// and a product written transposed (rows = dims, columns = tokens) leaves
-// exactly the same token and dims in the lane, so inputs, factors and results
-// meet in registers. LDS rows hold dim d at place 32 ks + 8 lq + 4 h + r, so
-// that a lane's eight values are one 16-byte chunk.
+// holds token lr = lane % 16 of it and the dims d = 32 ks + 8 lq + c (lq = lane
+// / 16): as an operand these are eight contracted places per ks, and a product
+// written transposed (rows = dims, columns = tokens) in blocks D = 2 ks + h of
+// the dims 32 ks + 8 (m / 4) + 4 h + m % 4, m = 0..15, leaves exactly the same
+// token and dims in the lane, so inputs, factors and results meet in registers
+// and a lane loads and stores 16 contiguous bytes of a row.
 //
 // With s the cumulative decay inside a sub-block (log2), tot its last value
 // and ref its value at the 8th token, the rows kept in LDS are
@@ -478,30 +468,39 @@ __global__ __launch_bounds__(kThreads) void bwd_scan_kernel(
 // ===========================================================================
 constexpr float kMaxSpan = 68.f;
 
-// LDS tiles have rows of W 16-bit places without padding; the 16-byte chunk c
-// of a row lies at chunk c ^ swz<W>(row). Eight neighbouring rows' equal chunks
-// (an operand read along rows) and the four rows' 8-byte pieces of a
-// transposed read then fall on different banks.
-template <int W>
+// LDS tiles have rows of W 16-bit values without padding; the 16-byte chunk c
+// of a row lies at chunk c ^ swz(row). The equal chunks of the eight rows that
+// an operand read along rows touches together, and the four rows' 8-byte
+// pieces of a transposed read, then fall on different banks. Rows of a tile
+// are tokens or, with kDims, the dims of a state, which are read in the blocks
+// described above.
+template <int W, bool kDims>
 __device__ __forceinline__ int swz(int row) {
-  return W == 64 ? ((row & 2) << 1) | ((row >> 1) & 2) | (row & 1) : (row >> 2) & 3;
+  const int far = row >> (kDims ? 3 : 2);
+  return W == 64 ? ((row & 2) << 1) | ((far & 1) << 1) | (row & 1) : far & 3;
 }
-template <int W>
+template <int W, bool kDims>
 __device__ __forceinline__ int at_chunk(int row, int c) {
-  return row * W + 8 * (c ^ swz<W>(row));
+  return row * W + 8 * (c ^ swz<W, kDims>(row));
 }
-// A lane's places in a tile, relative to a row that is a multiple of 16: its
-// eight contracted values of row lr, chunk 4 ks + lq; and its part of the
-// transposed read of column block D along rows 4 lq + 0..3.
-template <int W>
+// Row of a state that is row lr of block D.
+__device__ __forceinline__ int dim_row(int D, int lr) {
+  return 32 * (D / 2) + 8 * (lr >> 2) + 4 * (D % 2) + (lr & 3);
+}
+// A lane's places in a tile of tokens, relative to a row that is a multiple of
+// 16: its eight contracted values of row lr, chunk 4 ks + lq; and its part of
+// the transposed read of column block D along rows 4 lq + 0..3. In a state:
+// the same of block D's rows (`row` and 4 (D % 2) W further: the swizzle does
+// not look at that bit), and of column block E along rows 8 lq + 0..3.
+template <int W, bool kDims>
 struct Lane {
   int row[W / 32], col[W / 32];
   __device__ __forceinline__ Lane() {
     const int lr = threadIdx.x & 15, lq = (threadIdx.x >> 4) & 3;
 #pragma unroll
     for (int ks = 0; ks < W / 32; ++ks) {
-      row[ks] = at_chunk<W>(lr, 4 * ks + lq);
-      col[ks] = at_chunk<W>(4 * lq + (lr >> 2), 4 * ks + (lr & 3));
+      row[ks] = at_chunk<W, kDims>(kDims ? dim_row(0, lr) : lr, 4 * ks + lq);
+      col[ks] = at_chunk<W, kDims>((kDims ? 8 : 4) * lq + (lr >> 2), 4 * ks + (lr & 3));
     }
   }
   __device__ __forceinline__ bf8 rows(const __bf16* tl, int ks) const {
@@ -553,9 +552,10 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   const int lr = lane & 15, lq = lane >> 4;
   const int dir = dirs.get(b), t = 16 * wave + lr;
   const long bhn = ((long)b * H + h) * N + n;
-  auto dim = [&](int D) { return 16 * D + 4 * lq; };  // of a lane's dims 4 D + r in memory rows
-  const Lane<DK> lk;
-  const Lane<DV> lv;
+  auto dim = [&](int D) { return 32 * (D / 2) + 8 * lq + 4 * (D % 2); };  // the first of a lane's four in block D
+  const Lane<DK, false> lk;
+  const Lane<DV, false> lv;
+  const Lane<DV, true> lx;
 
   // -- this lane's token row
   const int rr = token_row(n * C + t, T, gh, gw, dir);
@@ -580,7 +580,7 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       const int u = tid + kThreads * i, d = u / LPR, e = 4 * (u % LPR);
-      const int p = at_chunk<DV>(d, 4 * (e / 32) + (e / 4) % 4) + 4 * ((e / 16) % 2);
+      const int p = at_chunk<DV, true>(d, e / 8) + e % 8;
       if constexpr (kHalf) {
         const bf8 x = __builtin_bit_cast(bf8, st[i]);
         *reinterpret_cast<bf4*>(&sX[0][p]) = __builtin_shufflevector(x, x, 0, 1, 2, 3);
@@ -665,9 +665,9 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
 #pragma unroll
     for (int i = 0; i < NT; ++i) lv.put(&sO[i][wave * VB], ks, os.t[i]);
     if constexpr (kHalf) {
-      lv.put(&sV[0][wave * VB], ks, __builtin_bit_cast(bf8, v.pack8(ks)));
-      pt = mfma16x16x32(v.pack8(ks), go.pack8(ks), pt);
-      pn = mfma16x16x32(go.pack8(ks), v.pack8(ks), pn);
+      lv.put(&sV[0][wave * VB], ks, __builtin_bit_cast(bf8, v.v[ks]));
+      pt = mfma16x16x32(v.v[ks], go.v[ks], pt);
+      pn = mfma16x16x32(go.v[ks], v.v[ks], pn);
     } else {
       const Split8<NT> vs = v.template terms<NT>(ks);
 #pragma unroll
@@ -685,6 +685,7 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
     for (int i = 0; i < NT; ++i) sp.t[i] = ln.rows(&tl[i][at], ks);
     return sp;
   };
+  auto state_at = [&](int D) { return 2 * (D / 2) * VB + 4 * (D % 2) * DV; };  // block D of a state's rows
   auto cols4 = [&](const auto& ln, const auto& tl, int at, int D) {
     Split4<NT> sp;
 #pragma unroll
@@ -698,7 +699,7 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
 #pragma unroll
     for (int ks = 0; ks < NES; ++ks) {
       if constexpr (kHalf) {
-        p = mfma16x16x32(__builtin_bit_cast(half8, lv.rows(&sV[0][J * VB], ks)), go.pack8(ks), p);
+        p = mfma16x16x32(__builtin_bit_cast(half8, lv.rows(&sV[0][J * VB], ks)), go.v[ks], p);
       } else {
         p = mm<NT>(rows8(lv, sV, J * VB, ks), go.template terms<NT>(ks), p);
       }
@@ -792,23 +793,24 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   for (int ks = 0; ks < NES; ++ks) {
     const Split8<NT> o = rows8(lv, sO, wave * VB, ks);
 #pragma unroll
-    for (int D = 0; D < ND; ++D) acc[D] = mm<NT>(rows8(lv, sX, D * VB, ks), o, acc[D]);
-    keep[ks] = rows8(lv, sX, (wave % ND) * VB, ks);
+    for (int D = 0; D < ND; ++D) acc[D] = mm<NT>(rows8(lx, sX, state_at(D), ks), o, acc[D]);
+    keep[ks] = rows8(lx, sX, state_at(wave % ND), ks);
   }
   // -- the brackets of the pairs of sub-blocks, and 2^(tot_J - ref_J) prod
   // 2^tot_M over all later sub-blocks M
-  for (int i = tid; i < (NP + NB) * DK; i += kThreads) {
-    const int pr = i / DK, d = i % DK;
-    int I = NB, J = pr - NP;
-    if (J < 0) {
-      I = pr < 1 ? 1 : pr < 3 ? 2 : 3;
-      J = pr - I * (I - 1) / 2;
-    }
-    float o = sEK[J][d];
+  if (tid < NB * DK) {
+    const int J = tid / DK, d = tid % DK;
+    float o = sEK[J][d], e[NB], eq[NB];
 #pragma unroll
-    for (int M = 1; M < NB; ++M) o *= M > J && M < I ? sE[M][d] : 1.f;
-    if (I < NB) sF[pr][d] = o * sEQ[I][d];
-    else sA[J][d] = o;
+    for (int M = 1; M < NB; ++M) e[M] = sE[M][d], eq[M] = sEQ[M][d];
+#pragma unroll
+    for (int M = 1; M < NB; ++M) {
+      if (M > J) {
+        sF[M * (M - 1) / 2 + J][d] = o * eq[M];
+        o *= e[M];
+      }
+    }
+    sA[J][d] = o;
   }
   __syncthreads();  // S_n is read, the factors are written
   put_state();      // D_n
@@ -833,20 +835,33 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   for (int D = 0; D < ND; ++D)
 #pragma unroll
     for (int r = 0; r < 4; ++r) gq[D][r] = fmaf(acc[D][r], cq[4 * D + r], gq[D][r]);
+  // (a store's wait would be the next one's: each goes out as it is ready)
+  const float self = sSelf[t];
+  if (!pad) {
+#pragma unroll
+    for (int ks = 0; ks < NKS; ++ks) {
+      float x[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) x[c] = fmaf(self, k[8 * ks + c], gq[2 * ks + c / 4][c % 4]);
+      store8(gqp + row * DK + dim(2 * ks), x);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < NEL; ++e) gq[e / 4][e % 4] = tile::mulw(q[e], gq[e / 4][e % 4]);  // all that is left to use
   // -- gk and gv from the later sub-blocks
 #pragma unroll
   for (int ks = 0; ks < NES; ++ks) vs[ks] = v.template terms<NT>(ks);
 #pragma unroll
   for (int D = 0; D < ND; ++D) acc[D] = zero4;
   for (int I = wave + 1; I < NB; ++I) {
-    const float* f = &sF[I * (I - 1) / 2 + wave][4 * lq];
+    const float* f = &sF[I * (I - 1) / 2 + wave][8 * lq];
     floatx4 a = zero4;
 #pragma unroll
     for (int ks = 0; ks < NKS; ++ks) {
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        x[i] = tile::mulw(k[8 * ks + i], ck[8 * ks + i] * f[32 * ks + 16 * (i / 4) + i % 4]);
+        x[i] = tile::mulw(k[8 * ks + i], ck[8 * ks + i] * f[32 * ks + i]);
       a = mm<NT>(rows8(lk, sQ, I * KB, ks), split8<NT>(x), a);
     }
     const Split4<NT> ps = split4<NT>(p_queries(I)), as = split4<NT>(a);
@@ -854,7 +869,7 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
     for (int D = 0; D < ND; ++D) {
       const floatx4 o = mm16<NT>(cols4(lk, sQ, I * KB, D), ps, zero4);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[D][r] = fmaf(o[r], f[16 * D + r], acc[D][r]);
+      for (int r = 0; r < 4; ++r) acc[D][r] = fmaf(o[r], f[32 * (D / 2) + 4 * (D % 2) + r], acc[D][r]);
     }
 #pragma unroll
     for (int E = 0; E < NE; ++E) gv[E] = mm16<NT>(cols4(lv, sO, I * VB, E), as, gv[E]);
@@ -881,16 +896,18 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
       Split8<NT> dt;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        dt.t[i] = join(lv.cols(&sX[i][2 * ks * VB], E), lv.cols(&sX[i][(2 * ks + 1) * VB], E));
+        dt.t[i] = join(lx.cols(&sX[i][2 * ks * VB], E), lx.cols(&sX[i][2 * ks * VB + 4 * DV], E));
       gv[E] = mm<NT>(dt, xs, gv[E]);
     }
   }
+  auto store_row = [&](InT* p, const floatx4* x, int ks) {
+    const float y[8] = {x[2 * ks][0], x[2 * ks][1], x[2 * ks][2], x[2 * ks][3],
+                        x[2 * ks + 1][0], x[2 * ks + 1][1], x[2 * ks + 1][2], x[2 * ks + 1][3]};
+    store8(p + dim(2 * ks), y);
+  };
   if (!pad) {
 #pragma unroll
-    for (int E = 0; E < NE; ++E) {
-      const float x[4] = {gv[E][0], gv[E][1], gv[E][2], gv[E][3]};
-      store4(gvp + row * DV + dim(E), x);
-    }
+    for (int ks = 0; ks < NES; ++ks) store_row(gvp + row * DV, gv, ks);
   }
 #pragma unroll
   for (int D = 0; D < ND; ++D) acc[D] = zero4;
@@ -898,46 +915,43 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
 #pragma unroll
   for (int ks = 0; ks < NES; ++ks) {
 #pragma unroll
-    for (int D = 0; D < ND; ++D) acc[D] = mm<NT>(rows8(lv, sX, D * VB, ks), vs[ks], acc[D]);
-    sd = mm<NT>(keep[ks], rows8(lv, sX, (wave % ND) * VB, ks), sd);
+    for (int D = 0; D < ND; ++D) acc[D] = mm<NT>(rows8(lx, sX, state_at(D), ks), vs[ks], acc[D]);
+    sd = mm<NT>(keep[ks], rows8(lx, sX, state_at(wave % ND), ks), sd);
   }
   // -- 2^B <S_n, D_n>: the diagonals of the blocks of S_n D_n^T
   if (wave < ND) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       if (4 * lq + r == lr) {
+        const int d = dim_row(wave, lr);
         float o = sd[r];
 #pragma unroll
-        for (int J = 0; J < NB; ++J) o *= sE[J][16 * wave + lr];
-        sAD[16 * wave + lr] = o;
+        for (int J = 0; J < NB; ++J) o *= sE[J][d];
+        sAD[d] = o;
       }
     }
   }
   // -- the decay's gradient: suffix sums of q gq - k gk^pairs, and sums of
   // k gk^state over the tokens before
-  const float self = sSelf[t];
-  float g2[NEL];
+  float z[NEL], w[NEL];
 #pragma unroll
-  for (int D = 0; D < ND; ++D) {
-    floatx4 z, w;
+  for (int e = 0; e < NEL; ++e) {  // no branch in between: the scans' steps interleave
+    acc[e / 4][e % 4] *= ck[e];
+    z[e] = row_suffix16(fmaf(-k[e], gk[e / 4][e % 4], gq[e / 4][e % 4]));
+    w[e] = row_scan16(tile::mulw(k[e], acc[e / 4][e % 4]));
+    gk[e / 4][e % 4] = fmaf(self, q[e], gk[e / 4][e % 4] + acc[e / 4][e % 4]);
+  }
+  if (!pad) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int e = 4 * D + r;
-      acc[D][r] *= ck[e];
-      z[r] = row_suffix16(fmaf(-k[e], gk[D][r], tile::mulw(q[e], gq[D][r])));
-      w[r] = row_scan16(tile::mulw(k[e], acc[D][r]));
-      g2[e] = z[r] + row_before16(w[r]);
-      gq[D][r] = fmaf(self, k[e], gq[D][r]);
-      gk[D][r] = fmaf(self, q[e], gk[D][r] + acc[D][r]);
-    }
-    if (lr == 0) *reinterpret_cast<floatx4*>(&sB[wave][dim(D)]) = z;
-    if (lr == 15) *reinterpret_cast<floatx4*>(&sEQ[wave][dim(D)]) = w;
-    if (!pad) {
-      const float x[4] = {gq[D][0], gq[D][1], gq[D][2], gq[D][3]};
-      const float y[4] = {gk[D][0], gk[D][1], gk[D][2], gk[D][3]};
-      store4(gqp + row * DK + dim(D), x);
-      store4(gkp + row * DK + dim(D), y);
-    }
+    for (int ks = 0; ks < NKS; ++ks) store_row(gkp + row * DK, gk, ks);
+  }
+  if (lr == 0) {
+#pragma unroll
+    for (int D = 0; D < ND; ++D) *reinterpret_cast<floatx4*>(&sB[wave][dim(D)]) = row4(z, D);
+  }
+  if (lr == 15) {
+#pragma unroll
+    for (int D = 0; D < ND; ++D) *reinterpret_cast<floatx4*>(&sEQ[wave][dim(D)]) = row4(w, D);
   }
   __syncthreads();
 #pragma unroll
@@ -946,10 +960,12 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
 #pragma unroll
     for (int J = 0; J < NB; ++J)  // the sums of the tokens behind, and of those before
       if (J != wave) o += *reinterpret_cast<const floatx4*>(J < wave ? &sEQ[J][dim(D)] : &sB[J][dim(D)]);
-    if (!pad) {
-      const float x[4] = {g2[4 * D] + o[0], g2[4 * D + 1] + o[1], g2[4 * D + 2] + o[2], g2[4 * D + 3] + o[3]};
-      store4(ggp + row * DK + dim(D), x);
-    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) gk[D][r] = o[r] + z[4 * D + r] + row_before16(w[4 * D + r]);
+  }
+  if (!pad) {
+#pragma unroll
+    for (int ks = 0; ks < NKS; ++ks) store_row(ggp + row * DK, gk, ks);
   }
 }
 
