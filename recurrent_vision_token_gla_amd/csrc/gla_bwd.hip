@@ -128,17 +128,6 @@ __device__ __forceinline__ floatx4 mm16(const Split4<NT>& x, const Split4<NT>& p
   return mma(x01, join(p.t[0], p.t[0]), c);
 }
 
-// Four rows of one column of a row-major 16-bit tile in LDS, through the
-// transposing read: lane (i = lane % 16, q = lane / 16) receives rows
-// GSTEP*q + 0..3 of column i of a 16-column block whose columns 4g..4g+3 lie
-// at blk + CSTEP*g.
-template <int STR, int GSTEP, int CSTEP>
-__device__ __forceinline__ bf4 tr4(const __bf16* blk) {
-  const int s = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
-  const __bf16* p = blk + (GSTEP * q + (s >> 2)) * STR + CSTEP * (s & 3);
-  return __builtin_bit_cast(bf4, __builtin_amdgcn_ds_read_tr16_b64_v4f16((tile::lds_fp16x4_t*)p));
-}
-
 // Orders a wave's LDS writes before its own later LDS reads (the LDS unit
 // keeps a wave's accesses in order; this keeps the compiler from moving them).
 __device__ __forceinline__ void wave_sync() {
@@ -182,110 +171,169 @@ __device__ __forceinline__ float row_before16(float scan) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(scan), 0x111, 0xf, 0xf, true));
 }
 
+// Lane n of each row of 16, on all of the row's lanes.
+template <int LANE>
+__device__ __forceinline__ float row_lane(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + LANE, 0xf, 0xf, true));
+}
+
+// LDS tiles have rows of W 16-bit values without padding; the 16-byte chunk c
+// of a row lies at chunk c ^ swz(row). The equal chunks of the eight rows that
+// an operand read along rows touches together, and the four rows' 8-byte
+// pieces of a transposed read, then fall on different banks. Rows of a tile
+// are tokens or, with kDims, the dims of a state.
+template <int W, bool kDims>
+__device__ __forceinline__ int swz(int row) {
+  const int far = row >> (kDims ? 3 : 2);
+  return W == 64 ? ((row & 2) << 1) | ((far & 1) << 1) | (row & 1) : far & 3;
+}
+template <int W, bool kDims>
+__device__ __forceinline__ int at_chunk(int row, int c) {
+  return row * W + 8 * (c ^ swz<W, kDims>(row));
+}
+// A lane works on eight neighbouring dims 32 ks + 8 lq + 0..7 (lq = lane / 16),
+// so the blocks D = 2 ks + h of 16 dims that a product takes are 32 ks + 8 (m /
+// 4) + 4 h + m % 4, m = 0..15: the dim of block D that is row (or column) m.
+__device__ __forceinline__ int dim_row(int D, int lr) {
+  return 32 * (D / 2) + 8 * (lr >> 2) + 4 * (D % 2) + (lr & 3);
+}
+// A lane's places in a tile of tokens, relative to a row that is a multiple of
+// 16: its eight contracted values of row lr, chunk 4 ks + lq; and its part of
+// the transposed read of column block D along rows 4 lq + 0..3. In a state:
+// the same of block D's rows (`row` and 4 (D % 2) W further: the swizzle does
+// not look at that bit), and of column block E along rows 8 lq + 0..3.
+// Chunk 4 ks + c is chunk c with bit 2 of the place flipped (W = 64), so ks may
+// be a variable.
+template <int W, bool kDims>
+struct Lane {
+  int row, col;
+  __device__ __forceinline__ Lane() {
+    const int lr = threadIdx.x & 15, lq = (threadIdx.x >> 4) & 3;
+    row = at_chunk<W, kDims>(kDims ? dim_row(0, lr) : lr, lq);
+    col = at_chunk<W, kDims>((kDims ? 8 : 4) * lq + (lr >> 2), lr & 3);
+  }
+  __device__ __forceinline__ bf8 rows(const __bf16* tl, int ks) const {
+    return *reinterpret_cast<const bf8*>(tl + (row ^ 32 * ks));
+  }
+  __device__ __forceinline__ void put(__bf16* tl, int ks, bf8 x) const {
+    *reinterpret_cast<bf8*>(tl + (row ^ 32 * ks)) = x;
+  }
+  __device__ __forceinline__ bf4 cols(const __bf16* tl, int D) const {
+    return __builtin_bit_cast(bf4, __builtin_amdgcn_ds_read_tr16_b64_v4f16(
+                                       (tile::lds_fp16x4_t*)(tl + (col ^ 32 * (D / 2)) + 4 * (D % 2))));
+  }
+};
+
 // ===========================================================================
 // Chunk summaries: one workgroup per (chunk, head, batch) and direction of
-// time: U_n and the decay a_n from (k, v) with factors 2^(B-b), or R_n from
-// (q, go) with factors 2^b. Both contract over tokens: the operands go to LDS
-// as token rows and come back through the transposing read.
+// time: U_n and the decay a_n from (k, v), or R_n from (q, go). A wave scales
+// the 16 tokens of its sub-block by their decay to the sub-block's end (k) or
+// from its start (q), and stages them as token rows; both operands of the
+// contraction over tokens come back through the transposing read. The sub-
+// blocks are added farthest from the chunk's end (k) or start (q) first, and
+// what is accumulated decays through each of them: a lane's column of the
+// transposed product is one key dim, so that is one factor per sub-block.
+// The scaled operand has NX bf16 terms: three for half inputs too (the other
+// is exact in two) where the initial state's gradient is returned, in float.
 // ===========================================================================
-template <int DK, int DV, typename InT, int NT>
-__global__ __launch_bounds__(kThreads) void bwd_summary_kernel(
+template <int DK, int DV, typename InT, int NT, int NX>
+__global__ __launch_bounds__(kThreads, 3) void bwd_summary_kernel(
     const InT* __restrict__ kp, const InT* __restrict__ vp, const InT* __restrict__ qp,
     const InT* __restrict__ dop, const InT* __restrict__ gp, float* __restrict__ Uws,
     float* __restrict__ Rws, float* __restrict__ Aws, int T, int H, int N, int gh, int gw,
     DirPack dirs) {
-  constexpr int NKS = DK / 32, NEL = 8 * NKS, ND = DK / 16, NE = DV / 16;
-  constexpr int XSTR = DK + 16, YSTR = DV + 16;
-  __shared__ __attribute__((aligned(16))) __bf16 sX[NT][C][XSTR];
-  __shared__ __attribute__((aligned(16))) __bf16 sY[NT][C][YSTR];
-  __shared__ __attribute__((aligned(16))) float sTot[NB][DK];
+  constexpr int NKS = DK / 32, NEL = 8 * NKS, NES = DV / 32, ND = DK / 16;
+  constexpr int KB = 16 * DK, VB = 16 * DV;  // 16 rows of a tile
+  __shared__ __attribute__((aligned(16))) __bf16 sX[NX][C * DK];
+  __shared__ __attribute__((aligned(16))) __bf16 sY[NT][C * DV];
+  __shared__ float sE[NB][DK];  // decay of a sub-block
   const bool rev = blockIdx.z & 1;
   const int n = blockIdx.x, h = blockIdx.y, b = blockIdx.z >> 1;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int lr = lane & 15, lq = lane >> 4, lk = 8 * lq;
-  const int dir = dirs.get(b), t = 16 * wave + lr;
-  const InT* xp = rev ? qp : kp;
-  const InT* yp = rev ? dop : vp;
-
-  const int rr = token_row(n * C + t, T, gh, gw, dir);
+  const int lr = lane & 15, lq = lane >> 4;
+  const int rr = token_row(n * C + 16 * wave + lr, T, gh, gw, dirs.get(b));
   const bool pad = rr < 0;
   const long row = ((long)b * T + (pad ? 0 : rr)) * H + h;
-  float x[NEL], g[NEL], y[DV / 4];
-#pragma unroll
-  for (int ks = 0; ks < NKS; ++ks) {
-    load8(xp + row * DK + 32 * ks + lk, reinterpret_cast<float(&)[8]>(x[8 * ks]));
-    load8(gp + row * DK + 32 * ks + lk, reinterpret_cast<float(&)[8]>(g[8 * ks]));
+  const Lane<DK, false> lk;
+  const Lane<DV, false> lv;
+  Raw<InT, NEL> x, g;
+  Raw<InT, 8 * NES> y;
+  g.load(gp + row * DK + 8 * lq);
+  x.load((rev ? qp : kp) + row * DK + 8 * lq);
+  y.load((rev ? dop : vp) + row * DV + 8 * lq);
+  if ((n + 1) * C > T) {  // the chain's last chunk: padding rows are zeros without decay
+    g.zero_if(pad);
+    x.zero_if(pad);
+    y.zero_if(pad);
   }
+  float s[NEL];
 #pragma unroll
-  for (int ks = 0; ks < DV / 32; ++ks)
-    load8(yp + row * DV + 32 * ks + lk, reinterpret_cast<float(&)[8]>(y[8 * ks]));
-#pragma unroll
-  for (int e = 0; e < NEL; ++e) {
-    x[e] = pad ? 0.f : x[e];
-    g[e] = row_scan16(pad ? 0.f : log2_decay(g[e]));
-  }
+  for (int e = 0; e < NEL; ++e) s[e] = row_scan16(log2_decay(g[e]));
   if (lr == 15) {
 #pragma unroll
-    for (int e = 0; e < NEL; ++e) sTot[wave][32 * (e / 8) + lk + e % 8] = g[e];
+    for (int e = 0; e < NEL; ++e) sE[wave][32 * (e / 8) + 8 * lq + e % 8] = fexp2(s[e]);
   }
-#pragma unroll
-  for (int ks = 0; ks < DV / 32; ++ks) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) y[8 * ks + c] = pad ? 0.f : y[8 * ks + c];
-    const Split8<NT> s = split8<NT>(y + 8 * ks);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) *reinterpret_cast<bf8*>(&sY[i][t][32 * ks + lk]) = s.t[i];
-  }
-  __syncthreads();
+  // exponents s (from the start) or tot - s (to the end), without a branch
+  const float to_end = rev ? 0.f : 1.f, sign = rev ? 1.f : -1.f;
 #pragma unroll
   for (int ks = 0; ks < NKS; ++ks) {
     float o[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) o[c] = rev ? 0.f : -g[8 * ks + c];
-#pragma unroll
-    for (int J = 0; J < NB; ++J) {
-      const bool in = rev ? J < wave : J >= wave;
-      float tt[8];
-      tile::lds8(&sTot[J][32 * ks + lk], tt);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) o[c] += in ? tt[c] : 0.f;
+    for (int c = 0; c < 8; ++c) {
+      const float se = s[8 * ks + c];
+      o[c] = tile::mulw(x[8 * ks + c], fexp2(fmaf(to_end, row_lane<15>(se), sign * se)));
     }
+    const Split8<NX> t = split8<NX>(o);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) o[c] = x[8 * ks + c] * fexp2(rev ? o[c] + g[8 * ks + c] : o[c]);
-    const Split8<NT> s = split8<NT>(o);
+    for (int i = 0; i < NX; ++i) lk.put(&sX[i][wave * KB], ks, t.t[i]);
+  }
 #pragma unroll
-    for (int i = 0; i < NT; ++i) *reinterpret_cast<bf8*>(&sX[i][t][32 * ks + lk]) = s.t[i];
+  for (int ks = 0; ks < NES; ++ks) {
+    const Split8<NT> t = y.template terms<NT>(ks);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) lv.put(&sY[i][wave * VB], ks, t.t[i]);
   }
   __syncthreads();
 
   const long bhn = ((long)b * H + h) * N + n;
   if (!rev && tid < DK) {
-    float B = 0.f;
+    float a = sE[0][tid];
 #pragma unroll
-    for (int J = 0; J < NB; ++J) B += sTot[J][tid];
-    Aws[bhn * DK + tid] = fexp2(B);
+    for (int J = 1; J < NB; ++J) a *= sE[J][tid];
+    Aws[bhn * DK + tid] = a;
   }
-  // the transposed product Y^T X in 16x16 blocks: a lane ends up with four
-  // consecutive value columns of one key dim
+  // Y^T X for pairs of value blocks (32 columns): a lane ends up with eight
+  // neighbouring value columns of one key dim
   float* out = (rev ? Rws : Uws) + bhn * (long)(DK * DV);
-  auto frag = [&](const __bf16* base, int str, auto read) {
-    Split8<NT> s;
+  constexpr int NPAIR = ND * NES, PPW = NPAIR / 4 > 0 ? NPAIR / 4 : 1;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) s.t[i] = join(read(base + i * C * str), read(base + i * C * str + 4 * str));
-    return s;
-  };
-  constexpr int NBLK = ND * NE, BPW = NBLK / 4;
+  for (int i = 0; i < PPW; ++i) {
+    const int pr = wave * PPW + i, D = pr / NES, ks = pr % NES;
+    if (pr >= NPAIR) break;
+    floatx4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    const int d = dim_row(D, lr);
 #pragma unroll
-  for (int i = 0; i < BPW; ++i) {
-    const int blk = wave * BPW + i, D = blk / NE, E = blk % NE;
-    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int step = 0; step < NB; ++step) {
+      const int J = rev ? NB - 1 - step : step;
+      Split4<NX> xs;
 #pragma unroll
-    for (int j = 0; j < C / 32; ++j) {
-      const Split8<NT> xa = frag(&sX[0][32 * j][16 * D], XSTR, [](const __bf16* p) { return tr4<XSTR, 8, 4>(p); });
-      const Split8<NT> ya = frag(&sY[0][32 * j][16 * E], YSTR, [](const __bf16* p) { return tr4<YSTR, 8, 4>(p); });
-      acc = mm<NT>(ya, xa, acc);
+      for (int m = 0; m < NX; ++m) xs.t[m] = lk.cols(&sX[m][J * KB], D);
+      const bf8 x01 = join(xs.t[0], xs.t[1]), x22 = join(xs.t[NX - 1], xs.t[NT == 3 ? 0 : NX - 1]);
+      const float e = sE[J][d];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        Split4<NT> ys;
+#pragma unroll
+        for (int m = 0; m < NT; ++m) ys.t[m] = lv.cols(&sY[m][J * VB], 2 * ks + hh);
+        if (step) acc[hh] *= e;
+        if (NX == 3) acc[hh] = mma(join(ys.t[0], ys.t[NT - 1]), x22, acc[hh]);
+        acc[hh] = mma(join(ys.t[1], ys.t[1]), x01, acc[hh]);
+        acc[hh] = mma(join(ys.t[0], ys.t[0]), x01, acc[hh]);
+      }
     }
-    *reinterpret_cast<floatx4*>(out + (16 * D + lr) * DV + 16 * E + 4 * lq) = acc;
+    float* o = out + d * DV + 32 * ks + 8 * lq;
+    *reinterpret_cast<floatx4*>(o) = acc[0];
+    *reinterpret_cast<floatx4*>(o + 4) = acc[1];
   }
 }
 
@@ -467,59 +515,6 @@ __global__ __launch_bounds__(kThreads) void bwd_scan_kernel(
 // own pairs directly in float.
 // ===========================================================================
 constexpr float kMaxSpan = 68.f;
-
-// LDS tiles have rows of W 16-bit values without padding; the 16-byte chunk c
-// of a row lies at chunk c ^ swz(row). The equal chunks of the eight rows that
-// an operand read along rows touches together, and the four rows' 8-byte
-// pieces of a transposed read, then fall on different banks. Rows of a tile
-// are tokens or, with kDims, the dims of a state, which are read in the blocks
-// described above.
-template <int W, bool kDims>
-__device__ __forceinline__ int swz(int row) {
-  const int far = row >> (kDims ? 3 : 2);
-  return W == 64 ? ((row & 2) << 1) | ((far & 1) << 1) | (row & 1) : far & 3;
-}
-template <int W, bool kDims>
-__device__ __forceinline__ int at_chunk(int row, int c) {
-  return row * W + 8 * (c ^ swz<W, kDims>(row));
-}
-// Row of a state that is row lr of block D.
-__device__ __forceinline__ int dim_row(int D, int lr) {
-  return 32 * (D / 2) + 8 * (lr >> 2) + 4 * (D % 2) + (lr & 3);
-}
-// A lane's places in a tile of tokens, relative to a row that is a multiple of
-// 16: its eight contracted values of row lr, chunk 4 ks + lq; and its part of
-// the transposed read of column block D along rows 4 lq + 0..3. In a state:
-// the same of block D's rows (`row` and 4 (D % 2) W further: the swizzle does
-// not look at that bit), and of column block E along rows 8 lq + 0..3.
-template <int W, bool kDims>
-struct Lane {
-  int row[W / 32], col[W / 32];
-  __device__ __forceinline__ Lane() {
-    const int lr = threadIdx.x & 15, lq = (threadIdx.x >> 4) & 3;
-#pragma unroll
-    for (int ks = 0; ks < W / 32; ++ks) {
-      row[ks] = at_chunk<W, kDims>(kDims ? dim_row(0, lr) : lr, 4 * ks + lq);
-      col[ks] = at_chunk<W, kDims>((kDims ? 8 : 4) * lq + (lr >> 2), 4 * ks + (lr & 3));
-    }
-  }
-  __device__ __forceinline__ bf8 rows(const __bf16* tl, int ks) const {
-    return *reinterpret_cast<const bf8*>(tl + row[ks]);
-  }
-  __device__ __forceinline__ void put(__bf16* tl, int ks, bf8 x) const {
-    *reinterpret_cast<bf8*>(tl + row[ks]) = x;
-  }
-  __device__ __forceinline__ bf4 cols(const __bf16* tl, int D) const {
-    return __builtin_bit_cast(
-        bf4, __builtin_amdgcn_ds_read_tr16_b64_v4f16((tile::lds_fp16x4_t*)(tl + col[D / 2] + 4 * (D % 2))));
-  }
-};
-
-// Lane n of each row of 16, on all of the row's lanes.
-template <int LANE>
-__device__ __forceinline__ float row_lane(float x) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + LANE, 0xf, 0xf, true));
-}
 
 template <int DK, int DV, typename InT, int NT>
 __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_kernel(
@@ -987,8 +982,8 @@ hipError_t bwd_t(const Problem& p, int b0, int nb, const DirPack& dirs, const Bw
   float* S = reinterpret_cast<float*>(ws + w.off_S) + bhn * DK * DV;
   float* D = reinterpret_cast<float*>(ws + w.off_D) + bhn * DK * DV;
   float* A = reinterpret_cast<float*>(ws + w.off_a) + bhn * DK;
-  hipLaunchKernelGGL((bwd_summary_kernel<DK, DV, InT, NT>), dim3(p.N, p.H, 2 * nb), dim3(kThreads),
-                     0, s, k, v, q, go, g, S, D, A, p.T, p.H, p.N, p.gh, p.gw, dirs);
+  auto summary = a.gs0 ? bwd_summary_kernel<DK, DV, InT, NT, 3> : bwd_summary_kernel<DK, DV, InT, NT, NT>;
+  hipLaunchKernelGGL(summary, dim3(p.N, p.H, 2 * nb), dim3(kThreads), 0, s, k, v, q, go, g, S, D, A, p.T, p.H, p.N, p.gh, p.gw, dirs);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr bool kTerms = NT == 2;

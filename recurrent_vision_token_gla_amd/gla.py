@@ -6,8 +6,8 @@ no fallback: if the library is not built, or a call fails, this module raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import weakref
 from typing import Optional, Sequence, Union
@@ -510,31 +510,73 @@ def spatial_swiglu(a: torch.Tensor, u: torch.Tensor, weight: torch.Tensor,
 
 # ---- gradients, single tokens and the norm before a mixer ---------------------
 
-@contextlib.contextmanager
-def _launching(device, stream, *inputs):
+# the current stream of a device as a pointer, without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _launching:
     """Device and stream of a call, as the raw stream pointer. On a stream
     other than the current one, what the call allocates belongs to that stream
     and the caller's tensors are not reused before its work is done (the
-    caller orders the streams themselves)."""
-    with _on_device(device):
-        if stream is None:
-            yield _stream_ptr(None)
-            return
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        with torch.cuda.stream(stream):
-            if not torch.cuda.is_current_stream_capturing():
-                for t in inputs:
-                    if t is not None:
-                        t.record_stream(stream)
-            yield _stream_ptr(stream)
+    caller orders the streams themselves). Nothing is switched where the
+    device is current and no stream is given: the small calls are bound by
+    what the host does."""
+    __slots__ = ("device", "stream", "inputs", "contexts")
+
+    def __init__(self, device, stream, *inputs):
+        self.device, self.stream, self.inputs, self.contexts = device, stream, inputs, ()
+
+    def __enter__(self) -> int:
+        if self.stream is None:
+            if torch.cuda.current_device() != self.device.index:
+                self._open(torch.cuda.device(self.device))
+            return _raw_stream(self.device.index)
+        if self.stream.device != self.device:
+            raise ValueError(f"stream is on {self.stream.device}, the tensors on {self.device}")
+        self._open(torch.cuda.device(self.device), torch.cuda.stream(self.stream))
+        if not torch.cuda.is_current_stream_capturing():
+            for t in self.inputs:
+                if t is not None:
+                    t.record_stream(self.stream)
+        return int(self.stream.cuda_stream)
+
+    def _open(self, *contexts) -> None:
+        self.contexts = contexts
+        for c in contexts:
+            c.__enter__()
+
+    def __exit__(self, *exc) -> None:
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
 
 
 def _like(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
-    if not t.is_cuda or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or \
-            not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
+
+
+def _on_gpu(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.device
+
+
+def _out_like(out: Optional[torch.Tensor], t: torch.Tensor) -> torch.Tensor:
+    """The caller's output tensor, checked against t, or a new one (t is
+    contiguous, so is empty_like's)."""
+    return torch.empty_like(t) if out is None else _out(out, t.shape, t.dtype, t.device)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace_bytes(rows: int, F: int) -> int:
+    return int(load().gla_add_rmsnorm_bwd_workspace_bytes(rows, F))
+
+
+@functools.lru_cache(maxsize=256)
+def _gate_workspace_bytes(rows: int, dv: int) -> int:
+    return int(load().gla_gate_bwd_workspace_bytes(rows, dv))
 
 
 def _scratch(workspace: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
@@ -548,6 +590,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=256)
 def bwd_workspace_bytes(B, H, grid_h, grid_w, dk, dv) -> int:
     return int(load().gla_bwd_workspace_bytes(B, H, grid_h, grid_w, dk, dv))
 
@@ -563,27 +606,40 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gk: torch.Tensor, go:
     gs_final [B, H, dk, dv] float32 is the gradient of the final state (None
     for zero). With return_gs0 the gradient of s0 follows (in gs0 if given,
     which may be gs_final). out: four tensors to write the gradients to."""
-    B, T, H, dk, dv = _shapes(q, k, v, gk, grid_h, grid_w)
-    _like(go, (B, T, H, dv), q.dtype, q.device, "go")
-    p0 = _state_ptr(s0, B, H, dk, dv, "s0", q.device)
-    pf = _state_ptr(gs_final, B, H, dk, dv, "gs_final", q.device)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, gk must be [B, T, H, dk] and v, go [B, T, H, dv]")
+    B, T, H, dk = keys = q.shape
+    dv, dev, dtype = v.shape[-1], _on_gpu(q, "q"), q.dtype
+    values = (B, T, H, dv)
+    if T != grid_h * grid_w:
+        raise ValueError(f"T={T} but grid is {grid_h}x{grid_w}")
+    _like(q, keys, dtype, dev, "q")
+    _like(k, keys, dtype, dev, "k")
+    _like(gk, keys, dtype, dev, "gk")
+    _like(v, values, dtype, dev, "v")
+    _like(go, values, dtype, dev, "go")
+    p0 = _state_ptr(s0, B, H, dk, dv, "s0", dev)
+    pf = _state_ptr(gs_final, B, H, dk, dv, "gs_final", dev)
     if gs0 is not None and not return_gs0:
         raise ValueError("gs0 is written with return_gs0 only")
     if out is not None and len(out) != 4:
         raise ValueError("out must be four tensors (gq, gkey, gv, ggk)")
-    with _launching(q.device, stream, q, k, v, gk, go, s0, gs_final, gs0, workspace, *(out or ())) as st_ptr:
-        outs = tuple(_out(None if out is None else out[i], t.shape, q.dtype, q.device)
-                     for i, t in enumerate((q, k, v, gk)))
+    with _launching(dev, stream, q, k, v, gk, go, s0, gs_final, gs0, workspace, *(out or ())) as st_ptr:
+        if out is None:
+            outs = (torch.empty_like(q), torch.empty_like(q), torch.empty_like(v), torch.empty_like(q))
+        else:
+            outs = tuple(_out_like(o, t) for o, t in zip(out, (q, k, v, gk)))
         if return_gs0 and gs0 is None:
-            gs0 = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
-        pg = _state_ptr(gs0, B, H, dk, dv, "gs0", q.device)
+            gs0 = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        pg = _state_ptr(gs0, B, H, dk, dv, "gs0", dev)
         if return_gs0 and T == 0 and gs0 is not gs_final:  # no token: the state passes through
             gs0.zero_() if gs_final is None else gs0.copy_(gs_final)
-        workspace = _scratch(workspace, bwd_workspace_bytes(B, H, grid_h, grid_w, dk, dv), q.device)
-        ws, nws = _ws(workspace, q.device)
+        workspace = _scratch(workspace, bwd_workspace_bytes(B, H, grid_h, grid_w, dk, dv), dev)
+        ws, nws = _ws(workspace, dev)
         st = load().gla_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), gk.data_ptr(), go.data_ptr(),
-                            *[t.data_ptr() for t in outs], B, H, grid_h, grid_w, dk, dv,
-                            _dirs(direction, B), _dtype_code(q), p0, pf, pg, ws, nws, st_ptr)
+                            outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
+                            outs[3].data_ptr(), B, H, grid_h, grid_w, dk, dv, _dirs(direction, B),
+                            _dtype_code(q), p0, pf, pg, ws, nws, st_ptr)
     _check(st, "gla_bwd")
     return outs + (gs0,) if return_gs0 else outs
 
@@ -591,10 +647,12 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gk: torch.Tensor, go:
 def _step(q, k, v, gk, state, slots, out, stream, gate=None, norm_weight=None, eps=0.0):
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k, gk must be [B, H, dk] and v [B, H, dv]")
-    B, H, dk = q.shape
-    dv, dev = v.shape[-1], q.device
-    for name, t, d in (("q", q, dk), ("k", k, dk), ("v", v, dv), ("gk", gk, dk)):
-        _like(t, (B, H, d), q.dtype, dev, name)
+    B, H, dk = keys = q.shape
+    dv, dev, dtype = v.shape[-1], _on_gpu(q, "q"), q.dtype
+    _like(q, keys, dtype, dev, "q")
+    _like(k, keys, dtype, dev, "k")
+    _like(gk, keys, dtype, dev, "gk")
+    _like(v, (B, H, dv), dtype, dev, "v")
     if state.dim() != 4:
         raise ValueError("state must be [n_slots, H, dk, dv]")
     _like(state, (state.shape[0], H, dk, dv), torch.float32, dev, "state")
@@ -603,10 +661,10 @@ def _step(q, k, v, gk, state, slots, out, stream, gate=None, norm_weight=None, e
     elif state.shape[0] < B:
         raise ValueError(f"{B} rows without slots need as many states, got {state.shape[0]}")
     if gate is not None:
-        _like(gate, (B, H, dv), q.dtype, dev, "gate")
+        _like(gate, (B, H, dv), dtype, dev, "gate")
         _like(norm_weight, (dv,), torch.float32, dev, "norm_weight")
     with _launching(dev, stream, q, k, v, gk, state, slots, out, gate, norm_weight) as st_ptr:
-        out = _out(out, (B, H, dv), q.dtype, dev)
+        out = _out(out, (B, H, dv), dtype, dev)
         tail = (out.data_ptr(), B, H, dk, dv, _dtype_code(q), state.data_ptr(), state.shape[0],
                 _ptr(slots), st_ptr)
         if gate is None:
@@ -639,12 +697,13 @@ def step_gated(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gk: torch.Tens
 
 
 def _norm_args(x, residual, weight):
-    if not x.is_cuda or not x.is_contiguous() or x.dim() < 1:
+    dev = _on_gpu(x, "x")
+    if not x.is_contiguous() or x.dim() < 1:
         raise ValueError("x must be a contiguous device tensor [..., F]")
     if residual is not None:
-        _like(residual, x.shape, x.dtype, x.device, "residual")
+        _like(residual, x.shape, x.dtype, dev, "residual")
     F = x.shape[-1]
-    _like(weight, (F,), torch.float32, x.device, "weight")
+    _like(weight, (F,), torch.float32, dev, "weight")
     return (x.numel() // F if F else 0), F
 
 
@@ -656,8 +715,8 @@ def add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch
     a multiple of 8. out and sum_out may be x or residual (not the same one)."""
     rows, F = _norm_args(x, residual, weight)
     with _launching(x.device, stream, x, residual, weight, out, sum_out) as st_ptr:
-        y = _out(out, x.shape, x.dtype, x.device)
-        s = _out(sum_out, x.shape, x.dtype, x.device)
+        y = _out_like(out, x)
+        s = _out_like(sum_out, x)
         st = load().gla_add_rmsnorm(x.data_ptr(), _ptr(residual), weight.data_ptr(), float(eps),
                                     s.data_ptr(), y.data_ptr(), rows, F, _dtype_code(x), st_ptr)
     _check(st, "gla_add_rmsnorm")
@@ -675,7 +734,7 @@ def add_rmsnorm_q8(x: torch.Tensor, residual: Optional[torch.Tensor], weight: to
     with _launching(x.device, stream, x, residual, weight, out, scales, sum_out) as st_ptr:
         y8 = _out(out, x.shape, torch.float8_e4m3fn, x.device)
         sc = _out(scales, x.shape[:-1], torch.float32, x.device)
-        s = _out(sum_out, x.shape, x.dtype, x.device)
+        s = _out_like(sum_out, x)
         st = load().gla_add_rmsnorm_q8(x.data_ptr(), _ptr(residual), weight.data_ptr(), float(eps),
                                        s.data_ptr(), y8.data_ptr(), sc.data_ptr(), rows, F,
                                        _dtype_code(x), st_ptr)
@@ -696,9 +755,9 @@ def add_rmsnorm_bwd(s: torch.Tensor, weight: torch.Tensor, eps: float, gy: torch
         gw = _out(gweight, (F,), torch.float32, s.device).zero_()
         return _out(out, s.shape, s.dtype, s.device), gw
     with _launching(s.device, stream, s, weight, gy, gsum, out, gweight, workspace) as st_ptr:
-        gx = _out(out, s.shape, s.dtype, s.device)
+        gx = _out_like(out, s)
         gw = _out(gweight, (F,), torch.float32, s.device)
-        workspace = _scratch(workspace, int(load().gla_add_rmsnorm_bwd_workspace_bytes(rows, F)), s.device)
+        workspace = _scratch(workspace, _norm_workspace_bytes(rows, F), s.device)
         ws, nws = _ws(workspace, s.device)
         st = load().gla_add_rmsnorm_bwd(s.data_ptr(), weight.data_ptr(), float(eps), gy.data_ptr(),
                                         _ptr(gsum), gx.data_ptr(), gw.data_ptr(), rows, F,
@@ -725,10 +784,10 @@ def gate_bwd(o: torch.Tensor, gate: torch.Tensor, norm_weight: torch.Tensor, eps
                 _out(out[1] if out else None, o.shape, o.dtype, o.device), gw)
     with _launching(o.device, stream, o, gate, norm_weight, gy, gnorm_weight, workspace,
                     *(out or ())) as st_ptr:
-        go = _out(out[0] if out else None, o.shape, o.dtype, o.device)
-        gz = _out(out[1] if out else None, o.shape, o.dtype, o.device)
+        go = _out_like(out[0] if out else None, o)
+        gz = _out_like(out[1] if out else None, o)
         gw = _out(gnorm_weight, (dv,), torch.float32, o.device)
-        workspace = _scratch(workspace, int(load().gla_gate_bwd_workspace_bytes(rows, dv)), o.device)
+        workspace = _scratch(workspace, _gate_workspace_bytes(rows, dv), o.device)
         ws, nws = _ws(workspace, o.device)
         st = load().gla_gate_bwd(o.data_ptr(), gate.data_ptr(), norm_weight.data_ptr(), float(eps),
                                  gy.data_ptr(), go.data_ptr(), gz.data_ptr(), gw.data_ptr(), rows, dv,
