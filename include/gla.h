@@ -365,8 +365,8 @@ int gla_bwd(const void* q, const void* k, const void* v, const void* gk,
  *   slots: int32 [B] device memory, or NULL (row b uses slot b, n_slots >= B).
  * A row whose slot is negative or not below n_slots is padding: it is skipped
  * and its o is left as it was. Rows that name the same slot are consecutive
- * tokens of one sequence and are applied in row order. B <= 65535. o and state
- * must not overlap each other or an input. */
+ * tokens of one sequence and are applied in row order. B, H <= 65535. o and
+ * state must not overlap each other or an input. */
 int gla_step(const void* q, const void* k, const void* v, const void* gk,
              void* o, int B, int H, int dk, int dv, int dtype, float* state,
              int64_t n_slots, const int32_t* slots, void* stream);

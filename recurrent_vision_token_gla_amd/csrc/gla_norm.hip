@@ -308,13 +308,20 @@ int gate_parts(long rows, int dv) { return even_parts(rows, 256 / (dv / 8)); }
 
 template <int TPR, int VPT, typename InT>
 hipError_t norm_t(const NormArgs& a, hipStream_t s) {
-  const long rpb = 256 / TPR;
-  const dim3 grid((unsigned)((a.rows + rpb - 1) / rpb));
+  // at most 2^22 workgroups (2^30 threads) per launch
+  constexpr long rpb = 256 / TPR, most = rpb << 22;
   auto kernel = a.y8 ? add_rmsnorm_kernel<TPR, VPT, InT, true> : add_rmsnorm_kernel<TPR, VPT, InT, false>;
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, static_cast<const InT*>(a.x),
-                     static_cast<const InT*>(a.residual), a.weight, a.eps, static_cast<InT*>(a.sum),
-                     static_cast<InT*>(a.y), static_cast<unsigned char*>(a.y8), a.scales, a.rows, a.F);
-  return hipGetLastError();
+  auto at = [](auto* p, long off) { return p ? p + off : p; };
+  for (long r0 = 0; r0 < a.rows; r0 += most) {
+    const long rows = a.rows - r0 < most ? a.rows - r0 : most, off = r0 * a.F;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((rows + rpb - 1) / rpb)), dim3(256), 0, s,
+                       static_cast<const InT*>(a.x) + off, at(static_cast<const InT*>(a.residual), off),
+                       a.weight, a.eps, at(static_cast<InT*>(a.sum), off), at(static_cast<InT*>(a.y), off),
+                       at(static_cast<unsigned char*>(a.y8), off), at(a.scales, r0), rows, a.F);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int TPR, int VPT, typename InT>

@@ -12,12 +12,29 @@
 // Rows of one call that name the same slot are consecutive tokens of one
 // sequence: the workgroup of the first such row applies all of them in row
 // order with the state in registers, and those of the others leave. Every wave
-// finds them by comparing the call's slots, 64 at a time.
+// finds them by comparing the call's slots, 512 per round of loads.
 #include "gla_step.h"
 #include "gla_tile.h"
 
 namespace gla {
 namespace step {
+
+// First row of [lo, hi) that names `slot`, or hi; the same on every lane.
+__device__ __forceinline__ int find_slot(const int32_t* __restrict__ slots, int slot, int lo, int hi) {
+  constexpr int W = 8;
+  const int lane = threadIdx.x & 63;
+  for (int j0 = lo; j0 < hi; j0 += 64 * W) {
+    int s[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) s[i] = slots[min(j0 + 64 * i + lane, hi - 1)];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const unsigned long long hit = __ballot(j0 + 64 * i + lane < hi && s[i] == slot);
+      if (hit) return j0 + 64 * i + __builtin_ctzll(hit);
+    }
+  }
+  return hi;
+}
 
 template <int DK, int DV, typename InT, bool kGate>
 __global__ __launch_bounds__(kThreads) void step_kernel(
@@ -37,12 +54,8 @@ __global__ __launch_bounds__(kThreads) void step_kernel(
   floatx4 s[NG];
 #pragma unroll
   for (int i = 0; i < NG; ++i) s[i] = *reinterpret_cast<const floatx4*>(S + i * RPP * DV);
-  if (slots) {
-    for (int j0 = 0; j0 < b; j0 += 64) {
-      const int j = j0 + lane;
-      if (__any(j < b && slots[j < b ? j : b] == (int32_t)slot)) return;  // the first such row does this one
-    }
-  }
+  // the first row of this slot does this one too
+  if (slots && find_slot(slots, (int)slot, 0, b) < b) return;
   for (int r = b;;) {
     const long row = (long)r * H + h;
     float x[4], o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -80,18 +93,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(
       op[row * DV + tid] = (InT)y;
     }
     // the next row of the same sequence
-    int next = B;
-    if (slots) {
-      for (int j0 = (r + 1) & ~63; j0 < B; j0 += 64) {
-        const int j = j0 + lane;
-        const unsigned long long hit =
-            __ballot(j > r && j < B && slots[j < B ? j : B - 1] == (int32_t)slot);
-        if (hit) {
-          next = j0 + __builtin_ctzll(hit);
-          break;
-        }
-      }
-    }
+    const int next = slots ? find_slot(slots, (int)slot, r + 1, B) : B;
     if (next >= B) break;
     r = next;
     __syncthreads();  // sPart is read

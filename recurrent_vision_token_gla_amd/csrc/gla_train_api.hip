@@ -83,7 +83,7 @@ int step_impl(const void* q, const void* k, const void* v, const void* gk, const
   if (B < 0 || H < 0 || n_slots < 0) return GLA_E_ARG;
   if (dtype != GLA_F16 && dtype != GLA_F32) return GLA_E_ARG;
   if ((dk != 32 && dk != 64) || (dv != 32 && dv != 64)) return GLA_E_UNSUPPORTED;
-  if (B > 65535 || n_slots > (1LL << 31)) return GLA_E_UNSUPPORTED;
+  if (B > 65535 || H > 65535 || n_slots > (1LL << 31)) return GLA_E_UNSUPPORTED;
   if (B == 0 || H == 0) return GLA_OK;
   GLA_TRY(check_tensor(q));
   GLA_TRY(check_tensor(k));
@@ -146,8 +146,12 @@ int gla_bwd(const void* q, const void* k, const void* v, const void* gk, const v
       {{q, nk}, {k, nk}, {v, nv}, {gk, nk}, {go, nv}, {s0, ns},
        {(const void*)gs_final == (const void*)gs0 ? nullptr : gs_final, ns}}));
   const gla::BwdArgs a{q, k, v, gk, go, gq, gkey, gv, ggk, s0, gs_final, gs0};
-  for (int b0 = 0; b0 < B; b0 += gla::kMaxBatchPerLaunch) {
-    const int nb = B - b0 < gla::kMaxBatchPerLaunch ? B - b0 : gla::kMaxBatchPerLaunch;
+  // at most 2^21 chains (batch elements x heads) per launch: the scans take a
+  // thread per four state elements
+  int most = (1 << 21) / H;
+  if (most > gla::kMaxBatchPerLaunch) most = gla::kMaxBatchPerLaunch;
+  for (int b0 = 0; b0 < B; b0 += most) {
+    const int nb = B - b0 < most ? B - b0 : most;
     const hipError_t e = gla::launch_bwd(p, b0, nb, pack_dirs(dir, b0, nb), a,
                                          static_cast<char*>(workspace),
                                          static_cast<hipStream_t>(stream));

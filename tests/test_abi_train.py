@@ -74,7 +74,7 @@ def test_step_refusals(lib):
         assert f(q=None) == A and f(o=None) == A and f(state=None) == A
         assert f(q=at(0, 4)) == A and f(state=at(5, 8)) == A and f(slots=at(6, 2)) == A
         assert f(B=-1) == A and f(n=-1) == A and f(dtype=3) == A
-        assert f(dk=16) == U and f(dv=96) == U and f(B=65536) == U
+        assert f(dk=16) == U and f(dv=96) == U and f(B=65536) == U and f(H=65536) == U
         assert f(slots=None, n=3) == A                      # four rows, three states
         assert f(o=at(0)) == A and f(o=at(5)) == A          # over an input, over the states
         assert f(state=at(6), n=1) == A                     # the slots inside the states

@@ -173,6 +173,30 @@ def test_more_batch_elements_than_one_launch():
     check(x, 1, 5, dirs)
 
 
+def test_many_chains_take_the_serial_scan():
+    """60 chains of 64/64 are 61,440 groups of four state elements: the scan
+    that walks each chain in order; ten chunks, whole windows and a rest."""
+    x, s0, gsf = inputs(4, 25, 25, 15, 64, 64, np.float16, 981, gate="mixed", carry=True)
+    check(x, 25, 25, [0, 1, 2, 3], s0, gsf)
+
+
+def test_offsets_past_32_bits():
+    """33.6 million token-heads: tensors of more than 2^31 elements. The last
+    batch element against a call of its own, bit for bit."""
+    B, H, gh, gw = 41, 16, 200, 256
+    rng = torch.Generator(device="cuda").manual_seed(5)
+    one = [torch.randn(1, gh * gw, H, 64, generator=rng, device="cuda").half() for _ in range(5)]
+    one[3] = -one[3].abs() / 8
+    big = [torch.zeros(B, gh * gw, H, 64, dtype=torch.float16, device="cuda") for _ in one]
+    for t, o in zip(big, one):
+        t[B - 1:] = o
+    want = gla.bwd(*one, gh, gw, 2)
+    got = gla.bwd(*big, gh, gw, 2)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a[B - 1:], b) and not bool(a[:B - 1].any())
+
+
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])
 def test_gradient_matches_differences(dtype):
     """Central differences of the float64 recurrence along random directions of

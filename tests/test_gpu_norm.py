@@ -258,3 +258,28 @@ def test_empty():
     gx, gw = gla.add_rmsnorm_bwd(e, w, EPS, e.clone())
     assert gx.shape == (0, 64) and not bool(gw.any())
     assert not bool(gla.gate_bwd(e, e.clone(), w, EPS, e.clone())[2].any())
+
+
+def test_more_rows_than_one_launch():
+    """17 million rows of 8 are two launches; the last rows against a call of
+    their own, bit for bit, for both outputs; and their weight gradient."""
+    rows = (1 << 24) + 777
+    x = torch.zeros(rows, 8, dtype=torch.float16, device="cuda")
+    r = torch.randn(rows, 8, device="cuda").half()
+    w = 1 + 0.1 * torch.randn(8, device="cuda")
+    x[-900:] = torch.randn(900, 8, device="cuda").half()
+    y, s = gla.add_rmsnorm(x, r, w, EPS)
+    y8, sc, s8 = gla.add_rmsnorm_q8(x, r, w, EPS)
+    ty, ts = gla.add_rmsnorm(x[-900:], r[-900:], w, EPS)
+    t8, tc, _ = gla.add_rmsnorm_q8(x[-900:], r[-900:], w, EPS)
+    torch.cuda.synchronize()
+    assert torch.equal(y[-900:], ty) and torch.equal(s[-900:], ts) and torch.equal(s, s8)
+    assert torch.equal(y8[-900:].view(torch.uint8), t8.view(torch.uint8)) and torch.equal(sc[-900:], tc)
+    g = torch.zeros_like(s)
+    g[-900:] = ty
+    _, gw = gla.add_rmsnorm_bwd(s, w, EPS, g)
+    _, tw = gla.add_rmsnorm_bwd(ts, w, EPS, ty)
+    torch.cuda.synchronize()
+    # the same 900 terms in another order: 900 u of their magnitudes
+    n = ts.double() / (ts.double().square().mean(1, keepdim=True) + EPS).sqrt()
+    assert bool(((gw - tw).abs().double() <= 900 * U * (n * ty.double()).abs().sum(0)).all())

@@ -116,6 +116,9 @@ def test_rows_of_one_slot_apply_in_order(dtype, gated):
 
 
 def test_one_row_and_many():
+    # more rows than one round of slot comparisons, slots shared far apart
+    r = np.random.default_rng(8)
+    check(1200, 1, 32, 32, 500, np.float16, [int(s) for s in r.integers(-1, 500, 1200)], False, 62)
     check(1, 1, 64, 64, 1, np.float16, None, False, 60)
     check(300, 3, 32, 32, 400, np.float16, [int(s) for s in np.random.default_rng(6).permutation(400)[:300]], True, 61)
 
