@@ -414,82 +414,66 @@ __global__ __launch_bounds__(kThreads) void bwd_scan_serial_kernel(
   if (rev && gs0) *reinterpret_cast<floatx4*>(gs0 + bh * DKDV + x4) = s;
 }
 
-// Few chains: the chunk axis in 16 segments of L chunks, one per lane of a DPP
-// row. Each lane folds its segment into (a, u), a row scan composes them, and
-// the lane replays its segment from the state that enters it. R: chunks kept
-// in registers between the two passes.
+// Few chains: a workgroup takes 64 groups of four elements (1 KB of a state, a
+// load or store of a wave) and windows of 16 segments of up to R chunks, a wave
+// each. A wave folds its segment into (a, u), the 16 are composed from LDS, and
+// the wave replays its segment, still in registers, from the state entering it.
 template <int R, bool kTerms>
-__global__ __launch_bounds__(kThreads) void bwd_scan_kernel(
+__global__ __launch_bounds__(1024) void bwd_scan_kernel(
     float* Uws, float* Rws, const float* __restrict__ Aws, const float* s0, const float* gsf,
-    float* gs0, int N, int DK, int DV, int L, long groups) {
-  const long gid = (long)blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
-  if (gid >= groups) return;  // whole DPP rows
-  const int seg = threadIdx.x & 15;
+    float* gs0, int N, int DK, int DV, int L) {
+  __shared__ floatx4 sU[16][64];
+  __shared__ float sA[16][64];
+  const int seg = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const bool rev = blockIdx.y;
-  const long DKDV = (long)DK * DV, per = DKDV / 4;
-  const long bh = gid / per;
-  const int x4 = 4 * (int)(gid - bh * per), d = x4 / DV;
+  const int DKDV = DK * DV, per = DKDV / 256;  // workgroups per chain
+  const long bh = blockIdx.x / per;
+  const int x4 = 4 * ((int)(blockIdx.x % per) * 64 + lane), d = x4 / DV;
+  // chunk i of the walk is chunk i, or N-1-i
   const long first = rev ? N - 1 : 0, sx = rev ? -DKDV : DKDV, sa = rev ? -DK : DK;
   float* X = (rev ? Rws : Uws) + (bh * N + first) * DKDV + x4;
   const float* A = Aws + (bh * N + first) * DK + d;
   const float* init = rev ? gsf : s0;
-  floatx4 st0 = {0.f, 0.f, 0.f, 0.f};
-  if (init) st0 = *reinterpret_cast<const floatx4*>(init + bh * DKDV + x4);
-  const int n0 = min(seg * L, N), n1 = min(n0 + L, N);
-  float ag = 1.f;
-  floatx4 ug = {0.f, 0.f, 0.f, 0.f}, u[R];
-  float a[R];
-  for (int nb = n0; nb < n1; nb += R) {
+  floatx4 s = {0.f, 0.f, 0.f, 0.f};
+  if (init) s = *reinterpret_cast<const floatx4*>(init + bh * DKDV + x4);
+  for (int base = 0; base < N; base += 16 * L) {
+    const int n0 = base + seg * L, m = min(L, N - n0);  // this wave's chunks, maybe none
+    floatx4 u[R], ug = {0.f, 0.f, 0.f, 0.f};
+    float a[R], ag = 1.f;
+    if (m > 0) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {  // clamped, all in flight together
-      const long m = min(nb + i, n1 - 1);
-      u[i] = *reinterpret_cast<const floatx4*>(X + m * sx);
-      a[i] = A[m * sa];
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (nb + i < n1) {
-        ug = step4(a[i], ug, u[i]);
-        ag *= a[i];
+      for (int i = 0; i < R; ++i) {  // clamped, all in flight together
+        const long c = n0 + min(i, m - 1);
+        u[i] = *reinterpret_cast<const floatx4*>(X + c * sx);
+        a[i] = A[c * sa];
       }
-    }
-  }
-  // inclusive composition over the row's segments, then shifted by one
-#define GLA_BWD_SCAN_STEP(CTRL)                                                                \
-  {                                                                                            \
-    const float ap = tile::dpp_row_shr<CTRL>(ag, 1.f);                                         \
-    _Pragma("unroll") for (int c = 0; c < 4; ++c) ug[c] =                                      \
-        fmaf(ag, tile::dpp_row_shr<CTRL>(ug[c], 0.f), ug[c]);                                  \
-    ag *= ap;                                                                                  \
-  }
-  GLA_BWD_SCAN_STEP(0x111)
-  GLA_BWD_SCAN_STEP(0x112)
-  GLA_BWD_SCAN_STEP(0x114)
-  GLA_BWD_SCAN_STEP(0x118)
-#undef GLA_BWD_SCAN_STEP
-  if (rev && gs0 && seg == 15) *reinterpret_cast<floatx4*>(gs0 + bh * DKDV + x4) = step4(ag, st0, ug);
-  const float ae = tile::dpp_row_shr<0x111>(ag, 1.f);
-  floatx4 s;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) s[c] = fmaf(ae, st0[c], tile::dpp_row_shr<0x111>(ug[c], 0.f));
-  const bool cached = n1 - n0 <= R;
-  for (int nb = n0; nb < n1; nb += R) {
-    if (!cached) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const long m = min(nb + i, n1 - 1);
-        u[i] = *reinterpret_cast<const floatx4*>(X + m * sx);
-        a[i] = A[m * sa];
+        if (i < m) {
+          ug = step4(a[i], ug, u[i]);
+          ag *= a[i];
+        }
       }
+    }
+    if (base) __syncthreads();  // the last window's sums are read
+    sU[seg][lane] = ug;
+    sA[seg][lane] = ag;
+    __syncthreads();
+    floatx4 x = s;  // the state that enters the segment
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      x = j == seg ? s : x;
+      s = step4(sA[j][lane], s, sU[j][lane]);
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (nb + i < n1) {
-        put_state4<kTerms>(X + (nb + i) * sx, s);
-        s = step4(a[i], s, u[i]);
+      if (i < m) {
+        put_state4<kTerms>(X + (n0 + i) * sx, x);
+        x = step4(a[i], x, u[i]);
       }
     }
   }
+  if (rev && gs0 && seg == 0) *reinterpret_cast<floatx4*>(gs0 + bh * DKDV + x4) = s;
 }
 
 // ===========================================================================
@@ -965,8 +949,16 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
 }
 
 // The serial scan replaces the segmented one from this many groups of four
-// state elements per launch and direction.
-constexpr long kSerialGroups = 32768;
+// state elements per launch and direction. Serial and segmented, in us, for
+// chains of 64/64 states (1024 groups each):
+//              25 chunks      100 chunks     256 chunks
+//    6 chains   6.2   4.8     15.7   9.9     34.4  19.8
+//   16 chains   8.2   7.4     18.7  20.5     72.2  48.2
+//   24 chains   8.6  11.5     24.7  29.8     81.4  76.7
+//   64 chains  16.9  23.6     66.2  76.2
+// Few chains leave the serial one waiting for its loads; many fill the card
+// either way, and the segments' exchange then costs more.
+constexpr long kSerialGroups = 24576;
 
 template <int DK, int DV, typename InT>
 hipError_t bwd_t(const Problem& p, int b0, int nb, const DirPack& dirs, const BwdArgs& a, char* ws,
@@ -987,19 +979,20 @@ hipError_t bwd_t(const Problem& p, int b0, int nb, const DirPack& dirs, const Bw
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr bool kTerms = NT == 2;
-  const long groups = (long)nb * p.H * (DK * DV / 4);
   const float* s0 = a.s0 ? a.s0 + bh0 * DK * DV : nullptr;
   const float* gsf = a.gs_final ? a.gs_final + bh0 * DK * DV : nullptr;
   float* gs0 = a.gs0 ? a.gs0 + bh0 * DK * DV : nullptr;
+  const long groups = (long)nb * p.H * (DK * DV / 4);
   if (groups >= kSerialGroups) {
     const dim3 grid((unsigned)((groups + kThreads - 1) / kThreads), 2);
     hipLaunchKernelGGL((bwd_scan_serial_kernel<8, kTerms>), grid, dim3(kThreads), 0, s, S, D, A, s0,
                        gsf, gs0, p.N, DK, DV, groups);
   } else {
-    const int L = (p.N + 15) / 16;
-    const dim3 grid((unsigned)((groups + kThreads / 16 - 1) / (kThreads / 16)), 2);
+    const int L = p.N > 16 * 8 ? 8 : (p.N + 15) / 16;
+    // the shortest window that holds the chain, in registers
     auto scan = L <= 2 ? bwd_scan_kernel<2, kTerms> : L <= 4 ? bwd_scan_kernel<4, kTerms> : bwd_scan_kernel<8, kTerms>;
-    hipLaunchKernelGGL(scan, grid, dim3(kThreads), 0, s, S, D, A, s0, gsf, gs0, p.N, DK, DV, L, groups);
+    hipLaunchKernelGGL(scan, dim3((unsigned)(groups / 64), 2), dim3(1024), 0, s, S, D, A, s0, gsf, gs0,
+                       p.N, DK, DV, L);
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;

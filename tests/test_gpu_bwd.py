@@ -180,6 +180,13 @@ def test_many_chains_take_the_serial_scan():
     check(x, 25, 25, [0, 1, 2, 3], s0, gsf)
 
 
+def test_more_chunks_than_one_window_of_the_scan():
+    """131 chunks: one whole window of 16 segments of eight, and a rest that
+    leaves most of the segments empty."""
+    x, s0, gsf = inputs(1, 43, 195, 2, 32, 32, np.float16, 983, gate="mixed", carry=True)
+    check(x, 43, 195, (2,), s0, gsf)
+
+
 def test_offsets_past_32_bits():
     """33.6 million token-heads: tensors of more than 2^31 elements. The last
     batch element against a call of its own, bit for bit."""
