@@ -832,7 +832,9 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   for (int ks = 0; ks < NES; ++ks) vs[ks] = v.template terms<NT>(ks);
 #pragma unroll
   for (int D = 0; D < ND; ++D) acc[D] = zero4;
-  for (int I = wave + 1; I < NB; ++I) {
+#pragma unroll
+  for (int I = 1; I < NB; ++I) {
+    if (I <= wave) continue;
     const float* f = &sF[I * (I - 1) / 2 + wave][8 * lq];
     floatx4 a = zero4;
 #pragma unroll

@@ -557,6 +557,13 @@ def _like(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
     return t
 
 
+def _alike(shape, dtype, device, **tensors) -> None:
+    """_like for tensors of one shape."""
+    for name, t in tensors.items():
+        if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+            _like(t, shape, dtype, device, name)
+
+
 def _on_gpu(t: torch.Tensor, name: str) -> torch.device:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
@@ -613,11 +620,8 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gk: torch.Tensor, go:
     values = (B, T, H, dv)
     if T != grid_h * grid_w:
         raise ValueError(f"T={T} but grid is {grid_h}x{grid_w}")
-    _like(q, keys, dtype, dev, "q")
-    _like(k, keys, dtype, dev, "k")
-    _like(gk, keys, dtype, dev, "gk")
-    _like(v, values, dtype, dev, "v")
-    _like(go, values, dtype, dev, "go")
+    _alike(keys, dtype, dev, q=q, k=k, gk=gk)
+    _alike(values, dtype, dev, v=v, go=go)
     p0 = _state_ptr(s0, B, H, dk, dv, "s0", dev)
     pf = _state_ptr(gs_final, B, H, dk, dv, "gs_final", dev)
     if gs0 is not None and not return_gs0:
@@ -649,23 +653,22 @@ def _step(q, k, v, gk, state, slots, out, stream, gate=None, norm_weight=None, e
         raise ValueError("q, k, gk must be [B, H, dk] and v [B, H, dv]")
     B, H, dk = keys = q.shape
     dv, dev, dtype = v.shape[-1], _on_gpu(q, "q"), q.dtype
-    _like(q, keys, dtype, dev, "q")
-    _like(k, keys, dtype, dev, "k")
-    _like(gk, keys, dtype, dev, "gk")
-    _like(v, (B, H, dv), dtype, dev, "v")
+    _alike(keys, dtype, dev, q=q, k=k, gk=gk)
+    _alike((B, H, dv), dtype, dev, v=v)
     if state.dim() != 4:
         raise ValueError("state must be [n_slots, H, dk, dv]")
-    _like(state, (state.shape[0], H, dk, dv), torch.float32, dev, "state")
+    n_slots = state.shape[0]
+    _alike((n_slots, H, dk, dv), torch.float32, dev, state=state)
     if slots is not None:
-        _like(slots, (B,), torch.int32, dev, "slots")
-    elif state.shape[0] < B:
-        raise ValueError(f"{B} rows without slots need as many states, got {state.shape[0]}")
+        _alike((B,), torch.int32, dev, slots=slots)
+    elif n_slots < B:
+        raise ValueError(f"{B} rows without slots need as many states, got {n_slots}")
     if gate is not None:
         _like(gate, (B, H, dv), dtype, dev, "gate")
         _like(norm_weight, (dv,), torch.float32, dev, "norm_weight")
     with _launching(dev, stream, q, k, v, gk, state, slots, out, gate, norm_weight) as st_ptr:
-        out = _out(out, (B, H, dv), dtype, dev)
-        tail = (out.data_ptr(), B, H, dk, dv, _dtype_code(q), state.data_ptr(), state.shape[0],
+        out = _out_like(out, v)
+        tail = (out.data_ptr(), B, H, dk, dv, _dtype_code(q), state.data_ptr(), n_slots,
                 _ptr(slots), st_ptr)
         if gate is None:
             st = load().gla_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), gk.data_ptr(), *tail)
@@ -751,12 +754,11 @@ def add_rmsnorm_bwd(s: torch.Tensor, weight: torch.Tensor, eps: float, gy: torch
     and of residual; out may be s, gy or gsum. gweight [F] float32."""
     rows, F = _norm_args(s, gsum, weight)
     _like(gy, s.shape, s.dtype, s.device, "gy")
-    if rows == 0 and F > 0:  # no rows: a sum of nothing
-        gw = _out(gweight, (F,), torch.float32, s.device).zero_()
-        return _out(out, s.shape, s.dtype, s.device), gw
     with _launching(s.device, stream, s, weight, gy, gsum, out, gweight, workspace) as st_ptr:
         gx = _out_like(out, s)
-        gw = _out(gweight, (F,), torch.float32, s.device)
+        gw = _out_like(gweight, weight)
+        if rows == 0 and F > 0:  # no rows: a sum of nothing
+            return gx, gw.zero_()
         workspace = _scratch(workspace, _norm_workspace_bytes(rows, F), s.device)
         ws, nws = _ws(workspace, s.device)
         st = load().gla_add_rmsnorm_bwd(s.data_ptr(), weight.data_ptr(), float(eps), gy.data_ptr(),
@@ -778,15 +780,13 @@ def gate_bwd(o: torch.Tensor, gate: torch.Tensor, norm_weight: torch.Tensor, eps
     _like(gy, o.shape, o.dtype, o.device, "gy")
     if out is not None and len(out) != 2:
         raise ValueError("out must be two tensors (go, ggate)")
-    if rows == 0 and dv > 0:
-        gw = _out(gnorm_weight, (dv,), torch.float32, o.device).zero_()
-        return (_out(out[0] if out else None, o.shape, o.dtype, o.device),
-                _out(out[1] if out else None, o.shape, o.dtype, o.device), gw)
     with _launching(o.device, stream, o, gate, norm_weight, gy, gnorm_weight, workspace,
                     *(out or ())) as st_ptr:
         go = _out_like(out[0] if out else None, o)
         gz = _out_like(out[1] if out else None, o)
-        gw = _out(gnorm_weight, (dv,), torch.float32, o.device)
+        gw = _out_like(gnorm_weight, norm_weight)
+        if rows == 0 and dv > 0:
+            return go, gz, gw.zero_()
         workspace = _scratch(workspace, _gate_workspace_bytes(rows, dv), o.device)
         ws, nws = _ws(workspace, o.device)
         st = load().gla_gate_bwd(o.data_ptr(), gate.data_ptr(), norm_weight.data_ptr(), float(eps),
