@@ -295,7 +295,9 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
 }
 
 // Workgroups of the two gradient kernels: enough to fill the GPU, few enough
-// that the partial sums stay small beside the rows.
+// that the partial sums stay small beside the rows. At most 512, 1024 or 2048
+// of them: the norm's gradient of 25,600 x 768 half rows 54, 41 or 47 us, the
+// gate's of 409,600 rows of 64 the same within 1 us.
 constexpr long kMaxParts = 1024;
 // every workgroup takes the same number of steps of `per` rows, but the last
 int even_parts(long rows, long per) {
@@ -337,13 +339,17 @@ hipError_t norm_bwd_t(const NormBwdArgs& a, float* ws, hipStream_t s) {
   return hipGetLastError();
 }
 
-// One wave per row up to 2048 columns, else one workgroup.
-#define GLA_NORM_DISPATCH(FN, InT, ...)                                    \
+// One wave per row up to `WAVE` columns (1024 or 2048), else one workgroup. The
+// norm of 12,800 half rows takes, with a wave or a workgroup per row, 29.7 or
+// 26.2 us for 1536 columns, 40.5 or 35.9 for 2048, and 50.2 or 44.5 for 2560;
+// its gradient 34.9 or 36.9, 45.5 or 43.4, and 102 or 53 (1024 rows of 2048
+// columns: 12.5 or 14.1).
+#define GLA_NORM_DISPATCH(FN, WAVE, InT, ...)                              \
   do {                                                                     \
     const int F_ = a.F;                                                    \
     if (F_ <= 512) return FN<64, 1, InT>(__VA_ARGS__);                     \
     if (F_ <= 1024) return FN<64, 2, InT>(__VA_ARGS__);                    \
-    if (F_ <= 2048) return FN<64, 4, InT>(__VA_ARGS__);                    \
+    if (F_ <= 2048) return FN<WAVE == 2048 ? 64 : 256, WAVE == 2048 ? 4 : 1, InT>(__VA_ARGS__); \
     if (F_ <= 4096) return FN<256, 2, InT>(__VA_ARGS__);                   \
     if (F_ <= 8192) return FN<256, 4, InT>(__VA_ARGS__);                   \
     return FN<256, 8, InT>(__VA_ARGS__);                                   \
@@ -365,8 +371,8 @@ hipError_t gate_bwd_t(const GateBwdArgs& a, float* ws, hipStream_t s) {
 }  // namespace norm
 
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s) {
-  if (a.dtype == 0) GLA_NORM_DISPATCH(norm::norm_t, half_t, a, s);
-  GLA_NORM_DISPATCH(norm::norm_t, float, a, s);
+  if (a.dtype == 0) GLA_NORM_DISPATCH(norm::norm_t, 1024, half_t, a, s);
+  GLA_NORM_DISPATCH(norm::norm_t, 1024, float, a, s);
 }
 
 size_t norm_bwd_workspace(long rows, int F) {
@@ -374,8 +380,8 @@ size_t norm_bwd_workspace(long rows, int F) {
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, float* ws, hipStream_t s) {
-  if (a.dtype == 0) GLA_NORM_DISPATCH(norm::norm_bwd_t, half_t, a, ws, s);
-  GLA_NORM_DISPATCH(norm::norm_bwd_t, float, a, ws, s);
+  if (a.dtype == 0) GLA_NORM_DISPATCH(norm::norm_bwd_t, 2048, half_t, a, ws, s);
+  GLA_NORM_DISPATCH(norm::norm_bwd_t, 2048, float, a, ws, s);
 }
 
 size_t gate_bwd_workspace(long rows, int dv) {

@@ -8,33 +8,51 @@
 // columns of every (256 / (dv/4))-th key dim, so a wave's accesses are
 // contiguous, and all of them are in flight before the first is used. The sum
 // over key dims goes through lane permutations and then LDS, in a fixed order.
+// 256 rows of 16 heads of 64/64 (134 MB): 23.5 us, 5.7 TB/s; 37 rows of 12
+// heads of 32/64: 3.8 us, one row of 6 heads: 3.3 us, both a launch's latency.
 //
 // Rows of one call that name the same slot are consecutive tokens of one
 // sequence: the workgroup of the first such row applies all of them in row
 // order with the state in registers, and those of the others leave. Every wave
-// finds them by comparing the call's slots, 512 per round of loads.
+// finds them by comparing the call's slots, 256 per round of loads; the first
+// round's go out before the state's, which would be waited for with them (29.5
+// us instead of 23.5 for the 256 rows).
 #include "gla_step.h"
 #include "gla_tile.h"
 
 namespace gla {
 namespace step {
 
-// First row of [lo, hi) that names `slot`, or hi; the same on every lane.
-__device__ __forceinline__ int find_slot(const int32_t* __restrict__ slots, int slot, int lo, int hi) {
-  constexpr int W = 8;
-  const int lane = threadIdx.x & 63;
-  for (int j0 = lo; j0 < hi; j0 += 64 * W) {
-    int s[W];
+// Which of the rows j0 .. j0 + 255 name a slot: four loads, then four ballots
+// (apart, so that a caller's loads can go out in between).
+struct Slots {
+  static constexpr int kRows = 256;
+  int32_t s[4];
+  unsigned long long hit[4];
+  __device__ __forceinline__ void load(const int32_t* __restrict__ slots, int j0, int B) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) s[i] = slots[min(j0 + 64 * i + lane, hi - 1)];
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const unsigned long long hit = __ballot(j0 + 64 * i + lane < hi && s[i] == slot);
-      if (hit) return j0 + 64 * i + __builtin_ctzll(hit);
+    for (int i = 0; i < 4; ++i) {
+      s[i] = 0;
+      if (j0 + 64 * i < B) s[i] = slots[min(j0 + 64 * i + (int)(threadIdx.x & 63), B - 1)];
     }
   }
-  return hi;
-}
+  __device__ __forceinline__ void compare(int slot, int j0, int B) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      hit[i] = __ballot(j0 + 64 * i + (int)(threadIdx.x & 63) < B && s[i] == slot);
+  }
+  // first hit of rows >= lo (of j0 ..), or B
+  __device__ __forceinline__ int first(int lo, int j0, int B) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int base = j0 + 64 * i;
+      const unsigned long long m =
+          lo <= base ? hit[i] : lo - base < 64 ? hit[i] & (~0ull << (lo - base)) : 0ull;
+      if (m) return base + __builtin_ctzll(m);
+    }
+    return B;
+  }
+};
 
 template <int DK, int DV, typename InT, bool kGate>
 __global__ __launch_bounds__(kThreads) void step_kernel(
@@ -50,12 +68,27 @@ __global__ __launch_bounds__(kThreads) void step_kernel(
   const int e4 = 4 * (tid % LPR), d0 = tid / LPR;
   const long slot = slots ? (long)slots[b] : (long)b;
   if (slot < 0 || slot >= n_slots) return;  // a padding row
+  Slots rows0;
+  if (slots) rows0.load(slots, 0, B);
   float* S = state + (slot * H + h) * (long)(DK * DV) + d0 * DV + e4;
   floatx4 s[NG];
 #pragma unroll
   for (int i = 0; i < NG; ++i) s[i] = *reinterpret_cast<const floatx4*>(S + i * RPP * DV);
-  // the first row of this slot does this one too
-  if (slots && find_slot(slots, (int)slot, 0, b) < b) return;
+  // first row >= lo of this slot, or B
+  auto find = [&](int lo) {
+    int r = lo < Slots::kRows ? rows0.first(lo, 0, B) : B;
+    for (int j0 = lo < Slots::kRows ? Slots::kRows : lo & -Slots::kRows; r >= B && j0 < B; j0 += Slots::kRows) {
+      Slots more;
+      more.load(slots, j0, B);
+      more.compare((int)slot, j0, B);
+      r = more.first(lo, j0, B);
+    }
+    return r;
+  };
+  if (slots) {
+    rows0.compare((int)slot, 0, B);
+    if (find(0) < b) return;  // that row's workgroup does this one too
+  }
   for (int r = b;;) {
     const long row = (long)r * H + h;
     float x[4], o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -93,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(
       op[row * DV + tid] = (InT)y;
     }
     // the next row of the same sequence
-    const int next = slots ? find_slot(slots, (int)slot, r + 1, B) : B;
+    const int next = slots ? find(r + 1) : B;
     if (next >= B) break;
     r = next;
     __syncthreads();  // sPart is read
