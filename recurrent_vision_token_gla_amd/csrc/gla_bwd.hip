@@ -500,8 +500,12 @@ __global__ __launch_bounds__(1024) void bwd_scan_kernel(
 // ===========================================================================
 constexpr float kMaxSpan = 68.f;
 
+// Two workgroups per CU where their LDS fits (at most 80 KB; a half input's
+// largest takes 79, a float's 80 with 32 key dims): one alone leaves the SIMDs
+// waiting more than half of the time (4,099 float tokens x 8 heads of 32/64
+// with one or two: 31 or 23 us).
 template <int DK, int DV, typename InT, int NT>
-__global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_kernel(
+__global__ __launch_bounds__(kThreads, sizeof(InT) == 2 || DK == 32 ? 2 : 1) void bwd_grad_kernel(
     const InT* __restrict__ qp, const InT* __restrict__ kp, const InT* __restrict__ vp,
     const InT* __restrict__ gp, const InT* __restrict__ dop, const float* __restrict__ Sws,
     const float* __restrict__ Dws, InT* __restrict__ gqp, InT* __restrict__ gkp,
@@ -515,7 +519,7 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
   __shared__ __attribute__((aligned(16))) __bf16 sQ[NT][C * DK];             // qx
   __shared__ __attribute__((aligned(16))) __bf16 sK[NT][C * DK];             // kx
   __shared__ __attribute__((aligned(16))) __bf16 sO[NT][C * DV];             // go
-  __shared__ __attribute__((aligned(16))) __bf16 sV[kHalf ? 1 : NT][C * DV];  // v (half inputs: as they are)
+  __shared__ __attribute__((aligned(16))) __bf16 sV[kHalf ? 1 : 2][C * DV];  // v as it is (float: upper and lower halves)
   __shared__ __attribute__((aligned(16))) __bf16 sX[NT][DK * DV];            // S_n, then D_n
   __shared__ __attribute__((aligned(16))) float sF[NP][DK];   // factors between two sub-blocks
   __shared__ __attribute__((aligned(16))) float sA[NB][DK];   // tot; factors to the chunk's end; sums
@@ -649,8 +653,15 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
       pn = mfma16x16x32(go.v[ks], v.v[ks], pn);
     } else {
       const Split8<NT> vs = v.template terms<NT>(ks);
+      tile::u32x4 hi, lo;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) lv.put(&sV[i][wave * VB], ks, vs.t[i]);
+      for (int c = 0; c < 4; ++c) {
+        const unsigned a = __float_as_uint(v.v[ks][2 * c]), b = __float_as_uint(v.v[ks][2 * c + 1]);
+        hi[c] = __builtin_amdgcn_perm(b, a, 0x07060302);
+        lo[c] = __builtin_amdgcn_perm(b, a, 0x05040100);
+      }
+      lv.put(&sV[0][wave * VB], ks, __builtin_bit_cast(bf8, hi));
+      lv.put(&sV[1][wave * VB], ks, __builtin_bit_cast(bf8, lo));
       pt = mm<NT>(vs, os, pt);
       pn = mm<NT>(os, vs, pn);
     }
@@ -680,7 +691,15 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 ? 2 : 1) void bwd_grad_k
       if constexpr (kHalf) {
         p = mfma16x16x32(__builtin_bit_cast(half8, lv.rows(&sV[0][J * VB], ks)), go.v[ks], p);
       } else {
-        p = mm<NT>(rows8(lv, sV, J * VB, ks), go.template terms<NT>(ks), p);
+        const tile::u32x4 hi = __builtin_bit_cast(tile::u32x4, lv.rows(&sV[0][J * VB], ks));
+        const tile::u32x4 lo = __builtin_bit_cast(tile::u32x4, lv.rows(&sV[1][J * VB], ks));
+        float x[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          x[2 * c] = __uint_as_float(__builtin_amdgcn_perm(hi[c], lo[c], 0x05040100));
+          x[2 * c + 1] = __uint_as_float(__builtin_amdgcn_perm(hi[c], lo[c], 0x07060302));
+        }
+        p = mm<NT>(split8<NT>(x), go.template terms<NT>(ks), p);
       }
     }
     return p;
