@@ -234,7 +234,16 @@ struct Lane {
 // what is accumulated decays through each of them: a lane's column of the
 // transposed product is one key dim, so that is one factor per sub-block.
 // The scaled operand has NX bf16 terms: three for half inputs too (the other
-// is exact in two) where the initial state's gradient is returned, in float.
+// is exact in two) where the initial state's gradient is returned, in float:
+// it is then off by 2e-7 of its size instead of 4e-6, for 4 us more at the
+// sizes below, while the other gradients, rounded to half, do not change.
+//
+// The memory bounds it: 25,600 half tokens x 16 heads of 64/64 (6,400 chunks,
+// 307 MB read and 206 written by the counters) take 99 us, 5.2 TB/s; the 150
+// chunks of 1,600 tokens x 6 heads 8.7 us, where a workgroup's own 9,000 cycles
+// of loads, factors and products in turn are what is left to wait for. Three
+// workgroups per CU: LDS holds four, and more registers per lane (up to 128),
+// or all sub-blocks' products before the first decay, changed nothing.
 // ===========================================================================
 template <int DK, int DV, typename InT, int NT, int NX>
 __global__ __launch_bounds__(kThreads, 3) void bwd_summary_kernel(
@@ -363,6 +372,8 @@ __device__ __forceinline__ floatx4 step4(float a, floatx4 s, floatx4 u) {
 // Many chains: one thread walks four elements of a chain in order, the next
 // W/2 to W chunks' loads in flight (the window is refilled half by half, and
 // whole windows run without a condition, which would wait for every load).
+// The memory bounds it: 64 chains of 100 chunks (211 MB read, 205 written)
+// take 68 us, 6.1 TB/s, part of it from the last-level cache.
 template <int W, bool kTerms>
 __global__ __launch_bounds__(kThreads) void bwd_scan_serial_kernel(
     float* Uws, float* Rws, const float* __restrict__ Aws, const float* s0, const float* gsf,
@@ -418,6 +429,8 @@ __global__ __launch_bounds__(kThreads) void bwd_scan_serial_kernel(
 // load or store of a wave) and windows of 16 segments of up to R chunks, a wave
 // each. A wave folds its segment into (a, u), the 16 are composed from LDS, and
 // the wave replays its segment, still in registers, from the state entering it.
+// 6 chains of 25 or 100 chunks: 5 or 9.7 us. (With the segments on the lanes of
+// a row, composed by lane permutations, accesses were 64 bytes wide: 12 us.)
 template <int R, bool kTerms>
 __global__ __launch_bounds__(1024) void bwd_scan_kernel(
     float* Uws, float* Rws, const float* __restrict__ Aws, const float* s0, const float* gsf,
@@ -494,9 +507,18 @@ __global__ __launch_bounds__(1024) void bwd_scan_kernel(
 //   2^(b_i-b_j) = 2^(s_i-ref_I) [2^ref_I prod_{J<M<I} 2^tot_M 2^(tot_J-ref_J)] 2^(ref_J-s_j).
 // Where no s - ref exceeds 68 in magnitude, values up to 65504 keep qx and kx
 // below 2^84 and every product finite (P is at most 64 products of two such
-// values); a 2^ref that underflows has all of its sub-block's q 2^s do so. A sub-block that decays more keeps q 2^s and k 2^(tot-s)
-// instead (its bracket then holds 1 for the two outer factors) and sums its
+// values); a 2^ref that underflows has all of its sub-block's q 2^s do so. A
+// sub-block that decays more keeps q 2^s and k 2^(tot-s) instead (its bracket then holds 1 for the two outer factors) and sums its
 // own pairs directly in float.
+//
+// A workgroup's own chain of steps bounds it: alone on a CU it takes 22,400
+// cycles, with a second one 25,200, in which each SIMD issues vector
+// instructions for 15,200 (1,906 per wave, half of them factors, splits and
+// scans; 172 matrix products). 25,600 half tokens x 16 heads of 64/64: 180 to
+// 205 us (461 MB read, 205 written: 3.5 TB/s); 1,600 tokens x 6 heads, less
+// than a workgroup per CU: 12 us. Eight waves with queries and keys apart have
+// 128 registers a lane and spilled (1.2 times the time); so did all gradients
+// stored at the end, or D_n's rows read again for <S_n, D_n>.
 // ===========================================================================
 constexpr float kMaxSpan = 68.f;
 
@@ -996,7 +1018,8 @@ hipError_t bwd_t(const Problem& p, int b0, int nb, const DirPack& dirs, const Bw
   float* D = reinterpret_cast<float*>(ws + w.off_D) + bhn * DK * DV;
   float* A = reinterpret_cast<float*>(ws + w.off_a) + bhn * DK;
   auto summary = a.gs0 ? bwd_summary_kernel<DK, DV, InT, NT, 3> : bwd_summary_kernel<DK, DV, InT, NT, NT>;
-  hipLaunchKernelGGL(summary, dim3(p.N, p.H, 2 * nb), dim3(kThreads), 0, s, k, v, q, go, g, S, D, A, p.T, p.H, p.N, p.gh, p.gw, dirs);
+  hipLaunchKernelGGL(summary, dim3(p.N, p.H, 2 * nb), dim3(kThreads), 0, s, k, v, q, go, g, S, D, A,
+                     p.T, p.H, p.N, p.gh, p.gw, dirs);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr bool kTerms = NT == 2;

@@ -587,9 +587,12 @@ def _gate_workspace_bytes(rows: int, dv: int) -> int:
 
 
 def _scratch(workspace: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
-    """The caller's workspace or a new one (inside _launching)."""
+    """The caller's workspace or a new one (inside _launching). The gradients
+    refuse a workspace prepared for the forward; a new one is nobody's, even
+    where a freed one was never released."""
     if workspace is None:
-        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        load().gla_workspace_release(workspace.data_ptr())
     return workspace
 
 

@@ -187,6 +187,23 @@ def test_more_chunks_than_one_window_of_the_scan():
     check(x, 43, 195, (2,), s0, gsf)
 
 
+def test_prepared_workspace_is_refused():
+    """A workspace prepared for the forward keeps control words that a gradient
+    would overwrite: refused, and the forward still runs in it."""
+    x, _, _ = inputs(1, 8, 24, 2, 64, 64, np.float16, 985)
+    d = [torch.from_numpy(a).cuda() for a in x]
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    gla.workspace_init(ws)
+    want = gla.fwd(*d[:4], 8, 24, 0, workspace=ws)
+    with pytest.raises(gla.GLAError) as e:
+        gla.bwd(*d, 8, 24, 0, workspace=ws)
+    assert e.value.status == gla.E_ARG
+    assert torch.equal(gla.fwd(*d[:4], 8, 24, 0, workspace=ws), want)
+    gla.workspace_release(ws)
+    for a, b in zip(gla.bwd(*d, 8, 24, 0, workspace=ws), gla.bwd(*d, 8, 24, 0)):
+        assert torch.equal(a, b)
+
+
 def test_offsets_past_32_bits():
     """33.6 million token-heads: tensors of more than 2^31 elements. The last
     batch element against a call of its own, bit for bit."""
