@@ -515,7 +515,7 @@ __global__ __launch_bounds__(1024) void bwd_scan_kernel(
 // cycles, with a second one 25,200, in which each SIMD issues vector
 // instructions for 15,200 (1,906 per wave, half of them factors, splits and
 // scans; 172 matrix products). 25,600 half tokens x 16 heads of 64/64: 180 to
-// 205 us (461 MB read, 205 written: 3.5 TB/s); 1,600 tokens x 6 heads, less
+// 205 us (461 MB read, 205 written: 3.2 to 3.7 TB/s); 1,600 tokens x 6 heads, less
 // than a workgroup per CU: 12 us. Eight waves with queries and keys apart have
 // 128 registers a lane and spilled (1.2 times the time); so did all gradients
 // stored at the end, or D_n's rows read again for <S_n, D_n>.
@@ -524,7 +524,7 @@ constexpr float kMaxSpan = 68.f;
 
 // Two workgroups per CU where their LDS fits (at most 80 KB; a half input's
 // largest takes 79, a float's 80 with 32 key dims): one alone leaves the SIMDs
-// waiting more than half of the time (4,099 float tokens x 8 heads of 32/64
+// waiting more than half of the time (2 x 4,099 float tokens x 4 heads of 32/64
 // with one or two: 31 or 23 us).
 template <int DK, int DV, typename InT, int NT>
 __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 || DK == 32 ? 2 : 1) void bwd_grad_kernel(
