@@ -515,22 +515,33 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-class _launching:
-    """Device and stream of a call, as the raw stream pointer. On a stream
-    other than the current one, what the call allocates belongs to that stream
-    and the caller's tensors are not reused before its work is done (the
-    caller orders the streams themselves). Nothing is switched where the
-    device is current and no stream is given: the small calls are bound by
-    what the host does."""
+class _Here:
+    """The current device and stream: nothing to switch, as in the small calls,
+    which are bound by what the host does."""
+    __slots__ = ("index",)
+
+    def __init__(self, index: int):
+        self.index = index
+
+    def __enter__(self) -> int:
+        return _raw_stream(self.index)
+
+    def __exit__(self, *exc) -> None:
+        pass
+
+
+class _There:
+    """Another device or a given stream. What the call allocates belongs to
+    that stream, and the caller's tensors are not reused before its work is
+    done (the caller orders the streams themselves)."""
     __slots__ = ("device", "stream", "inputs", "contexts")
 
-    def __init__(self, device, stream, *inputs):
+    def __init__(self, device, stream, inputs):
         self.device, self.stream, self.inputs, self.contexts = device, stream, inputs, ()
 
     def __enter__(self) -> int:
         if self.stream is None:
-            if torch.cuda.current_device() != self.device.index:
-                self._open(torch.cuda.device(self.device))
+            self._open(torch.cuda.device(self.device))
             return _raw_stream(self.device.index)
         if self.stream.device != self.device:
             raise ValueError(f"stream is on {self.stream.device}, the tensors on {self.device}")
@@ -551,17 +562,25 @@ class _launching:
             c.__exit__(*exc)
 
 
+def _launching(device, stream, *inputs):
+    """Device and stream of a call, as a context with the raw stream pointer."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _Here(device.index)
+    return _There(device, stream, inputs)
+
+
 def _like(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
     if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
 
-def _alike(shape, dtype, device, **tensors) -> None:
+def _alike(shape, dtype, device, names: str, *tensors) -> None:
     """_like for tensors of one shape."""
-    for name, t in tensors.items():
+    for t in tensors:
         if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
-            _like(t, shape, dtype, device, name)
+            for name, u in zip(names.split(), tensors):
+                _like(u, shape, dtype, device, name)
 
 
 def _on_gpu(t: torch.Tensor, name: str) -> torch.device:
@@ -623,8 +642,8 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gk: torch.Tensor, go:
     values = (B, T, H, dv)
     if T != grid_h * grid_w:
         raise ValueError(f"T={T} but grid is {grid_h}x{grid_w}")
-    _alike(keys, dtype, dev, q=q, k=k, gk=gk)
-    _alike(values, dtype, dev, v=v, go=go)
+    _alike(keys, dtype, dev, "q k gk", q, k, gk)
+    _alike(values, dtype, dev, "v go", v, go)
     p0 = _state_ptr(s0, B, H, dk, dv, "s0", dev)
     pf = _state_ptr(gs_final, B, H, dk, dv, "gs_final", dev)
     if gs0 is not None and not return_gs0:
@@ -656,14 +675,14 @@ def _step(q, k, v, gk, state, slots, out, stream, gate=None, norm_weight=None, e
         raise ValueError("q, k, gk must be [B, H, dk] and v [B, H, dv]")
     B, H, dk = keys = q.shape
     dv, dev, dtype = v.shape[-1], _on_gpu(q, "q"), q.dtype
-    _alike(keys, dtype, dev, q=q, k=k, gk=gk)
-    _alike((B, H, dv), dtype, dev, v=v)
+    _alike(keys, dtype, dev, "q k gk", q, k, gk)
+    _alike((B, H, dv), dtype, dev, "v", v)
     if state.dim() != 4:
         raise ValueError("state must be [n_slots, H, dk, dv]")
     n_slots = state.shape[0]
-    _alike((n_slots, H, dk, dv), torch.float32, dev, state=state)
+    _alike((n_slots, H, dk, dv), torch.float32, dev, "state", state)
     if slots is not None:
-        _alike((B,), torch.int32, dev, slots=slots)
+        _alike((B,), torch.int32, dev, "slots", slots)
     elif n_slots < B:
         raise ValueError(f"{B} rows without slots need as many states, got {n_slots}")
     if gate is not None:
