@@ -9,7 +9,7 @@
 // over rows in a fixed order (per workgroup, then over the workgroups'
 // partial sums in a second kernel), so it does not change from run to run.
 // Measured, half: norm of 6,400 x 768 9.4 us (4.2 TB/s), with the 8-bit output
-// of 25,600 x 768 27.2 us (5.1 TB/s); gradients of 25,600 x 768 34.8 us (4.5
+// of 25,600 x 768 27.2 us (5.1 TB/s); gradients of 25,600 x 768 31.1 us (5.1
 // TB/s) and of 409,600 gate rows of 64 44 us (5.9 TB/s), each with 4.7 us of
 // column sums. (A copy of 256 MB runs at 5.4 TB/s.)
 #include "gla_norm.h"
@@ -126,6 +126,9 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(
     const InT* sp, const InT* gyp, const InT* gsp, const float* __restrict__ wp, float eps, InT* gxp,
     float* __restrict__ part, long rows, int F) {
   constexpr int RPB = 256 / TPR;  // rows per workgroup and step
+  // gsum is loaded with the others (25,600 x 768 half: 31 us, or 35 where it
+  // waits for the sums), but not where its registers would not be left
+  constexpr bool kEarly = VPT <= 4;
   __shared__ float lds[4];
   __shared__ float sW[RPB > 1 ? RPB * TPR * VPT * 8 : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR, nv = F / 8;
@@ -135,16 +138,17 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(
 #pragma unroll
     for (int c = 0; c < 8; ++c) gw[i][c] = 0.f;
   for (long row = (long)blockIdx.x * RPB + sub; row < rows; row += (long)gridDim.x * RPB) {
-    float s[VPT][8], g[VPT][8], ss = 0.f;
+    float s[VPT][8], g[VPT][8], x[kEarly ? VPT : 1][8], ss = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int u = t + TPR * i;
       const long at = row * F + 8 * u;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) s[i][c] = g[i][c] = 0.f;
+      for (int c = 0; c < 8; ++c) s[i][c] = g[i][c] = x[kEarly ? i : 0][c] = 0.f;
       if (u < nv) {
         load8(sp + at, s[i]);
         load8(gyp + at, g[i]);
+        if (kEarly && gsp) load8(gsp + at, x[kEarly ? i : 0]);
       }
 #pragma unroll
       for (int c = 0; c < 8; ++c) ss = fmaf(s[i][c], s[i][c], ss);
@@ -171,11 +175,15 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(
       const int u = t + TPR * i;
       const long at = row * F + 8 * u;
       if (u < nv) {
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (gsp) load8(gsp + at, x);
+        float(&y)[8] = x[kEarly ? i : 0];
+        if (!kEarly) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = fmaf(rstd, g[i][c] - s[i][c] * dot, x[c]);
-        store8(gxp + at, x);
+          for (int c = 0; c < 8; ++c) y[c] = 0.f;
+          if (gsp) load8(gsp + at, y);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) y[c] = fmaf(rstd, g[i][c] - s[i][c] * dot, y[c]);
+        store8(gxp + at, y);
       }
     }
   }
@@ -301,7 +309,7 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
 
 // Workgroups of the two gradient kernels: enough to fill the GPU, few enough
 // that the partial sums stay small beside the rows. At most 512, 1024 or 2048
-// of them: the norm's gradient of 25,600 x 768 half rows 54, 41 or 47 us, the
+// of them: the norm's gradient of 25,600 x 768 half rows 42, 37 or 41 us, the
 // gate's of 409,600 rows of 64 the same within 1 us.
 constexpr long kMaxParts = 1024;
 // every workgroup takes the same number of steps of `per` rows, but the last
@@ -310,7 +318,7 @@ int even_parts(long rows, long per) {
   const long each = (steps + kMaxParts - 1) / kMaxParts;
   return (int)((steps + each - 1) / each);
 }
-int norm_parts(long rows, int F) { return even_parts(rows, F <= 2048 ? 4 : 1); }
+int norm_parts(long rows, int F) { return even_parts(rows, F <= 1024 ? 4 : 1); }
 int gate_parts(long rows, int dv) { return even_parts(rows, 256 / (dv / 8)); }
 
 template <int TPR, int VPT, typename InT>
@@ -344,17 +352,16 @@ hipError_t norm_bwd_t(const NormBwdArgs& a, float* ws, hipStream_t s) {
   return hipGetLastError();
 }
 
-// One wave per row up to `WAVE` columns (1024 or 2048), else one workgroup. The
-// norm of 12,800 half rows takes, with a wave or a workgroup per row, 29.7 or
-// 26.2 us for 1536 columns, 40.5 or 35.9 for 2048, and 50.2 or 44.5 for 2560;
-// its gradient 34.9 or 36.9, 45.5 or 43.4, and 102 or 53 (1024 rows of 2048
-// columns: 12.5 or 14.1).
-#define GLA_NORM_DISPATCH(FN, WAVE, InT, ...)                              \
+// One wave per row up to 1024 columns, else one workgroup. 12,800 half rows
+// take, with a wave or a workgroup per row, 29.7 or 26.2 us for 1536 columns
+// and 40.5 or 35.9 for 2048, their gradient 38.9 or 36.5 and 50.0 or 43.3 (but
+// of 1024 rows of 2048 13.2 or 14.3).
+#define GLA_NORM_DISPATCH(FN, InT, ...)                                    \
   do {                                                                     \
     const int F_ = a.F;                                                    \
     if (F_ <= 512) return FN<64, 1, InT>(__VA_ARGS__);                     \
     if (F_ <= 1024) return FN<64, 2, InT>(__VA_ARGS__);                    \
-    if (F_ <= 2048) return FN<WAVE == 2048 ? 64 : 256, WAVE == 2048 ? 4 : 1, InT>(__VA_ARGS__); \
+    if (F_ <= 2048) return FN<256, 1, InT>(__VA_ARGS__);                   \
     if (F_ <= 4096) return FN<256, 2, InT>(__VA_ARGS__);                   \
     if (F_ <= 8192) return FN<256, 4, InT>(__VA_ARGS__);                   \
     return FN<256, 8, InT>(__VA_ARGS__);                                   \
@@ -376,8 +383,8 @@ hipError_t gate_bwd_t(const GateBwdArgs& a, float* ws, hipStream_t s) {
 }  // namespace norm
 
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s) {
-  if (a.dtype == 0) GLA_NORM_DISPATCH(norm::norm_t, 1024, half_t, a, s);
-  GLA_NORM_DISPATCH(norm::norm_t, 1024, float, a, s);
+  if (a.dtype == 0) GLA_NORM_DISPATCH(norm::norm_t, half_t, a, s);
+  GLA_NORM_DISPATCH(norm::norm_t, float, a, s);
 }
 
 size_t norm_bwd_workspace(long rows, int F) {
@@ -385,8 +392,8 @@ size_t norm_bwd_workspace(long rows, int F) {
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, float* ws, hipStream_t s) {
-  if (a.dtype == 0) GLA_NORM_DISPATCH(norm::norm_bwd_t, 2048, half_t, a, ws, s);
-  GLA_NORM_DISPATCH(norm::norm_bwd_t, 2048, float, a, ws, s);
+  if (a.dtype == 0) GLA_NORM_DISPATCH(norm::norm_bwd_t, half_t, a, ws, s);
+  GLA_NORM_DISPATCH(norm::norm_bwd_t, float, a, ws, s);
 }
 
 size_t gate_bwd_workspace(long rows, int dv) {
