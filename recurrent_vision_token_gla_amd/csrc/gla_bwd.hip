@@ -255,7 +255,7 @@ __global__ __launch_bounds__(kThreads, 3) void bwd_summary_kernel(
   constexpr int KB = 16 * DK, VB = 16 * DV;  // 16 rows of a tile
   __shared__ __attribute__((aligned(16))) __bf16 sX[NX][C * DK];
   __shared__ __attribute__((aligned(16))) __bf16 sY[NT][C * DV];
-  __shared__ float sE[NB][DK];  // decay of a sub-block
+  __shared__ __attribute__((aligned(16))) float sE[NB][DK];  // decay of a sub-block
   const bool rev = blockIdx.z & 1;
   const int n = blockIdx.x, h = blockIdx.y, b = blockIdx.z >> 1;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -280,8 +280,12 @@ __global__ __launch_bounds__(kThreads, 3) void bwd_summary_kernel(
   for (int e = 0; e < NEL; ++e) s[e] = row_scan16(log2_decay(g[e]));
   if (lr == 15) {
 #pragma unroll
-    for (int e = 0; e < NEL; ++e) sE[wave][32 * (e / 8) + 8 * lq + e % 8] = fexp2(s[e]);
+    for (int e = 0; e < NEL; e += 4)
+      *reinterpret_cast<floatx4*>(&sE[wave][32 * (e / 8) + 8 * lq + e % 8]) =
+          floatx4{s[e], s[e + 1], s[e + 2], s[e + 3]};
   }
+  wave_sync();
+  for (int d = lane; d < DK; d += 64) sE[wave][d] = fexp2(sE[wave][d]);
   // exponents s (from the start) or tot - s (to the end), without a branch
   const float to_end = rev ? 0.f : 1.f, sign = rev ? 1.f : -1.f;
 #pragma unroll
