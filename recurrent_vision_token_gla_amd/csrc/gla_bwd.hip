@@ -1036,9 +1036,11 @@ hipError_t bwd_t(const Problem& p, int b0, int nb, const DirPack& dirs, const Bw
     hipLaunchKernelGGL((bwd_scan_serial_kernel<8, kTerms>), grid, dim3(kThreads), 0, s, S, D, A, s0,
                        gsf, gs0, p.N, DK, DV, groups);
   } else {
+    // windows of 64 chunks where one holds the chain (16 chains of 64 chunks
+    // 12.2 us, in room for 128 15.3), else of 128 (1 chain of 256 12.1, in
+    // windows of 64 14.5; with more chains the two are within 15%)
     const int L = p.N > 16 * 8 ? 8 : (p.N + 15) / 16;
-    // the shortest window that holds the chain, in registers
-    auto scan = L <= 2 ? bwd_scan_kernel<2, kTerms> : L <= 4 ? bwd_scan_kernel<4, kTerms> : bwd_scan_kernel<8, kTerms>;
+    auto scan = L <= 4 ? bwd_scan_kernel<4, kTerms> : bwd_scan_kernel<8, kTerms>;
     hipLaunchKernelGGL(scan, dim3((unsigned)(groups / 64), 2), dim3(1024), 0, s, S, D, A, s0, gsf, gs0,
                        p.N, DK, DV, L);
   }
