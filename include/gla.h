@@ -325,10 +325,11 @@ int gla_spatial_swiglu(const void* a, const void* u, const float* weight,
  * `stream` without allocating or synchronising, so every call can be captured
  * in a graph. Workspaces may hold anything on entry and nothing is kept in
  * them between calls; calls that may overlap in time (two streams, two graphs
- * replayed at once) need a workspace each, and one that gla_workspace_init has
- * prepared for the forward is refused (GLA_E_ARG). Values are not checked: a NaN or
- * Inf makes the outputs that depend on it non-finite, and in the gradients may
- * reach every token of its 64-token chunk. Results do not change from run to
+ * replayed at once) need a workspace each, and one that holds any of the
+ * control words (the first 64 KiB) of a workspace prepared for the forward is
+ * refused (GLA_E_ARG). Values are not checked: a NaN or Inf makes the outputs
+ * that depend on it non-finite, and in the gradients may reach every token of
+ * its 64-token chunk. Results do not change from run to
  * run. An empty problem (no row, token or head) returns GLA_OK and writes
  * nothing. */
 

@@ -7,28 +7,24 @@
 #include <string.h>
 
 #include <mutex>
-#include <unordered_map>
 
 #include "gla.h"
 #include "gla_check.h"
 #include "gla_launch.h"
+#include "gla_prepared.h"
 
 using namespace gla::api;
 
 namespace {
 
-// Workspaces whose control words gla_workspace_init has zeroed (start address
-// -> bytes). The single pass trusts those words only on such a workspace; any
-// other workspace runs the three phases, which read no control words, so a
-// workspace of arbitrary contents always gives correct results.
-std::mutex g_prepared_mu;
-std::unordered_map<uintptr_t, size_t> g_prepared;
+// Workspaces whose control words gla_workspace_init has zeroed. The single
+// pass trusts those words only on such a workspace; any other workspace runs
+// the three phases, which read no control words, so a workspace of arbitrary
+// contents always gives correct results.
+constexpr size_t kCtrlBytes = (size_t)gla::kCtrlWords * sizeof(unsigned);
+gla::Prepared g_prepared(kCtrlBytes);
 
-bool is_prepared(const void* ws) {
-  std::lock_guard<std::mutex> lk(g_prepared_mu);
-  const auto it = g_prepared.find(reinterpret_cast<uintptr_t>(ws));
-  return it != g_prepared.end() && it->second >= (size_t)gla::kCtrlWords * sizeof(unsigned);
-}
+bool is_prepared(const void* ws) { return g_prepared.contains(ws); }
 
 int check_ws(const gla::Problem& p, const void* ws, size_t ws_bytes) {
   const gla::WsLayout w = gla::workspace_layout(p);
@@ -203,6 +199,10 @@ char* g_scratch_ptr[kMaxDevices] = {};
 
 }  // namespace
 
+bool gla::api::holds_control_words(const void* p, size_t n) {
+  return g_prepared.control_words_in(p, n);
+}
+
 static __device__ __align__(256) char scratch[kScratchBytes];
 
 namespace {
@@ -223,10 +223,7 @@ int scratch_for_device(hipStream_t stream, char** out) {
     if (e != hipSuccess || !ptr) return fail_hip(e, "hipGetSymbolAddress(scratch)");
     e = gla::launch_ctrl_clear(static_cast<char*>(ptr), stream);
     if (e != hipSuccess) return fail_hip(e, "scratch control-word clear");
-    {
-      std::lock_guard<std::mutex> lk2(g_prepared_mu);
-      g_prepared[reinterpret_cast<uintptr_t>(ptr)] = kScratchBytes;
-    }
+    g_prepared.add(ptr, kScratchBytes);
     g_scratch_ptr[dev] = static_cast<char*>(ptr);
   }
   *out = g_scratch_ptr[dev];
@@ -388,19 +385,17 @@ int gla_auto_schedule(int B, int H, int grid_h, int grid_w, int dk, int dv, int 
 
 int gla_workspace_init(void* workspace, size_t workspace_bytes, void* stream) {
   if (!workspace || !aligned(workspace, 256)) return GLA_E_ARG;
-  if (workspace_bytes < (size_t)gla::kCtrlWords * sizeof(unsigned)) return GLA_E_WORKSPACE;
+  if (workspace_bytes < kCtrlBytes) return GLA_E_WORKSPACE;
   const hipError_t e =
       gla::launch_ctrl_clear(static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail_hip(e, "workspace init launch");
-  std::lock_guard<std::mutex> lk(g_prepared_mu);
-  g_prepared[reinterpret_cast<uintptr_t>(workspace)] = workspace_bytes;
+  g_prepared.add(workspace, workspace_bytes);
   return GLA_OK;
 }
 
 int gla_workspace_release(const void* workspace) {
   if (!workspace) return GLA_E_ARG;
-  std::lock_guard<std::mutex> lk(g_prepared_mu);
-  g_prepared.erase(reinterpret_cast<uintptr_t>(workspace));
+  g_prepared.remove(workspace);
   return GLA_OK;
 }
 
@@ -411,7 +406,7 @@ int gla_workspace_is_prepared(const void* workspace) {
 int gla_workspace_status(void* workspace, size_t workspace_bytes, uint32_t* error_bits, int clear,
                          void* stream) {
   if (!workspace || !aligned(workspace, 256) || !error_bits) return GLA_E_ARG;
-  if (workspace_bytes < (size_t)gla::kCtrlWords * sizeof(unsigned)) return GLA_E_WORKSPACE;
+  if (workspace_bytes < kCtrlBytes) return GLA_E_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint32_t word = 0;
   hipError_t e = hipMemcpyAsync(&word, workspace, sizeof(word), hipMemcpyDeviceToHost, s);

@@ -62,6 +62,10 @@ inline gla::DirPack pack_dirs(const int32_t* dir, int b0, int nb) {
 
 inline int check_tensor(const void* t) { return (t && aligned(t, 16)) ? GLA_OK : GLA_E_ARG; }
 
+// Some control word of a workspace prepared for the single pass lies in
+// [p, p + n).
+bool holds_control_words(const void* p, size_t n);
+
 #define GLA_TRY(...)               \
   do {                             \
     const int rc_ = (__VA_ARGS__); \

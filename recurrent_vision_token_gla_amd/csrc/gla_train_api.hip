@@ -33,10 +33,10 @@ int check_disjoint(const Range (&out)[NO], const Range (&in)[NI]) {
 
 int check_optional(const void* t) { return t ? check_tensor(t) : GLA_OK; }
 
-// A prepared workspace is refused: its control words, which the forward's
-// single pass relies on, would be overwritten.
+// Memory that holds the control words of a workspace prepared for the forward
+// is refused: the single pass relies on them, and they would be overwritten.
 int check_workspace(const void* ws, size_t have, size_t need) {
-  if (!ws || !aligned(ws, 256) || gla_workspace_is_prepared(ws)) return GLA_E_ARG;
+  if (!ws || !aligned(ws, 256) || holds_control_words(ws, have < need ? have : need)) return GLA_E_ARG;
   return have < need ? GLA_E_WORKSPACE : GLA_OK;
 }
 

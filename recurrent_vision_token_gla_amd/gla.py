@@ -179,13 +179,11 @@ def workspace_layout(B, H, grid_h, grid_w, dk, dv, chunk=64):
 def alloc_workspace(B, H, grid_h, grid_w, dk, dv, chunk=64, device=None,
                     prepare: bool = True) -> torch.Tensor:
     """A workspace for this problem. With prepare (the default) it is prepared
-    for the single pass by gla_workspace_init, and released from the
-    library's record of prepared workspaces when the tensor is collected."""
+    for the single pass by workspace_init."""
     n = workspace_bytes(B, H, grid_h, grid_w, dk, dv, chunk)
     ws = torch.empty(max(n, CTRL_BYTES), dtype=torch.uint8, device=device or "cuda")
     if prepare:
         workspace_init(ws)
-        weakref.finalize(ws, load().gla_workspace_release, ws.data_ptr())
     return ws
 
 
@@ -200,11 +198,13 @@ def auto_schedule(B, H, grid_h, grid_w, dk, dv, chunk=64) -> int:
 
 def workspace_init(workspace: torch.Tensor, stream=None) -> None:
     """Prepare a workspace for the single pass: zero its control words (and
-    the sticky error word) with a kernel and record it as prepared."""
+    the sticky error word) with a kernel and record it as prepared, until
+    workspace_release or until its memory is freed."""
     ws, nws = _ws(workspace, workspace.device)
     with _on_device(workspace.device):
         st = load().gla_workspace_init(ws, nws, _stream_ptr(stream))
     _check(st, "gla_workspace_init")
+    weakref.finalize(workspace.untyped_storage(), load().gla_workspace_release, ws)
 
 
 def workspace_release(workspace: torch.Tensor) -> None:
@@ -607,8 +607,8 @@ def _gate_workspace_bytes(rows: int, dv: int) -> int:
 
 def _scratch(workspace: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
     """The caller's workspace or a new one (inside _launching). The gradients
-    refuse a workspace prepared for the forward; a new one is nobody's, even
-    where a freed one was never released."""
+    refuse memory with the control words of a workspace prepared for the
+    forward; a new one is nobody's, even where a freed one was never released."""
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
         load().gla_workspace_release(workspace.data_ptr())
