@@ -6,6 +6,7 @@ no fallback: if the library is not built, or a call fails, this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -537,29 +538,27 @@ class _There:
     __slots__ = ("device", "stream", "inputs", "contexts")
 
     def __init__(self, device, stream, inputs):
-        self.device, self.stream, self.inputs, self.contexts = device, stream, inputs, ()
+        self.device, self.stream, self.inputs = device, stream, inputs
 
     def __enter__(self) -> int:
-        if self.stream is None:
-            self._open(torch.cuda.device(self.device))
-            return _raw_stream(self.device.index)
-        if self.stream.device != self.device:
-            raise ValueError(f"stream is on {self.stream.device}, the tensors on {self.device}")
-        self._open(torch.cuda.device(self.device), torch.cuda.stream(self.stream))
-        if not torch.cuda.is_current_stream_capturing():
-            for t in self.inputs:
-                if t is not None:
-                    t.record_stream(self.stream)
-        return int(self.stream.cuda_stream)
-
-    def _open(self, *contexts) -> None:
-        self.contexts = contexts
-        for c in contexts:
-            c.__enter__()
+        with contextlib.ExitStack() as contexts:  # left again if anything below fails
+            if self.stream is not None and self.stream.device != self.device:
+                raise ValueError(f"stream is on {self.stream.device}, the tensors on {self.device}")
+            contexts.enter_context(torch.cuda.device(self.device))
+            if self.stream is None:
+                ptr = _raw_stream(self.device.index)
+            else:
+                contexts.enter_context(torch.cuda.stream(self.stream))
+                if not torch.cuda.is_current_stream_capturing():
+                    for t in self.inputs:  # those elsewhere are refused by the call
+                        if t is not None and t.device == self.device:
+                            t.record_stream(self.stream)
+                ptr = int(self.stream.cuda_stream)
+            self.contexts = contexts.pop_all()
+        return ptr
 
     def __exit__(self, *exc) -> None:
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
+        self.contexts.__exit__(*exc)
 
 
 def _launching(device, stream, *inputs):
