@@ -569,7 +569,7 @@ def _launching(device, stream, *inputs):
 
 
 def _like(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t is None or t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
@@ -669,7 +669,7 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gk: torch.Tensor, go:
     return outs + (gs0,) if return_gs0 else outs
 
 
-def _step(q, k, v, gk, state, slots, out, stream, gate=None, norm_weight=None, eps=0.0):
+def _step(q, k, v, gk, state, slots, out, stream, gated=False, gate=None, norm_weight=None, eps=0.0):
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k, gk must be [B, H, dk] and v [B, H, dv]")
     B, H, dk = keys = q.shape
@@ -684,19 +684,19 @@ def _step(q, k, v, gk, state, slots, out, stream, gate=None, norm_weight=None, e
         _alike((B,), torch.int32, dev, "slots", slots)
     elif n_slots < B:
         raise ValueError(f"{B} rows without slots need as many states, got {n_slots}")
-    if gate is not None:
+    if gated:
         _like(gate, (B, H, dv), dtype, dev, "gate")
         _like(norm_weight, (dv,), torch.float32, dev, "norm_weight")
     with _launching(dev, stream, q, k, v, gk, state, slots, out, gate, norm_weight) as st_ptr:
         out = _out_like(out, v)
         tail = (out.data_ptr(), B, H, dk, dv, _dtype_code(q), state.data_ptr(), n_slots,
                 _ptr(slots), st_ptr)
-        if gate is None:
+        if not gated:
             st = load().gla_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), gk.data_ptr(), *tail)
         else:
             st = load().gla_step_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), gk.data_ptr(),
                                        gate.data_ptr(), norm_weight.data_ptr(), float(eps), *tail)
-    _check(st, "gla_step" if gate is None else "gla_step_gated")
+    _check(st, "gla_step_gated" if gated else "gla_step")
     return out
 
 
@@ -717,7 +717,7 @@ def step_gated(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gk: torch.Tens
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """step with the output gate, y = RMSNorm(o) * norm_weight * silu(gate);
     gate [B, H, dv] in q's dtype, norm_weight [dv] float32."""
-    return _step(q, k, v, gk, state, slots, out, stream, gate, norm_weight, eps)
+    return _step(q, k, v, gk, state, slots, out, stream, True, gate, norm_weight, eps)
 
 
 def _norm_args(x, residual, weight):
@@ -797,7 +797,8 @@ def gate_bwd(o: torch.Tensor, gate: torch.Tensor, norm_weight: torch.Tensor, eps
     norm_weight * silu(gate) (fwd_gated's, with o what fwd gives); o, gate, gy
     [..., dv]; norm_weight and its gradient [dv] float32. out: two tensors to
     write go and ggate to."""
-    rows, dv = _norm_args(o, gate, norm_weight)
+    rows, dv = _norm_args(o, None, norm_weight)
+    _like(gate, o.shape, o.dtype, o.device, "gate")
     _like(gy, o.shape, o.dtype, o.device, "gy")
     if out is not None and len(out) != 2:
         raise ValueError("out must be two tensors (go, ggate)")
