@@ -45,8 +45,11 @@ typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 
 constexpr int C = kBwdChunk, NB = C / 16;
 // A token's decay is taken as at least 2^-160: float rounds anything beyond
-// 2^-149 to zero, and the cumulative sums stay small enough that their
-// differences keep their low bits.
+// 2^-149 to zero. A token that forgets everything puts that much into a
+// cumulative sum, whose last bits are then coarse (2^-17 at 160, 2^-13 at
+// 2048), so no decay between two tokens is a difference of sums that hold more
+// than the decay of a sub-block with a reference: sums run from the token to
+// where they are needed, or the tokens' decays are multiplied.
 constexpr float kMinLog2 = -160.f;
 __device__ __forceinline__ float log2_decay(float gk) {
   const float x = gk * kLog2e;
@@ -158,8 +161,7 @@ template <typename InT, int NEL> struct Raw {
   }
 };
 
-// Inclusive suffix sum over the 16 lanes of a DPP row, and the sum of the
-// lanes before each one.
+// Inclusive suffix sum over the 16 lanes of a DPP row; neighbours' values.
 __device__ __forceinline__ float row_suffix16(float x) {
   x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x101, 0xf, 0xf, true));
   x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x102, 0xf, 0xf, true));
@@ -167,8 +169,11 @@ __device__ __forceinline__ float row_suffix16(float x) {
   x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x108, 0xf, 0xf, true));
   return x;
 }
-__device__ __forceinline__ float row_before16(float scan) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(scan), 0x111, 0xf, 0xf, true));
+__device__ __forceinline__ float row_before16(float x) {  // the lane before's, or zero
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x111, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row_after16(float x) {  // the next lane's, or zero
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x101, 0xf, 0xf, true));
 }
 
 // Lane n of each row of 16, on all of the row's lanes.
@@ -275,10 +280,17 @@ __global__ __launch_bounds__(kThreads, 3) void bwd_summary_kernel(
     x.zero_if(pad);
     y.zero_if(pad);
   }
+  // cumulative decay from the sub-block's start to each token (q), or from
+  // behind it to the end (k): sums of just the tokens between
   float s[NEL];
+  if (rev) {
 #pragma unroll
-  for (int e = 0; e < NEL; ++e) s[e] = row_scan16(log2_decay(g[e]));
-  if (lr == 15) {
+    for (int e = 0; e < NEL; ++e) s[e] = row_scan16(log2_decay(g[e]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < NEL; ++e) s[e] = row_suffix16(log2_decay(g[e]));
+  }
+  if (lr == (rev ? 15 : 0)) {
 #pragma unroll
     for (int e = 0; e < NEL; e += 4)
       *reinterpret_cast<floatx4*>(&sE[wave][32 * (e / 8) + 8 * lq + e % 8]) =
@@ -286,16 +298,15 @@ __global__ __launch_bounds__(kThreads, 3) void bwd_summary_kernel(
   }
   wave_sync();
   for (int d = lane; d < DK; d += 64) sE[wave][d] = fexp2(sE[wave][d]);
-  // exponents s (from the start) or tot - s (to the end), without a branch
-  const float to_end = rev ? 0.f : 1.f, sign = rev ? 1.f : -1.f;
+  if (!rev) {
+#pragma unroll
+    for (int e = 0; e < NEL; ++e) s[e] = row_after16(s[e]);
+  }
 #pragma unroll
   for (int ks = 0; ks < NKS; ++ks) {
     float o[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float se = s[8 * ks + c];
-      o[c] = tile::mulw(x[8 * ks + c], fexp2(fmaf(to_end, row_lane<15>(se), sign * se)));
-    }
+    for (int c = 0; c < 8; ++c) o[c] = tile::mulw(x[8 * ks + c], fexp2(s[8 * ks + c]));
     const Split8<NX> t = split8<NX>(o);
 #pragma unroll
     for (int i = 0; i < NX; ++i) lk.put(&sX[i][wave * KB], ks, t.t[i]);
@@ -635,8 +646,10 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 || DK == 32 ? 2 : 1) voi
   } else {
 #pragma unroll
     for (int e = 0; e < NEL; ++e) {
-      ck[e] = fexp2(row_lane<15>(s[e]) - s[e]);
+      const float x = log2_decay(g[e]);
+      ck[e] = fexp2(row_after16(row_suffix16(x)));
       cq[e] = fexp2(s[e]);
+      s[e] = fexp2(x);  // the token's own decay is what the pairs below take
     }
   }
   wave_sync();  // tot and ref
@@ -768,34 +781,45 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 || DK == 32 ? 2 : 1) voi
       }
     }
   } else {
-    // every pair on its own: 2^(s_i - s_j) <= 1 for j <= i; component x of the
-    // 16 that P and A spread over the four lanes of a token
-#pragma unroll
-    for (int D = 0; D < ND; ++D) gq[D] = gk[D] = zero4;
-    auto component = [&](const floatx4& p, int x) {
-      const float a = (x & 1) ? p[1] : p[0], c = (x & 1) ? p[3] : p[2];
-      return __shfl((x & 2) ? c : a, 16 * (x / 4) + lr);
+    // every pair on its own, at distance x = i - j from 0 to 15: with a_t the
+    // tokens' decays, k_{i-x} a_{i-x+1} .. a_i is the lane before's of x - 1
+    // times a_i, and q_{j+x} a_{j+1} .. a_{j+x} the next lane's times its a; a
+    // lane without one reads zero. Component y of the 16 that P and A spread
+    // over the four lanes of a token:
+    auto component = [&](const floatx4& p, int y) {
+      const float a = (y & 1) ? p[1] : p[0], c = (y & 1) ? p[3] : p[2];
+      return __shfl((y & 2) ? c : a, 16 * ((y & 15) / 4) + lr);
     };
     an = zero4;
-#pragma unroll 1
-    for (int j = 0; j < 16; ++j) {
-      const float pij = component(pt, j), pji = component(pn, j);  // P[lr][j], P[j][lr]
-      float aij = 0.f;
 #pragma unroll
-      for (int e = 0; e < NEL; ++e) {
-        const int src = (lane & 48) | j;
-        const float sj = __shfl(s[e], src), kj = __shfl(k[e], src), qj = __shfl(q[e], src);
-        // token j as the key of this lane's query, and as the query of its key
-        const float fq = j < lr ? fexp2(s[e] - sj) : 0.f;
-        const float fk = j >= lr ? fexp2(sj - s[e]) : 0.f;
-        gq[e / 4][e % 4] = fmaf(j < lr ? pij * kj : 0.f, fq, gq[e / 4][e % 4]);
-        gk[e / 4][e % 4] = fmaf(j > lr ? pji * qj : 0.f, fk, gk[e / 4][e % 4]);
-        aij = fmaf(qj * k[e], fk, aij);
+    for (int D = 0; D < ND; ++D) gq[D] = gk[D] = zero4;
+#pragma unroll
+    for (int ks = 0; ks < NKS; ++ks) {  // eight dims at a time: more do not fit the registers
+      float m[8], w[8], aij = 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        m[c] = k[8 * ks + c], w[c] = q[8 * ks + c];
+        aij = fmaf(w[c], m[c], aij);
       }
-      aij += __shfl_xor(aij, 16);
-      aij += __shfl_xor(aij, 32);
+#pragma unroll 1
+      for (int x = 0;;) {
+        aij += __shfl_xor(aij, 16);
+        aij += __shfl_xor(aij, 32);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) an[r] = 4 * lq + r == j ? aij : an[r];
+        for (int r = 0; r < 4; ++r) an[r] += 4 * lq + r == lr + x ? aij : 0.f;
+        if (++x == 16) break;
+        const float pij = component(pt, lr - x), pji = component(pn, lr + x);  // P[lr][lr-x], P[lr+x][lr]
+        aij = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int e = 8 * ks + c;
+          m[c] = row_before16(m[c]) * s[e];
+          w[c] = row_after16(w[c] * s[e]);
+          gq[e / 4][e % 4] = fmaf(pij, m[c], gq[e / 4][e % 4]);
+          gk[e / 4][e % 4] = fmaf(pji, w[c], gk[e / 4][e % 4]);
+          aij = fmaf(w[c], k[e], aij);
+        }
+      }
     }
   }
 #pragma unroll
