@@ -352,7 +352,10 @@ size_t gla_bwd_workspace_bytes(int B, int H, int grid_h, int grid_w, int dk,
  * Sums and states are float. Products run on the matrix cores over operands
  * split into bf16 terms: 16 bits for GLA_F16, 24 for GLA_F32 (whose q, k, v
  * are not rounded to half here; they and go must not exceed 65504 in
- * magnitude). gk <= 0; a token's decay below 2^-160 counts as 2^-160. */
+ * magnitude). gk <= 0; a token's decay below 2^-160 counts as 2^-160, and a
+ * product of decays below 2^-60 may count as zero. Beyond the rounding of its
+ * exponent (2^-22 of its log2), the decay between two tokens is off by at most
+ * 2^-14 of itself, however much the tokens before them forgot. */
 int gla_bwd(const void* q, const void* k, const void* v, const void* gk,
             const void* go, void* gq, void* gkey, void* gv, void* ggk, int B,
             int H, int grid_h, int grid_w, int dk, int dv, const int32_t* dir,

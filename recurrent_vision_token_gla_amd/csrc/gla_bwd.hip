@@ -176,6 +176,28 @@ __device__ __forceinline__ float row_after16(float x) {  // the next lane's, or 
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x101, 0xf, 0xf, true));
 }
 
+template <int CTRL>
+__device__ __forceinline__ float row_add(float x) {  // x plus the lane's that CTRL shifts in
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+// For values x of 16 tokens, s = the sum over tokens 8..i, or less the sum over
+// i+1..7; and, on lane 0, lo = the sum over 0..7. (Step by step over all values:
+// a lane permutation waits for the instruction before it.)
+template <int N>
+__device__ __forceinline__ void from_middle16(const float (&x)[N], float (&s)[N], float (&lo)[N]) {
+  const bool low = (threadIdx.x & 8) == 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) lo[e] = low ? x[e] : 0.f, s[e] = low ? 0.f : x[e];
+#pragma unroll
+  for (int e = 0; e < N; ++e) lo[e] = row_add<0x101>(lo[e]), s[e] = row_add<0x111>(s[e]);
+#pragma unroll
+  for (int e = 0; e < N; ++e) lo[e] = row_add<0x102>(lo[e]), s[e] = row_add<0x112>(s[e]);
+#pragma unroll
+  for (int e = 0; e < N; ++e) lo[e] = row_add<0x104>(lo[e]), s[e] = row_add<0x114>(s[e]);
+#pragma unroll
+  for (int e = 0; e < N; ++e) s[e] -= row_after16(lo[e]);
+}
+
 // Lane n of each row of 16, on all of the row's lanes.
 template <int LANE>
 __device__ __forceinline__ float row_lane(float x) {
@@ -519,12 +541,17 @@ __global__ __launch_bounds__(1024) void bwd_scan_kernel(
 //   qx = q 2^(s-ref),  kx = k 2^(ref-s),
 // so the pairs inside the sub-block need no other factor, and pairs of two
 // sub-blocks I > J only factors by dim, all <= 1 (tables in LDS):
-//   2^(b_i-b_j) = 2^(s_i-ref_I) [2^ref_I prod_{J<M<I} 2^tot_M 2^(tot_J-ref_J)] 2^(ref_J-s_j).
-// Where no s - ref exceeds 68 in magnitude, values up to 65504 keep qx and kx
-// below 2^84 and every product finite (P is at most 64 products of two such
-// values); a 2^ref that underflows has all of its sub-block's q 2^s do so. A
-// sub-block that decays more keeps q 2^s and k 2^(tot-s) instead (its bracket then holds 1 for the two outer factors) and sums its
-// own pairs directly in float.
+//   2^(b_i-b_j) = 2^(s_i-ref_I) [2^ref_I prod_{J<M<I} 2^tot_M] [2^(tot_J-ref_J) 2^(ref_J-s_j)].
+// s - ref is summed from the 8th token outwards, so it holds the decays between
+// the two tokens only (a first token that forgets everything is in ref alone).
+// Where none exceeds 66 in magnitude, values up to 65504 keep qx and kx below
+// 2^82 and every product finite (P is at most 64 products of two such values).
+// The factors are applied so that no intermediate underflows unless the pair's
+// whole factor is below 2^-60: gq's sums take 2^(tot_J-ref_J) and then 2^ref_I,
+// which is a normal float unless the first token alone decays by 2^-60; a key's
+// last bracket is multiplied first, to 2^(tot_J-s_j) <= 1. A sub-block that
+// decays more keeps q 2^s and k 2^(tot-s) instead (2^ref and 2^(tot-ref) are
+// then 1) and takes its own pairs from products of the tokens' decays.
 //
 // A workgroup's own chain of steps bounds it: alone on a CU it takes 22,400
 // cycles, with a second one 25,200, in which each SIMD issues vector
@@ -535,7 +562,7 @@ __global__ __launch_bounds__(1024) void bwd_scan_kernel(
 // 128 registers a lane and spilled (1.2 times the time); so did all gradients
 // stored at the end, or D_n's rows read again for <S_n, D_n>.
 // ===========================================================================
-constexpr float kMaxSpan = 68.f;
+constexpr float kMaxSpan = 66.f;
 
 // Two workgroups per CU where their LDS fits (at most 80 KB; a half input's
 // largest takes 79, a float's 80 with 32 key dims): one alone leaves the SIMDs
@@ -620,44 +647,50 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 || DK == 32 ? 2 : 1) voi
     v.zero_if(pad);
     go.zero_if(pad);
   }
-  float s[NEL];
+  // -- decay between each token and the sub-block's 8th: s - ref, a sum over
+  // tokens 8..i, or less one over i+1..7; the first token's own is in ref alone
+  float s[NEL], lo[NEL];
+  {
+    float x[NEL];
 #pragma unroll
-  for (int e = 0; e < NEL; ++e) s[e] = row_scan16(log2_decay(g[e]));
+    for (int e = 0; e < NEL; ++e) x[e] = log2_decay(g[e]);
+    from_middle16(x, s, lo);
+  }
   auto row4 = [&](const float* x, int D) { return floatx4{x[4 * D], x[4 * D + 1], x[4 * D + 2], x[4 * D + 3]}; };
-  if ((lr | 8) == 15) {
-    float(*dst)[DK] = lr == 15 ? sA : sB;
+  if (lr == 15) {
 #pragma unroll
-    for (int D = 0; D < ND; ++D) *reinterpret_cast<floatx4*>(&dst[wave][dim(D)]) = row4(s, D);
+    for (int D = 0; D < ND; ++D) *reinterpret_cast<floatx4*>(&sA[wave][dim(D)]) = row4(s, D);
   }
-  // -- the sub-block's reference, its rows of qx and kx
-  float cq[NEL], ck[NEL], span = 0.f;  // the factors, which the gradients take too
+  if (lr == 0) {
 #pragma unroll
-  for (int e = 0; e < NEL; ++e) {
-    cq[e] = s[e] - row_lane<7>(s[e]);
-    span = fmaxf(span, fabsf(cq[e]));
+    for (int D = 0; D < ND; ++D) *reinterpret_cast<floatx4*>(&sB[wave][dim(D)]) = row4(lo, D);
   }
+  // -- the factors, which the gradients take too
+  float cq[NEL], ck[NEL], span = 0.f;
+#pragma unroll
+  for (int e = 0; e < NEL; ++e) span = fmaxf(span, fabsf(s[e]));
   const bool direct = !__all(span <= kMaxSpan);
   if (!direct) {
 #pragma unroll
     for (int e = 0; e < NEL; ++e) {
-      ck[e] = fexp2(-cq[e]);
-      cq[e] = fexp2(cq[e]);
+      ck[e] = fexp2(-s[e]);
+      cq[e] = fexp2(s[e]);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < NEL; ++e) {
       const float x = log2_decay(g[e]);
       ck[e] = fexp2(row_after16(row_suffix16(x)));
-      cq[e] = fexp2(s[e]);
+      cq[e] = fexp2(row_scan16(x));
       s[e] = fexp2(x);  // the token's own decay is what the pairs below take
     }
   }
-  wave_sync();  // tot and ref
+  wave_sync();  // tot - ref and ref
   for (int d = lane; d < DK; d += 64) {
     const float td = sA[wave][d], rd = sB[wave][d];
-    sE[wave][d] = fexp2(td);
+    sE[wave][d] = fexp2(td + rd);
     sEQ[wave][d] = direct ? 1.f : fexp2(rd);
-    sEK[wave][d] = direct ? 1.f : fexp2(td - rd);
+    sEK[wave][d] = direct ? 1.f : fexp2(td);
   }
   if (lane == 0) sDirect[wave] = direct;
   const floatx4 zero4 = {0.f, 0.f, 0.f, 0.f};
@@ -844,11 +877,11 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 || DK == 32 ? 2 : 1) voi
     for (int D = 0; D < ND; ++D) acc[D] = mm<NT>(rows8(lx, sX, state_at(D), ks), o, acc[D]);
     keep[ks] = rows8(lx, sX, state_at(wave % ND), ks);
   }
-  // -- the brackets of the pairs of sub-blocks, and 2^(tot_J - ref_J) prod
-  // 2^tot_M over all later sub-blocks M
+  // -- the first brackets of the pairs of sub-blocks, and prod 2^tot_M over all
+  // later sub-blocks M
   if (tid < NB * DK) {
     const int J = tid / DK, d = tid % DK;
-    float o = sEK[J][d], e[NB], eq[NB];
+    float o = 1.f, e[NB], eq[NB];
 #pragma unroll
     for (int M = 1; M < NB; ++M) e[M] = sE[M][d], eq[M] = sEQ[M][d];
 #pragma unroll
@@ -867,9 +900,9 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 || DK == 32 ? 2 : 1) voi
   auto decay = [&](int J, const float(*tab)[DK]) {  // from block J-1's end to tab's point in block J
 #pragma unroll
     for (int D = 0; D < ND; ++D) {
-      floatx4 f = *reinterpret_cast<const floatx4*>(&tab[J][dim(D)]);
-      if (J > 0) f *= *reinterpret_cast<const floatx4*>(&sEK[J - 1][dim(D)]);
-      acc[D] *= f;
+      // one factor after the other: their product alone may be too small
+      if (J > 0) acc[D] *= *reinterpret_cast<const floatx4*>(&sEK[J - 1][dim(D)]);
+      acc[D] *= *reinterpret_cast<const floatx4*>(&tab[J][dim(D)]);
     }
   };
   for (int J = 0; J < wave; ++J) {
@@ -900,7 +933,12 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 || DK == 32 ? 2 : 1) voi
 #pragma unroll
   for (int ks = 0; ks < NES; ++ks) vs[ks] = v.template terms<NT>(ks);
 #pragma unroll
-  for (int D = 0; D < ND; ++D) acc[D] = zero4;
+  for (int D = 0; D < ND; ++D) {
+    acc[D] = zero4;
+    const floatx4 f = *reinterpret_cast<const floatx4*>(&sEK[wave][dim(D)]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) ck[4 * D + r] *= f[r];  // 2^(tot - s)
+  }
 #pragma unroll
   for (int I = 1; I < NB; ++I) {
     if (I <= wave) continue;

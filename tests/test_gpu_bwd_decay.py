@@ -1,5 +1,6 @@
 """GPU: gradients of the recurrence (gla_bwd) in float where decays change
-sharply: tokens that forget everything beside tokens that keep. Every pair of
+sharply: tokens that forget everything beside tokens that keep, and sub-blocks
+of 16 tokens near the largest decay that shares one reference. Every pair of
 tokens is held to the decay between its own two tokens (tests/pairs.py), however
 deep a reset before them was.
 
@@ -13,9 +14,11 @@ Bounds, in units u = 2^-24 of a pair's term:
     decays, 15 of them, 45 u;
   * its exponent: a token's decay is rounded once, sums of up to 16 of them in a
     tree of four steps: 5 u of the decay between the two tokens, times ln 2: c1 =
-    3.5 u per unit of log2; and 4 u of what the sub-block's mild tokens add up to,
-    at most 2, four times;
-  * a factor below 2^-60 may be lost in float's or bf16's subnormals.
+    3.5 u per unit of log2; where a sub-block has a reference, two tokens'
+    distances to it, at most 66 each, with 4 u each: 4 * 66 * 2 ln 2 = 366 u, and
+    for two sub-blocks the references' distances to the blocks' ends as well: 735 u;
+  * a factor below 2^-60 may be lost in float's or bf16's subnormals: floor 2^-62
+    where only sums in float pass through them, 2^-60 otherwise.
 Plus half a step of float of the value."""
 import numpy as np
 import pytest
@@ -107,6 +110,28 @@ def test_single_pairs_behind_resets(dk, dv):
     compare(x, None, None, 4 + 3 * 9 + 45 + 23 + 12 * 3)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("deep", [-20.0, -55.0, -90.0, -400.0])
+@pytest.mark.parametrize("token", [0, 7, 8])
+def test_single_pairs_behind_one_reset(token, deep):
+    """The same with one reset per sub-block in all dims, of any depth: at its
+    first token (rows of a grid that forget the row before), and beside its
+    middle. Two tokens on one side of it have distances to the reference that
+    hold it both, 366 u, or none."""
+    T = 144
+    say(f"one reset of 2^{deep} at token {token}")
+    x, _, _, r = make(T, 32, 32, 17, carry=False)
+    g = -r.uniform(0.005, 0.06, (T, 32))
+    g[token::16] = deep
+    x[3] = gate(g)
+    for i, at in ((0, 15), (1, 13), (2, 13), (4, 15)):
+        keep = x[i][at::16].copy()
+        x[i][:] = 0
+        x[i][at::16] = keep
+    x[2][:, 1:] = 0
+    x[4][:, 1:] = 0
+    compare(x, None, None, 4 + 3 * 9 + 45 + 23 + 12 * 3 + (366 if deep > -66 and token > 7 else 0))
+
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dk,dv", [(32, 32), (64, 64)])
@@ -119,6 +144,57 @@ def test_dense_values_among_resets(dk, dv):
     x[3] = resets(T, dk, r)
     compare(x, s0, gsf, 4 + 3 * 64 + 3 + 45 + 23 + 12 * 3)
 
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("log2", [-2.0, -5.0, -7.2, -8.24, -8.26, -8.49, -8.51, -9.0, -12.0, -30.0])
+def test_constant_decays(log2):
+    """Every token decays alike, around the largest decay with a reference (66
+    over eight tokens)."""
+    say(f"constant 2^{log2}")
+    x, s0, gsf, r = make(100, 64, 32, 13)
+    x[3] = gate(np.full((100, 64), log2))
+    compare(x, s0, gsf, 4 + 3 * 64 + 2 + 45 + 735 + 12 * 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("deep", [7.9, 8.5, 9.3])
+@pytest.mark.parametrize("between", [0, 1, 2])
+def test_pairs_between_two_strong_stretches(deep, between):
+    """Seven strong tokens at the end of one sub-block but its last, and seven
+    after the first token of a later one: the tokens next to them keep each
+    other through one or two sub-blocks that decay by 2^-14 each, however small
+    the factor between the two blocks' references is."""
+    say(f"strong stretches of 7 x 2^-{deep}, {between} sub-blocks between")
+    T = 80
+    x, s0, gsf, r = make(T, 32, 32, 14)
+    g = np.full((T, 32), -0.01)
+    g[8:15] = -deep
+    g[16:16 * (between + 1)] = -14 / 16
+    i = 16 * (between + 1)
+    g[i + 1:i + 8] = -deep
+    x[3] = gate(g)
+    for a in (x[1], x[2]):
+        a[np.arange(T) != 15] = 0
+    for a in (x[0], x[4]):
+        a[np.arange(T) != i] = 0
+    compare(x, None, None, 4 + 3 * 32 + 45 + 735)
+
+
+@pytest.mark.gpu
+def test_state_behind_a_reset_and_strong_tokens():
+    """A sub-block whose first token decays by 2^-58 and the next seven to 2^-126:
+    what its first query takes from the entering state is 2^-58 of it, and there
+    is no key whose own pair would hide that."""
+    say("state behind a reset and strong tokens")
+    x, s0, gsf, r = make(32, 32, 32, 15)
+    g = np.full((32, 32), -0.01)
+    g[0] = -58.5
+    g[1:8] = -68.0 / 7
+    x[3] = gate(g)
+    x[1][:] = 0
+    x[0][1:] = 0
+    x[4][1:] = 0
+    compare(x, s0, None, 4 + 3 * 32 + 45 + 735, floor=2.0 ** -62)
 
 
 @pytest.mark.gpu
