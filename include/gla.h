@@ -327,9 +327,10 @@ int gla_spatial_swiglu(const void* a, const void* u, const float* weight,
  * them between calls; calls that may overlap in time (two streams, two graphs
  * replayed at once) need a workspace each, and one that holds any of the
  * control words (the first 64 KiB) of a workspace prepared for the forward is
- * refused (GLA_E_ARG). Values are not checked: a NaN or Inf makes the outputs
- * that depend on it non-finite, and in the gradients may reach every token of
- * its 64-token chunk. Results do not change from run to
+ * refused (GLA_E_ARG). Values are not checked: with a NaN or Inf the outputs that
+ * depend on it are what the formulas give in float (a norm's row with an
+ * infinite sum is NaN there and 0 elsewhere), and in the recurrence's gradient
+ * it may reach every token of its 64-token chunk. Results do not change from run to
  * run. An empty problem (no row, token or head) returns GLA_OK and writes
  * nothing. */
 
@@ -392,15 +393,18 @@ int gla_step_gated(const void* q, const void* k, const void* v, const void* gk,
  * x, residual, sum, y: [rows][F] GLA_F16 or GLA_F32; weight: float [F];
  * eps >= 0. sum may be NULL. sum and y may each be x or residual themselves
  * (not both the same one) but must not overlap anything otherwise. A row of
- * zeros with eps 0 gives NaN. */
+ * zeros with eps 0 gives NaN. Squares are summed in float: a GLA_F32 row's
+ * mean(sum^2) + eps must be a normal float (2^-126 to 2^128 / F), here and in
+ * the gradients below. */
 int gla_add_rmsnorm(const void* x, const void* residual, const float* weight,
                     float eps, void* sum, void* y, int64_t rows, int F,
                     int dtype, void* stream);
 
 /* The same with y in 8 bits (OCP e4m3, one byte per value) and a float scale
- * per row, for products in 8 bits: scale = max|y| / 448 (at least 2^-126; 1
- * for a row of zeros), y8 = e4m3(y / scale), to nearest even. y8 and scales
- * must not overlap any other argument. */
+ * per row, for products in 8 bits: scale = max|y| / 448 over the values that
+ * are not NaN (at least 2^-126; 1 where they are all zero), y8 = e4m3(y /
+ * scale), to nearest even, NaN for NaN. y8 and scales must not overlap any other
+ * argument. */
 int gla_add_rmsnorm_q8(const void* x, const void* residual,
                        const float* weight, float eps, void* sum, void* y8,
                        float* scales, int64_t rows, int F, int dtype,
