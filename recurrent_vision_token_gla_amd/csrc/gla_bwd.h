@@ -11,7 +11,8 @@ constexpr int kBwdChunk = 64;  // tokens per chunk of the backward pass
 // Byte offsets inside the workspace of gla_bwd, per (batch, head, chunk): the
 // chunk's forward summary U_n, replaced by the state S_n entering the chunk;
 // its reverse summary R_n, replaced by D_n, the gradient of the state behind
-// the chunk (both float [dk][dv]); and the chunk's decay a_n (float [dk]).
+// the chunk (summaries float [dk][dv]; states too, or for half inputs their two
+// bf16 terms in the same 32 bits); and the chunk's decay a_n (float [dk]).
 struct BwdLayout {
   size_t off_S, off_D, off_a, total;
 };

@@ -28,8 +28,9 @@
 // (x = t0 + t1 [+ t2], each the rounding of what is left): bf16 has float's
 // range, so no operand needs a scale, two terms hold 16 bits (half inputs are
 // exact in them) and three hold float's 24. The products of two operands'
-// terms are added in float, the smallest ones left out. States between chunks
-// are float.
+// terms are added in float, the smallest ones left out. The scans carry states
+// from chunk to chunk in float; what the gradients read of each is float too,
+// or for half inputs its two bf16 terms.
 #include "gla_bwd.h"
 #include "gla_tile.h"
 
@@ -266,8 +267,8 @@ struct Lane {
 // sizes below, while the other gradients, rounded to half, do not change.
 //
 // The memory bounds it: 25,600 half tokens x 16 heads of 64/64 (6,400 chunks,
-// 307 MB read and 206 written by the counters) take 99 us, 5.2 TB/s; the 150
-// chunks of 1,600 tokens x 6 heads 8.7 us, where a workgroup's own 9,000 cycles
+// 307 MB read and 206 written by the counters) take 87 us, 5.9 TB/s; the 150
+// chunks of 1,600 tokens x 6 heads 8.2 us, where a workgroup's own 9,000 cycles
 // of loads, factors and products in turn are what is left to wait for. Three
 // workgroups per CU: LDS holds four, and more registers per lane (up to 128),
 // or all sub-blocks' products before the first decay, changed nothing.
@@ -410,7 +411,7 @@ __device__ __forceinline__ floatx4 step4(float a, floatx4 s, floatx4 u) {
 // W/2 to W chunks' loads in flight (the window is refilled half by half, and
 // whole windows run without a condition, which would wait for every load).
 // The memory bounds it: 64 chains of 100 chunks (211 MB read, 205 written)
-// take 68 us, 6.1 TB/s, part of it from the last-level cache.
+// take 67 us, 6.2 TB/s, part of it from the last-level cache.
 template <int W, bool kTerms>
 __global__ __launch_bounds__(kThreads) void bwd_scan_serial_kernel(
     float* Uws, float* Rws, const float* __restrict__ Aws, const float* s0, const float* gsf,
@@ -466,7 +467,7 @@ __global__ __launch_bounds__(kThreads) void bwd_scan_serial_kernel(
 // load or store of a wave) and windows of 16 segments of up to R chunks, a wave
 // each. A wave folds its segment into (a, u), the 16 are composed from LDS, and
 // the wave replays its segment, still in registers, from the state entering it.
-// 6 chains of 25 or 100 chunks: 5 or 9.7 us. (With the segments on the lanes of
+// 6 chains of 25 or 100 chunks: 4.8 or 9.6 us. (With the segments on the lanes of
 // a row, composed by lane permutations, accesses were 64 bytes wide: 12 us.)
 template <int R, bool kTerms>
 __global__ __launch_bounds__(1024) void bwd_scan_kernel(
@@ -553,21 +554,26 @@ __global__ __launch_bounds__(1024) void bwd_scan_kernel(
 // decays more keeps q 2^s and k 2^(tot-s) instead (2^ref and 2^(tot-ref) are
 // then 1) and takes its own pairs from products of the tokens' decays.
 //
-// A workgroup's own chain of steps bounds it: alone on a CU it takes 22,400
-// cycles, with a second one 25,200, in which each SIMD issues vector
-// instructions for 15,200 (1,906 per wave, half of them factors, splits and
-// scans; 172 matrix products). 25,600 half tokens x 16 heads of 64/64: 180 to
-// 205 us (461 MB read, 205 written: 3.2 to 3.7 TB/s); 1,600 tokens x 6 heads, less
-// than a workgroup per CU: 12 us. Eight waves with queries and keys apart have
-// 128 registers a lane and spilled (1.2 times the time); so did all gradients
-// stored at the end, or D_n's rows read again for <S_n, D_n>.
+// A workgroup's own chain of steps bounds it: alone on a CU it takes 22,100
+// cycles, with a second one 24,400, in which each SIMD issues vector
+// instructions for 15,800 (1,979 per wave, half of them factors, splits and
+// scans; 172 matrix products). 25,600 half tokens x 16 heads of 64/64: 166 us
+// (461 MB read, 205 written: 4.0 TB/s); 1,600 tokens x 6 heads, less than a
+// workgroup per CU: 12 us. Pairs taken from products of decays cost a wave that
+// does so 15 steps of a permutation and five products per dim: the whole pass of
+// those 25,600 tokens takes 321 us without, 332 with a token that forgets
+// everything in every 1,000 and 426 with one in every 23. Eight waves with
+// queries and keys apart have 128 registers a lane and spilled (1.2 times the
+// time); so did all gradients stored at the end, or D_n's rows read again for
+// <S_n, D_n>.
 // ===========================================================================
 constexpr float kMaxSpan = 66.f;
 
 // Two workgroups per CU where their LDS fits (at most 80 KB; a half input's
 // largest takes 79, a float's 80 with 32 key dims): one alone leaves the SIMDs
 // waiting more than half of the time (2 x 4,099 float tokens x 4 heads of 32/64
-// with one or two: 31 or 23 us).
+// with one or two: 31 or 23 us). A float's 64/64 takes 119 KB and has one: a
+// pass of 2 x 3,600 tokens x 8 heads 92 us, of half inputs 53.
 template <int DK, int DV, typename InT, int NT>
 __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 || DK == 32 ? 2 : 1) void bwd_grad_kernel(
     const InT* __restrict__ qp, const InT* __restrict__ kp, const InT* __restrict__ vp,

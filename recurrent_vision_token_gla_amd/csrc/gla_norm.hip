@@ -8,10 +8,12 @@
 // store. Statistics and weight gradients are float; a weight gradient sums
 // over rows in a fixed order (per workgroup, then over the workgroups'
 // partial sums in a second kernel), so it does not change from run to run.
-// Measured, half: norm of 6,400 x 768 9.4 us (4.2 TB/s), with the 8-bit output
-// of 25,600 x 768 27.2 us (5.1 TB/s); gradients of 25,600 x 768 31.1 us (5.1
-// TB/s) and of 409,600 gate rows of 64 44 us (5.9 TB/s), each with 4.7 us of
-// column sums. (A copy of 256 MB runs at 5.4 TB/s.)
+// Measured, half: norm of 6,400 x 768 9.0 us (4.4 TB/s), with the 8-bit output
+// of 25,600 x 768 26.1 us (5.3 TB/s); gradients of 25,600 x 768 30.6 us (5.1
+// TB/s) and of 409,600 gate rows of 64 43 us (6.1 TB/s), with 4.0 and 4.7 us of
+// column sums. (A copy of 256 MB runs at 5.4 TB/s.) Rows of less than 512 columns
+// leave lanes of their wave idle: the norm of 409,600 x 64 takes 83 us (2.5
+// TB/s), of 409,600 x 128 127 us (3.3 TB/s).
 #include "gla_norm.h"
 #include "gla_tile.h"
 
@@ -307,10 +309,13 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
   }
 }
 
-// Workgroups of the two gradient kernels: enough to fill the GPU, few enough
-// that the partial sums stay small beside the rows. At most 512, 1024 or 2048
+// Workgroups of the two gradient kernels: enough to fill the GPU, and few enough
+// that the partial sums stay small beside many rows. At most 512, 1024 or 2048
 // of them: the norm's gradient of 25,600 x 768 half rows 42, 37 or 41 us, the
-// gate's of 409,600 rows of 64 the same within 1 us.
+// gate's of 409,600 rows of 64 the same within 1 us. Few wide rows are not
+// many: up to 1,024 rows of more than 1,024 columns each have a partial sum of
+// their own, more bytes than half rows (1,024 x 4,096 19.7 us, 4,096 x 4,096
+// 27.9).
 constexpr long kMaxParts = 1024;
 // every workgroup takes the same number of steps of `per` rows, but the last
 int even_parts(long rows, long per) {
