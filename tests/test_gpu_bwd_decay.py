@@ -19,7 +19,7 @@ Bounds, in units u = 2^-24 of a pair's term:
     for two sub-blocks the references' distances to the blocks' ends as well: 735 u;
   * a factor below 2^-60 may be lost in float's or bf16's subnormals: floor 2^-62
     where only sums in float pass through them, 2^-60 otherwise.
-Plus half a step of float of the value."""
+Plus half a step of the output's type of the value."""
 import numpy as np
 import pytest
 import torch
@@ -58,8 +58,9 @@ def compare(x, s0, gsf, c0, c1=3.5, floor=2.0 ** -60):
     tol = pair_bounds(x, s0, gsf, c0 * U, c1 * U, floor)
     bad = []
     for name, a, w, t in zip(NAMES, got, want, tol):
+        step = 2.0 ** -11 * np.abs(w) + 2.0 ** -25 if a.dtype == torch.float16 else U * np.abs(w) + 1e-36
         a = a.double().cpu().numpy().reshape(w.shape)
-        worst = float(np.max(np.abs(a - w) / (t + U * np.abs(w) + 1e-36)))
+        worst = float(np.max(np.abs(a - w) / (t + step)))
         say(f"  {name}: {worst:.3f} of the bound")
         bad += [name] if not worst <= 1 else []
     assert not bad
@@ -208,3 +209,29 @@ def test_chunks_between_resets():
     x[3] = gate(g)
     say("resets every 50 tokens")
     compare(x, s0, gsf, 4 + 3 * 64 + 5 + 45 + 23 + 12 * 5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(16))
+def test_random_decays(seed):
+    """Each sub-block of its own kind: mild, constant by dim, from weak to strong,
+    deep tokens in some dims, tokens that forget everything, just at the largest
+    distance with a reference. Half inputs add the 512 u of two-term operands
+    (8 * 2^-18) and half a step of their type."""
+    r = np.random.default_rng(1900 + seed)
+    T, half, carry = int(r.integers(1, 200)), bool(seed % 2), bool(r.integers(2))
+    dk, dv = (int(r.choice([32, 64])) for _ in range(2))
+    say(f"random decays seed={seed} T={T} {dk}/{dv} half={half} carry={carry}")
+    x, s0, gsf, _ = make(T, dk, dv, 1950 + seed, carry=carry)
+    g = np.zeros((T, dk))
+    for m in range(0, T, 16):
+        s = g[m:m + 16].shape
+        g[m:m + 16] = [lambda: -r.uniform(0, 0.1, s), lambda: -r.uniform(0, 9, (1, dk)),
+                       lambda: -np.exp(r.uniform(-8, 5, s)),
+                       lambda: np.where(r.random(s) < 0.1, -r.uniform(20, 70), -0.02),
+                       lambda: np.where(r.random((s[0], 1)) < 0.1, -8e4, -0.02),
+                       lambda: -r.uniform(6, 9.4)][int(r.integers(6))]()
+    x[3] = gate(g)
+    if half:
+        x = [a.astype(np.float16) for a in x]
+    compare(x, s0, gsf, 4 + 3 * 64 + 45 + 735 + 12 * 4 + (512 if half else 0))
