@@ -199,12 +199,6 @@ __device__ __forceinline__ void from_middle16(const float (&x)[N], float (&s)[N]
   for (int e = 0; e < N; ++e) s[e] -= row_after16(lo[e]);
 }
 
-// Lane n of each row of 16, on all of the row's lanes.
-template <int LANE>
-__device__ __forceinline__ float row_lane(float x) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + LANE, 0xf, 0xf, true));
-}
-
 // LDS tiles have rows of W 16-bit values without padding; the 16-byte chunk c
 // of a row lies at chunk c ^ swz(row). The equal chunks of the eight rows that
 // an operand read along rows touches together, and the four rows' 8-byte
@@ -847,7 +841,9 @@ __global__ __launch_bounds__(kThreads, sizeof(InT) == 2 || DK == 32 ? 2 : 1) voi
 #pragma unroll
         for (int r = 0; r < 4; ++r) an[r] += 4 * lq + r == lr + x ? aij : 0.f;
         if (++x == 16) break;
-        const float pij = component(pt, lr - x), pji = component(pn, lr + x);  // P[lr][lr-x], P[lr+x][lr]
+        float pij = component(pt, lr - x), pji = component(pn, lr + x);  // P[lr][lr-x], P[lr+x][lr]
+        pij = x <= lr ? pij : 0.f;
+        pji = x < 16 - lr ? pji : 0.f;
         aij = 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
