@@ -327,12 +327,12 @@ int gla_spatial_swiglu(const void* a, const void* u, const float* weight,
  * them between calls; calls that may overlap in time (two streams, two graphs
  * replayed at once) need a workspace each, and one that holds any of the
  * control words (the first 64 KiB) of a workspace prepared for the forward is
- * refused (GLA_E_ARG). Values are not checked: with a NaN or Inf the outputs that
- * depend on it are what the formulas give in float (a norm's row with an
+ * refused (GLA_E_ARG). Values are not checked: with a NaN or Inf the outputs
+ * that depend on it are what the formulas give in float (a norm's row with an
  * infinite sum is NaN there and 0 elsewhere), and in the recurrence's gradient
- * it may reach every token of its 64-token chunk. Results do not change from run to
- * run. An empty problem (no row, token or head) returns GLA_OK and writes
- * nothing. */
+ * it may reach every token of its 64-token chunk. Results do not change from
+ * run to run. An empty problem (no row, token or head) returns GLA_OK and
+ * writes nothing. */
 
 /* Bytes of workspace gla_bwd needs (0 for an empty or unsupported problem):
  * two float states and a decay row per (batch, head, 64-token chunk). */
@@ -350,10 +350,12 @@ size_t gla_bwd_workspace_bytes(int B, int H, int grid_h, int grid_w, int dk,
  *   s0, gs_final, gs0: float [B][H][dk][dv], each may be NULL (gs0 NULL: not
  *   returned). gs0 may be gs_final; no other output may overlap an input,
  *   another output or the workspace (GLA_E_ARG).
- * Sums and states are float. Products run on the matrix cores over operands
- * split into bf16 terms: 16 bits for GLA_F16, 24 for GLA_F32 (whose q, k, v
- * are not rounded to half here; they and go must not exceed 65504 in
- * magnitude). gk <= 0; a token's decay below 2^-160 counts as 2^-160, and a
+ * Sums are float, and so are states on their way from chunk to chunk. Products
+ * run on the matrix cores over operands (states among them) split into bf16
+ * terms: 16 bits for GLA_F16, 24 for GLA_F32 (whose q, k, v are not rounded to
+ * half here; they and go must not exceed 65504 in magnitude). ggk is taken from
+ * differences of sums over its 64-token chunk, and is off by that share of the
+ * chunk's terms, not of its own. gk <= 0; a token's decay below 2^-160 counts as 2^-160, and a
  * product of decays below 2^-60 may count as zero. Beyond the rounding of its
  * exponent (2^-22 of its log2), the decay between two tokens is off by at most
  * 2^-14 of itself, however much the tokens before them forgot. */
