@@ -235,3 +235,30 @@ def test_random_decays(seed):
     if half:
         x = [a.astype(np.float16) for a in x]
     compare(x, s0, gsf, 4 + 3 * 64 + 45 + 735 + 12 * 4 + (512 if half else 0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("reset", [False, True])
+def test_nan_reaches_only_the_pairs_that_have_it(reset):
+    """A NaN in one token's v, and in another's go, inside one sub-block, with and
+    without a token that forgets everything: queries before the first and keys
+    behind the second do not meet them."""
+    say(f"NaN inside a sub-block, reset={reset}")
+    x, _, _, r = make(16, 32, 32, 18, carry=False)
+    g = -r.uniform(0.005, 0.06, (16, 32))
+    if reset:
+        g[7] = -400.0
+    x[3] = gate(g)
+    dev = to_dev(*[a.reshape(1, 16, 1, -1) for a in x])
+    clean = gla.bwd(*dev, 1, 16, 0)
+    v, go = dev[2].clone(), dev[4].clone()
+    v[0, 10, 0, 3] = go[0, 4, 0, 5] = float("nan")
+    got_v = gla.bwd(dev[0], dev[1], v, dev[3], dev[4], 1, 16, 0)
+    got_go = gla.bwd(*dev[:4], go, 1, 16, 0)
+    torch.cuda.synchronize()
+    keep = [t for t in range(16) if t != 10]
+    assert torch.equal(got_v[0][0, :10], clean[0][0, :10]) and bool(got_v[0][0, 10:].isnan().all())
+    assert torch.equal(got_v[1][0, keep], clean[1][0, keep]) and torch.equal(got_v[2], clean[2])
+    assert torch.equal(got_go[1][0, 5:], clean[1][0, 5:]) and bool(got_go[1][0, :5].isnan().all())
+    keep = [t for t in range(16) if t != 4]
+    assert torch.equal(got_go[0][0, keep], clean[0][0, keep])
