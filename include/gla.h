@@ -444,6 +444,125 @@ int gla_gate_bwd(const void* o, const void* gate, const float* norm_weight,
                  float* gnorm_weight, int64_t rows, int dv, int dtype,
                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- the products and norms between a block's mixers ------------------------
+ *
+ * The calls below follow the rules of the gradients above (memory, checks,
+ * streams, capture, workspaces, NaN and Inf, results that do not change from
+ * run to run). Matrices are row-major and contiguous: x [rows][K], a weight
+ * [N][K] in the input dtype (as a linear layer keeps it), y [rows][N]. K and N
+ * are multiples of 8, at most 65536 (GLA_E_UNSUPPORTED otherwise, and for K 0
+ * where there are outputs); any number of rows up to 2^31. Sums are float, over
+ * half operands or, for GLA_F32, over whole float ones; every output is rounded
+ * once. Any finite values: an output beyond the half range is +-Inf in GLA_F16.
+ * An empty problem (no row or no output) returns GLA_OK and writes nothing.
+ *
+ * Activations, of z in float: silu z / (1 + exp(-z)), gelu z Phi(z) with Phi
+ * the normal distribution's integral (not the tanh form), logsigmoid
+ * -log(1 + exp(-z)). */
+enum { GLA_ACT_NONE = 0, GLA_ACT_SILU = 1, GLA_ACT_GELU = 2, GLA_ACT_LOGSIGMOID = 3 };
+
+/* A linear product with its epilogue, for the projections of a block (q, k, v;
+ * the decay with GLA_ACT_LOGSIGMOID and alpha 1/16; the way back into the
+ * residual stream):
+ *   y = alpha * act(x W^T + bias) + residual.
+ * bias: float [N], 16-byte aligned, or NULL; residual: [rows][N] in the input
+ * dtype or NULL; pre: [rows][N] takes x W^T + bias for the gradient, or NULL.
+ * y may be residual itself; nothing else may overlap. Up to 64 rows (the new
+ * tokens of as many sequences) run in a form of their own, which reads the
+ * weight once. */
+int gla_linear(const void* x, const void* weight, const float* bias,
+               const void* residual, void* pre, void* y, int64_t rows, int K,
+               int N, int act, float alpha, int dtype, void* stream);
+
+/* Bytes of workspace gla_linear_bwd needs (0 for an empty or unsupported
+ * problem). */
+size_t gla_linear_bwd_workspace_bytes(int64_t rows, int K, int N, int act,
+                                      int dtype);
+
+/* Gradient of gla_linear from gy = dL/dy (which is the residual's gradient as
+ * it stands) and the kept pre (unused for GLA_ACT_NONE): with gp = gy act'(pre),
+ *   gx = alpha gp W  ([rows][K]),   gweight = alpha gp^T x  ([N][K]),
+ *   gbias = alpha sum over rows of gp  (float [N], 16-byte aligned);
+ * gx and gweight in the input dtype. Each may be NULL: not wanted (then x, or
+ * weight, is not looked at). gp is rounded to the input dtype for the products,
+ * not for gbias. No output may overlap an input, another output or the
+ * workspace. */
+int gla_linear_bwd(const void* x, const void* weight, const void* pre,
+                   const void* gy, void* gx, void* gweight, float* gbias,
+                   int64_t rows, int K, int N, int act, float alpha, int dtype,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gated feed-forward product (a channel mixer without the spatial filter),
+ * both projections, the activation and the product in one kernel:
+ *   h = act(x Wg^T) * (x Wu^T),   Wg, Wu [F][K],   h [rows][F].
+ * gate and up take x Wg^T and x Wu^T for the gradient; each may be NULL. */
+int gla_gated_ff(const void* x, const void* gate_weight, const void* up_weight,
+                 void* gate, void* up, void* h, int64_t rows, int K, int F,
+                 int act, int dtype, void* stream);
+
+/* Bytes of workspace gla_gated_ff_bwd needs (0 for an empty or unsupported
+ * problem). */
+size_t gla_gated_ff_bwd_workspace_bytes(int64_t rows, int K, int F, int dtype);
+
+/* Gradient of gla_gated_ff from gh = dL/dh and the kept a = gate, u = up: with
+ * ga = gh u act'(a) and gu = gh act(a),
+ *   gx = ga Wg + gu Wu,   ggate_weight = ga^T x,   gup_weight = gu^T x,
+ * all in the input dtype; ga and gu are rounded to it for the products. gx may
+ * be NULL, and both weights' gradients may be (not one of them: GLA_E_ARG). No
+ * output may overlap an input, another output or the workspace. */
+int gla_gated_ff_bwd(const void* x, const void* gate_weight,
+                     const void* up_weight, const void* gate, const void* up,
+                     const void* gh, void* gx, void* ggate_weight,
+                     void* gup_weight, int64_t rows, int K, int F, int act,
+                     int dtype, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* What stands between two blocks that are normed on both sides: the norm behind
+ * the one block, its gate and residual scale, the addition to the stream and
+ * the norm before the next, for `rows` rows of F values (F as in
+ * gla_add_rmsnorm):
+ *   p   = x / sqrt(mean(x^2) + eps) * post_weight   (x where post_weight is NULL),
+ *   sum = residual + scale * gate * p   (rounded to the input dtype),
+ *   y   = sum / sqrt(mean(sum^2) + eps) * weight.
+ * gate: [groups][F] in the input dtype, one row for each of `groups` equal runs
+ * of rows (groups = batch size: one for each image; groups = rows: one for each
+ * token; groups must divide rows), or NULL (groups is not looked at); scale,
+ * post_weight: float [F] or NULL. sum may be NULL. sum and y may each be x or
+ * residual themselves (not both the same one) but must not overlap anything
+ * otherwise. Squares are summed in float (see gla_add_rmsnorm). */
+int gla_gated_add_rmsnorm(const void* x, const void* residual,
+                          const float* post_weight, const void* gate,
+                          int64_t groups, const float* scale,
+                          const float* weight, float eps, void* sum, void* y,
+                          int64_t rows, int F, int dtype, void* stream);
+
+/* Bytes of workspace gla_gated_add_rmsnorm_bwd needs (0 for an empty or
+ * unsupported problem; groups 1 without a gate). */
+size_t gla_gated_add_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t groups,
+                                                 int F);
+
+/* Gradient of gla_gated_add_rmsnorm from x and its `sum`, gy = dL/dy and gsum,
+ * what reaches the sum itself (NULL for none). With n = x / rms(x) (x without
+ * post_weight), m = sum / rms(sum), f = scale * gate * post_weight:
+ *   gresidual = gS = gsum + (gy w - m mean(gy w m)) / rms(sum),
+ *   gx = (gS f - n mean(gS f n)) / rms(x)   (gS f without post_weight),
+ *   gweight = sum over rows of gy m,   gpost_weight = sum of gS scale gate n,
+ *   gscale = sum of gS gate p,   ggate = sum of gS scale p over a group's rows.
+ * gx, gresidual: [rows][F], ggate: [groups][F], in the input dtype; the others
+ * float [F], 16-byte aligned. ggate, gpost_weight and gscale may be NULL (not
+ * wanted) and must be where there is no gate, post_weight or scale (GLA_E_ARG).
+ * gx and gresidual may each be x, sum, gy or gsum themselves (not both the same
+ * one); nothing else may overlap. */
+int gla_gated_add_rmsnorm_bwd(const void* x, const void* sum,
+                              const float* post_weight, const void* gate,
+                              int64_t groups, const float* scale,
+                              const float* weight, float eps, const void* gy,
+                              const void* gsum, void* gx, void* gresidual,
+                              float* gpost_weight, void* ggate, float* gscale,
+                              float* gweight, int64_t rows, int F, int dtype,
+                              void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* Static text for a status code; never NULL. */
 const char* gla_status_string(int status);
 

@@ -17,6 +17,8 @@ Contents:
                  value branch times SiLU of the gate branch)
   backward    -- the recurrence's and the gate's gradients, the residual norm
                  with its gradient, and the values of 8-bit e4m3
+  products    -- linear and gated products with their activations, the norms
+                 around a block, and the gradients of all of them
 
 Every function here is pinned by the CPU tests (tests/test_oracle_*.py)
 against hand-derived fixtures, a brute-force closed form, textbook special
@@ -28,9 +30,12 @@ from .chunkwise import chunkwise
 from .epilogue import rmsnorm_gate, silu, spatial_swiglu
 from .backward import (add_rmsnorm, add_rmsnorm_backward, e4m3_values, gla_backward,
                        recurrence_backward, rmsnorm_gate_backward)
+from .products import (act, act_slope, gated_add_rmsnorm, gated_add_rmsnorm_backward, gated_ff,
+                       gated_ff_backward, linear, linear_backward)
 
 __all__ = ["L2R", "R2L", "T2B", "B2T", "scan_order", "to_scan", "to_raster",
            "gla_forward", "recurrence_c", "recurrence_numpy", "oracle_threads",
            "chunkwise", "rmsnorm_gate", "silu", "spatial_swiglu", "gla_backward",
            "recurrence_backward", "rmsnorm_gate_backward", "add_rmsnorm", "add_rmsnorm_backward",
-           "e4m3_values"]
+           "e4m3_values", "act", "act_slope", "linear", "linear_backward", "gated_ff",
+           "gated_ff_backward", "gated_add_rmsnorm", "gated_add_rmsnorm_backward"]

@@ -1,5 +1,5 @@
 // Argument checks and the error detail shared by the C-ABI entry points
-// (gla_api.hip, gla_train_api.hip).
+// (gla_api.hip, gla_train_api.hip, gla_block_api.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -9,6 +9,7 @@
 
 #include "gla.h"
 #include "gla_launch.h"
+#include "gla_norm.h"
 
 namespace gla {
 namespace api {
@@ -71,6 +72,44 @@ bool holds_control_words(const void* p, size_t n);
     const int rc_ = (__VA_ARGS__); \
     if (rc_ != GLA_OK) return rc_; \
   } while (0)
+
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+// GLA_E_ARG if an output overlaps an input or another output (null ranges are
+// left out).
+template <int NO, int NI>
+int check_disjoint(const Range (&out)[NO], const Range (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    if (!out[i].p) continue;
+    for (int j = 0; j < i; ++j)
+      if (out[j].p && overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return GLA_E_ARG;
+    for (int j = 0; j < NI; ++j)
+      if (in[j].p && overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return GLA_E_ARG;
+  }
+  return GLA_OK;
+}
+
+inline int check_optional(const void* t) { return t ? check_tensor(t) : GLA_OK; }
+
+// Memory that holds the control words of a workspace prepared for the forward
+// is refused: the single pass relies on them, and they would be overwritten.
+inline int check_workspace(const void* ws, size_t have, size_t need) {
+  if (!ws || !aligned(ws, 256) || holds_control_words(ws, have < need ? have : need)) return GLA_E_ARG;
+  return have < need ? GLA_E_WORKSPACE : GLA_OK;
+}
+
+inline size_t elem(int dtype) { return dtype == GLA_F16 ? 2 : 4; }
+
+// Rows and width of the norm entry points.
+inline int check_rows(int64_t rows, int F, int dtype) {
+  if (rows < 0 || F < 0) return GLA_E_ARG;
+  if (dtype != GLA_F16 && dtype != GLA_F32) return GLA_E_ARG;
+  if (F % 8 != 0 || F > gla::kNormMaxF || rows > (1LL << 31)) return GLA_E_UNSUPPORTED;
+  return GLA_OK;
+}
 
 }  // namespace api
 }  // namespace gla

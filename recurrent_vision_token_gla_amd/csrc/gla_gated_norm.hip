@@ -1,0 +1,424 @@
+// Norms after and before a block with its gate and residual scale,
+//   p = x / sqrt(mean(x^2) + eps) * post,  s = residual + scale gate p,
+//   y = s / sqrt(mean(s^2) + eps) * w,
+// and their gradient. A few flops per byte: memory bounds them. A team of TPR
+// threads holds a row in registers, VPT groups of eight columns a thread, from
+// its loads to its stores, and walks rows, so that the weights are read once.
+// Statistics, weight gradients and the gate's gradient are summed in float in a
+// fixed order.
+#include "gla_gated_norm.h"
+
+#include "gla_rows.h"
+#include "gla_tile.h"
+
+namespace gla {
+namespace norm {
+
+// Sums of N values over the TPR threads of a team (TPR > 64: the workgroup).
+template <int TPR, int N>
+__device__ __forceinline__ void team_sums(float (&x)[N], float* lds) {
+  constexpr int kIn = TPR < 64 ? TPR : 64;
+#pragma unroll
+  for (int m = kIn / 2; m >= 1; m >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) x[n] += __shfl_xor(x[n], m);
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    __syncthreads();  // earlier readers of lds are done
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) lds[n * W + (threadIdx.x >> 6)] = x[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      x[n] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) x[n] += lds[n * W + w];
+    }
+  }
+}
+
+// scale * post of a thread's columns (1 where neither is)
+__device__ __forceinline__ void factor8(const float* post, const float* scale, int col, float (&f)[8]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) f[c] = 1.f;
+  if (post) tile::load_f8(post + col, f);
+  if (scale) {
+    float x[8];
+    tile::load_f8(scale + col, x);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) f[c] *= x[c];
+  }
+}
+
+template <int TPR>
+constexpr int kTeamThreads = TPR > 256 ? TPR : 256;
+
+// sum and y may be x or residual: a thread has read its columns when it writes them.
+template <int TPR, int VPT, typename T>
+__global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_kernel(
+    const T* xp, const T* rp, const float* __restrict__ post, const T* __restrict__ gate,
+    const float* __restrict__ scale, const float* __restrict__ wp, float eps, T* sp, T* yp, long rows,
+    long per, int F) {
+  constexpr int RPB = kTeamThreads<TPR> / TPR;
+  __shared__ float lds[TPR > 64 ? TPR / 64 : 1];
+  const int t = threadIdx.x % TPR, nv = F / 8;
+  const float over = 1.f / (float)F;
+  float f[VPT][8], w[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int u = t + TPR * i;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) f[i][c] = w[i][c] = 0.f;
+    if (u < nv) {
+      factor8(post, scale, 8 * u, f[i]);
+      tile::load_f8(wp + 8 * u, w[i]);
+    }
+  }
+  for (long row = (long)blockIdx.x * RPB + threadIdx.x / TPR; row < rows; row += (long)gridDim.x * RPB) {
+    float x[VPT][8], r[VPT][8], g[VPT][8], ss[1] = {0.f};
+    const long grow = gate ? row / per : 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int u = t + TPR * i;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) x[i][c] = r[i][c] = 0.f, g[i][c] = 1.f;
+      if (u < nv) {
+        load8(xp + row * F + 8 * u, x[i]);
+        load8(rp + row * F + 8 * u, r[i]);
+        if (gate) load8(gate + grow * F + 8 * u, g[i]);
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) ss[0] = fmaf(x[i][c], x[i][c], ss[0]);
+    }
+    float rx = 1.f;
+    if (post) {
+      team_sums<TPR>(ss, lds);
+      rx = __builtin_amdgcn_rsqf(fmaf(ss[0], over, eps));
+    }
+    ss[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        x[i][c] = round_to(fmaf(x[i][c] * rx, f[i][c] * g[i][c], r[i][c]), T());
+        ss[0] = fmaf(x[i][c], x[i][c], ss[0]);
+      }
+    team_sums<TPR>(ss, lds);
+    const float rs = __builtin_amdgcn_rsqf(fmaf(ss[0], over, eps));
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int u = t + TPR * i;
+      if (u < nv) {
+        const long at = row * F + 8 * u;
+        if (sp) store8(sp + at, x[i]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[i][c] *= rs * w[i][c];
+        store8(yp + at, x[i]);
+      }
+    }
+  }
+}
+
+// Gradient. With n = x rx and m = s rs (rx, rs the reciprocal roots; n = x without
+// post), f = scale post gate:
+//   gS = gsum + rs (gy w - m mean(gy w m)),     gresidual = gS,
+//   gx = rx (gS f - n mean(gS f n))             (gS f without post),
+//   gw = sum gy m,   Q = sum over a group's rows of gS n:
+//   ggate = scale post Q,  gpost = scale sum gate Q,  gscale = post sum gate Q.
+// mean(gS f n) is put together from sums that do not wait for gS, so that all
+// six sums of a row go over the team at once:
+//   sum gS f n = rx (sum gsum f x + rs sum gy w f x - rs^2 mean(gy w m) sum f x s).
+// kOwn: a team takes whole groups and writes ggate itself; part[workgroup] holds
+// gw and sum gate Q. Else a workgroup takes rows of one chunk of a group;
+// part[group][chunk] holds gw and Q.
+template <int TPR, int VPT, typename T, bool kOwn>
+__global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_bwd_kernel(
+    const T* xp, const T* sp, const T* gyp, const T* gsp, const float* __restrict__ post,
+    const T* __restrict__ gate, const float* __restrict__ scale, const float* __restrict__ wp, float eps,
+    T* gxp, T* grp, T* __restrict__ ggp, float* __restrict__ part, long groups, long per, int chunks, int F) {
+  constexpr int RPB = kTeamThreads<TPR> / TPR, NS = 6;
+  __shared__ float lds[TPR > 64 ? NS * TPR / 64 : 1];
+  __shared__ float join[RPB > 1 ? kTeamThreads<TPR> * VPT * 8 : 1];
+  const int t = threadIdx.x % TPR, team = threadIdx.x / TPR, nv = F / 8;
+  const float over = 1.f / (float)F;
+  float f[VPT][8], w[VPT][8], gw[VPT][8], q[VPT][8], p[kOwn ? VPT : 1][8], g[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int u = t + TPR * i;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) f[i][c] = w[i][c] = gw[i][c] = q[i][c] = p[kOwn ? i : 0][c] = 0.f, g[i][c] = 1.f;
+    if (u < nv) {
+      factor8(post, scale, 8 * u, f[i]);
+      tile::load_f8(wp + 8 * u, w[i]);
+    }
+  }
+  auto load_gate = [&](long group) {
+    if (!gate) return;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (t + TPR * i < nv) load8(gate + group * F + 8 * (t + TPR * i), g[i]);
+  };
+  auto do_row = [&](long row) {
+    float x[VPT][8], s[VPT][8], gy[VPT][8], gs[VPT][8], z[NS] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int u = t + TPR * i;
+      const long at = row * F + 8 * u;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) x[i][c] = s[i][c] = gy[i][c] = gs[i][c] = 0.f;
+      if (u < nv) {
+        load8(xp + at, x[i]);
+        load8(sp + at, s[i]);
+        load8(gyp + at, gy[i]);
+        if (gsp) load8(gsp + at, gs[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float fx = f[i][c] * g[i][c] * x[i][c], gm = gy[i][c] * w[i][c];
+        z[0] = fmaf(s[i][c], s[i][c], z[0]);
+        z[1] = fmaf(x[i][c], x[i][c], z[1]);
+        z[2] = fmaf(gm, s[i][c], z[2]);
+        z[3] = fmaf(gs[i][c], fx, z[3]);
+        z[4] = fmaf(gm, fx, z[4]);
+        z[5] = fmaf(fx, s[i][c], z[5]);
+      }
+    team_sums<TPR>(z, lds);
+    const float rs = __builtin_amdgcn_rsqf(fmaf(z[0], over, eps));
+    const float rx = post ? __builtin_amdgcn_rsqf(fmaf(z[1], over, eps)) : 1.f;
+    const float dot = z[2] * rs * over;  // mean(gy w m)
+    const float mean = post ? rx * over * fmaf(rs, fmaf(-rs * dot, z[5], z[4]), z[3]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int u = t + TPR * i;
+      const long at = row * F + 8 * u;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float m = s[i][c] * rs, n = x[i][c] * rx;
+        gw[i][c] = fmaf(gy[i][c], m, gw[i][c]);
+        gs[i][c] = fmaf(rs, fmaf(gy[i][c], w[i][c], -m * dot), gs[i][c]);
+        q[i][c] = fmaf(gs[i][c], n, q[i][c]);
+        x[i][c] = rx * fmaf(gs[i][c], f[i][c] * g[i][c], -n * mean);
+      }
+      if (u < nv) {
+        store8(grp + at, gs[i]);
+        store8(gxp + at, x[i]);
+      }
+    }
+  };
+  if constexpr (kOwn) {
+    // every team of the workgroup takes as many steps (their sums meet at barriers)
+    for (long g0 = (long)blockIdx.x * RPB; g0 < groups; g0 += (long)gridDim.x * RPB) {
+      const long group = g0 + team;
+      if (group >= groups) break;  // whole teams; with more than a wave a team there is one
+      load_gate(group);
+      for (long r = 0; r < per; ++r) do_row(group * per + r);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        float y[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          y[c] = f[i][c] * q[i][c];
+          p[i][c] = fmaf(g[i][c], q[i][c], p[i][c]);
+          q[i][c] = 0.f;
+        }
+        if (ggp && t + TPR * i < nv) store8(ggp + group * F + 8 * (t + TPR * i), y);
+      }
+    }
+  } else {
+    const long group = blockIdx.x / chunks;
+    const int chunk = blockIdx.x % chunks;
+    load_gate(group);
+    for (long r = (long)chunk * RPB + team; r < per; r += (long)chunks * RPB) do_row(group * per + r);
+  }
+  float* out = part + 2L * blockIdx.x * F;
+  auto write = [&](float* to, float (&a)[VPT][8]) {
+    if constexpr (RPB > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) join[(team * VPT + i) * (TPR * 8) + 8 * t + c] = a[i][c];
+      __syncthreads();
+      for (int col = threadIdx.x; col < F; col += kTeamThreads<TPR>) {
+        float y = 0.f;
+        for (int r = 0; r < RPB; ++r) y += join[(r * VPT + col / (TPR * 8)) * (TPR * 8) + col % (TPR * 8)];
+        to[col] = y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (t + TPR * i < nv) tile::store_f8(to + 8 * (t + TPR * i), a[i]);
+    }
+  };
+  write(out, gw);
+  if constexpr (kOwn) write(out + F, p);
+  else write(out + F, q);
+}
+
+// Sums of the pairs of rows part[2 (blockIdx.y count + 0 .. count - 1)], gw and Q
+// (or sum gate Q): 16 columns and 64 groups of rows per workgroup. gate: the
+// sums are Q, of which ggate (if wanted) and gate Q are made. kLast: into the
+// weights' gradients. Else into pair blockIdx.y of `next`.
+template <typename T, bool kLast>
+__global__ __launch_bounds__(1024) void gated_norm_join_kernel(
+    const float* __restrict__ part, float* __restrict__ next, int count, int F, const float* __restrict__ post,
+    const T* __restrict__ gate, const float* __restrict__ scale, T* __restrict__ ggp, float* __restrict__ gpost,
+    float* __restrict__ gscale, float* __restrict__ gweight) {
+  constexpr int W = 8;
+  __shared__ float s[2][64][17];
+  const int c = threadIdx.x & 15, g = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
+  const long group = blockIdx.y;
+  part += 2 * group * count * F;
+  float y[2] = {0.f, 0.f};
+  if (col < F) {
+    for (int p = g; p < count; p += 64 * W) {
+      float x[2][W];
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[h][i] = p + 64 * i < count ? part[(2L * (p + 64 * i) + h) * F + col] : 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) y[0] += x[0][i], y[1] += x[1][i];
+    }
+  }
+  s[0][g][c] = y[0], s[1][g][c] = y[1];
+  __syncthreads();
+  if (g < 8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      y[h] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[h] += s[h][g + 8 * i][c];
+      s[h][g][c] = y[h];  // no other thread reads row g
+    }
+  }
+  __syncthreads();
+  if (g != 0 || col >= F) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    y[h] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[h] += s[h][i][c];
+  }
+  const float a = post ? post[col] : 1.f, b = scale ? scale[col] : 1.f;
+  if (gate) {
+    if (ggp) ggp[group * F + col] = (T)(a * b * y[1]);
+    y[1] *= (float)gate[group * F + col];
+  }
+  if constexpr (kLast) {
+    gweight[col] = y[0];
+    if (gpost) gpost[col] = b * y[1];
+    if (gscale) gscale[col] = a * y[1];
+  } else {
+    next[2 * group * F + col] = y[0];
+    next[(2 * group + 1) * F + col] = y[1];
+  }
+}
+
+// How the gradient's rows are shared out: teams that own groups once there are
+// enough of them, else chunks of each group's rows.
+constexpr long kMaxParts2 = 1024;
+int teams(int F) { return F <= 64 ? 32 : F <= 256 ? 16 : F <= 512 ? 8 : F <= 1024 ? 4 : 1; }
+struct GroupPlan {
+  bool own;
+  int chunks;   // of each group
+  long blocks;  // workgroups of the first kernel
+};
+GroupPlan group_plan(long rows, long groups, int F) {
+  GroupPlan p;
+  const long rpb = teams(F), per = rows / groups;
+  p.own = groups >= kMaxParts2;
+  p.chunks = 1;
+  if (p.own) {
+    const long steps = (groups + rpb - 1) / rpb, each = (steps + kMaxParts2 - 1) / kMaxParts2;
+    p.blocks = (steps + each - 1) / each;
+  } else {
+    const long steps = (per + rpb - 1) / rpb;
+    long most = kMaxParts2 / groups;
+    if (most < 1) most = 1;
+    const long each = (steps + most - 1) / most;
+    p.chunks = (int)((steps + each - 1) / each);
+    p.blocks = groups * p.chunks;
+  }
+  return p;
+}
+
+template <int TPR, int VPT, typename T>
+hipError_t gated_norm_t(const GatedNormArgs& a, hipStream_t s) {
+  constexpr long rpb = kTeamThreads<TPR> / TPR;
+  const long steps = (a.rows + rpb - 1) / rpb, blocks = steps < 4096 ? steps : 4096;
+  hipLaunchKernelGGL((gated_norm_kernel<TPR, VPT, T>), dim3((unsigned)blocks), dim3(kTeamThreads<TPR>), 0, s,
+                     static_cast<const T*>(a.x), static_cast<const T*>(a.residual), a.post,
+                     static_cast<const T*>(a.gate), a.scale, a.weight, a.eps, static_cast<T*>(a.sum),
+                     static_cast<T*>(a.y), a.rows, a.rows / a.groups, a.F);
+  return hipGetLastError();
+}
+
+template <int TPR, int VPT, typename T>
+hipError_t gated_norm_bwd_t(const GatedNormBwdArgs& a, float* ws, hipStream_t s) {
+  const GroupPlan p = group_plan(a.rows, a.groups, a.F);
+  const long per = a.rows / a.groups;
+  auto kernel = p.own ? gated_norm_bwd_kernel<TPR, VPT, T, true> : gated_norm_bwd_kernel<TPR, VPT, T, false>;
+  const T* gate = static_cast<const T*>(a.gate);
+  T* ggate = static_cast<T*>(a.ggate);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)p.blocks), dim3(kTeamThreads<TPR>), 0, s,
+                     static_cast<const T*>(a.x), static_cast<const T*>(a.sum), static_cast<const T*>(a.gy),
+                     static_cast<const T*>(a.gsum), a.post, gate, a.scale, a.weight, a.eps,
+                     static_cast<T*>(a.gx), static_cast<T*>(a.gresidual), p.own ? ggate : nullptr, ws,
+                     a.groups, per, p.chunks, a.F);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const unsigned cols = (unsigned)((a.F + 15) / 16);
+  const float* part = ws;
+  int count = (int)p.blocks;
+  bool joined = p.own;  // the gate is in the sums
+  if (!p.own && a.groups > 1) {
+    float* next = ws + 2 * p.blocks * a.F;
+    hipLaunchKernelGGL((gated_norm_join_kernel<T, false>), dim3(cols, (unsigned)a.groups), dim3(1024), 0, s,
+                       ws, next, p.chunks, a.F, a.post, gate, a.scale, ggate, nullptr, nullptr, nullptr);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    part = next, count = (int)a.groups, joined = true;
+  }
+  hipLaunchKernelGGL((gated_norm_join_kernel<T, true>), dim3(cols), dim3(1024), 0, s, part, nullptr, count,
+                     a.F, a.post, joined ? nullptr : gate, a.scale, ggate, a.gpost, a.gscale, a.gweight);
+  return hipGetLastError();
+}
+
+#define GLA_TEAM_DISPATCH(FN, T, ...)                    \
+  do {                                                   \
+    const int F_ = a.F;                                  \
+    if (F_ <= 64) return FN<8, 1, T>(__VA_ARGS__);       \
+    if (F_ <= 128) return FN<16, 1, T>(__VA_ARGS__);     \
+    if (F_ <= 256) return FN<16, 2, T>(__VA_ARGS__);     \
+    if (F_ <= 512) return FN<32, 2, T>(__VA_ARGS__);     \
+    if (F_ <= 1024) return FN<64, 2, T>(__VA_ARGS__);    \
+    if (F_ <= 4096) return FN<256, 2, T>(__VA_ARGS__);   \
+    if (F_ <= 8192) return FN<512, 2, T>(__VA_ARGS__);   \
+    return FN<1024, 2, T>(__VA_ARGS__);                  \
+  } while (0)
+
+}  // namespace norm
+
+hipError_t launch_gated_norm(const GatedNormArgs& a, hipStream_t s) {
+  if (a.dtype == 0) GLA_TEAM_DISPATCH(norm::gated_norm_t, half_t, a, s);
+  GLA_TEAM_DISPATCH(norm::gated_norm_t, float, a, s);
+}
+
+size_t gated_norm_bwd_workspace(long rows, long groups, int F) {
+  const norm::GroupPlan p = norm::group_plan(rows, groups, F);
+  const long joined = !p.own && groups > 1 ? groups : 0;
+  return (size_t)2 * (p.blocks + joined) * F * sizeof(float);
+}
+
+hipError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, float* ws, hipStream_t s) {
+  if (a.dtype == 0) GLA_TEAM_DISPATCH(norm::gated_norm_bwd_t, half_t, a, ws, s);
+  GLA_TEAM_DISPATCH(norm::gated_norm_bwd_t, float, a, ws, s);
+}
+
+}  // namespace gla

@@ -1,0 +1,423 @@
+// Tiles of a matrix product D[m][n] = sum_k A(m, k) B(n, k) on the matrix
+// cores, for the linear products and their gradients: either operand is stored
+// with the contraction along its rows ([m][k]) or down its columns ([k][m]).
+//
+// A workgroup takes BM x BN outputs. Each step of the contraction brings 128
+// bytes of every row (64 halves, 32 floats) into LDS by buffer loads that write
+// LDS directly; a load past the operand's end gives zero. While a step is
+// multiplied the next ones are in flight (kStages buffers, one barrier a step).
+// Half operands go through the 16x16x32 product, float ones through 16x16x4,
+// which keeps them whole; sums are float.
+#pragma once
+
+#include <type_traits>
+
+#include "gla_tile.h"
+
+namespace gla {
+namespace gemm {
+
+constexpr unsigned kOut = 0x80000000u;  // an offset past every buffer's end
+constexpr int kXcds = 8;
+
+template <typename T>
+struct Num {
+  static constexpr int kUnit = 16 / (int)sizeof(T);   // elements of 16 bytes
+  static constexpr int kStep = 128 / (int)sizeof(T);  // elements of the contraction per step
+};
+
+__device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // all but the last N loads, and all LDS reads
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void barrier() {  // no LDS read or load moves across it
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// One operand's R rows (or columns) of a step in LDS, R * 128 bytes, in 16-byte
+// units. Stored along the contraction: R rows of 8 units, unit u of row r in
+// slot u ^ (r mod 8), so that the 16 rows a fragment reads lie in distinct
+// banks. Stored down the columns: kStep rows of R elements, as they are in
+// memory, with unit u of row r in slot u ^ g(r), for the transposing read (half)
+// or plain reads (float) of 16 neighbouring columns.
+template <typename T, int R, bool kCol>
+struct Operand {
+  static constexpr int kUnit = Num<T>::kUnit, kStep = Num<T>::kStep;
+  static constexpr int kPerRow = kCol ? R / kUnit : 8;  // units per stored row
+  static constexpr int kBytes = R * 128;
+
+  static __device__ __forceinline__ int twist(int row) {
+    if (!kCol) return row & 7;
+    if (sizeof(T) == 2) return (2 * (row & 3) | (row & 8)) & (kPerRow - 1);
+    return (row & 4) & (kPerRow - 1);
+  }
+
+  // 16 bytes of contraction for row r0 + lane % 16: elements
+  // 4 kUnit ks + kUnit q + 0..kUnit-1 with q = lane / 16 (both operands alike)
+  static __device__ __forceinline__ void read(const char* lds, int r0, int ks, half8& x) {
+    const int i = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
+    if constexpr (!kCol) {
+      const int row = r0 + i;
+      x = *reinterpret_cast<const half8*>(lds + row * 128 + 16 * ((4 * ks + q) ^ twist(row)));
+    } else {
+      half4 h[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int row = 32 * ks + 8 * q + 4 * p + (i >> 2), col = r0 + 4 * (i & 3);
+        const char* at = lds + row * (2 * R) + 16 * ((col >> 3) ^ twist(row)) + 2 * (col & 7);
+        h[p] = __builtin_bit_cast(half4, __builtin_amdgcn_ds_read_tr16_b64_v4f16((tile::lds_fp16x4_t*)at));
+      }
+      x = half8{h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
+    }
+  }
+  static __device__ __forceinline__ void read(const char* lds, int r0, int ks, floatx4& x) {
+    const int i = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
+    if constexpr (!kCol) {
+      const int row = r0 + i;
+      x = *reinterpret_cast<const floatx4*>(lds + row * 128 + 16 * ((4 * ks + q) ^ twist(row)));
+    } else {
+      const int col = r0 + i;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = 16 * ks + 4 * q + j;
+        x[j] = *reinterpret_cast<const float*>(lds + row * (4 * R) + 16 * ((col >> 2) ^ twist(row)) + 4 * (col & 3));
+      }
+    }
+  }
+
+  // How a thread of NT loads its units of a step.
+  template <int NT>
+  struct Loader {
+    static constexpr int kLoads = R * 8 / NT;
+    unsigned off[kLoads];  // bytes from the step's first element
+    // left: rows (columns) of the tile that exist
+    __device__ __forceinline__ void init(long left, long ld) {
+#pragma unroll
+      for (int it = 0; it < kLoads; ++it) {
+        const int j = threadIdx.x + NT * it, row = j / kPerRow, unit = (j % kPerRow) ^ twist(row);
+        const bool in = kCol ? unit * kUnit < left : row < left;
+        off[it] = in ? (unsigned)((row * ld + unit * kUnit) * (long)sizeof(T)) : kOut;
+      }
+    }
+    // unit `it` of the step at base, of which `left` elements of the
+    // contraction exist
+    __device__ __forceinline__ void one(const void* base, long left, char* lds, int it) const {
+      const int j = threadIdx.x + NT * it, row = j / kPerRow, unit = (j % kPerRow) ^ twist(row);
+      const bool in = left >= kStep || (kCol ? row : unit * kUnit) < left;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000),
+          (__attribute__((address_space(3))) void*)(lds + 16 * (NT * it + 64 * wave())), 16,
+          in ? off[it] : kOut, 0, 0, 0);
+    }
+  };
+};
+
+__device__ __forceinline__ floatx4 product(half8 a, half8 b, floatx4 c) { return mfma16x16x32(a, b, c); }
+__device__ __forceinline__ floatx4 product(floatx4 a, floatx4 b, floatx4 c) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+  return c;
+}
+
+// A neighbouring pair of 16-column blocks, of which each lane holds four
+// columns 4q.. of both: afterwards x holds the eight columns
+// 16 (q mod 2) + 8 (q / 2) .. of the pair (rows of 16 lanes swapped).
+__device__ __forceinline__ void pair8(floatx4 lo, floatx4 hi, float (&x)[8]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(lo[r]), __float_as_uint(hi[r]), false, false);
+    x[r] = __uint_as_float(y[0]);
+    x[4 + r] = __uint_as_float(y[1]);
+  }
+}
+
+// Values of the activations and of their derivatives (codes of gla.h), in
+// float and within 2^-21 of themselves, on the reciprocal and exp2 units.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.f + tile::fexp2(-z * kLog2e));
+}
+// exp(-z^2 / 2)
+__device__ __forceinline__ float bell(float z) { return tile::fexp2(z * z * (-0.5f * kLog2e)); }
+// The normal distribution's integral up to z, erfc(-z / sqrt 2) / 2: for x >= 0
+// erfc(x) exp(x^2) (1 + x / 2) is smooth in t = 1 / (1 + x / 2), and this
+// polynomial in t, a least-squares fit weighted to even out its relative error,
+// is within 5e-8 of it on 0.14 <= t <= 1 (beyond, x > 12, exp(-x^2) is zero in
+// float). The lower tail keeps its digits.
+__device__ __forceinline__ float normal_below(float z) {
+  const float x = fabsf(z) * 0.70710678118654752f, t = __builtin_amdgcn_rcpf(fmaf(0.5f, x, 1.f));
+  float p = -0.059374962002038956f;
+  p = fmaf(p, t, 0.2860681116580963f);
+  p = fmaf(p, t, -0.49029138684272766f);
+  p = fmaf(p, t, 0.2816026210784912f);
+  p = fmaf(p, t, -0.029059266671538353f);
+  p = fmaf(p, t, 0.20371514558792114f);
+  p = fmaf(p, t, 0.24284444749355316f);
+  p = fmaf(p, t, 0.2824108302593231f);
+  p = fmaf(p, t, 0.2820844054222107f);
+  const float tail = 0.5f * p * t * bell(z);
+  return z < 0.f ? tail : 1.f - tail;
+}
+// log(1 + e) for 0 <= e <= 1, as 2 artanh(s) with s = e / (2 + e) <= 1/3: the
+// series' first terms left out are below 2^-25 of it
+__device__ __forceinline__ float log_1p(float e) {
+  const float s = e * __builtin_amdgcn_rcpf(2.f + e), y = s * s;
+  float p = 1.f / 15.f;
+  p = fmaf(p, y, 1.f / 13.f);
+  p = fmaf(p, y, 1.f / 11.f);
+  p = fmaf(p, y, 1.f / 9.f);
+  p = fmaf(p, y, 1.f / 7.f);
+  p = fmaf(p, y, 1.f / 5.f);
+  p = fmaf(p, y, 1.f / 3.f);
+  p = fmaf(p, y, 1.f);
+  return 2.f * s * p;
+}
+template <int W>
+__device__ __forceinline__ void activate(float (&z)[W], int act) {
+  if (act == 1) {  // silu
+#pragma unroll
+    for (int c = 0; c < W; ++c) z[c] *= sigmoid(z[c]);
+  } else if (act == 2) {  // gelu
+#pragma unroll
+    for (int c = 0; c < W; ++c) z[c] *= normal_below(z[c]);
+  } else if (act == 3) {  // log sigmoid
+#pragma unroll
+    for (int c = 0; c < W; ++c) z[c] = fminf(z[c], 0.f) - log_1p(tile::fexp2(-fabsf(z[c]) * kLog2e));
+  }
+}
+__device__ __forceinline__ float slope(float z, int act) {
+  if (act == 1) {
+    const float s = sigmoid(z);
+    return s * fmaf(z, 1.f - s, 1.f);
+  }
+  if (act == 2) return fmaf(z * 0.39894228040143268f, bell(z), normal_below(z));
+  if (act == 3) return sigmoid(-z);
+  return 1.f;
+}
+
+struct Args {
+  const void *a[2], *b[2];
+  long lda, ldb;  // elements between stored rows
+  long M, N, K;   // outputs of one part of the rows, and contraction of one part
+  int parts;      // parts of the contraction, one behind the other (a[p], b[p])
+  int mparts;     // parts of the rows (a[p], out[p])
+  int tiles_m, tiles_n;  // of one part of the rows
+  int splits;            // of the contraction
+  long steps, each;      // steps of the contraction, and of one split
+  void* out[2];
+  float* partial;  // [split][mparts * M][N] float instead of out
+  void* pre;       // x W^T + bias, or nullptr
+  const float* bias;
+  const void* residual;
+  float alpha;
+  int act;
+  void *gate_out, *up_out;  // the gated product's two sides, or nullptr
+};
+
+enum { kLinear, kGated, kPartial };
+
+template <typename T>
+__device__ __forceinline__ void load_to(const T* p, float (&x)[8]) { load8(p, x); }
+template <typename T>
+__device__ __forceinline__ void store_from(T* p, const float (&x)[8]) { store8(p, x); }
+template <typename T>
+__device__ __forceinline__ void load_to(const T* p, float (&x)[4]) {
+  typedef T vec __attribute__((ext_vector_type(4)));
+  const vec v = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) x[c] = (float)v[c];
+}
+template <typename T>
+__device__ __forceinline__ void store_from(T* p, const float (&x)[4]) {
+  typedef T vec __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<vec*>(p) = vec{(T)x[0], (T)x[1], (T)x[2], (T)x[3]};
+}
+
+// W neighbouring outputs from their sums: y = alpha act(sum + bias) + residual.
+template <typename T, int W>
+__device__ __forceinline__ void finish(const Args& g, int part, long m, long n, float (&x)[W]) {
+  const long o = m * g.N + n;
+  if (g.bias) {
+    float b[W];
+    load_to(g.bias + n, b);
+#pragma unroll
+    for (int c = 0; c < W; ++c) x[c] += b[c];
+  }
+  if (g.pre) store_from(static_cast<T*>(g.pre) + o, x);
+  activate(x, g.act);
+#pragma unroll
+  for (int c = 0; c < W; ++c) x[c] *= g.alpha;
+  if (g.residual) {
+    float r[W];
+    load_to(static_cast<const T*>(g.residual) + o, r);
+#pragma unroll
+    for (int c = 0; c < W; ++c) x[c] += r[c];
+  }
+  store_from(static_cast<T*>(g.out[part]) + o, x);
+}
+
+// and of the gated product: h = act(x) u.
+template <typename T, int W>
+__device__ __forceinline__ void finish_gated(const Args& g, long m, long n, float (&x)[W], const float (&u)[W]) {
+  const long o = m * g.N + n;
+  if (g.gate_out) store_from(static_cast<T*>(g.gate_out) + o, x);
+  if (g.up_out) store_from(static_cast<T*>(g.up_out) + o, u);
+  activate(x, g.act);
+#pragma unroll
+  for (int c = 0; c < W; ++c) x[c] *= u[c];
+  store_from(static_cast<T*>(g.out[0]) + o, x);
+}
+
+// The tile a workgroup takes: the numbers of one XCD's workgroups are brought
+// together, so that they share rows of both operands in its L2, in groups of
+// eight row tiles by all column tiles.
+struct Place {
+  int split, part, mt, nt;
+  __device__ __forceinline__ Place(const Args& g) {
+    const int total = gridDim.x, x = blockIdx.x % kXcds, q = total / kXcds, r = total % kXcds;
+    const int lin = x * q + min(x, r) + blockIdx.x / kXcds;
+    const int tm = g.tiles_m * g.mparts, tiles = tm * g.tiles_n;
+    split = lin / tiles;
+    const int t = lin % tiles, band = 8 * g.tiles_n, first = t / band * 8, in = min(8, tm - first);
+    const int m = first + t % band % in;
+    nt = t % band / in;
+    part = m / g.tiles_m;
+    mt = m % g.tiles_m;
+  }
+};
+
+template <typename T, int BM, int BN, int WM, int WN, int kStages, bool kColA, bool kColB, int kEpi>
+__device__ __forceinline__ void gemm_tile(const Args& g) {
+  constexpr int NT = 64 * WM * WN, MI = BM / WM / 16, NI = BN / WN / 16;
+  constexpr bool kDual = kEpi == kGated;  // columns: BN/2 of b[0], then BN/2 of b[1]
+  constexpr int BNC = kDual ? BN / 2 : BN;
+  using OA = Operand<T, BM, kColA>;
+  using OB = Operand<T, BN, kColB>;
+  using LA = typename OA::template Loader<NT>;
+  using LB = typename OB::template Loader<NT>;
+  using Frag = typename std::conditional<sizeof(T) == 2, half8, floatx4>::type;
+  constexpr int kStep = Num<T>::kStep, kStageBytes = OA::kBytes + OB::kBytes;
+  constexpr int kInFlight = LA::kLoads + LB::kLoads;
+  static_assert(!kDual || !kColB, "both sides of a gated product lie along the contraction");
+  __shared__ __attribute__((aligned(1024))) char smem[kStages * kStageBytes];
+  const Place at(g);
+  const int wm = wave() / WN, wn = wave() % WN;
+  const long m0 = (long)at.mt * BM, n0 = (long)at.nt * BNC;
+  const long steps_part = g.steps / g.parts;
+  const long s0 = at.split * g.each, s1 = min(s0 + g.each, g.steps);
+  const T* pa[2] = {static_cast<const T*>(g.a[g.parts > 1 ? 0 : at.part]) + m0 * (kColA ? 1 : g.lda),
+                    static_cast<const T*>(g.a[1]) + m0 * (kColA ? 1 : g.lda)};
+  const T* pb[2] = {static_cast<const T*>(g.b[0]) + n0 * (kColB ? 1 : g.ldb),
+                    static_cast<const T*>(g.b[1]) + n0 * (kColB ? 1 : g.ldb)};
+  LA la;
+  LB lb;
+  la.init(g.M - m0, g.lda);
+  if constexpr (kDual) {
+    // rows 0 .. BN/2 - 1 of the tile are b[0]'s, the others b[1]'s
+#pragma unroll
+    for (int it = 0; it < LB::kLoads; ++it) {
+      const int j = threadIdx.x + NT * it, row = j / 8 % BNC, unit = (j % 8) ^ OB::twist(row);
+      lb.off[it] = row < g.N - n0 ? (unsigned)((row * g.ldb + unit * Num<T>::kUnit) * (long)sizeof(T)) : kOut;
+    }
+  } else {
+    lb.init(g.N - n0, g.ldb);
+  }
+  auto load = [&](long s, int stage) {
+    const int p = g.parts > 1 && s >= steps_part;
+    const long k0 = (p ? s - steps_part : s) * kStep, left = g.K - k0;
+    char* lds = smem + stage * kStageBytes;
+    const T* ra = pa[p] + k0 * (kColA ? g.lda : 1);
+#pragma unroll
+    for (int it = 0; it < LA::kLoads; ++it) la.one(ra, left, lds, it);
+    if constexpr (kDual) {
+      const T *rg = pb[0] + k0, *ru = pb[1] + k0;
+#pragma unroll
+      for (int it = 0; it < LB::kLoads; ++it)
+        lb.one(it < LB::kLoads / 2 ? rg : ru, left, lds + OA::kBytes, it);
+    } else {
+      const T* rb = pb[p] + k0 * (kColB ? g.ldb : 1);
+#pragma unroll
+      for (int it = 0; it < LB::kLoads; ++it) lb.one(rb, left, lds + OA::kBytes, it);
+    }
+  };
+  floatx4 acc[MI][NI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s)
+    if (s0 + s < s1) load(s0 + s, s);
+  int stage = 0;
+  for (long s = s0; s < s1; ++s) {
+    // this step's loads are done in every wave, and the buffer that the loads
+    // below refill has been read by all of them
+    if (s + kStages - 2 < s1) wait_loads<kInFlight * (kStages - 2)>();
+    else wait_loads<0>();
+    barrier();
+    const int next = stage == 0 ? kStages - 1 : stage - 1;
+    if (s + kStages - 1 < s1) load(s + kStages - 1, next);
+    const char* sa = smem + stage * kStageBytes;
+    const char* sb = sa + OA::kBytes;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      Frag fa[MI], fb[NI];
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) OA::read(sa, (wm * MI + mi) * 16, ks, fa[mi]);
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        // gated: a wave's first NI/2 blocks are of b[0], the others, of the same columns, of b[1]
+        const int blk = kDual ? (ni < NI / 2 ? wn * (NI / 2) + ni : BNC / 16 + wn * (NI / 2) + ni - NI / 2)
+                              : wn * NI + ni;
+        OB::read(sb, blk * 16, ks, fb[ni]);
+      }
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = product(fb[ni], fa[mi], acc[mi][ni]);
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+
+  // each lane: row lane % 16 of the row blocks, eight columns of each pair of column blocks
+  const int i = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3, c8 = 16 * (q & 1) + 8 * (q >> 1);
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    const long m = m0 + (wm * MI + mi) * 16 + i;
+    if constexpr (kDual) {
+#pragma unroll
+      for (int p = 0; p < NI / 4; ++p) {
+        float x[8], u[8];
+        pair8(acc[mi][2 * p], acc[mi][2 * p + 1], x);
+        pair8(acc[mi][NI / 2 + 2 * p], acc[mi][NI / 2 + 2 * p + 1], u);
+        const long n = n0 + wn * (NI / 2) * 16 + 32 * p + c8;
+        if (m < g.M && n < g.N) finish_gated<T>(g, m, n, x, u);
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < NI / 2; ++p) {
+        float x[8];
+        pair8(acc[mi][2 * p], acc[mi][2 * p + 1], x);
+        const long n = n0 + wn * NI * 16 + 32 * p + c8;
+        if (m < g.M && n < g.N) {
+          if constexpr (kEpi == kPartial)
+            store8(g.partial + ((long)at.split * g.mparts + at.part) * g.M * g.N + m * g.N + n, x);
+          else
+            finish<T>(g, at.part, m, n, x);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int kStages, bool kColA, bool kColB, int kEpi>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const Args g) {
+  gemm_tile<T, BM, BN, WM, WN, kStages, kColA, kColB, kEpi>(g);
+}
+
+}  // namespace gemm
+}  // namespace gla

@@ -14,37 +14,15 @@
 // column sums. (A copy of 256 MB runs at 5.4 TB/s.) Rows of less than 512 columns
 // leave lanes of their wave idle: the norm of 409,600 x 64 takes 83 us (2.5
 // TB/s), of 409,600 x 128 127 us (3.3 TB/s).
+#include "gla_colsum.h"
 #include "gla_norm.h"
+#include "gla_rows.h"
 #include "gla_tile.h"
 
 namespace gla {
 namespace norm {
 
 using tile::fexp2;
-
-// Sum or largest value over the TPR threads of a row (64: one wave; 256: the
-// workgroup, through LDS).
-template <int TPR, bool kMax>
-__device__ __forceinline__ float row_reduce(float x, float* lds) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    const float y = __shfl_xor(x, m);
-    x = kMax ? fmaxf(x, y) : x + y;
-  }
-  if constexpr (TPR > 64) {
-    __syncthreads();  // earlier readers of lds are done
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = lds[0];
-#pragma unroll
-    for (int w = 1; w < TPR / 64; ++w) x = kMax ? fmaxf(x, lds[w]) : x + lds[w];
-  }
-  return x;
-}
-
-// s rounded to the stream's type (what is stored, and what the norm is of)
-__device__ __forceinline__ float round_to(float x, half_t) { return (float)(half_t)x; }
-__device__ __forceinline__ float round_to(float x, float) { return x; }
 
 __device__ __forceinline__ void load_w(const float* p, float (&x)[8]) { tile::load_f8(p, x); }
 
@@ -270,43 +248,6 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(
   if (threadIdx.x < DV)
     part[(long)blockIdx.x * DV + threadIdx.x] =
         (sW[0][threadIdx.x] + sW[1][threadIdx.x]) + (sW[2][threadIdx.x] + sW[3][threadIdx.x]);
-}
-
-// out[col] = sum over the P partial rows: 16 columns and 64 groups of rows per
-// workgroup, each thread with 16 loads in flight, the groups joined in LDS in
-// a fixed order. 915 rows of 768: 4.7 us, a launch's latency and one round of
-// loads. (With 16 groups and one load at a time it took 20 us, two thirds of
-// the gradient it finishes.)
-__global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ part,
-                                                          float* __restrict__ out, int P, int F) {
-  constexpr int W = 16;
-  __shared__ float s[64][17];
-  const int c = threadIdx.x & 15, g = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
-  float y = 0.f;
-  if (col < F) {
-    for (int p = g; p < P; p += 64 * W) {
-      float x[W];
-#pragma unroll
-      for (int i = 0; i < W; ++i) x[i] = p + 64 * i < P ? part[(long)(p + 64 * i) * F + col] : 0.f;
-#pragma unroll
-      for (int i = 0; i < W; ++i) y += x[i];
-    }
-  }
-  s[g][c] = y;
-  __syncthreads();
-  if (g < 8) {
-    y = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y += s[g + 8 * i][c];
-    s[g][c] = y;  // no other thread reads row g
-  }
-  __syncthreads();
-  if (g == 0 && col < F) {
-    y = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y += s[i][c];
-    out[col] = y;
-  }
 }
 
 // Workgroups of the two gradient kernels: enough to fill the GPU, and few enough

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgla_mi35
 
 L2R, R2L, T2B, B2T = 0, 1, 2, 3
 F16, F32 = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_LOGSIGMOID = 0, 1, 2, 3
 SCHED_AUTO, SCHED_SINGLE_PASS, SCHED_THREE_PHASE, SCHED_RUNS = 0, 1, 2, 3
 CTRL_BYTES = 65536  # control words at the start of every workspace
 OK, E_ARG, E_UNSUPPORTED, E_WORKSPACE, E_HIP, E_UNPREPARED = 0, -1, -2, -3, -4, -5
@@ -33,7 +34,10 @@ EXPORTS = ["gla_abi_version", "gla_fwd_workspace_bytes", "gla_workspace_layout",
            "gla_status_string", "gla_last_error_detail", "gla_fwd_noalloc",
            "gla_bwd_workspace_bytes", "gla_bwd", "gla_step", "gla_step_gated", "gla_add_rmsnorm",
            "gla_add_rmsnorm_q8", "gla_add_rmsnorm_bwd_workspace_bytes", "gla_add_rmsnorm_bwd",
-           "gla_gate_bwd_workspace_bytes", "gla_gate_bwd"]
+           "gla_gate_bwd_workspace_bytes", "gla_gate_bwd",
+           "gla_linear", "gla_linear_bwd_workspace_bytes", "gla_linear_bwd", "gla_gated_ff",
+           "gla_gated_ff_bwd_workspace_bytes", "gla_gated_ff_bwd", "gla_gated_add_rmsnorm",
+           "gla_gated_add_rmsnorm_bwd_workspace_bytes", "gla_gated_add_rmsnorm_bwd"]
 
 # With check_errors(True), every forward call made through this module waits
 # for its stream and raises if the workspace's sticky error word is set
@@ -129,6 +133,26 @@ def load():
     lib.gla_gate_bwd_workspace_bytes.argtypes = [_i64, _i32]
     lib.gla_gate_bwd.restype = _i32
     lib.gla_gate_bwd.argtypes = [_vp, _vp, _vp, _f32] + [_vp] * 4 + [_i64, _i32, _i32, _vp, _sz, _vp]
+    lib.gla_linear.restype = _i32
+    lib.gla_linear.argtypes = [_vp] * 6 + [_i64, _i32, _i32, _i32, _f32, _i32, _vp]
+    lib.gla_linear_bwd_workspace_bytes.restype = _sz
+    lib.gla_linear_bwd_workspace_bytes.argtypes = [_i64] + [_i32] * 4
+    lib.gla_linear_bwd.restype = _i32
+    lib.gla_linear_bwd.argtypes = [_vp] * 7 + [_i64, _i32, _i32, _i32, _f32, _i32, _vp, _sz, _vp]
+    lib.gla_gated_ff.restype = _i32
+    lib.gla_gated_ff.argtypes = [_vp] * 6 + [_i64] + [_i32] * 4 + [_vp]
+    lib.gla_gated_ff_bwd_workspace_bytes.restype = _sz
+    lib.gla_gated_ff_bwd_workspace_bytes.argtypes = [_i64] + [_i32] * 3
+    lib.gla_gated_ff_bwd.restype = _i32
+    lib.gla_gated_ff_bwd.argtypes = [_vp] * 9 + [_i64] + [_i32] * 4 + [_vp, _sz, _vp]
+    lib.gla_gated_add_rmsnorm.restype = _i32
+    lib.gla_gated_add_rmsnorm.argtypes = ([_vp] * 4 + [_i64, _vp, _vp, _f32, _vp, _vp, _i64, _i32,
+                                                       _i32, _vp])
+    lib.gla_gated_add_rmsnorm_bwd_workspace_bytes.restype = _sz
+    lib.gla_gated_add_rmsnorm_bwd_workspace_bytes.argtypes = [_i64, _i64, _i32]
+    lib.gla_gated_add_rmsnorm_bwd.restype = _i32
+    lib.gla_gated_add_rmsnorm_bwd.argtypes = ([_vp] * 4 + [_i64, _vp, _vp, _f32] + [_vp] * 8 +
+                                              [_i64, _i32, _i32, _vp, _sz, _vp])
     lib.gla_status_string.restype = ctypes.c_char_p
     lib.gla_status_string.argtypes = [_i32]
     lib.gla_last_error_detail.restype = ctypes.c_char_p
@@ -816,3 +840,239 @@ def gate_bwd(o: torch.Tensor, gate: torch.Tensor, norm_weight: torch.Tensor, eps
                                  _dtype_code(o), ws, nws, st_ptr)
     _check(st, "gla_gate_bwd")
     return go, gz, gw
+
+
+# ---- the products and norms between a block's mixers
+
+
+def _rows_of(x: torch.Tensor, name: str):
+    """(device, rows, width) of a contiguous device tensor [..., width]."""
+    dev = _on_gpu(x, name)
+    if x.dim() < 1 or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous device tensor [..., K]")
+    K = x.shape[-1]
+    return dev, (x.numel() // K if K else 0), K
+
+
+def _weight_of(weight: torch.Tensor, x: torch.Tensor, K: int, name: str) -> int:
+    """Rows of a weight [N, K] in x's dtype, on x's device."""
+    if weight.dim() != 2:
+        raise ValueError(f"{name} must be [N, K]")
+    _like(weight, (weight.shape[0], K), x.dtype, x.device, name)
+    return weight.shape[0]
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_workspace_bytes(rows: int, K: int, N: int, act: int, dtype: int) -> int:
+    return int(load().gla_linear_bwd_workspace_bytes(rows, K, N, act, dtype))
+
+
+@functools.lru_cache(maxsize=256)
+def _gated_ff_workspace_bytes(rows: int, K: int, F: int, dtype: int) -> int:
+    return int(load().gla_gated_ff_bwd_workspace_bytes(rows, K, F, dtype))
+
+
+@functools.lru_cache(maxsize=256)
+def _gated_norm_workspace_bytes(rows: int, groups: int, F: int) -> int:
+    return int(load().gla_gated_add_rmsnorm_bwd_workspace_bytes(rows, groups, F))
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+           act: int = ACT_NONE, alpha: float = 1.0, residual: Optional[torch.Tensor] = None,
+           return_pre: bool = False, out: Optional[torch.Tensor] = None,
+           pre: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """y = alpha * act(x weight^T + bias) + residual, or (y, pre) with
+    return_pre, pre = x weight^T + bias for linear_bwd (written to `pre` if
+    given). x [..., K], weight [N, K], residual, y and pre [..., N] in one
+    dtype (float16 or float32), bias [N] float32; K and N multiples of 8. out
+    may be residual."""
+    dev, rows, K = _rows_of(x, "x")
+    N = _weight_of(weight, x, K, "weight")
+    shape = x.shape[:-1] + (N,)
+    if bias is not None:
+        _like(bias, (N,), torch.float32, dev, "bias")
+    if residual is not None:
+        _like(residual, shape, x.dtype, dev, "residual")
+    if pre is not None and not return_pre:
+        raise ValueError("pre is written with return_pre only")
+    with _launching(dev, stream, x, weight, bias, residual, out, pre) as st_ptr:
+        y = _out(out, shape, x.dtype, dev)
+        p = _out(pre, shape, x.dtype, dev) if return_pre else None
+        st = load().gla_linear(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(residual), _ptr(p),
+                               y.data_ptr(), rows, K, N, act, float(alpha), _dtype_code(x), st_ptr)
+    _check(st, "gla_linear")
+    return (y, p) if return_pre else y
+
+
+def linear_bwd(x: torch.Tensor, weight: torch.Tensor, gy: torch.Tensor, act: int = ACT_NONE,
+               alpha: float = 1.0, pre: Optional[torch.Tensor] = None, need_x: bool = True,
+               need_weight: bool = True, need_bias: bool = True, gx: Optional[torch.Tensor] = None,
+               gweight: Optional[torch.Tensor] = None, gbias: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """(gx, gweight, gbias) of linear from gy = dL/dy and the forward's pre
+    (not needed for ACT_NONE); the residual's gradient is gy. None for those
+    not needed. gx and gweight have x's dtype, gbias is float32."""
+    dev, rows, K = _rows_of(x, "x")
+    N = _weight_of(weight, x, K, "weight")
+    shape = x.shape[:-1] + (N,)
+    _like(gy, shape, x.dtype, dev, "gy")
+    if act != ACT_NONE:
+        _like(pre, shape, x.dtype, dev, "pre")
+    with _launching(dev, stream, x, weight, gy, pre, gx, gweight, gbias, workspace) as st_ptr:
+        gx = _out_like(gx, x) if need_x else None
+        gw = _out_like(gweight, weight) if need_weight else None
+        gb = _out(gbias, (N,), torch.float32, dev) if need_bias else None
+        code = _dtype_code(x)
+        if rows == 0 or N == 0:  # sums of nothing
+            for g in (gx, gw, gb):
+                if g is not None:
+                    g.zero_()
+            return gx, gw, gb
+        workspace = _scratch(workspace, _linear_workspace_bytes(rows, K, N, act, code), dev)
+        ws, nws = _ws(workspace, dev)
+        st = load().gla_linear_bwd(x.data_ptr(), weight.data_ptr(),
+                                   pre.data_ptr() if act != ACT_NONE else None, gy.data_ptr(), _ptr(gx),
+                                   _ptr(gw), _ptr(gb), rows, K, N, act, float(alpha), code, ws, nws,
+                                   st_ptr)
+    _check(st, "gla_linear_bwd")
+    return gx, gw, gb
+
+
+def gated_ff(x: torch.Tensor, gate_weight: torch.Tensor, up_weight: torch.Tensor, act: int = ACT_SILU,
+             return_parts: bool = False, out: Optional[torch.Tensor] = None,
+             parts: Optional[Sequence[torch.Tensor]] = None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """h = act(x gate_weight^T) * (x up_weight^T), or (h, a, u) with
+    return_parts, the two products for gated_ff_bwd (written to `parts` if
+    given). x [..., K], weights [F, K], h, a, u [..., F] in one dtype."""
+    dev, rows, K = _rows_of(x, "x")
+    F = _weight_of(gate_weight, x, K, "gate_weight")
+    _like(up_weight, gate_weight.shape, x.dtype, dev, "up_weight")
+    if parts is not None and (not return_parts or len(parts) != 2):
+        raise ValueError("parts must be two tensors (a, u), written with return_parts only")
+    shape = x.shape[:-1] + (F,)
+    with _launching(dev, stream, x, gate_weight, up_weight, out, *(parts or ())) as st_ptr:
+        h = _out(out, shape, x.dtype, dev)
+        a = u = None
+        if return_parts:
+            a = _out(parts[0] if parts else None, shape, x.dtype, dev)
+            u = _out(parts[1] if parts else None, shape, x.dtype, dev)
+        st = load().gla_gated_ff(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(), _ptr(a),
+                                 _ptr(u), h.data_ptr(), rows, K, F, act, _dtype_code(x), st_ptr)
+    _check(st, "gla_gated_ff")
+    return (h, a, u) if return_parts else h
+
+
+def gated_ff_bwd(x: torch.Tensor, gate_weight: torch.Tensor, up_weight: torch.Tensor, a: torch.Tensor,
+                 u: torch.Tensor, gh: torch.Tensor, act: int = ACT_SILU, need_x: bool = True,
+                 need_weights: bool = True, gx: Optional[torch.Tensor] = None,
+                 gweights: Optional[Sequence[torch.Tensor]] = None,
+                 workspace: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None):
+    """(gx, ggate_weight, gup_weight) of gated_ff from gh = dL/dh and the
+    forward's a, u; None for those not needed. All in x's dtype."""
+    dev, rows, K = _rows_of(x, "x")
+    F = _weight_of(gate_weight, x, K, "gate_weight")
+    _like(up_weight, gate_weight.shape, x.dtype, dev, "up_weight")
+    _alike(x.shape[:-1] + (F,), x.dtype, dev, "a u gh", a, u, gh)
+    if gweights is not None and len(gweights) != 2:
+        raise ValueError("gweights must be two tensors (ggate_weight, gup_weight)")
+    with _launching(dev, stream, x, gate_weight, up_weight, a, u, gh, gx, workspace,
+                    *(gweights or ())) as st_ptr:
+        gx = _out_like(gx, x) if need_x else None
+        gg = gu = None
+        if need_weights:
+            gg = _out_like(gweights[0] if gweights else None, gate_weight)
+            gu = _out_like(gweights[1] if gweights else None, up_weight)
+        code = _dtype_code(x)
+        if rows == 0 or F == 0:  # sums of nothing
+            for g in (gx, gg, gu):
+                if g is not None:
+                    g.zero_()
+            return gx, gg, gu
+        workspace = _scratch(workspace, _gated_ff_workspace_bytes(rows, K, F, code), dev)
+        ws, nws = _ws(workspace, dev)
+        st = load().gla_gated_ff_bwd(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(),
+                                     a.data_ptr(), u.data_ptr(), gh.data_ptr(), _ptr(gx), _ptr(gg),
+                                     _ptr(gu), rows, K, F, act, code, ws, nws, st_ptr)
+    _check(st, "gla_gated_ff_bwd")
+    return gx, gg, gu
+
+
+def _gated_norm_args(x, weight, post_weight, gate, scale):
+    """(device, rows, F, groups) of the norms around a block."""
+    dev, rows, F = _rows_of(x, "x")
+    _like(weight, (F,), torch.float32, dev, "weight")
+    if post_weight is not None:
+        _like(post_weight, (F,), torch.float32, dev, "post_weight")
+    if scale is not None:
+        _like(scale, (F,), torch.float32, dev, "scale")
+    groups = 1
+    if gate is not None:
+        _like(gate, gate.shape[:-1] + (F,), x.dtype, dev, "gate")
+        groups = gate.numel() // F if F else 1
+        if groups < 1 or rows % groups:
+            raise ValueError(f"gate must have one row for each of equal groups of the {rows} rows, got {groups}")
+    return dev, rows, F, groups
+
+
+def gated_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, eps: float,
+                      post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                      scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      sum_out: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None):
+    """(y, s): s = residual + scale * gate * p rounded to x's dtype, with p =
+    RMSNorm(x) * post_weight (x without it), and y = RMSNorm(s) * weight. x,
+    residual [..., F]; gate [..., F] in x's dtype, one row for each of equal
+    runs of x's rows; weight, post_weight, scale [F] float32; scale and gate
+    count as 1 where None. out and sum_out may be x or residual."""
+    dev, rows, F, groups = _gated_norm_args(x, weight, post_weight, gate, scale)
+    _like(residual, x.shape, x.dtype, dev, "residual")
+    with _launching(dev, stream, x, residual, weight, post_weight, gate, scale, out, sum_out) as st_ptr:
+        y = _out_like(out, x)
+        s = _out_like(sum_out, x)
+        st = load().gla_gated_add_rmsnorm(x.data_ptr(), residual.data_ptr(), _ptr(post_weight), _ptr(gate),
+                                          groups, _ptr(scale), weight.data_ptr(), float(eps), s.data_ptr(),
+                                          y.data_ptr(), rows, F, _dtype_code(x), st_ptr)
+    _check(st, "gla_gated_add_rmsnorm")
+    return y, s
+
+
+def gated_add_rmsnorm_bwd(x: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, eps: float,
+                          gy: torch.Tensor, post_weight: Optional[torch.Tensor] = None,
+                          gate: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                          gsum: Optional[torch.Tensor] = None, gx: Optional[torch.Tensor] = None,
+                          gresidual: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None):
+    """(gx, gresidual, gweight, gpost_weight, ggate, gscale) of
+    gated_add_rmsnorm from its x and s, gy = dL/dy and gsum, the gradient that
+    reaches s itself (None for none); None for those without an input. gx and
+    gresidual may be written to x, s, gy or gsum; ggate has gate's shape and
+    dtype, the weights' gradients are float32."""
+    dev, rows, F, groups = _gated_norm_args(x, weight, post_weight, gate, scale)
+    _alike(x.shape, x.dtype, dev, "s gy", s, gy)
+    if gsum is not None:
+        _like(gsum, x.shape, x.dtype, dev, "gsum")
+    with _launching(dev, stream, x, s, weight, gy, post_weight, gate, scale, gsum, gx, gresidual,
+                    workspace) as st_ptr:
+        gx = _out_like(gx, x)
+        gr = _out_like(gresidual, x)
+        gw = torch.empty_like(weight)
+        gp = None if post_weight is None else torch.empty_like(post_weight)
+        gg = None if gate is None else torch.empty_like(gate)
+        gs = None if scale is None else torch.empty_like(scale)
+        if rows == 0 and F > 0:  # sums of nothing
+            for g in (gw, gp, gg, gs):
+                if g is not None:
+                    g.zero_()
+            return gx, gr, gw, gp, gg, gs
+        workspace = _scratch(workspace, _gated_norm_workspace_bytes(rows, groups, F), dev)
+        ws, nws = _ws(workspace, dev)
+        st = load().gla_gated_add_rmsnorm_bwd(x.data_ptr(), s.data_ptr(), _ptr(post_weight), _ptr(gate),
+                                              groups, _ptr(scale), weight.data_ptr(), float(eps),
+                                              gy.data_ptr(), _ptr(gsum), gx.data_ptr(), gr.data_ptr(),
+                                              _ptr(gp), _ptr(gg), _ptr(gs), gw.data_ptr(), rows, F,
+                                              _dtype_code(x), ws, nws, st_ptr)
+    _check(st, "gla_gated_add_rmsnorm_bwd")
+    return gx, gr, gw, gp, gg, gs
