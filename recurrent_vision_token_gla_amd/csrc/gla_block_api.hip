@@ -73,7 +73,8 @@ int gla_linear_bwd(const void* x, const void* weight, const void* pre, const voi
   if (act != GLA_ACT_NONE) GLA_TRY(check_tensor(pre));
   for (const void* t : {(const void*)gx, (const void*)gweight, (const void*)gbias})
     GLA_TRY(check_optional(t));
-  const size_t need = gla::linear_bwd_layout((long)rows, K, N, act, dtype).total;
+  const gla::LinearBwdLayout layout = gla::linear_bwd_layout((long)rows, K, N, act, dtype);
+  const size_t need = layout.total;
   GLA_TRY(check_workspace(workspace, workspace_bytes, need));
   const size_t es = elem(dtype), nx = (size_t)rows * K * es, nw = (size_t)N * K * es;
   const size_t ny = (size_t)rows * N * es;
@@ -83,7 +84,7 @@ int gla_linear_bwd(const void* x, const void* weight, const void* pre, const voi
        {act != GLA_ACT_NONE ? pre : nullptr, ny}, {gy, ny}}));
   gla::LinearBwdArgs a{(long)rows, K, N, act, dtype, alpha, x, weight, pre, gy, gx, gweight, gbias};
   const hipError_t e =
-      gla::launch_linear_bwd(a, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+      gla::launch_linear_bwd(a, layout, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail_hip(e, "linear backward launch");
   return GLA_OK;
 }
@@ -127,7 +128,8 @@ int gla_gated_ff_bwd(const void* x, const void* gate_weight, const void* up_weig
   }
   for (const void* t : {(const void*)gx, (const void*)ggate_weight, (const void*)gup_weight})
     GLA_TRY(check_optional(t));
-  const size_t need = gla::gated_bwd_layout((long)rows, K, F, dtype).total;
+  const gla::LinearBwdLayout layout = gla::gated_bwd_layout((long)rows, K, F, dtype);
+  const size_t need = layout.total;
   GLA_TRY(check_workspace(workspace, workspace_bytes, need));
   const size_t es = elem(dtype), nx = (size_t)rows * K * es, nw = (size_t)F * K * es;
   const size_t nh = (size_t)rows * F * es;
@@ -138,7 +140,7 @@ int gla_gated_ff_bwd(const void* x, const void* gate_weight, const void* up_weig
   gla::GatedBwdArgs a{(long)rows, K, F, act, dtype, x, gate_weight, up_weight, gate, up, gh,
                       gx, ggate_weight, gup_weight};
   const hipError_t e =
-      gla::launch_gated_bwd(a, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+      gla::launch_gated_bwd(a, layout, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail_hip(e, "gated feed-forward backward launch");
   return GLA_OK;
 }

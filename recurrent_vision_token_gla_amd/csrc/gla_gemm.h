@@ -28,9 +28,8 @@ struct Num {
 
 __device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-template <int N>
-__device__ __forceinline__ void wait_loads() {  // all but the last N loads, and all LDS reads
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+__device__ __forceinline__ void wait_loads() {  // of memory and of LDS
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }
 
 __device__ __forceinline__ void barrier() {  // no LDS read or load moves across it
@@ -92,7 +91,8 @@ struct Operand {
   // How a thread of NT loads its units of a step.
   template <int NT>
   struct Loader {
-    static constexpr int kLoads = R * 8 / NT;
+    static constexpr int kUnits = R * 8, kLoads = (kUnits + NT - 1) / NT;
+    static_assert(kUnits % 64 == 0, "whole waves load");
     unsigned off[kLoads];  // bytes from the step's first element
     // left: rows (columns) of the tile that exist
     __device__ __forceinline__ void init(long left, long ld) {
@@ -108,6 +108,7 @@ struct Operand {
     __device__ __forceinline__ void one(const void* base, long left, char* lds, int it) const {
       const int j = threadIdx.x + NT * it, row = j / kPerRow, unit = (j % kPerRow) ^ twist(row);
       const bool in = left >= kStep || (kCol ? row : unit * kUnit) < left;
+      if (NT * it + 64 * wave() >= kUnits) return;  // the last round may be some waves'
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000),
           (__attribute__((address_space(3))) void*)(lds + 16 * (NT * it + 64 * wave())), 16,
@@ -275,22 +276,24 @@ __device__ __forceinline__ void finish_gated(const Args& g, long m, long n, floa
 // together, so that they share rows of both operands in its L2, in groups of
 // eight row tiles by all column tiles.
 struct Place {
-  int split, part, mt, nt;
-  __device__ __forceinline__ Place(const Args& g) {
+  int split, part;
+  long m0, n0;  // of the part's rows, and of the columns
+  __device__ __forceinline__ Place(const Args& g, int BM, int BN) {
     const int total = gridDim.x, x = blockIdx.x % kXcds, q = total / kXcds, r = total % kXcds;
     const int lin = x * q + min(x, r) + blockIdx.x / kXcds;
     const int tm = g.tiles_m * g.mparts, tiles = tm * g.tiles_n;
     split = lin / tiles;
-    const int t = lin % tiles, band = 8 * g.tiles_n, first = t / band * 8, in = min(8, tm - first);
-    const int m = first + t % band % in;
-    nt = t % band / in;
+    const int t = lin % tiles, band = 8 * g.tiles_n, f = t / band * 8, in = min(8, tm - f);
+    const int m = f + t % band % in;
     part = m / g.tiles_m;
-    mt = m % g.tiles_m;
+    m0 = (long)(m % g.tiles_m) * BM;
+    n0 = (long)(t % band / in) * BN;
   }
 };
 
-template <typename T, int BM, int BN, int WM, int WN, int kStages, bool kColA, bool kColB, int kEpi>
-__device__ __forceinline__ void gemm_tile(const Args& g) {
+template <typename T, int BM, int BN, int WM, int WN, bool kColA, bool kColB, int kEpi>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const Args g) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host's pass does not take the loads' builtin in a template
   constexpr int NT = 64 * WM * WN, MI = BM / WM / 16, NI = BN / WN / 16;
   constexpr bool kDual = kEpi == kGated;  // columns: BN/2 of b[0], then BN/2 of b[1]
   constexpr int BNC = kDual ? BN / 2 : BN;
@@ -300,12 +303,11 @@ __device__ __forceinline__ void gemm_tile(const Args& g) {
   using LB = typename OB::template Loader<NT>;
   using Frag = typename std::conditional<sizeof(T) == 2, half8, floatx4>::type;
   constexpr int kStep = Num<T>::kStep, kStageBytes = OA::kBytes + OB::kBytes;
-  constexpr int kInFlight = LA::kLoads + LB::kLoads;
   static_assert(!kDual || !kColB, "both sides of a gated product lie along the contraction");
-  __shared__ __attribute__((aligned(1024))) char smem[kStages * kStageBytes];
-  const Place at(g);
   const int wm = wave() / WN, wn = wave() % WN;
-  const long m0 = (long)at.mt * BM, n0 = (long)at.nt * BNC;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kStageBytes];
+  const Place at(g, BM, BNC);
+  const long m0 = at.m0, n0 = at.n0;
   const long steps_part = g.steps / g.parts;
   const long s0 = at.split * g.each, s1 = min(s0 + g.each, g.steps);
   const T* pa[2] = {static_cast<const T*>(g.a[g.parts > 1 ? 0 : at.part]) + m0 * (kColA ? 1 : g.lda),
@@ -349,18 +351,14 @@ __device__ __forceinline__ void gemm_tile(const Args& g) {
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s)
-    if (s0 + s < s1) load(s0 + s, s);
-  int stage = 0;
+  if (s0 < s1) load(s0, 0);
   for (long s = s0; s < s1; ++s) {
+    const int stage = (int)(s - s0) & 1;
     // this step's loads are done in every wave, and the buffer that the loads
     // below refill has been read by all of them
-    if (s + kStages - 2 < s1) wait_loads<kInFlight * (kStages - 2)>();
-    else wait_loads<0>();
+    wait_loads();
     barrier();
-    const int next = stage == 0 ? kStages - 1 : stage - 1;
-    if (s + kStages - 1 < s1) load(s + kStages - 1, next);
+    if (s + 1 < s1) load(s + 1, stage ^ 1);
     const char* sa = smem + stage * kStageBytes;
     const char* sb = sa + OA::kBytes;
 #pragma unroll
@@ -380,7 +378,6 @@ __device__ __forceinline__ void gemm_tile(const Args& g) {
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = product(fb[ni], fa[mi], acc[mi][ni]);
     }
-    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
 
   // each lane: row lane % 16 of the row blocks, eight columns of each pair of column blocks
@@ -412,11 +409,52 @@ __device__ __forceinline__ void gemm_tile(const Args& g) {
       }
     }
   }
+#endif
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int kStages, bool kColA, bool kColB, int kEpi>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const Args g) {
-  gemm_tile<T, BM, BN, WM, WN, kStages, kColA, kColB, kEpi>(g);
+// Tiles that the products are cut into, by what a launch of them costs. A step
+// (128 bytes of every row) costs a CU about 0.45 us, the meeting of the waves
+// and the latency of LDS, and 1.3 us for each 256 x 256 half outputs (7 us for
+// float ones, whose matrix instructions do a sixteenth of the work in as much
+// time); a tile starts and ends in 2 us and 5 us for as many outputs. Measured,
+// half, 25,600 x 2,048 x 768 with 320, 256, 192 and 128 rows of 256 columns and
+// with 128 x 128: 77, 113, 89, 106 and 98 us (0.94, 1.17, 1.57, 2.34 rounds of
+// the CUs, and 2.34 of two workgroups a CU); 25,600 x 768 x 4,096, gated: 173,
+// 189, 194, 232 and 216.
+enum Tile { k320x256, k256x256, k192x256, k128x256, k128x128, k64x64, kTiles };
+struct TileShape {
+  int m, n;
+  int per_cu;  // workgroups that a CU holds at once
+};
+constexpr TileShape kTileShapes[kTiles] = {{320, 256, 1}, {256, 256, 1}, {192, 256, 1},
+                                           {128, 256, 1}, {128, 128, 2}, {64, 64, 4}};
+constexpr int kCus = 256;
+
+template <typename T>
+float tile_cost(int tile, long M, long N, long others, long steps) {
+  const TileShape s = kTileShapes[tile];
+  const long count = ((M + s.m - 1) / s.m) * ((N + s.n - 1) / s.n) * others;
+  const long slots = (long)kCus * s.per_cu, whole = count / slots, rest = count % slots;
+  const float area = s.m * s.n / 65536.f, per_step = sizeof(T) == 2 ? 1.3f : 7.f;
+  auto round = [&](long on) {  // with `on` workgroups on a CU
+    return steps * (0.45f + per_step * area * on) + 2.f + 5.f * area * on;
+  };
+  return whole * round(s.per_cu) + (rest ? round((rest + kCus - 1) / kCus) : 0.f);
+}
+// Float tiles gain nothing above 128 x 128: the matrix instructions bound them.
+template <typename T>
+constexpr int kFirstTile = sizeof(T) == 2 ? 0 : (int)k128x128;
+
+// M x N outputs, `others` such products at once, `steps` steps each.
+template <typename T>
+int best_tile(long M, long N, long others, long steps) {
+  int best = kFirstTile<T>;
+  float least = tile_cost<T>(best, M, N, others, steps);
+  for (int t = best + 1; t < kTiles; ++t) {
+    const float c = tile_cost<T>(t, M, N, others, steps);
+    if (c < least) least = c, best = t;
+  }
+  return best;
 }
 
 }  // namespace gemm

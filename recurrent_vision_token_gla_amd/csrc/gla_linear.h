@@ -32,12 +32,15 @@ struct GatedArgs {
 };
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s);
 
-// The workspace of a gradient, by byte offsets.
+// The workspace of a gradient, by byte offsets, and how the weights' gradient is
+// cut up: its tiles and the splits of the rows it sums over.
 struct LinearBwdLayout {
   size_t g[2];     // gradients behind the activation, [rows][N] each
   size_t colsum;   // float [parts][N]
   size_t partial;  // float [splits][parts of the weights][N][K]
   size_t total;
+  int tile, splits;
+  long steps, each;
 };
 
 struct LinearBwdArgs {
@@ -49,7 +52,7 @@ struct LinearBwdArgs {
   float* gbias;        // or nullptr
 };
 LinearBwdLayout linear_bwd_layout(long rows, int K, int N, int act, int dtype);
-hipError_t launch_linear_bwd(const LinearBwdArgs& a, char* ws, hipStream_t s);
+hipError_t launch_linear_bwd(const LinearBwdArgs& a, const LinearBwdLayout& l, char* ws, hipStream_t s);
 
 struct GatedBwdArgs {
   long rows;
@@ -58,6 +61,6 @@ struct GatedBwdArgs {
   void *gx, *ggate_weight, *gup_weight;
 };
 LinearBwdLayout gated_bwd_layout(long rows, int K, int F, int dtype);
-hipError_t launch_gated_bwd(const GatedBwdArgs& a, char* ws, hipStream_t s);
+hipError_t launch_gated_bwd(const GatedBwdArgs& a, const LinearBwdLayout& l, char* ws, hipStream_t s);
 
 }  // namespace gla

@@ -88,22 +88,30 @@ hipError_t skinny(const Args& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int kStages, int kEpi>
+template <typename T, int BM, int BN, int WM, int WN, int kEpi>
 hipError_t tiles(Args g, hipStream_t s) {
   constexpr int BNC = kEpi == kGated ? BN / 2 : BN;
   g.tiles_m = (int)((g.M + BM - 1) / BM);
   g.tiles_n = (int)((g.N + BNC - 1) / BNC);
-  hipLaunchKernelGGL((gemm_kernel<T, BM, BN, WM, WN, kStages, false, false, kEpi>),
+  hipLaunchKernelGGL((gemm_kernel<T, BM, BN, WM, WN, false, false, kEpi>),
                      dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(64 * WM * WN), 0, s, g);
   return hipGetLastError();
 }
 
 template <typename T, int kEpi>
 hipError_t forward(const Args& g, hipStream_t s) {
-  if (g.M <= 64) return skinny<T, kEpi == kGated>(g, s);
-  const long n = kEpi == kGated ? 2 * g.N : g.N;
-  if ((g.M + 127) / 128 * ((n + 127) / 128) >= 256) return tiles<T, 128, 128, 2, 2, 2, kEpi>(g, s);
-  return tiles<T, 64, kEpi == kGated ? 128 : 64, 2, 2, 2, kEpi>(g, s);
+  constexpr bool kDual = kEpi == kGated;
+  if (g.M <= 64) return skinny<T, kDual>(g, s);
+  const int tile = best_tile<T>(g.M, kDual ? 2 * g.N : g.N, 1, g.steps);
+  if constexpr (sizeof(T) == 2) {
+    if (tile == k320x256) return tiles<T, 320, 256, 4, 4, kEpi>(g, s);
+    if (tile == k256x256) return tiles<T, 256, 256, 4, 4, kEpi>(g, s);
+    if (tile == k192x256) return tiles<T, 192, 256, 4, 4, kEpi>(g, s);
+    if (tile == k128x256) return tiles<T, 128, 256, 4, 4, kEpi>(g, s);
+  }
+  if (tile == k128x128) return tiles<T, 128, 128, 2, 2, kEpi>(g, s);
+  // the gated product needs two column blocks of each weight in a wave
+  return tiles<T, 64, 64, kDual ? 4 : 2, kDual ? 1 : 2, kEpi>(g, s);
 }
 
 // at most 2^22 rows per launch, so that the grid's numbers fit 32 bits

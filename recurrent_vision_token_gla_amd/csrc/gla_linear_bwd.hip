@@ -94,31 +94,32 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
 // Workgroups that a grid-stride pass over `n` units takes.
 unsigned spread(long n) { return (unsigned)(n < 4096 ? n : 4096); }
 
-// The weights' gradient: output tiles and splits of the rows.
-struct WeightPlan {
-  int tile, splits;
-  long steps, each;
-};
-WeightPlan weight_plan(long rows, int K, int N, int mparts, int dtype) {
-  WeightPlan p;
-  const long step = dtype == 0 ? 64 : 32;
-  p.steps = (rows + step - 1) / step;
-  auto count = [&](long t) { return mparts * ((N + t - 1) / t) * ((K + t - 1) / t); };
-  p.tile = count(128) * ((p.steps + 7) / 8) >= 512 ? 128 : 64;
-  long s = 512 / count(p.tile);
-  if (s > p.steps / 8) s = p.steps / 8;
-  if (s < 1) s = 1;
-  p.each = (p.steps + s - 1) / s;
-  p.splits = (int)((p.steps + p.each - 1) / p.each);
-  return p;
+// The weights' gradient: its tiles, and the splits of its long contraction, by
+// the tiles' cost and that of the partial sums' way through memory (4 TB/s and
+// a launch).
+template <typename T>
+void weight_plan(long rows, int K, int N, int mparts, LinearBwdLayout* l) {
+  const long step = Num<T>::kStep, steps = (rows + step - 1) / step;
+  float least = 0.f;
+  for (long s : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32}) {
+    if (s > 1 && steps < 4 * s) break;
+    const long each = (steps + s - 1) / s, splits = (steps + each - 1) / each;
+    const float join = splits > 1 ? 4.f + 2e-6f * splits * mparts * N * K : 0.f;
+    for (int t = kFirstTile<T>; t < kTiles; ++t) {
+      if (t == k320x256 || t == k192x256 || t == k128x256) continue;
+      const float c = join + tile_cost<T>(t, N, K, mparts * splits, each);
+      if (least == 0.f || c < least) least = c, l->tile = t, l->splits = (int)splits, l->each = each;
+    }
+  }
+  l->steps = steps;
 }
 
-template <typename T, int BM, bool kColA, int kEpi>
+template <typename T, int BM, int BN, int WM, int WN, bool kColA, int kEpi>
 hipError_t tiles(Args g, hipStream_t s) {
   g.tiles_m = (int)((g.M + BM - 1) / BM);
-  g.tiles_n = (int)((g.N + BM - 1) / BM);
-  hipLaunchKernelGGL((gemm_kernel<T, BM, BM, 2, 2, 2, kColA, true, kEpi>),
-                     dim3((unsigned)(g.tiles_m * g.mparts * g.tiles_n * g.splits)), dim3(256), 0, s, g);
+  g.tiles_n = (int)((g.N + BN - 1) / BN);
+  hipLaunchKernelGGL((gemm_kernel<T, BM, BN, WM, WN, kColA, true, kEpi>),
+                     dim3((unsigned)(g.tiles_m * g.mparts * g.tiles_n * g.splits)), dim3(64 * WM * WN), 0, s, g);
   return hipGetLastError();
 }
 
@@ -134,28 +135,42 @@ hipError_t input_gradient(Args g, long rows, int C, int N, int parts, float alph
     g.M = rows - r < most ? rows - r : most;
     for (int p = 0; p < 2; ++p) g.a[p] = a[p] + (a[p] ? r * C : 0);
     g.out[0] = g.out[1] = gx + r * N;
-    const bool big = (g.M + 127) / 128 * ((N + 127) / 128) >= 256;
-    const hipError_t e = big ? tiles<T, 128, false, kLinear>(g, s) : tiles<T, 64, false, kLinear>(g, s);
+    const int t = best_tile<T>(g.M, N, 1, g.steps);
+    hipError_t e;
+    if (t == k128x128) e = tiles<T, 128, 128, 2, 2, false, kLinear>(g, s);
+    else if (t == k64x64) e = tiles<T, 64, 64, 2, 2, false, kLinear>(g, s);
+    else if constexpr (sizeof(T) == 2) {
+      if (t == k320x256) e = tiles<T, 320, 256, 4, 4, false, kLinear>(g, s);
+      else if (t == k256x256) e = tiles<T, 256, 256, 4, 4, false, kLinear>(g, s);
+      else if (t == k192x256) e = tiles<T, 192, 256, 4, 4, false, kLinear>(g, s);
+      else e = tiles<T, 128, 256, 4, 4, false, kLinear>(g, s);
+    }
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
+template <typename T, int kEpi>
+hipError_t weight_tiles(const Args& g, int tile, hipStream_t s) {
+  if constexpr (sizeof(T) == 2)
+    if (tile == k256x256) return tiles<T, 256, 256, 4, 4, true, kEpi>(g, s);
+  if (tile == k128x128) return tiles<T, 128, 128, 2, 2, true, kEpi>(g, s);
+  return tiles<T, 64, 64, 2, 2, true, kEpi>(g, s);
+}
+
 // out[p] = alpha a[p]^T x, a[p] [rows][N], x [rows][K]
 template <typename T>
-hipError_t weight_gradient(Args g, long rows, int K, int N, int mparts, float alpha, float* partial,
-                           hipStream_t s) {
-  const WeightPlan p = weight_plan(rows, K, N, mparts, sizeof(T) == 2 ? 0 : 1);
+hipError_t weight_gradient(Args g, long rows, int K, int N, int mparts, float alpha, const LinearBwdLayout& l,
+                           float* partial, hipStream_t s) {
   g.lda = N, g.ldb = K, g.M = N, g.N = K, g.K = rows, g.alpha = alpha;
-  g.parts = 1, g.mparts = mparts, g.splits = p.splits, g.steps = p.steps, g.each = p.each;
+  g.parts = 1, g.mparts = mparts, g.splits = l.splits, g.steps = l.steps, g.each = l.each;
   g.partial = partial;
-  if (p.splits == 1)
-    return p.tile == 128 ? tiles<T, 128, true, kLinear>(g, s) : tiles<T, 64, true, kLinear>(g, s);
-  hipError_t e = p.tile == 128 ? tiles<T, 128, true, kPartial>(g, s) : tiles<T, 64, true, kPartial>(g, s);
+  if (l.splits == 1) return weight_tiles<T, kLinear>(g, l.tile, s);
+  const hipError_t e = weight_tiles<T, kPartial>(g, l.tile, s);
   if (e != hipSuccess) return e;
   const long per_part = (long)N * K / 8, groups = mparts * per_part;
   hipLaunchKernelGGL((join_kernel<T>), dim3(spread((groups + 255) / 256)), dim3(256), 0, s, partial,
-                     static_cast<T*>(g.out[0]), static_cast<T*>(g.out[1]), alpha, p.splits, groups, per_part);
+                     static_cast<T*>(g.out[0]), static_cast<T*>(g.out[1]), alpha, l.splits, groups, per_part);
   return hipGetLastError();
 }
 
@@ -189,15 +204,15 @@ LinearBwdLayout layout(long rows, int K, int N, int dtype, int sides, bool sums,
   l.colsum = at;
   if (sums) at += pad((size_t)slope_plan(rows, N).parts * N * sizeof(float));
   l.partial = at;
-  const WeightPlan p = weight_plan(rows, K, N, mparts, dtype);
-  if (p.splits > 1) at += pad((size_t)p.splits * mparts * N * K * sizeof(float));
+  if (dtype == 0) weight_plan<half_t>(rows, K, N, mparts, &l);
+  else weight_plan<float>(rows, K, N, mparts, &l);
+  if (l.splits > 1) at += pad((size_t)l.splits * mparts * N * K * sizeof(float));
   l.total = at ? at : 256;
   return l;
 }
 
 template <typename T>
-hipError_t linear_bwd_t(const LinearBwdArgs& a, char* ws, hipStream_t s) {
-  const LinearBwdLayout l = linear_bwd_layout(a.rows, a.K, a.N, a.act, a.dtype);
+hipError_t linear_bwd_t(const LinearBwdArgs& a, const LinearBwdLayout& l, char* ws, hipStream_t s) {
   T* gp = reinterpret_cast<T*>(ws + l.g[0]);
   float* sums = reinterpret_cast<float*>(ws + l.colsum);
   const bool own = a.act != 0;
@@ -228,12 +243,11 @@ hipError_t linear_bwd_t(const LinearBwdArgs& a, char* ws, hipStream_t s) {
   if (!a.gweight) return hipSuccess;
   args.b[0] = args.b[1] = a.x;
   args.out[0] = args.out[1] = a.gweight;
-  return weight_gradient<T>(args, a.rows, a.K, a.N, 1, a.alpha, reinterpret_cast<float*>(ws + l.partial), s);
+  return weight_gradient<T>(args, a.rows, a.K, a.N, 1, a.alpha, l, reinterpret_cast<float*>(ws + l.partial), s);
 }
 
 template <typename T>
-hipError_t gated_bwd_t(const GatedBwdArgs& a, char* ws, hipStream_t s) {
-  const LinearBwdLayout l = gated_bwd_layout(a.rows, a.K, a.F, a.dtype);
+hipError_t gated_bwd_t(const GatedBwdArgs& a, const LinearBwdLayout& l, char* ws, hipStream_t s) {
   T *ga = reinterpret_cast<T*>(ws + l.g[0]), *gu = reinterpret_cast<T*>(ws + l.g[1]);
   const long groups = a.rows * a.F / 8;
   hipLaunchKernelGGL((gated_slope_kernel<T>), dim3(spread((groups + 255) / 256)), dim3(256), 0, s,
@@ -250,7 +264,7 @@ hipError_t gated_bwd_t(const GatedBwdArgs& a, char* ws, hipStream_t s) {
   if (!a.ggate_weight) return hipSuccess;
   args.b[0] = args.b[1] = a.x;
   args.out[0] = a.ggate_weight, args.out[1] = a.gup_weight;
-  return weight_gradient<T>(args, a.rows, a.K, a.F, 2, 1.f, reinterpret_cast<float*>(ws + l.partial), s);
+  return weight_gradient<T>(args, a.rows, a.K, a.F, 2, 1.f, l, reinterpret_cast<float*>(ws + l.partial), s);
 }
 
 }  // namespace gemm
@@ -262,11 +276,11 @@ LinearBwdLayout gated_bwd_layout(long rows, int K, int F, int dtype) {
   return gemm::layout(rows, K, F, dtype, 2, false, 2);
 }
 
-hipError_t launch_linear_bwd(const LinearBwdArgs& a, char* ws, hipStream_t s) {
-  return a.dtype == 0 ? gemm::linear_bwd_t<half_t>(a, ws, s) : gemm::linear_bwd_t<float>(a, ws, s);
+hipError_t launch_linear_bwd(const LinearBwdArgs& a, const LinearBwdLayout& l, char* ws, hipStream_t s) {
+  return a.dtype == 0 ? gemm::linear_bwd_t<half_t>(a, l, ws, s) : gemm::linear_bwd_t<float>(a, l, ws, s);
 }
-hipError_t launch_gated_bwd(const GatedBwdArgs& a, char* ws, hipStream_t s) {
-  return a.dtype == 0 ? gemm::gated_bwd_t<half_t>(a, ws, s) : gemm::gated_bwd_t<float>(a, ws, s);
+hipError_t launch_gated_bwd(const GatedBwdArgs& a, const LinearBwdLayout& l, char* ws, hipStream_t s) {
+  return a.dtype == 0 ? gemm::gated_bwd_t<half_t>(a, l, ws, s) : gemm::gated_bwd_t<float>(a, l, ws, s);
 }
 
 }  // namespace gla
