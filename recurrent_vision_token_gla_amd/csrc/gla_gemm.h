@@ -28,8 +28,9 @@ struct Num {
 
 __device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-__device__ __forceinline__ void wait_loads() {  // of memory and of LDS
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // all but the last N loads, and all LDS reads
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void barrier() {  // no LDS read or load moves across it
@@ -88,30 +89,30 @@ struct Operand {
     }
   }
 
-  // How a thread of NT loads its units of a step.
+  // How thread `tid` of NT, of wave w, loads its units of a step.
   template <int NT>
   struct Loader {
     static constexpr int kUnits = R * 8, kLoads = (kUnits + NT - 1) / NT;
     static_assert(kUnits % 64 == 0, "whole waves load");
     unsigned off[kLoads];  // bytes from the step's first element
     // left: rows (columns) of the tile that exist
-    __device__ __forceinline__ void init(long left, long ld) {
+    __device__ __forceinline__ void init(long left, long ld, int tid) {
 #pragma unroll
       for (int it = 0; it < kLoads; ++it) {
-        const int j = threadIdx.x + NT * it, row = j / kPerRow, unit = (j % kPerRow) ^ twist(row);
+        const int j = tid + NT * it, row = j / kPerRow, unit = (j % kPerRow) ^ twist(row);
         const bool in = kCol ? unit * kUnit < left : row < left;
         off[it] = in ? (unsigned)((row * ld + unit * kUnit) * (long)sizeof(T)) : kOut;
       }
     }
     // unit `it` of the step at base, of which `left` elements of the
     // contraction exist
-    __device__ __forceinline__ void one(const void* base, long left, char* lds, int it) const {
-      const int j = threadIdx.x + NT * it, row = j / kPerRow, unit = (j % kPerRow) ^ twist(row);
+    __device__ __forceinline__ void one(const void* base, long left, char* lds, int it, int tid, int w) const {
+      const int j = tid + NT * it, row = j / kPerRow, unit = (j % kPerRow) ^ twist(row);
       const bool in = left >= kStep || (kCol ? row : unit * kUnit) < left;
-      if (NT * it + 64 * wave() >= kUnits) return;  // the last round may be some waves'
+      if (NT * it + 64 * w >= kUnits) return;  // the last round may be some waves'
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000),
-          (__attribute__((address_space(3))) void*)(lds + 16 * (NT * it + 64 * wave())), 16,
+          (__attribute__((address_space(3))) void*)(lds + 16 * (NT * it + 64 * w)), 16,
           in ? off[it] : kOut, 0, 0, 0);
     }
   };
@@ -291,8 +292,11 @@ struct Place {
   }
 };
 
-template <typename T, int BM, int BN, int WM, int WN, bool kColA, bool kColB, int kEpi>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const Args g) {
+// kStages steps of LDS: one is multiplied while the others are on their way.
+// kGroups: the workgroup's waves form as many groups, which take a part of the
+// steps each and add their sums up at the end (few tiles, a long contraction).
+template <typename T, int BM, int BN, int WM, int WN, int kStages, int kGroups, bool kColA, bool kColB, int kEpi>
+__global__ __launch_bounds__(64 * WM * WN * kGroups) void gemm_kernel(const Args g) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host's pass does not take the loads' builtin in a template
   constexpr int NT = 64 * WM * WN, MI = BM / WM / 16, NI = BN / WN / 16;
   constexpr bool kDual = kEpi == kGated;  // columns: BN/2 of b[0], then BN/2 of b[1]
@@ -304,28 +308,34 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const Args g) {
   using Frag = typename std::conditional<sizeof(T) == 2, half8, floatx4>::type;
   constexpr int kStep = Num<T>::kStep, kStageBytes = OA::kBytes + OB::kBytes;
   static_assert(!kDual || !kColB, "both sides of a gated product lie along the contraction");
-  const int wm = wave() / WN, wn = wave() % WN;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * kStageBytes];
+  constexpr int kInFlight = LA::kLoads + LB::kLoads;
+  static_assert(kStages == 2 || (LA::kUnits % NT == 0 && LB::kUnits % NT == 0), "as many loads in every wave");
+  const int group = wave() / (WM * WN), w = wave() % (WM * WN), wm = w / WN, wn = w % WN;
+  const int tid = threadIdx.x % NT;
+  __shared__ __attribute__((aligned(1024))) char shared[kGroups * kStages * kStageBytes];
+  char* const smem = shared + group * kStages * kStageBytes;
   const Place at(g, BM, BNC);
   const long m0 = at.m0, n0 = at.n0;
   const long steps_part = g.steps / g.parts;
-  const long s0 = at.split * g.each, s1 = min(s0 + g.each, g.steps);
+  const long from = at.split * g.each, to = min(from + g.each, g.steps);
+  const long rounds = (to - from + kGroups - 1) / kGroups;  // of each group
+  const long s0 = from + group * rounds, s1 = min(s0 + rounds, to);
   const T* pa[2] = {static_cast<const T*>(g.a[g.parts > 1 ? 0 : at.part]) + m0 * (kColA ? 1 : g.lda),
                     static_cast<const T*>(g.a[1]) + m0 * (kColA ? 1 : g.lda)};
   const T* pb[2] = {static_cast<const T*>(g.b[0]) + n0 * (kColB ? 1 : g.ldb),
                     static_cast<const T*>(g.b[1]) + n0 * (kColB ? 1 : g.ldb)};
   LA la;
   LB lb;
-  la.init(g.M - m0, g.lda);
+  la.init(g.M - m0, g.lda, tid);
   if constexpr (kDual) {
     // rows 0 .. BN/2 - 1 of the tile are b[0]'s, the others b[1]'s
 #pragma unroll
     for (int it = 0; it < LB::kLoads; ++it) {
-      const int j = threadIdx.x + NT * it, row = j / 8 % BNC, unit = (j % 8) ^ OB::twist(row);
+      const int j = tid + NT * it, row = j / 8 % BNC, unit = (j % 8) ^ OB::twist(row);
       lb.off[it] = row < g.N - n0 ? (unsigned)((row * g.ldb + unit * Num<T>::kUnit) * (long)sizeof(T)) : kOut;
     }
   } else {
-    lb.init(g.N - n0, g.ldb);
+    lb.init(g.N - n0, g.ldb, tid);
   }
   auto load = [&](long s, int stage) {
     const int p = g.parts > 1 && s >= steps_part;
@@ -333,16 +343,16 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const Args g) {
     char* lds = smem + stage * kStageBytes;
     const T* ra = pa[p] + k0 * (kColA ? g.lda : 1);
 #pragma unroll
-    for (int it = 0; it < LA::kLoads; ++it) la.one(ra, left, lds, it);
+    for (int it = 0; it < LA::kLoads; ++it) la.one(ra, left, lds, it, tid, w);
     if constexpr (kDual) {
       const T *rg = pb[0] + k0, *ru = pb[1] + k0;
 #pragma unroll
       for (int it = 0; it < LB::kLoads; ++it)
-        lb.one(it < LB::kLoads / 2 ? rg : ru, left, lds + OA::kBytes, it);
+        lb.one(it < LB::kLoads / 2 ? rg : ru, left, lds + OA::kBytes, it, tid, w);
     } else {
       const T* rb = pb[p] + k0 * (kColB ? g.ldb : 1);
 #pragma unroll
-      for (int it = 0; it < LB::kLoads; ++it) lb.one(rb, left, lds + OA::kBytes, it);
+      for (int it = 0; it < LB::kLoads; ++it) lb.one(rb, left, lds + OA::kBytes, it, tid, w);
     }
   };
   floatx4 acc[MI][NI];
@@ -351,14 +361,19 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const Args g) {
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  if (s0 < s1) load(s0, 0);
-  for (long s = s0; s < s1; ++s) {
-    const int stage = (int)(s - s0) & 1;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s)
+    if (s0 + s < s1) load(s0 + s, s);
+  for (long round = 0; round < rounds; ++round) {
+    const long s = s0 + round;
+    const int stage = (int)round % kStages;
     // this step's loads are done in every wave, and the buffer that the loads
     // below refill has been read by all of them
-    wait_loads();
+    if (s + kStages - 2 < s1) wait_loads<kInFlight * (kStages - 2)>();
+    else wait_loads<0>();
     barrier();
-    if (s + 1 < s1) load(s + 1, stage ^ 1);
+    if (s + kStages - 1 < s1) load(s + kStages - 1, (stage + kStages - 1) % kStages);
+    if (kGroups > 1 && s >= s1) continue;  // the last group may have fewer steps
     const char* sa = smem + stage * kStageBytes;
     const char* sb = sa + OA::kBytes;
 #pragma unroll
@@ -378,6 +393,25 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const Args g) {
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = product(fb[ni], fa[mi], acc[mi][ni]);
     }
+  }
+
+  if constexpr (kGroups > 1) {
+    static_assert((kGroups - 1) * BM * BN * 4 <= kGroups * kStages * kStageBytes, "sums fit");
+    floatx4* const sums = reinterpret_cast<floatx4*>(shared);
+    __syncthreads();  // the buffers are read
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+        if (group > 0) sums[((group - 1) * MI * NI + mi * NI + ni) * NT + tid] = acc[mi][ni];
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int o = 0; o < kGroups - 1; ++o)
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) acc[mi][ni] += sums[(o * MI * NI + mi * NI + ni) * NT + tid];
   }
 
   // each lane: row lane % 16 of the row blocks, eight columns of each pair of column blocks
@@ -421,13 +455,14 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const Args g) {
 // with 128 x 128: 77, 113, 89, 106 and 98 us (0.94, 1.17, 1.57, 2.34 rounds of
 // the CUs, and 2.34 of two workgroups a CU); 25,600 x 768 x 4,096, gated: 173,
 // 189, 194, 232 and 216.
-enum Tile { k320x256, k256x256, k192x256, k128x256, k128x128, k64x64, kTiles };
+enum Tile { k320x256, k256x256, k192x256, k128x256, k128x128, k64x64, k64x64by2, k64x64by4, kTiles };
 struct TileShape {
   int m, n;
   int per_cu;  // workgroups that a CU holds at once
+  int groups;  // of waves that share a tile's steps
 };
-constexpr TileShape kTileShapes[kTiles] = {{320, 256, 1}, {256, 256, 1}, {192, 256, 1},
-                                           {128, 256, 1}, {128, 128, 2}, {64, 64, 4}};
+constexpr TileShape kTileShapes[kTiles] = {{320, 256, 1, 1}, {256, 256, 1, 1}, {192, 256, 1, 1}, {128, 256, 1, 1},
+                                           {128, 128, 2, 1}, {64, 64, 2, 1},   {64, 64, 1, 2},   {64, 64, 1, 4}};
 constexpr int kCus = 256;
 
 template <typename T>
@@ -437,7 +472,8 @@ float tile_cost(int tile, long M, long N, long others, long steps) {
   const long slots = (long)kCus * s.per_cu, whole = count / slots, rest = count % slots;
   const float area = s.m * s.n / 65536.f, per_step = sizeof(T) == 2 ? 1.3f : 7.f;
   auto round = [&](long on) {  // with `on` workgroups on a CU
-    return steps * (0.45f + per_step * area * on) + 2.f + 5.f * area * on;
+    return (steps + s.groups - 1) / s.groups * (0.45f + per_step * area * on * s.groups) + 2.f + 5.f * area * on +
+           0.5f * (s.groups - 1);
   };
   return whole * round(s.per_cu) + (rest ? round((rest + kCus - 1) / kCus) : 0.f);
 }
@@ -456,6 +492,40 @@ int best_tile(long M, long N, long others, long steps) {
   }
   return best;
 }
+
+template <typename T, int BM, int BN, int WM, int WN, int kStages, int kGroups, bool kColA, bool kColB, int kEpi>
+hipError_t launch_tiles(Args g, hipStream_t s) {
+  constexpr int BNC = kEpi == kGated ? BN / 2 : BN;
+  g.tiles_m = (int)((g.M + BM - 1) / BM);
+  g.tiles_n = (int)((g.N + BNC - 1) / BNC);
+  hipLaunchKernelGGL((gemm_kernel<T, BM, BN, WM, WN, kStages, kGroups, kColA, kColB, kEpi>),
+                     dim3((unsigned)(g.tiles_m * g.mparts * g.tiles_n * g.splits)),
+                     dim3(64 * WM * WN * kGroups), 0, s, g);
+  return hipGetLastError();
+}
+
+// One product on tiles of the given kind (those above 128 x 128: half, and not
+// for every layout).
+template <typename T, bool kColA, bool kColB, int kEpi>
+hipError_t launch_product(const Args& g, int tile, hipStream_t s) {
+  // the gated product needs two column blocks of each weight in a wave
+  constexpr int m = kEpi == kGated ? 4 : 2, n = kEpi == kGated ? 1 : 2;
+  if constexpr (sizeof(T) == 2 && !kColB) {
+    if (tile == k320x256) return launch_tiles<T, 320, 256, 4, 4, 2, 1, kColA, kColB, kEpi>(g, s);
+    if (tile == k192x256) return launch_tiles<T, 192, 256, 4, 4, 2, 1, kColA, kColB, kEpi>(g, s);
+    if (tile == k128x256) return launch_tiles<T, 128, 256, 4, 4, 2, 1, kColA, kColB, kEpi>(g, s);
+  }
+  if constexpr (sizeof(T) == 2 && kColA == kColB)
+    if (tile == k256x256) return launch_tiles<T, 256, 256, 4, 4, 2, 1, kColA, kColB, kEpi>(g, s);
+  if (tile == k128x128) return launch_tiles<T, 128, 128, 2, 2, 2, 1, kColA, kColB, kEpi>(g, s);
+  if (tile == k64x64by4) return launch_tiles<T, 64, 64, m, n, 2, 4, kColA, kColB, kEpi>(g, s);
+  if (tile == k64x64by2) return launch_tiles<T, 64, 64, m, n, 4, 2, kColA, kColB, kEpi>(g, s);
+  return launch_tiles<T, 64, 64, m, n, 4, 1, kColA, kColB, kEpi>(g, s);
+}
+
+// y = alpha act(sum of a[p] b[p]^T + bias) + residual, or the gated product, of
+// any number of rows: both operands lie along the contraction (gla_linear.hip).
+hipError_t products(const Args& g, bool gated, int dtype, hipStream_t s);
 
 }  // namespace gemm
 }  // namespace gla

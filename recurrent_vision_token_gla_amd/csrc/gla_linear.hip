@@ -88,53 +88,34 @@ hipError_t skinny(const Args& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int kEpi>
-hipError_t tiles(Args g, hipStream_t s) {
-  constexpr int BNC = kEpi == kGated ? BN / 2 : BN;
-  g.tiles_m = (int)((g.M + BM - 1) / BM);
-  g.tiles_n = (int)((g.N + BNC - 1) / BNC);
-  hipLaunchKernelGGL((gemm_kernel<T, BM, BN, WM, WN, false, false, kEpi>),
-                     dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(64 * WM * WN), 0, s, g);
-  return hipGetLastError();
-}
-
 template <typename T, int kEpi>
 hipError_t forward(const Args& g, hipStream_t s) {
   constexpr bool kDual = kEpi == kGated;
-  if (g.M <= 64) return skinny<T, kDual>(g, s);
-  const int tile = best_tile<T>(g.M, kDual ? 2 * g.N : g.N, 1, g.steps);
-  if constexpr (sizeof(T) == 2) {
-    if (tile == k320x256) return tiles<T, 320, 256, 4, 4, kEpi>(g, s);
-    if (tile == k256x256) return tiles<T, 256, 256, 4, 4, kEpi>(g, s);
-    if (tile == k192x256) return tiles<T, 192, 256, 4, 4, kEpi>(g, s);
-    if (tile == k128x256) return tiles<T, 128, 256, 4, 4, kEpi>(g, s);
-  }
-  if (tile == k128x128) return tiles<T, 128, 128, 2, 2, kEpi>(g, s);
-  // the gated product needs two column blocks of each weight in a wave
-  return tiles<T, 64, 64, kDual ? 4 : 2, kDual ? 1 : 2, kEpi>(g, s);
+  if (g.M <= 64 && g.parts == 1) return skinny<T, kDual>(g, s);
+  return launch_product<T, false, false, kEpi>(g, best_tile<T>(g.M, kDual ? 2 * g.N : g.N, 1, g.steps), s);
 }
 
 // at most 2^22 rows per launch, so that the grid's numbers fit 32 bits
-template <int kEpi>
-hipError_t in_bands(Args g, int dtype, hipStream_t s) {
+hipError_t products(const Args& all, bool gated, int dtype, hipStream_t s) {
   constexpr long most = 1L << 22;
-  const long M = g.M, es = dtype == 0 ? 2 : 4;
+  const long es = dtype == 0 ? 2 : 4;
   auto on = [&](auto* p, long rows, long width) {
     return p ? (decltype(p))((uintptr_t)p + (size_t)(rows * width * es)) : p;
   };
-  const Args all = g;
-  g.lda = g.ldb = g.K;
-  g.parts = g.mparts = g.splits = 1;
-  g.steps = g.each = (g.K * es + 127) / 128;
-  for (long r = 0; r < M; r += most) {
-    g.M = M - r < most ? M - r : most;
-    g.a[0] = g.a[1] = on(all.a[0], r, g.K);
-    g.out[0] = g.out[1] = on(all.out[0], r, g.N);
+  Args g = all;
+  g.mparts = g.splits = 1;
+  g.steps = g.each = g.parts * ((g.K * es + 127) / 128);
+  for (long r = 0; r < all.M; r += most) {
+    g.M = all.M - r < most ? all.M - r : most;
+    for (int p = 0; p < 2; ++p) g.a[p] = on(all.a[p], r, g.lda);
+    g.out[0] = on(all.out[0], r, g.N);
     g.pre = on(all.pre, r, g.N);
     g.residual = on(all.residual, r, g.N);
     g.gate_out = on(all.gate_out, r, g.N);
     g.up_out = on(all.up_out, r, g.N);
-    const hipError_t e = dtype == 0 ? forward<half_t, kEpi>(g, s) : forward<float, kEpi>(g, s);
+    hipError_t e;
+    if (gated) e = dtype == 0 ? forward<half_t, kGated>(g, s) : forward<float, kGated>(g, s);
+    else e = dtype == 0 ? forward<half_t, kLinear>(g, s) : forward<float, kLinear>(g, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -144,18 +125,18 @@ hipError_t in_bands(Args g, int dtype, hipStream_t s) {
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   gemm::Args g = {};
-  g.a[0] = a.x, g.b[0] = g.b[1] = a.weight, g.out[0] = a.y;
-  g.M = a.rows, g.N = a.N, g.K = a.K;
+  g.a[0] = a.x, g.b[0] = a.weight, g.out[0] = a.y;
+  g.M = a.rows, g.N = a.N, g.K = g.lda = g.ldb = a.K, g.parts = 1;
   g.pre = a.pre, g.bias = a.bias, g.residual = a.residual, g.alpha = a.alpha, g.act = a.act;
-  return gemm::in_bands<gemm::kLinear>(g, a.dtype, s);
+  return gemm::products(g, false, a.dtype, s);
 }
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
   gemm::Args g = {};
   g.a[0] = a.x, g.b[0] = a.gate_weight, g.b[1] = a.up_weight, g.out[0] = a.h;
-  g.M = a.rows, g.N = a.F, g.K = a.K;
+  g.M = a.rows, g.N = a.F, g.K = g.lda = g.ldb = a.K, g.parts = 1;
   g.gate_out = a.gate_out, g.up_out = a.up_out, g.act = a.act;
-  return gemm::in_bands<gemm::kGated>(g, a.dtype, s);
+  return gemm::products(g, true, a.dtype, s);
 }
 
 }  // namespace gla
