@@ -38,6 +38,14 @@ __device__ __forceinline__ void barrier() {  // no LDS read or load moves across
   asm volatile("" ::: "memory");
 }
 
+// The transposing read of a tile's rows (tile::ld_tr), told apart from the loads
+// that write LDS: `restrict` gives it a scope of its own, without which the
+// compiler waits for every load in flight before each such read. The waits that
+// it needs stand at the barriers.
+__device__ __forceinline__ half4 read_turned(tile::lds_fp16x4_t* __restrict__ p) {
+  return __builtin_bit_cast(half4, __builtin_amdgcn_ds_read_tr16_b64_v4f16(p));
+}
+
 // One operand's R rows (or columns) of a step in LDS, R * 128 bytes, in 16-byte
 // units. Stored along the contraction: R rows of 8 units, unit u of row r in
 // slot u ^ (r mod 8), so that the 16 rows a fragment reads lie in distinct
@@ -69,7 +77,7 @@ struct Operand {
       for (int p = 0; p < 2; ++p) {
         const int row = 32 * ks + 8 * q + 4 * p + (i >> 2), col = r0 + 4 * (i & 3);
         const char* at = lds + row * (2 * R) + 16 * ((col >> 3) ^ twist(row)) + 2 * (col & 7);
-        h[p] = __builtin_bit_cast(half4, __builtin_amdgcn_ds_read_tr16_b64_v4f16((tile::lds_fp16x4_t*)at));
+        h[p] = read_turned((tile::lds_fp16x4_t*)at);
       }
       x = half8{h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
     }
@@ -94,26 +102,27 @@ struct Operand {
   struct Loader {
     static constexpr int kUnits = R * 8, kLoads = (kUnits + NT - 1) / NT;
     static_assert(kUnits % 64 == 0, "whole waves load");
-    unsigned off[kLoads];  // bytes from the step's first element
-    // left: rows (columns) of the tile that exist
-    __device__ __forceinline__ void init(long left, long ld, int tid) {
+    // bytes from a whole step's first element, and from the last one's, of which
+    // `tail` elements of the contraction exist
+    unsigned off[kLoads], last[kLoads];
+    // left: rows (columns) of the tile that exist; wrap: rows that lie
+    // one behind the other in memory (a tile of two operands has two such runs)
+    __device__ __forceinline__ void init(long left, long ld, int tail, int tid, int wrap = R) {
 #pragma unroll
       for (int it = 0; it < kLoads; ++it) {
         const int j = tid + NT * it, row = j / kPerRow, unit = (j % kPerRow) ^ twist(row);
-        const bool in = kCol ? unit * kUnit < left : row < left;
-        off[it] = in ? (unsigned)((row * ld + unit * kUnit) * (long)sizeof(T)) : kOut;
+        const int at = kCol ? row : row % wrap;
+        const bool in = kCol ? unit * kUnit < left : at < left;
+        off[it] = in ? (unsigned)((at * ld + unit * kUnit) * (long)sizeof(T)) : kOut;
+        last[it] = (kCol ? row : unit * kUnit) < tail ? off[it] : kOut;
       }
     }
-    // unit `it` of the step at base, of which `left` elements of the
-    // contraction exist
-    __device__ __forceinline__ void one(const void* base, long left, char* lds, int it, int tid, int w) const {
-      const int j = tid + NT * it, row = j / kPerRow, unit = (j % kPerRow) ^ twist(row);
-      const bool in = left >= kStep || (kCol ? row : unit * kUnit) < left;
+    __device__ __forceinline__ void one(const char* base, bool ends, char* lds, int it, int w) const {
       if (NT * it + 64 * w >= kUnits) return;  // the last round may be some waves'
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000),
-          (__attribute__((address_space(3))) void*)(lds + 16 * (NT * it + 64 * w)), 16,
-          in ? off[it] : kOut, 0, 0, 0);
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, 0x7fffffff, 0x00020000),
+          (__attribute__((address_space(3))) void*)(lds + 16 * (NT * it + 64 * w)), 16, ends ? last[it] : off[it],
+          0, 0, 0);
     }
   };
 };
@@ -316,43 +325,39 @@ __global__ __launch_bounds__(64 * WM * WN * kGroups) void gemm_kernel(const Args
   char* const smem = shared + group * kStages * kStageBytes;
   const Place at(g, BM, BNC);
   const long m0 = at.m0, n0 = at.n0;
-  const long steps_part = g.steps / g.parts;
-  const long from = at.split * g.each, to = min(from + g.each, g.steps);
-  const long rounds = (to - from + kGroups - 1) / kGroups;  // of each group
-  const long s0 = from + group * rounds, s1 = min(s0 + rounds, to);
-  const T* pa[2] = {static_cast<const T*>(g.a[g.parts > 1 ? 0 : at.part]) + m0 * (kColA ? 1 : g.lda),
-                    static_cast<const T*>(g.a[1]) + m0 * (kColA ? 1 : g.lda)};
-  const T* pb[2] = {static_cast<const T*>(g.b[0]) + n0 * (kColB ? 1 : g.ldb),
-                    static_cast<const T*>(g.b[1]) + n0 * (kColB ? 1 : g.ldb)};
+  // this group's steps, and the step that its next loads are of: number k of
+  // its part of the contraction, at pa and pb
+  const int from = at.split * (int)g.each, to = min(from + (int)g.each, (int)g.steps);
+  const int rounds = (to - from + kGroups - 1) / kGroups, s0 = from + group * rounds;
+  const int todo = max(min(rounds, to - s0), 0), of_part = (int)g.steps / g.parts;
+  constexpr bool kParts = kEpi == kLinear && !kColA;  // the contraction may have two
+  const bool second = kParts && s0 >= of_part;
+  int k = second ? s0 - of_part : s0;
+  const long da = (kColA ? kStep * g.lda : kStep) * (long)sizeof(T), db = (kColB ? kStep * g.ldb : kStep) * (long)sizeof(T);
+  auto start = [](const void* p, long first, bool col, long ld) {
+    return static_cast<const char*>(p) + first * (col ? 1 : ld) * (long)sizeof(T);
+  };
+  const char* pa = start(g.a[second ? 1 : at.part], m0, kColA, g.lda) + k * da;
+  const char* pb = start(g.b[second], n0, kColB, g.ldb) + k * db;
+  const char* pu = kDual ? start(g.b[1], n0, false, g.ldb) + k * db : nullptr;
+  const int tail = (int)(g.K - (of_part - 1) * (long)kStep);
   LA la;
   LB lb;
-  la.init(g.M - m0, g.lda, tid);
-  if constexpr (kDual) {
-    // rows 0 .. BN/2 - 1 of the tile are b[0]'s, the others b[1]'s
-#pragma unroll
-    for (int it = 0; it < LB::kLoads; ++it) {
-      const int j = tid + NT * it, row = j / 8 % BNC, unit = (j % 8) ^ OB::twist(row);
-      lb.off[it] = row < g.N - n0 ? (unsigned)((row * g.ldb + unit * Num<T>::kUnit) * (long)sizeof(T)) : kOut;
-    }
-  } else {
-    lb.init(g.N - n0, g.ldb, tid);
-  }
-  auto load = [&](long s, int stage) {
-    const int p = g.parts > 1 && s >= steps_part;
-    const long k0 = (p ? s - steps_part : s) * kStep, left = g.K - k0;
+  la.init(g.M - m0, g.lda, tail, tid);
+  lb.init(g.N - n0, g.ldb, tail, tid, BNC);
+  auto load = [&](int stage) {
+    const bool ends = k == of_part - 1;
     char* lds = smem + stage * kStageBytes;
-    const T* ra = pa[p] + k0 * (kColA ? g.lda : 1);
 #pragma unroll
-    for (int it = 0; it < LA::kLoads; ++it) la.one(ra, left, lds, it, tid, w);
-    if constexpr (kDual) {
-      const T *rg = pb[0] + k0, *ru = pb[1] + k0;
+    for (int it = 0; it < LA::kLoads; ++it) la.one(pa, ends, lds, it, w);
 #pragma unroll
-      for (int it = 0; it < LB::kLoads; ++it)
-        lb.one(it < LB::kLoads / 2 ? rg : ru, left, lds + OA::kBytes, it, tid, w);
-    } else {
-      const T* rb = pb[p] + k0 * (kColB ? g.ldb : 1);
-#pragma unroll
-      for (int it = 0; it < LB::kLoads; ++it) lb.one(rb, left, lds + OA::kBytes, it, tid, w);
+    for (int it = 0; it < LB::kLoads; ++it)
+      lb.one(kDual && it >= LB::kLoads / 2 ? pu : pb, ends, lds + OA::kBytes, it, w);
+    pa += da, pb += db, pu += db, ++k;
+    if (kParts && k == of_part && g.parts > 1) {
+      k = 0;
+      pa = start(g.a[1], m0, kColA, g.lda);
+      pb = start(g.b[1], n0, kColB, g.ldb);
     }
   };
   floatx4 acc[MI][NI];
@@ -363,17 +368,16 @@ __global__ __launch_bounds__(64 * WM * WN * kGroups) void gemm_kernel(const Args
 
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s)
-    if (s0 + s < s1) load(s0 + s, s);
-  for (long round = 0; round < rounds; ++round) {
-    const long s = s0 + round;
-    const int stage = (int)round % kStages;
+    if (s < todo) load(s);
+  int stage = 0;
+  for (int r = 0; r < rounds; ++r) {
     // this step's loads are done in every wave, and the buffer that the loads
     // below refill has been read by all of them
-    if (s + kStages - 2 < s1) wait_loads<kInFlight * (kStages - 2)>();
+    if (kStages > 2 && r + kStages - 2 < todo) wait_loads<kInFlight * (kStages - 2)>();
     else wait_loads<0>();
     barrier();
-    if (s + kStages - 1 < s1) load(s + kStages - 1, (stage + kStages - 1) % kStages);
-    if (kGroups > 1 && s >= s1) continue;  // the last group may have fewer steps
+    if (r + kStages - 1 < todo) load(stage == 0 ? kStages - 1 : stage - 1);
+    if (kGroups > 1 && r >= todo) continue;  // the last group may have fewer steps
     const char* sa = smem + stage * kStageBytes;
     const char* sb = sa + OA::kBytes;
 #pragma unroll
@@ -393,6 +397,7 @@ __global__ __launch_bounds__(64 * WM * WN * kGroups) void gemm_kernel(const Args
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = product(fb[ni], fa[mi], acc[mi][ni]);
     }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
 
   if constexpr (kGroups > 1) {
@@ -446,50 +451,62 @@ __global__ __launch_bounds__(64 * WM * WN * kGroups) void gemm_kernel(const Args
 #endif
 }
 
-// Tiles that the products are cut into, by what a launch of them costs. A step
-// (128 bytes of every row) costs a CU about 0.45 us, the meeting of the waves
-// and the latency of LDS, and 1.3 us for each 256 x 256 half outputs (7 us for
-// float ones, whose matrix instructions do a sixteenth of the work in as much
-// time); a tile starts and ends in 2 us and 5 us for as many outputs. Measured,
-// half, 25,600 x 2,048 x 768 with 320, 256, 192 and 128 rows of 256 columns and
-// with 128 x 128: 77, 113, 89, 106 and 98 us (0.94, 1.17, 1.57, 2.34 rounds of
-// the CUs, and 2.34 of two workgroups a CU); 25,600 x 768 x 4,096, gated: 173,
-// 189, 194, 232 and 216.
-enum Tile { k320x256, k256x256, k192x256, k128x256, k128x128, k64x64, k64x64by2, k64x64by4, kTiles };
+// Tiles that the products are cut into, by what a launch of them costs, in us. A
+// step (128 bytes of every row) costs a CU about 0.28, the meeting of the waves
+// and the latency of LDS, and 1.3 for each 256 x 256 half outputs (7 for float
+// ones, whose matrix instructions do a sixteenth of the work in as much time); a
+// tile starts and ends in 2 and 5 for as many outputs, and groups of waves add
+// their sums up. Within 20% of what was measured over 100 to 25,600 rows of 100
+// to 4,096 values. Half, 25,600 x 2,048 x 768 with 320, 256, 192 and 128 rows
+// of 256 columns: 77, 107, 90 and 106 (0.94, 1.17, 1.57 and 2.34 rounds of the
+// CUs); 1,600 x 768 x 768 with 128 x 128 12.7, 64 x 64 8.5, by two groups 11.3;
+// 130 x 768 x 768 11.8, 6.4, 6.1, and with 32 x 32 by four groups 5.0.
+enum Tile { k320x256, k256x256, k192x256, k128x256, k128x128, k64x64, k64x64by2, k64x64by4,
+            k32x32by4, k32x32by8, kTiles };
 struct TileShape {
   int m, n;
   int per_cu;  // workgroups that a CU holds at once
   int groups;  // of waves that share a tile's steps
 };
 constexpr TileShape kTileShapes[kTiles] = {{320, 256, 1, 1}, {256, 256, 1, 1}, {192, 256, 1, 1}, {128, 256, 1, 1},
-                                           {128, 128, 2, 1}, {64, 64, 2, 1},   {64, 64, 1, 2},   {64, 64, 1, 4}};
+                                           {128, 128, 2, 1}, {64, 64, 2, 1},   {64, 64, 1, 2},   {64, 64, 1, 4},
+                                           {32, 32, 2, 4},   {32, 32, 1, 8}};
 constexpr int kCus = 256;
 
 template <typename T>
 float tile_cost(int tile, long M, long N, long others, long steps) {
   const TileShape s = kTileShapes[tile];
   const long count = ((M + s.m - 1) / s.m) * ((N + s.n - 1) / s.n) * others;
-  const long slots = (long)kCus * s.per_cu, whole = count / slots, rest = count % slots;
+  const int per_cu = sizeof(T) == 4 && tile == k64x64 ? 4 : s.per_cu;  // two stages instead of four
+  const long slots = (long)kCus * per_cu, whole = count / slots, rest = count % slots;
   const float area = s.m * s.n / 65536.f, per_step = sizeof(T) == 2 ? 1.3f : 7.f;
   auto round = [&](long on) {  // with `on` workgroups on a CU
-    return (steps + s.groups - 1) / s.groups * (0.45f + per_step * area * on * s.groups) + 2.f + 5.f * area * on +
-           0.5f * (s.groups - 1);
+    return (steps + s.groups - 1) / s.groups * (0.28f + per_step * area * on * s.groups) + 2.f + 5.f * area * on +
+           (s.groups - 1) * (0.25f + 8.f * area);
   };
-  return whole * round(s.per_cu) + (rest ? round((rest + kCus - 1) / kCus) : 0.f);
+  return whole * round(per_cu) + (rest ? round((rest + kCus - 1) / kCus) : 0.f);
 }
 // Float tiles gain nothing above 128 x 128: the matrix instructions bound them.
-template <typename T>
-constexpr int kFirstTile = sizeof(T) == 2 ? 0 : (int)k128x128;
+// The weights' gradients take no others of 256 columns than 256 x 256 (320 rows
+// need more registers than there are).
+template <typename T, bool kColA, int kEpi>
+constexpr bool has_tile(int t) {
+  if (t < k128x128) return sizeof(T) == 2 && (!kColA || t == k256x256);
+  return t < k32x32by4 || kEpi != kGated;  // the gated product needs two column blocks of each weight in a wave
+}
 
-// M x N outputs, `others` such products at once, `steps` steps each.
-template <typename T>
-int best_tile(long M, long N, long others, long steps) {
-  int best = kFirstTile<T>;
-  float least = tile_cost<T>(best, M, N, others, steps);
-  for (int t = best + 1; t < kTiles; ++t) {
+// M x N outputs, `others` such products at once, `steps` steps each; what it
+// costs in *cost.
+template <typename T, bool kColA, int kEpi>
+int best_tile(long M, long N, long others, long steps, float* cost = nullptr) {
+  int best = -1;
+  float least = 0.f;
+  for (int t = 0; t < kTiles; ++t) {
+    if (!has_tile<T, kColA, kEpi>(t)) continue;
     const float c = tile_cost<T>(t, M, N, others, steps);
-    if (c < least) least = c, best = t;
+    if (best < 0 || c < least) least = c, best = t;
   }
+  if (cost) *cost = least;
   return best;
 }
 
@@ -504,28 +521,26 @@ hipError_t launch_tiles(Args g, hipStream_t s) {
   return hipGetLastError();
 }
 
-// One product on tiles of the given kind (those above 128 x 128: half, and not
-// for every layout).
+// One product on tiles of the given kind.
 template <typename T, bool kColA, bool kColB, int kEpi>
 hipError_t launch_product(const Args& g, int tile, hipStream_t s) {
-  // the gated product needs two column blocks of each weight in a wave
-  constexpr int m = kEpi == kGated ? 4 : 2, n = kEpi == kGated ? 1 : 2;
-  if constexpr (sizeof(T) == 2 && !kColB) {
-    if (tile == k320x256) return launch_tiles<T, 320, 256, 4, 4, 2, 1, kColA, kColB, kEpi>(g, s);
-    if (tile == k192x256) return launch_tiles<T, 192, 256, 4, 4, 2, 1, kColA, kColB, kEpi>(g, s);
-    if (tile == k128x256) return launch_tiles<T, 128, 256, 4, 4, 2, 1, kColA, kColB, kEpi>(g, s);
-  }
-  if constexpr (sizeof(T) == 2 && kColA == kColB)
-    if (tile == k256x256) return launch_tiles<T, 256, 256, 4, 4, 2, 1, kColA, kColB, kEpi>(g, s);
-  if (tile == k128x128) return launch_tiles<T, 128, 128, 2, 2, 2, 1, kColA, kColB, kEpi>(g, s);
-  if (tile == k64x64by4) return launch_tiles<T, 64, 64, m, n, 2, 4, kColA, kColB, kEpi>(g, s);
-  if (tile == k64x64by2) return launch_tiles<T, 64, 64, m, n, 4, 2, kColA, kColB, kEpi>(g, s);
-  return launch_tiles<T, 64, 64, m, n, 4, 1, kColA, kColB, kEpi>(g, s);
+  constexpr int m = kEpi == kGated ? 4 : 2, n = kEpi == kGated ? 1 : 2, stages = sizeof(T) == 2 ? 4 : 2;
+#define GLA_TILE(TILE, ...) \
+  if constexpr (has_tile<T, kColA, kEpi>(TILE)) \
+    if (tile == TILE) return launch_tiles<T, __VA_ARGS__, kColA, kColB, kEpi>(g, s);
+  GLA_TILE(k320x256, 320, 256, 4, 4, 2, 1)
+  GLA_TILE(k256x256, 256, 256, 4, 4, 2, 1)
+  GLA_TILE(k192x256, 192, 256, 4, 4, 2, 1)
+  GLA_TILE(k128x256, 128, 256, 4, 4, 2, 1)
+  GLA_TILE(k128x128, 128, 128, 2, 2, 2, 1)
+  GLA_TILE(k64x64, 64, 64, m, n, stages, 1)
+  GLA_TILE(k64x64by2, 64, 64, m, n, 4, 2)
+  GLA_TILE(k64x64by4, 64, 64, m, n, 2, 4)
+  GLA_TILE(k32x32by4, 32, 32, 1, 1, 2, 4)
+  GLA_TILE(k32x32by8, 32, 32, 1, 1, 2, 8)
+#undef GLA_TILE
+  return hipErrorInvalidValue;
 }
-
-// y = alpha act(sum of a[p] b[p]^T + bias) + residual, or the gated product, of
-// any number of rows: both operands lie along the contraction (gla_linear.hip).
-hipError_t products(const Args& g, bool gated, int dtype, hipStream_t s);
 
 }  // namespace gemm
 }  // namespace gla

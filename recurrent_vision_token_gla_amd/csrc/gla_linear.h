@@ -33,17 +33,14 @@ struct GatedArgs {
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s);
 
 // The workspace of a gradient, by byte offsets, and how its products are cut up:
-// the tiles of both, the splits of the rows that the weights' sums over, and
-// whether the input's takes the weights' transposes.
+// the tiles of both, and the splits of the rows that the weights' sums over.
 struct LinearBwdLayout {
   size_t g[2];     // gradients behind the activation, [rows][N] each
   size_t colsum;   // float [parts][N]
   size_t partial;  // float [splits][parts of the weights][N][K]
-  size_t turn;     // the weights' transposes, [parts of the weights][K][N]
   size_t total;
   int tile_x, tile_w, splits;
   long steps, each;
-  bool turned;
 };
 
 struct LinearBwdArgs {

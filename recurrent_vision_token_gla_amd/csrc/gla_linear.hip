@@ -91,31 +91,31 @@ hipError_t skinny(const Args& g, hipStream_t s) {
 template <typename T, int kEpi>
 hipError_t forward(const Args& g, hipStream_t s) {
   constexpr bool kDual = kEpi == kGated;
-  if (g.M <= 64 && g.parts == 1) return skinny<T, kDual>(g, s);
-  return launch_product<T, false, false, kEpi>(g, best_tile<T>(g.M, kDual ? 2 * g.N : g.N, 1, g.steps), s);
+  if (g.M <= 64) return skinny<T, kDual>(g, s);
+  return launch_product<T, false, false, kEpi>(g, best_tile<T, false, kEpi>(g.M, kDual ? 2 * g.N : g.N, 1, g.steps), s);
 }
 
-// at most 2^22 rows per launch, so that the grid's numbers fit 32 bits
-hipError_t products(const Args& all, bool gated, int dtype, hipStream_t s) {
+// Any number of rows: at most 2^22 per launch, so that the grid's numbers fit 32
+// bits.
+template <int kEpi>
+hipError_t products(const Args& all, int dtype, hipStream_t s) {
   constexpr long most = 1L << 22;
   const long es = dtype == 0 ? 2 : 4;
   auto on = [&](auto* p, long rows, long width) {
     return p ? (decltype(p))((uintptr_t)p + (size_t)(rows * width * es)) : p;
   };
   Args g = all;
-  g.mparts = g.splits = 1;
-  g.steps = g.each = g.parts * ((g.K * es + 127) / 128);
+  g.parts = g.mparts = g.splits = 1;
+  g.steps = g.each = (g.K * es + 127) / 128;
   for (long r = 0; r < all.M; r += most) {
     g.M = all.M - r < most ? all.M - r : most;
-    for (int p = 0; p < 2; ++p) g.a[p] = on(all.a[p], r, g.lda);
+    g.a[0] = on(all.a[0], r, g.lda);
     g.out[0] = on(all.out[0], r, g.N);
     g.pre = on(all.pre, r, g.N);
     g.residual = on(all.residual, r, g.N);
     g.gate_out = on(all.gate_out, r, g.N);
     g.up_out = on(all.up_out, r, g.N);
-    hipError_t e;
-    if (gated) e = dtype == 0 ? forward<half_t, kGated>(g, s) : forward<float, kGated>(g, s);
-    else e = dtype == 0 ? forward<half_t, kLinear>(g, s) : forward<float, kLinear>(g, s);
+    const hipError_t e = dtype == 0 ? forward<half_t, kEpi>(g, s) : forward<float, kEpi>(g, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -126,17 +126,17 @@ hipError_t products(const Args& all, bool gated, int dtype, hipStream_t s) {
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   gemm::Args g = {};
   g.a[0] = a.x, g.b[0] = a.weight, g.out[0] = a.y;
-  g.M = a.rows, g.N = a.N, g.K = g.lda = g.ldb = a.K, g.parts = 1;
+  g.M = a.rows, g.N = a.N, g.K = g.lda = g.ldb = a.K;
   g.pre = a.pre, g.bias = a.bias, g.residual = a.residual, g.alpha = a.alpha, g.act = a.act;
-  return gemm::products(g, false, a.dtype, s);
+  return gemm::products<gemm::kLinear>(g, a.dtype, s);
 }
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s) {
   gemm::Args g = {};
   g.a[0] = a.x, g.b[0] = a.gate_weight, g.b[1] = a.up_weight, g.out[0] = a.h;
-  g.M = a.rows, g.N = a.F, g.K = g.lda = g.ldb = a.K, g.parts = 1;
+  g.M = a.rows, g.N = a.F, g.K = g.lda = g.ldb = a.K;
   g.gate_out = a.gate_out, g.up_out = a.up_out, g.act = a.act;
-  return gemm::products(g, true, a.dtype, s);
+  return gemm::products<gemm::kGated>(g, a.dtype, s);
 }
 
 }  // namespace gla

@@ -91,35 +91,6 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   }
 }
 
-// out[part][c][r] = w[part][r][c]: 64 x 64 values through LDS, 16 bytes at a
-// time on both sides.
-template <typename T>
-__global__ __launch_bounds__(256) void turn_kernel(const T* __restrict__ w0, const T* __restrict__ w1,
-                                                   T* __restrict__ out, int R, int C) {
-  constexpr int U = Num<T>::kUnit, kPerRow = 64 / U;
-  typedef T vec __attribute__((ext_vector_type(U)));
-  __shared__ T tile[64][64 + 4 / sizeof(T)];
-  const T* w = blockIdx.z ? w1 : w0;
-  out += (long)blockIdx.z * R * C;
-  const int r0 = 64 * blockIdx.y, c0 = 64 * blockIdx.x;
-  for (int t = threadIdx.x; t < 64 * kPerRow; t += 256) {
-    const int r = t / kPerRow, c = U * (t % kPerRow);
-    vec v = {};
-    if (r0 + r < R && c0 + c < C) v = *reinterpret_cast<const vec*>(w + (long)(r0 + r) * C + c0 + c);
-#pragma unroll
-    for (int e = 0; e < U; ++e) tile[r][c + e] = v[e];
-  }
-  __syncthreads();
-  for (int t = threadIdx.x; t < 64 * kPerRow; t += 256) {
-    const int c = t / kPerRow, r = U * (t % kPerRow);
-    if (r0 + r >= R || c0 + c >= C) continue;
-    vec v;
-#pragma unroll
-    for (int e = 0; e < U; ++e) v[e] = tile[r + e][c];
-    *reinterpret_cast<vec*>(out + (long)(c0 + c) * R + r0 + r) = v;
-  }
-}
-
 // Workgroups that a grid-stride pass over `n` units takes.
 unsigned spread(long n) { return (unsigned)(n < 4096 ? n : 4096); }
 
@@ -134,38 +105,27 @@ void weight_plan(long rows, int K, int N, int mparts, LinearBwdLayout* l) {
     if (s > 1 && steps < 4 * s) break;
     const long each = (steps + s - 1) / s, splits = (steps + each - 1) / each;
     const float join = splits > 1 ? 4.f + 2e-6f * splits * mparts * N * K : 0.f;
-    for (int t = kFirstTile<T>; t < kTiles; ++t) {
-      if (t == k320x256 || t == k192x256 || t == k128x256) continue;
-      const float c = join + tile_cost<T>(t, N, K, mparts * splits, each);
-      if (least == 0.f || c < least) least = c, l->tile_w = t, l->splits = (int)splits, l->each = each;
-    }
+    float c;
+    const int t = best_tile<T, true, kPartial>(N, K, mparts * splits, each, &c);
+    c += join;
+    if (least == 0.f || c < least) least = c, l->tile_w = t, l->splits = (int)splits, l->each = each;
   }
   l->steps = steps;
 }
 
-// gx = alpha (a[0] b[0] + a[1] b[1]), a [rows][C], b [C][N], and where
-// l.turned says so through the weights' transposes in `turned`.
+// gx = alpha (a[0] b[0] + a[1] b[1]), a [rows][C], b [C][N]
 template <typename T>
-hipError_t input_gradient(Args g, long rows, int C, int N, int parts, float alpha, T* gx,
-                          const LinearBwdLayout& l, T* turned, hipStream_t s) {
+hipError_t input_gradient(Args g, long rows, int C, int N, int parts, float alpha, T* gx, int tile,
+                          hipStream_t s) {
   constexpr long most = 1L << 22, step = Num<T>::kStep;
   g.K = g.lda = C, g.ldb = g.N = N, g.alpha = alpha, g.parts = parts, g.mparts = g.splits = 1;
-  g.M = rows, g.out[0] = gx;
-  if (l.turned) {
-    hipLaunchKernelGGL((turn_kernel<T>), dim3((N + 63) / 64, (C + 63) / 64, parts), dim3(256), 0, s,
-                       static_cast<const T*>(g.b[0]), static_cast<const T*>(g.b[1]), turned, C, N);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    g.b[0] = turned, g.b[1] = turned + (long)C * N, g.ldb = C;
-    return products(g, false, sizeof(T) == 2 ? 0 : 1, s);
-  }
   const T* a[2] = {static_cast<const T*>(g.a[0]), static_cast<const T*>(g.a[1])};
   g.steps = g.each = parts * ((C + step - 1) / step);
   for (long r = 0; r < rows; r += most) {
     g.M = rows - r < most ? rows - r : most;
     for (int p = 0; p < parts; ++p) g.a[p] = a[p] + r * C;
     g.out[0] = gx + r * N;
-    const hipError_t e = launch_product<T, false, true, kLinear>(g, l.tile_x, s);
+    const hipError_t e = launch_product<T, false, true, kLinear>(g, tile, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -206,15 +166,10 @@ SlopePlan slope_plan(long rows, int N) {
 
 size_t pad(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// The input's gradient: its tiles. The large ones take the weights' transposes
-// (25,600 x 2 x 2,048 x 768 half: 132 us, or 196 with the weights as they are,
-// whose transposing LDS reads run at half the rate).
 template <typename T>
 void input_plan(long rows, int K, int N, int parts, LinearBwdLayout* l) {
-  const long step = Num<T>::kStep, steps = parts * ((N + step - 1) / step);
-  if (rows > 1L << 22) rows = 1L << 22;
-  l->tile_x = best_tile<T>(rows, K, 1, steps);
-  l->turned = l->tile_x < k128x128;
+  const long step = Num<T>::kStep;
+  l->tile_x = best_tile<T, false, kLinear>(rows < 1L << 22 ? rows : 1L << 22, K, 1, parts * ((N + step - 1) / step));
 }
 
 LinearBwdLayout layout(long rows, int K, int N, int dtype, int sides, bool sums, int mparts) {
@@ -231,8 +186,6 @@ LinearBwdLayout layout(long rows, int K, int N, int dtype, int sides, bool sums,
   if (dtype == 0) weight_plan<half_t>(rows, K, N, mparts, &l), input_plan<half_t>(rows, K, N, mparts, &l);
   else weight_plan<float>(rows, K, N, mparts, &l), input_plan<float>(rows, K, N, mparts, &l);
   if (l.splits > 1) at += pad((size_t)l.splits * mparts * N * K * sizeof(float));
-  l.turn = at;
-  if (l.turned) at += pad((size_t)mparts * N * K * es);
   l.total = at ? at : 256;
   return l;
 }
@@ -263,8 +216,8 @@ hipError_t linear_bwd_t(const LinearBwdArgs& a, const LinearBwdLayout& l, char* 
   args.a[0] = g;
   if (a.gx) {
     args.b[0] = args.b[1] = a.weight;
-    const hipError_t e = input_gradient<T>(args, a.rows, a.N, a.K, 1, a.alpha, static_cast<T*>(a.gx), l,
-                                             reinterpret_cast<T*>(ws + l.turn), s);
+    const hipError_t e = input_gradient<T>(args, a.rows, a.N, a.K, 1, a.alpha, static_cast<T*>(a.gx),
+                                             l.tile_x, s);
     if (e != hipSuccess) return e;
   }
   if (!a.gweight) return hipSuccess;
@@ -285,7 +238,7 @@ hipError_t gated_bwd_t(const GatedBwdArgs& a, const LinearBwdLayout& l, char* ws
   Args args = {};
   args.a[0] = ga, args.a[1] = gu, args.b[0] = a.gate_weight, args.b[1] = a.up_weight;
   if (a.gx) {
-    e = input_gradient<T>(args, a.rows, a.F, a.K, 2, 1.f, static_cast<T*>(a.gx), l, reinterpret_cast<T*>(ws + l.turn), s);
+    e = input_gradient<T>(args, a.rows, a.F, a.K, 2, 1.f, static_cast<T*>(a.gx), l.tile_x, s);
     if (e != hipSuccess) return e;
   }
   if (!a.ggate_weight) return hipSuccess;
