@@ -219,7 +219,7 @@ struct Args {
   int splits;            // of the contraction
   long steps, each;      // steps of the contraction, and of one split
   void* out[2];
-  float* partial;  // [split][mparts * M][N] float instead of out
+  float* partial;  // [split][mparts * M][N] float instead of out, where there are splits
   void* pre;       // x W^T + bias, or nullptr
   const float* bias;
   const void* residual;
@@ -228,7 +228,7 @@ struct Args {
   void *gate_out, *up_out;  // the gated product's two sides, or nullptr
 };
 
-enum { kLinear, kGated, kPartial };
+enum { kLinear, kGated };
 
 template <typename T>
 __device__ __forceinline__ void load_to(const T* p, float (&x)[8]) { load8(p, x); }
@@ -288,9 +288,9 @@ __device__ __forceinline__ void finish_gated(const Args& g, long m, long n, floa
 struct Place {
   int split, part;
   long m0, n0;  // of the part's rows, and of the columns
-  __device__ __forceinline__ Place(const Args& g, int BM, int BN) {
-    const int total = gridDim.x, x = blockIdx.x % kXcds, q = total / kXcds, r = total % kXcds;
-    const int lin = x * q + min(x, r) + blockIdx.x / kXcds;
+  __device__ __forceinline__ Place(const Args& g, int id, int count, int BM, int BN) {
+    const int x = id % kXcds, q = count / kXcds, r = count % kXcds;
+    const int lin = x * q + min(x, r) + id / kXcds;
     const int tm = g.tiles_m * g.mparts, tiles = tm * g.tiles_n;
     split = lin / tiles;
     const int t = lin % tiles, band = 8 * g.tiles_n, f = t / band * 8, in = min(8, tm - f);
@@ -301,12 +301,52 @@ struct Place {
   }
 };
 
-// kStages steps of LDS: one is multiplied while the others are on their way.
-// kGroups: the workgroup's waves form as many groups, which take a part of the
-// steps each and add their sums up at the end (few tiles, a long contraction).
-template <typename T, int BM, int BN, int WM, int WN, int kStages, int kGroups, bool kColA, bool kColB, int kEpi>
-__global__ __launch_bounds__(64 * WM * WN * kGroups) void gemm_kernel(const Args g) {
-#if defined(__HIP_DEVICE_COMPILE__)  // the host's pass does not take the loads' builtin in a template
+// Tiles that the products are cut into: rows and columns, waves over both, steps
+// that LDS holds (one is multiplied while the others are on their way),
+// workgroups that a CU holds at once, and groups of such waves in a workgroup,
+// which take a part of the steps each and add their sums up at the end (few
+// tiles, a long contraction).
+enum Tile { k320x256, k256x256, k192x256, k128x256, k128x128, k64x64, k64x64by2, k64x64by4,
+            k32x32by4, k32x32by8, kTiles };
+struct TileShape {
+  int m, n, wm, wn, stages, per_cu, groups;
+};
+constexpr TileShape kTileShapes[kTiles] = {
+    {320, 256, 4, 4, 2, 1, 1}, {256, 256, 4, 4, 2, 1, 1}, {192, 256, 4, 4, 2, 1, 1}, {128, 256, 4, 4, 2, 1, 1},
+    {128, 128, 2, 2, 2, 2, 1}, {64, 64, 2, 2, 4, 2, 1},   {64, 64, 2, 2, 4, 1, 2},   {64, 64, 2, 2, 2, 1, 4},
+    {32, 32, 1, 1, 2, 2, 4},   {32, 32, 1, 1, 2, 1, 8}};
+constexpr TileShape tile_shape(int tile, bool is_float, bool gated) {
+  TileShape s = kTileShapes[tile];
+  // the matrix instructions bound float: more workgroups instead of more steps in flight
+  if (is_float && tile == k64x64) s.stages = 2, s.per_cu = 4;
+  // the gated product needs two column blocks of each weight in a wave
+  if (gated && s.m == 64) s.wm = 4, s.wn = 1;
+  return s;
+}
+// Float tiles gain nothing above 128 x 128; the weights' gradients take no
+// others of 256 columns than 256 x 256 (320 rows need more registers than there
+// are); 32 columns are too few for the gated product.
+template <typename T, bool kColA, int kEpi>
+constexpr bool has_tile(int t) {
+  if (t < k128x128) return sizeof(T) == 2 && (!kColA || t == k256x256);
+  return t < k32x32by4 || kEpi != kGated;
+}
+
+// Workgroup `id` of `count` of one product, with kTileBytes of LDS.
+template <typename T, int kTile, bool kGatedTile>
+constexpr int kTileBytes = tile_shape(kTile, sizeof(T) == 4, kGatedTile).groups *
+                           tile_shape(kTile, sizeof(T) == 4, kGatedTile).stages * 128 *
+                           (tile_shape(kTile, sizeof(T) == 4, kGatedTile).m +
+                            tile_shape(kTile, sizeof(T) == 4, kGatedTile).n);
+template <typename T, int kTile, bool kGatedTile>
+constexpr int kTileThreads = 64 * tile_shape(kTile, sizeof(T) == 4, kGatedTile).groups *
+                             tile_shape(kTile, sizeof(T) == 4, kGatedTile).wm *
+                             tile_shape(kTile, sizeof(T) == 4, kGatedTile).wn;
+
+template <typename T, int kTile, bool kColA, bool kColB, int kEpi>
+__device__ __forceinline__ void gemm_tile(const Args& g, int id, int count, char* shared) {
+  constexpr TileShape S = tile_shape(kTile, sizeof(T) == 4, kEpi == kGated);
+  constexpr int BM = S.m, BN = S.n, WM = S.wm, WN = S.wn, kStages = S.stages, kGroups = S.groups;
   constexpr int NT = 64 * WM * WN, MI = BM / WM / 16, NI = BN / WN / 16;
   constexpr bool kDual = kEpi == kGated;  // columns: BN/2 of b[0], then BN/2 of b[1]
   constexpr int BNC = kDual ? BN / 2 : BN;
@@ -321,9 +361,8 @@ __global__ __launch_bounds__(64 * WM * WN * kGroups) void gemm_kernel(const Args
   static_assert(kStages == 2 || (LA::kUnits % NT == 0 && LB::kUnits % NT == 0), "as many loads in every wave");
   const int group = wave() / (WM * WN), w = wave() % (WM * WN), wm = w / WN, wn = w % WN;
   const int tid = threadIdx.x % NT;
-  __shared__ __attribute__((aligned(1024))) char shared[kGroups * kStages * kStageBytes];
   char* const smem = shared + group * kStages * kStageBytes;
-  const Place at(g, BM, BNC);
+  const Place at(g, id, count, BM, BNC);
   const long m0 = at.m0, n0 = at.n0;
   // this group's steps, and the step that its next loads are of: number k of
   // its part of the contraction, at pa and pb
@@ -440,7 +479,7 @@ __global__ __launch_bounds__(64 * WM * WN * kGroups) void gemm_kernel(const Args
         pair8(acc[mi][2 * p], acc[mi][2 * p + 1], x);
         const long n = n0 + wn * NI * 16 + 32 * p + c8;
         if (m < g.M && n < g.N) {
-          if constexpr (kEpi == kPartial)
+          if (kColA && g.splits > 1)
             store8(g.partial + ((long)at.split * g.mparts + at.part) * g.M * g.N + m * g.N + n, x);
           else
             finish<T>(g, at.part, m, n, x);
@@ -448,98 +487,77 @@ __global__ __launch_bounds__(64 * WM * WN * kGroups) void gemm_kernel(const Args
       }
     }
   }
+}
+
+template <typename T, int kTile, bool kColA, bool kColB, int kEpi>
+__global__ __launch_bounds__((kTileThreads<T, kTile, kEpi == kGated>)) void gemm_kernel(const Args g) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host's pass does not take the loads' builtin in a template
+  __shared__ __attribute__((aligned(1024))) char shared[kTileBytes<T, kTile, kEpi == kGated>];
+  gemm_tile<T, kTile, kColA, kColB, kEpi>(g, blockIdx.x, gridDim.x, shared);
 #endif
 }
 
-// Tiles that the products are cut into, by what a launch of them costs, in us. A
-// step (128 bytes of every row) costs a CU about 0.28, the meeting of the waves
-// and the latency of LDS, and 1.3 for each 256 x 256 half outputs (7 for float
-// ones, whose matrix instructions do a sixteenth of the work in as much time); a
-// tile starts and ends in 2 and 5 for as many outputs, and groups of waves add
-// their sums up. Within 20% of what was measured over 100 to 25,600 rows of 100
-// to 4,096 values. Half, 25,600 x 2,048 x 768 with 320, 256, 192 and 128 rows
-// of 256 columns: 77, 107, 90 and 106 (0.94, 1.17, 1.57 and 2.34 rounds of the
-// CUs); 1,600 x 768 x 768 with 128 x 128 12.7, 64 x 64 8.5, by two groups 11.3;
-// 130 x 768 x 768 11.8, 6.4, 6.1, and with 32 x 32 by four groups 5.0.
-enum Tile { k320x256, k256x256, k192x256, k128x256, k128x128, k64x64, k64x64by2, k64x64by4,
-            k32x32by4, k32x32by8, kTiles };
-struct TileShape {
-  int m, n;
-  int per_cu;  // workgroups that a CU holds at once
-  int groups;  // of waves that share a tile's steps
-};
-constexpr TileShape kTileShapes[kTiles] = {{320, 256, 1, 1}, {256, 256, 1, 1}, {192, 256, 1, 1}, {128, 256, 1, 1},
-                                           {128, 128, 2, 1}, {64, 64, 2, 1},   {64, 64, 1, 2},   {64, 64, 1, 4},
-                                           {32, 32, 2, 4},   {32, 32, 1, 8}};
+// What a launch costs, in us. A step (128 bytes of every row) costs a CU about
+// 0.28, the meeting of the waves and the latency of LDS, and 1.3 for each 256 x
+// 256 half outputs (7 for float ones, whose matrix instructions do a sixteenth of
+// the work in as much time); a tile starts and ends in 2 and 5 for as many
+// outputs, and groups of waves add their sums up. Within 20% of what was measured
+// over 100 to 25,600 rows of 100 to 4,096 values. Half, 25,600 x 2,048 x 768 with
+// 320, 256, 192 and 128 rows of 256 columns: 77, 107, 90 and 106 (0.94, 1.17, 1.57
+// and 2.34 rounds of the CUs); 1,600 x 768 x 768 with 128 x 128 12.7, 64 x 64 8.5,
+// by two groups 11.3; 130 x 768 x 768 11.8, 6.4, 6.1, and with 32 x 32 by four
+// groups 5.0.
 constexpr int kCus = 256;
 
+inline long tile_count(const TileShape& s, long M, long N) { return ((M + s.m - 1) / s.m) * ((N + s.n - 1) / s.n); }
+
+// One round of tiles, `on` workgroups on every CU.
 template <typename T>
-float tile_cost(int tile, long M, long N, long others, long steps) {
-  const TileShape s = kTileShapes[tile];
-  const long count = ((M + s.m - 1) / s.m) * ((N + s.n - 1) / s.n) * others;
-  const int per_cu = sizeof(T) == 4 && tile == k64x64 ? 4 : s.per_cu;  // two stages instead of four
-  const long slots = (long)kCus * per_cu, whole = count / slots, rest = count % slots;
+float round_cost(const TileShape& s, long steps, long on) {
   const float area = s.m * s.n / 65536.f, per_step = sizeof(T) == 2 ? 1.3f : 7.f;
-  auto round = [&](long on) {  // with `on` workgroups on a CU
-    return (steps + s.groups - 1) / s.groups * (0.28f + per_step * area * on * s.groups) + 2.f + 5.f * area * on +
-           (s.groups - 1) * (0.25f + 8.f * area);
-  };
-  return whole * round(per_cu) + (rest ? round((rest + kCus - 1) / kCus) : 0.f);
-}
-// Float tiles gain nothing above 128 x 128: the matrix instructions bound them.
-// The weights' gradients take no others of 256 columns than 256 x 256 (320 rows
-// need more registers than there are).
-template <typename T, bool kColA, int kEpi>
-constexpr bool has_tile(int t) {
-  if (t < k128x128) return sizeof(T) == 2 && (!kColA || t == k256x256);
-  return t < k32x32by4 || kEpi != kGated;  // the gated product needs two column blocks of each weight in a wave
+  return (steps + s.groups - 1) / s.groups * (0.28f + per_step * area * on * s.groups) + 2.f + 5.f * area * on +
+         (s.groups - 1) * (0.25f + 8.f * area);
 }
 
-// M x N outputs, `others` such products at once, `steps` steps each; what it
-// costs in *cost.
+// M x N outputs, `others` such products at once, `steps` steps each: the best
+// tile, and what it costs in *cost.
 template <typename T, bool kColA, int kEpi>
 int best_tile(long M, long N, long others, long steps, float* cost = nullptr) {
   int best = -1;
   float least = 0.f;
   for (int t = 0; t < kTiles; ++t) {
     if (!has_tile<T, kColA, kEpi>(t)) continue;
-    const float c = tile_cost<T>(t, M, N, others, steps);
+    const TileShape s = tile_shape(t, sizeof(T) == 4, false);
+    const long count = tile_count(s, M, N) * others, slots = (long)kCus * s.per_cu;
+    const long whole = count / slots, rest = count % slots;
+    const float c = whole * round_cost<T>(s, steps, s.per_cu) +
+                    (rest ? round_cost<T>(s, steps, (rest + kCus - 1) / kCus) : 0.f);
     if (best < 0 || c < least) least = c, best = t;
   }
   if (cost) *cost = least;
   return best;
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int kStages, int kGroups, bool kColA, bool kColB, int kEpi>
+// One product on tiles of the given kind.
+template <typename T, int kTile, bool kColA, bool kColB, int kEpi>
 hipError_t launch_tiles(Args g, hipStream_t s) {
-  constexpr int BNC = kEpi == kGated ? BN / 2 : BN;
-  g.tiles_m = (int)((g.M + BM - 1) / BM);
-  g.tiles_n = (int)((g.N + BNC - 1) / BNC);
-  hipLaunchKernelGGL((gemm_kernel<T, BM, BN, WM, WN, kStages, kGroups, kColA, kColB, kEpi>),
+  constexpr TileShape S = tile_shape(kTile, sizeof(T) == 4, kEpi == kGated);
+  g.tiles_m = (int)((g.M + S.m - 1) / S.m);
+  g.tiles_n = (int)((g.N + (kEpi == kGated ? S.n / 2 : S.n) - 1) / (kEpi == kGated ? S.n / 2 : S.n));
+  hipLaunchKernelGGL((gemm_kernel<T, kTile, kColA, kColB, kEpi>),
                      dim3((unsigned)(g.tiles_m * g.mparts * g.tiles_n * g.splits)),
-                     dim3(64 * WM * WN * kGroups), 0, s, g);
+                     dim3(kTileThreads<T, kTile, kEpi == kGated>), 0, s, g);
   return hipGetLastError();
 }
-
-// One product on tiles of the given kind.
-template <typename T, bool kColA, bool kColB, int kEpi>
+template <typename T, bool kColA, bool kColB, int kEpi, int kTile = 0>
 hipError_t launch_product(const Args& g, int tile, hipStream_t s) {
-  constexpr int m = kEpi == kGated ? 4 : 2, n = kEpi == kGated ? 1 : 2, stages = sizeof(T) == 2 ? 4 : 2;
-#define GLA_TILE(TILE, ...) \
-  if constexpr (has_tile<T, kColA, kEpi>(TILE)) \
-    if (tile == TILE) return launch_tiles<T, __VA_ARGS__, kColA, kColB, kEpi>(g, s);
-  GLA_TILE(k320x256, 320, 256, 4, 4, 2, 1)
-  GLA_TILE(k256x256, 256, 256, 4, 4, 2, 1)
-  GLA_TILE(k192x256, 192, 256, 4, 4, 2, 1)
-  GLA_TILE(k128x256, 128, 256, 4, 4, 2, 1)
-  GLA_TILE(k128x128, 128, 128, 2, 2, 2, 1)
-  GLA_TILE(k64x64, 64, 64, m, n, stages, 1)
-  GLA_TILE(k64x64by2, 64, 64, m, n, 4, 2)
-  GLA_TILE(k64x64by4, 64, 64, m, n, 2, 4)
-  GLA_TILE(k32x32by4, 32, 32, 1, 1, 2, 4)
-  GLA_TILE(k32x32by8, 32, 32, 1, 1, 2, 8)
-#undef GLA_TILE
-  return hipErrorInvalidValue;
+  if constexpr (kTile == kTiles) {
+    return hipErrorInvalidValue;
+  } else {
+    if constexpr (has_tile<T, kColA, kEpi>(kTile))
+      if (tile == kTile) return launch_tiles<T, kTile, kColA, kColB, kEpi>(g, s);
+    return launch_product<T, kColA, kColB, kEpi, kTile + 1>(g, tile, s);
+  }
 }
 
 }  // namespace gemm

@@ -33,7 +33,8 @@ struct GatedArgs {
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s);
 
 // The workspace of a gradient, by byte offsets, and how its products are cut up:
-// the tiles of both, and the splits of the rows that the weights' sums over.
+// the tiles of both, the splits of the rows that the weights' sums over, and
+// whether one launch takes both (on tiles of one kind).
 struct LinearBwdLayout {
   size_t g[2];     // gradients behind the activation, [rows][N] each
   size_t colsum;   // float [parts][N]
@@ -41,6 +42,7 @@ struct LinearBwdLayout {
   size_t total;
   int tile_x, tile_w, splits;
   long steps, each;
+  bool pair;
 };
 
 struct LinearBwdArgs {

@@ -94,56 +94,153 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
 // Workgroups that a grid-stride pass over `n` units takes.
 unsigned spread(long n) { return (unsigned)(n < 4096 ? n : 4096); }
 
-// The weights' gradient: its tiles, and the splits of its long contraction, by
-// the tiles' cost and that of the partial sums' way through memory (4 TB/s and
-// a launch).
+// The sums over a gradient's partial rows, in the launch of its products.
+struct Sums {
+  const float* part;  // [parts][N], or nullptr
+  float* out;
+  int parts, N;
+};
+
+// Both products of a gradient and its column sums in one launch, for those that
+// leave CUs idle or cost little more than a launch: workgroups 0 .. nw - 1 take
+// the weights' tiles, the next nx the input's, the others 16 columns each.
+template <typename T, int kTile>
+__global__ __launch_bounds__((kTileThreads<T, kTile, false>)) void pair_kernel(const Args x, const Args w, const Sums sums,
+                                                                          int nx, int nw) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) char shared[kTileBytes<T, kTile, false>];
+  const int id = blockIdx.x;
+  if (id < nw) {
+    gemm_tile<T, kTile, true, true, kLinear>(w, id, nw, shared);
+  } else if (id < nw + nx) {
+    gemm_tile<T, kTile, false, true, kLinear>(x, id - nw, nx, shared);
+  } else {
+    constexpr int G = kTileThreads<T, kTile, false> / 16, W = 8;
+    float(*s)[17] = reinterpret_cast<float(*)[17]>(shared);
+    const int c = threadIdx.x & 15, g = threadIdx.x >> 4, col = (id - nw - nx) * 16 + c;
+    float y = 0.f;
+    if (col < sums.N) {
+      for (int p = g; p < sums.parts; p += G * W) {
+        float v[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = p + G * i < sums.parts ? sums.part[(long)(p + G * i) * sums.N + col] : 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) y += v[i];
+      }
+    }
+    s[g][c] = y;
+    __syncthreads();
+    if (g == 0 && col < sums.N) {
+      for (int i = 1; i < G; ++i) y += s[i][c];
+      sums.out[col] = y;
+    }
+  }
+#endif
+}
+
+template <typename T, int kTile = k128x128>
+hipError_t launch_pair(Args x, Args w, const Sums& sums, int tile, hipStream_t s) {
+  if constexpr (kTile == kTiles) {
+    return hipErrorInvalidValue;
+  } else {
+    if (tile != kTile) return launch_pair<T, kTile + 1>(x, w, sums, tile, s);
+    constexpr TileShape S = tile_shape(kTile, sizeof(T) == 4, false);
+    for (Args* g : {&x, &w}) g->tiles_m = (int)((g->M + S.m - 1) / S.m), g->tiles_n = (int)((g->N + S.n - 1) / S.n);
+    const int nx = x.tiles_m * x.tiles_n, nw = w.tiles_m * w.mparts * w.tiles_n * w.splits;
+    const int ns = sums.part ? (sums.N + 15) / 16 : 0;
+    hipLaunchKernelGGL((pair_kernel<T, kTile>), dim3((unsigned)(nx + nw + ns)), dim3(kTileThreads<T, kTile, false>), 0, s,
+                       x, w, sums, nx, nw);
+    return hipGetLastError();
+  }
+}
+
+// Tiles of both products and splits of the weights' long contraction, by the
+// tiles' cost, that of the partial sums' way through memory (4 TB/s and a
+// launch), and whether one launch for both is less (a launch costs 3 us, and
+// half of the longer tile is left at its end).
 template <typename T>
-void weight_plan(long rows, int K, int N, int mparts, LinearBwdLayout* l) {
-  const long step = Num<T>::kStep, steps = (rows + step - 1) / step;
-  float least = 0.f;
+void plan(long rows, int K, int N, int mparts, LinearBwdLayout* l) {
+  const long step = Num<T>::kStep, steps = (rows + step - 1) / step, steps_x = mparts * ((N + step - 1) / step);
+  float x, least = 0.f;
+  l->tile_x = best_tile<T, false, kLinear>(rows < 1L << 22 ? rows : 1L << 22, K, 1, steps_x, &x);
+  l->steps = steps;
   for (long s : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32}) {
     if (s > 1 && steps < 4 * s) break;
     const long each = (steps + s - 1) / s, splits = (steps + each - 1) / each;
     const float join = splits > 1 ? 4.f + 2e-6f * splits * mparts * N * K : 0.f;
-    float c;
-    const int t = best_tile<T, true, kPartial>(N, K, mparts * splits, each, &c);
-    c += join;
-    if (least == 0.f || c < least) least = c, l->tile_w = t, l->splits = (int)splits, l->each = each;
+    float w;
+    const int t = best_tile<T, true, kLinear>(N, K, mparts * splits, each, &w);
+    float c = w + join + x + 3.f;
+    if (least == 0.f || c < least) least = c, l->tile_w = t, l->splits = (int)splits, l->each = each, l->pair = false;
+    for (int p = k128x128; rows <= 1L << 20 && p < kTiles; ++p) {
+      const TileShape a = tile_shape(p, sizeof(T) == 4, false);
+      const long nx = tile_count(a, rows, K), nw = tile_count(a, N, K) * mparts * splits;
+      const long slots = (long)kCus * a.per_cu, per = (nx + nw + kCus - 1) / kCus;
+      const long on = per < a.per_cu ? per : a.per_cu;
+      const float rx = round_cost<T>(a, steps_x, on), rw = round_cost<T>(a, each, on), longer = rx > rw ? rx : rw;
+      c = join + (nx + nw <= slots ? longer : (nx * rx + nw * rw) / slots + 0.5f * longer);
+      if (c < least) least = c, l->tile_w = l->tile_x = p, l->splits = (int)splits, l->each = each, l->pair = true;
+    }
+    if (!l->pair) l->tile_x = best_tile<T, false, kLinear>(rows < 1L << 22 ? rows : 1L << 22, K, 1, steps_x);
   }
-  l->steps = steps;
 }
 
 // gx = alpha (a[0] b[0] + a[1] b[1]), a [rows][C], b [C][N]
 template <typename T>
-hipError_t input_gradient(Args g, long rows, int C, int N, int parts, float alpha, T* gx, int tile,
-                          hipStream_t s) {
-  constexpr long most = 1L << 22, step = Num<T>::kStep;
-  g.K = g.lda = C, g.ldb = g.N = N, g.alpha = alpha, g.parts = parts, g.mparts = g.splits = 1;
-  const T* a[2] = {static_cast<const T*>(g.a[0]), static_cast<const T*>(g.a[1])};
-  g.steps = g.each = parts * ((C + step - 1) / step);
-  for (long r = 0; r < rows; r += most) {
-    g.M = rows - r < most ? rows - r : most;
-    for (int p = 0; p < parts; ++p) g.a[p] = a[p] + r * C;
-    g.out[0] = gx + r * N;
+Args input_gradient(const void* a0, const void* a1, const void* b0, const void* b1, long rows, int C, int N, int parts,
+                    float alpha, void* gx) {
+  Args g = {};
+  g.a[0] = a0, g.a[1] = a1, g.b[0] = b0, g.b[1] = b1, g.out[0] = gx, g.alpha = alpha;
+  g.M = rows, g.K = g.lda = C, g.ldb = g.N = N, g.parts = parts, g.mparts = g.splits = 1;
+  g.steps = g.each = parts * ((C + Num<T>::kStep - 1) / Num<T>::kStep);
+  return g;
+}
+// out[p] = alpha a[p]^T x, a[p] [rows][N], x [rows][K]
+template <typename T>
+Args weight_gradient(const void* a0, const void* a1, const void* x, long rows, int K, int N, int mparts, float alpha,
+                     void* out0, void* out1, const LinearBwdLayout& l, char* ws) {
+  Args g = {};
+  g.a[0] = a0, g.a[1] = a1, g.b[0] = g.b[1] = x, g.out[0] = out0, g.out[1] = out1, g.alpha = alpha;
+  g.M = g.lda = N, g.N = g.ldb = K, g.K = rows, g.parts = 1, g.mparts = mparts;
+  g.splits = l.splits, g.steps = l.steps, g.each = l.each;
+  g.partial = reinterpret_cast<float*>(ws + l.partial);
+  return g;
+}
+
+template <typename T>
+hipError_t launch_input(Args g, int tile, hipStream_t s) {
+  constexpr long most = 1L << 22;  // rows per launch, so that the grid's numbers fit 32 bits
+  const Args all = g;
+  for (long r = 0; r < all.M; r += most) {
+    g.M = all.M - r < most ? all.M - r : most;
+    for (int p = 0; p < g.parts; ++p) g.a[p] = static_cast<const T*>(all.a[p]) + r * g.lda;
+    g.out[0] = static_cast<T*>(all.out[0]) + r * g.N;
     const hipError_t e = launch_product<T, false, true, kLinear>(g, tile, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-// out[p] = alpha a[p]^T x, a[p] [rows][N], x [rows][K]
+// The products of a gradient, each wanted where its output is, and its column
+// sums where they are.
 template <typename T>
-hipError_t weight_gradient(Args g, long rows, int K, int N, int mparts, float alpha, const LinearBwdLayout& l,
-                           float* partial, hipStream_t s) {
-  g.lda = N, g.ldb = K, g.M = N, g.N = K, g.K = rows, g.alpha = alpha;
-  g.parts = 1, g.mparts = mparts, g.splits = l.splits, g.steps = l.steps, g.each = l.each;
-  g.partial = partial;
-  if (l.splits == 1) return launch_product<T, true, true, kLinear>(g, l.tile_w, s);
-  const hipError_t e = launch_product<T, true, true, kPartial>(g, l.tile_w, s);
-  if (e != hipSuccess) return e;
-  const long per_part = (long)N * K / 8, groups = mparts * per_part;
-  hipLaunchKernelGGL((join_kernel<T>), dim3(spread((groups + 255) / 256)), dim3(256), 0, s, partial,
-                     static_cast<T*>(g.out[0]), static_cast<T*>(g.out[1]), alpha, l.splits, groups, per_part);
+hipError_t launch_products(const Args& x, const Args& w, const Sums& sums, const LinearBwdLayout& l, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  if (l.pair && x.out[0] && w.out[0]) {
+    e = launch_pair<T>(x, w, sums, l.tile_x, s);
+  } else {
+    if (sums.part) {
+      hipLaunchKernelGGL(norm::column_sum_kernel, dim3((sums.N + 15) / 16), dim3(1024), 0, s, sums.part, sums.out,
+                         sums.parts, sums.N);
+      e = hipGetLastError();
+    }
+    if (e == hipSuccess && x.out[0]) e = launch_input<T>(x, l.tile_x, s);
+    if (e == hipSuccess && w.out[0]) e = launch_product<T, true, true, kLinear>(w, l.tile_w, s);
+  }
+  if (e != hipSuccess || !w.out[0] || w.splits == 1) return e;
+  const long per_part = w.M * w.N / 8, groups = w.mparts * per_part;
+  hipLaunchKernelGGL((join_kernel<T>), dim3(spread((groups + 255) / 256)), dim3(256), 0, s, w.partial,
+                     static_cast<T*>(w.out[0]), static_cast<T*>(w.out[1]), w.alpha, w.splits, groups, per_part);
   return hipGetLastError();
 }
 
@@ -166,12 +263,6 @@ SlopePlan slope_plan(long rows, int N) {
 
 size_t pad(size_t n) { return (n + 255) & ~(size_t)255; }
 
-template <typename T>
-void input_plan(long rows, int K, int N, int parts, LinearBwdLayout* l) {
-  const long step = Num<T>::kStep;
-  l->tile_x = best_tile<T, false, kLinear>(rows < 1L << 22 ? rows : 1L << 22, K, 1, parts * ((N + step - 1) / step));
-}
-
 LinearBwdLayout layout(long rows, int K, int N, int dtype, int sides, bool sums, int mparts) {
   LinearBwdLayout l = {};
   const size_t es = dtype == 0 ? 2 : 4;
@@ -183,8 +274,8 @@ LinearBwdLayout layout(long rows, int K, int N, int dtype, int sides, bool sums,
   l.colsum = at;
   if (sums) at += pad((size_t)slope_plan(rows, N).parts * N * sizeof(float));
   l.partial = at;
-  if (dtype == 0) weight_plan<half_t>(rows, K, N, mparts, &l), input_plan<half_t>(rows, K, N, mparts, &l);
-  else weight_plan<float>(rows, K, N, mparts, &l), input_plan<float>(rows, K, N, mparts, &l);
+  if (dtype == 0) plan<half_t>(rows, K, N, mparts, &l);
+  else plan<float>(rows, K, N, mparts, &l);
   if (l.splits > 1) at += pad((size_t)l.splits * mparts * N * K * sizeof(float));
   l.total = at ? at : 256;
   return l;
@@ -193,37 +284,22 @@ LinearBwdLayout layout(long rows, int K, int N, int dtype, int sides, bool sums,
 template <typename T>
 hipError_t linear_bwd_t(const LinearBwdArgs& a, const LinearBwdLayout& l, char* ws, hipStream_t s) {
   T* gp = reinterpret_cast<T*>(ws + l.g[0]);
-  float* sums = reinterpret_cast<float*>(ws + l.colsum);
-  const bool own = a.act != 0;
-  const bool wanted = a.gx || a.gweight;
-  if ((own && wanted) || a.gbias) {
+  Sums sums = {};
+  const bool own = a.act != 0, products = a.gx || a.gweight;
+  if ((own && products) || a.gbias) {
     const SlopePlan p = slope_plan(a.rows, a.N);
+    if (a.gbias) sums = Sums{reinterpret_cast<float*>(ws + l.colsum), a.gbias, p.parts, a.N};
     hipLaunchKernelGGL((slope_kernel<T>), dim3(p.blocks, p.parts), dim3(256), 0, s,
                        own ? static_cast<const T*>(a.pre) : nullptr, static_cast<const T*>(a.gy),
-                       own && wanted ? gp : nullptr, a.gbias ? sums : nullptr, a.alpha, a.act, a.rows, a.N,
+                       own && products ? gp : nullptr, const_cast<float*>(sums.part), a.alpha, a.act, a.rows, a.N,
                        p.shift);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (a.gbias) {
-      hipLaunchKernelGGL(norm::column_sum_kernel, dim3((a.N + 15) / 16), dim3(1024), 0, s, sums, a.gbias,
-                         p.parts, a.N);
-      e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
   }
   const void* g = own ? gp : a.gy;
-  Args args = {};
-  args.a[0] = g;
-  if (a.gx) {
-    args.b[0] = args.b[1] = a.weight;
-    const hipError_t e = input_gradient<T>(args, a.rows, a.N, a.K, 1, a.alpha, static_cast<T*>(a.gx),
-                                             l.tile_x, s);
-    if (e != hipSuccess) return e;
-  }
-  if (!a.gweight) return hipSuccess;
-  args.b[0] = args.b[1] = a.x;
-  args.out[0] = args.out[1] = a.gweight;
-  return weight_gradient<T>(args, a.rows, a.K, a.N, 1, a.alpha, l, reinterpret_cast<float*>(ws + l.partial), s);
+  return launch_products<T>(
+      input_gradient<T>(g, nullptr, a.weight, nullptr, a.rows, a.N, a.K, 1, a.alpha, a.gx),
+      weight_gradient<T>(g, nullptr, a.x, a.rows, a.K, a.N, 1, a.alpha, a.gweight, a.gweight, l, ws), sums, l, s);
 }
 
 template <typename T>
@@ -233,18 +309,11 @@ hipError_t gated_bwd_t(const GatedBwdArgs& a, const LinearBwdLayout& l, char* ws
   hipLaunchKernelGGL((gated_slope_kernel<T>), dim3(spread((groups + 255) / 256)), dim3(256), 0, s,
                      static_cast<const T*>(a.gate), static_cast<const T*>(a.up),
                      static_cast<const T*>(a.gh), ga, gu, a.act, groups);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  Args args = {};
-  args.a[0] = ga, args.a[1] = gu, args.b[0] = a.gate_weight, args.b[1] = a.up_weight;
-  if (a.gx) {
-    e = input_gradient<T>(args, a.rows, a.F, a.K, 2, 1.f, static_cast<T*>(a.gx), l.tile_x, s);
-    if (e != hipSuccess) return e;
-  }
-  if (!a.ggate_weight) return hipSuccess;
-  args.b[0] = args.b[1] = a.x;
-  args.out[0] = a.ggate_weight, args.out[1] = a.gup_weight;
-  return weight_gradient<T>(args, a.rows, a.K, a.F, 2, 1.f, l, reinterpret_cast<float*>(ws + l.partial), s);
+  return launch_products<T>(
+      input_gradient<T>(ga, gu, a.gate_weight, a.up_weight, a.rows, a.F, a.K, 2, 1.f, a.gx),
+      weight_gradient<T>(ga, gu, a.x, a.rows, a.K, a.F, 2, 1.f, a.ggate_weight, a.gup_weight, l, ws), Sums{}, l, s);
 }
 
 }  // namespace gemm
