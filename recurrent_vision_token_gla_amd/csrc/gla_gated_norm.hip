@@ -52,6 +52,25 @@ __device__ __forceinline__ void factor8(const float* post, const float* scale, i
   }
 }
 
+// Eight columns as loaded, converted where they are used.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<half_t> {
+  half8 v;
+  __device__ __forceinline__ void load(const half_t* p) { v = *reinterpret_cast<const half8*>(p); }
+  __device__ __forceinline__ float operator[](int c) const { return (float)v[c]; }
+};
+template <>
+struct Raw8<float> {
+  floatx4 v[2];
+  __device__ __forceinline__ void load(const float* p) {
+    v[0] = *reinterpret_cast<const floatx4*>(p);
+    v[1] = *reinterpret_cast<const floatx4*>(p + 4);
+  }
+  __device__ __forceinline__ float operator[](int c) const { return v[c / 4][c % 4]; }
+};
+
 template <int TPR>
 constexpr int kTeamThreads = TPR > 256 ? TPR : 256;
 
@@ -76,22 +95,35 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_kernel(
       tile::load_f8(wp + 8 * u, w[i]);
     }
   }
-  for (long row = (long)blockIdx.x * RPB + threadIdx.x / TPR; row < rows; row += (long)gridDim.x * RPB) {
+  const long stride = (long)gridDim.x * RPB;
+  long row = (long)blockIdx.x * RPB + threadIdx.x / TPR;
+  Raw8<T> nx[VPT], nr[VPT], ng[VPT];  // the next row
+  auto fetch = [&](long at) {
+    const long grow = gate ? at / per : 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int u = t + TPR * i;
+      if (u < nv) {
+        nx[i].load(xp + at * F + 8 * u);
+        nr[i].load(rp + at * F + 8 * u);
+        if (gate) ng[i].load(gate + grow * F + 8 * u);
+      }
+    }
+  };
+  if (row < rows) fetch(row);
+  for (; row < rows; row += stride) {
     float x[VPT][8], r[VPT][8], g[VPT][8], ss[1] = {0.f};
-    const long grow = gate ? row / per : 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int u = t + TPR * i;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) x[i][c] = r[i][c] = 0.f, g[i][c] = 1.f;
-      if (u < nv) {
-        load8(xp + row * F + 8 * u, x[i]);
-        load8(rp + row * F + 8 * u, r[i]);
-        if (gate) load8(gate + grow * F + 8 * u, g[i]);
+      for (int c = 0; c < 8; ++c) {
+        x[i][c] = u < nv ? nx[i][c] : 0.f, r[i][c] = u < nv ? nr[i][c] : 0.f;
+        g[i][c] = u < nv && gate ? ng[i][c] : 1.f;
+        ss[0] = fmaf(x[i][c], x[i][c], ss[0]);
       }
-#pragma unroll
-      for (int c = 0; c < 8; ++c) ss[0] = fmaf(x[i][c], x[i][c], ss[0]);
     }
+    if (row + stride < rows) fetch(row + stride);
     float rx = 1.f;
     if (post) {
       team_sums<TPR>(ss, lds);
@@ -260,69 +292,81 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_bwd_kernel(
   else write(out + F, q);
 }
 
-// Sums of the pairs of rows part[2 (blockIdx.y count + 0 .. count - 1)], gw and Q
-// (or sum gate Q): 16 columns and 64 groups of rows per workgroup. gate: the
-// sums are Q, of which ggate (if wanted) and gate Q are made. kLast: into the
-// weights' gradients. Else into pair blockIdx.y of `next`.
+// Sums of the pairs of rows of part, gw and Q (or sum gate Q), `count` of them in
+// each of `groups` groups (kLast; else in group blockIdx.y): 16 columns and 64
+// rows of threads per workgroup. gate: the sums are Q, of which ggate (if wanted)
+// and gate Q are made. kLast: into the weights' gradients. Else into pair
+// blockIdx.y of `next`.
 template <typename T, bool kLast>
 __global__ __launch_bounds__(1024) void gated_norm_join_kernel(
-    const float* __restrict__ part, float* __restrict__ next, int count, int F, const float* __restrict__ post,
-    const T* __restrict__ gate, const float* __restrict__ scale, T* __restrict__ ggp, float* __restrict__ gpost,
-    float* __restrict__ gscale, float* __restrict__ gweight) {
+    const float* __restrict__ part, float* __restrict__ next, int count, int groups, int F,
+    const float* __restrict__ post, const T* __restrict__ gate, const float* __restrict__ scale,
+    T* __restrict__ ggp, float* __restrict__ gpost, float* __restrict__ gscale, float* __restrict__ gweight) {
   constexpr int W = 8;
   __shared__ float s[2][64][17];
   const int c = threadIdx.x & 15, g = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
-  const long group = blockIdx.y;
-  part += 2 * group * count * F;
+  // `each` rows of threads to a group, a power of two and at least eight
+  const int each = groups == 1 ? 64 : groups == 2 ? 32 : groups <= 4 ? 16 : 8, o = g / each, r = g % each;
+  const long group = kLast ? o : blockIdx.y;
   float y[2] = {0.f, 0.f};
-  if (col < F) {
-    for (int p = g; p < count; p += 64 * W) {
+  if (col < F && o < groups) {
+    const float* from = part + 2 * group * count * F + col;
+    for (int p = r; p < count; p += each * W) {
       float x[2][W];
 #pragma unroll
       for (int i = 0; i < W; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) x[h][i] = p + 64 * i < count ? part[(2L * (p + 64 * i) + h) * F + col] : 0.f;
+        for (int h = 0; h < 2; ++h) x[h][i] = p + each * i < count ? from[(2L * (p + each * i) + h) * F] : 0.f;
 #pragma unroll
       for (int i = 0; i < W; ++i) y[0] += x[0][i], y[1] += x[1][i];
     }
   }
   s[0][g][c] = y[0], s[1][g][c] = y[1];
   __syncthreads();
-  if (g < 8) {
+  if (g % 8 == 0) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       y[h] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[h] += s[h][g + 8 * i][c];
-      s[h][g][c] = y[h];  // no other thread reads row g
+      for (int i = 0; i < 8; ++i) y[h] += s[h][g + i][c];
+      s[h][g][c] = y[h];  // no other thread reads rows g .. g + 7
     }
   }
   __syncthreads();
-  if (g != 0 || col >= F) return;
+  const float a = post && col < F ? post[col] : 1.f, b = scale && col < F ? scale[col] : 1.f;
+  if (r == 0 && o < groups && col < F) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    y[h] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[h] += s[h][i][c];
-  }
-  const float a = post ? post[col] : 1.f, b = scale ? scale[col] : 1.f;
-  if (gate) {
-    if (ggp) ggp[group * F + col] = (T)(a * b * y[1]);
-    y[1] *= (float)gate[group * F + col];
+    for (int h = 0; h < 2; ++h)
+      for (int i = 8; i < each; i += 8) y[h] += s[h][g + i][c];
+    if (gate) {
+      if (ggp) ggp[group * F + col] = (T)(a * b * y[1]);
+      y[1] *= (float)gate[group * F + col];
+    }
+    if constexpr (!kLast) {
+      next[2 * group * F + col] = y[0];
+      next[(2 * group + 1) * F + col] = y[1];
+    } else {
+      s[0][g][c] = y[0], s[1][g][c] = y[1];
+    }
   }
   if constexpr (kLast) {
-    gweight[col] = y[0];
-    if (gpost) gpost[col] = b * y[1];
-    if (gscale) gscale[col] = a * y[1];
-  } else {
-    next[2 * group * F + col] = y[0];
-    next[(2 * group + 1) * F + col] = y[1];
+    __syncthreads();
+    if (g == 0 && col < F) {
+      for (int i = 1; i < groups; ++i) y[0] += s[0][i * each][c], y[1] += s[1][i * each][c];
+      gweight[col] = y[0];
+      if (gpost) gpost[col] = b * y[1];
+      if (gscale) gscale[col] = a * y[1];
+    }
   }
 }
 
 // How the gradient's rows are shared out: teams that own groups once there are
-// enough of them, else chunks of each group's rows.
-constexpr long kMaxParts2 = 1024;
+// enough of them, else chunks of each group's rows, in as many workgroups as the
+// CUs hold at once (25,600 x 768 half: 58.6 us with 512, 70.7 with 1,024). Up to
+// eight groups the last
+// launch takes side by side (four of 6,400 rows of 768: 5.4 us instead of 9.1 for
+// two launches).
+constexpr long kMaxParts2 = 512, kMaxAtOnce = 8;
 int teams(int F) { return F <= 64 ? 32 : F <= 256 ? 16 : F <= 512 ? 8 : F <= 1024 ? 4 : 1; }
 struct GroupPlan {
   bool own;
@@ -351,7 +395,11 @@ GroupPlan group_plan(long rows, long groups, int F) {
 template <int TPR, int VPT, typename T>
 hipError_t gated_norm_t(const GatedNormArgs& a, hipStream_t s) {
   constexpr long rpb = kTeamThreads<TPR> / TPR;
-  const long steps = (a.rows + rpb - 1) / rpb, blocks = steps < 4096 ? steps : 4096;
+  // as many workgroups as the CUs hold at once, each with its next row in flight
+  // (25,600 x 768 half, inputs from memory: 768 workgroups 30.0 us, 512 and 1,024
+  // 30.6 and 36.3; 4,096 without the row in flight 38.4)
+  constexpr long most = VPT == 1 ? 1536 : 768;
+  const long steps = (a.rows + rpb - 1) / rpb, blocks = steps < most ? steps : most;
   hipLaunchKernelGGL((gated_norm_kernel<TPR, VPT, T>), dim3((unsigned)blocks), dim3(kTeamThreads<TPR>), 0, s,
                      static_cast<const T*>(a.x), static_cast<const T*>(a.residual), a.post,
                      static_cast<const T*>(a.gate), a.scale, a.weight, a.eps, static_cast<T*>(a.sum),
@@ -375,18 +423,19 @@ hipError_t gated_norm_bwd_t(const GatedNormBwdArgs& a, float* ws, hipStream_t s)
   if (e != hipSuccess) return e;
   const unsigned cols = (unsigned)((a.F + 15) / 16);
   const float* part = ws;
-  int count = (int)p.blocks;
-  bool joined = p.own;  // the gate is in the sums
-  if (!p.own && a.groups > 1) {
+  // the sums of teams that own groups have the gate in them
+  int count = p.own ? (int)p.blocks : p.chunks, groups = p.own ? 1 : (int)a.groups;
+  bool gated = p.own;
+  if (groups > kMaxAtOnce) {
     float* next = ws + 2 * p.blocks * a.F;
-    hipLaunchKernelGGL((gated_norm_join_kernel<T, false>), dim3(cols, (unsigned)a.groups), dim3(1024), 0, s,
-                       ws, next, p.chunks, a.F, a.post, gate, a.scale, ggate, nullptr, nullptr, nullptr);
+    hipLaunchKernelGGL((gated_norm_join_kernel<T, false>), dim3(cols, (unsigned)groups), dim3(1024), 0, s, ws, next,
+                       count, 1, a.F, a.post, gate, a.scale, ggate, nullptr, nullptr, nullptr);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    part = next, count = (int)a.groups, joined = true;
+    part = next, count = groups, groups = 1, gated = true;
   }
-  hipLaunchKernelGGL((gated_norm_join_kernel<T, true>), dim3(cols), dim3(1024), 0, s, part, nullptr, count,
-                     a.F, a.post, joined ? nullptr : gate, a.scale, ggate, a.gpost, a.gscale, a.gweight);
+  hipLaunchKernelGGL((gated_norm_join_kernel<T, true>), dim3(cols), dim3(1024), 0, s, part, nullptr, count, groups,
+                     a.F, a.post, gated ? nullptr : gate, a.scale, ggate, a.gpost, a.gscale, a.gweight);
   return hipGetLastError();
 }
 
@@ -412,7 +461,7 @@ hipError_t launch_gated_norm(const GatedNormArgs& a, hipStream_t s) {
 
 size_t gated_norm_bwd_workspace(long rows, long groups, int F) {
   const norm::GroupPlan p = norm::group_plan(rows, groups, F);
-  const long joined = !p.own && groups > 1 ? groups : 0;
+  const long joined = !p.own && groups > norm::kMaxAtOnce ? groups : 0;
   return (size_t)2 * (p.blocks + joined) * F * sizeof(float);
 }
 

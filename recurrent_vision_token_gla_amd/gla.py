@@ -538,6 +538,8 @@ def spatial_swiglu(a: torch.Tensor, u: torch.Tensor, weight: torch.Tensor,
 # the current stream of a device as a pointer, without building a Stream object
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+# the current device, where a device tensor is at hand (so that the runtime is up)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 class _Here:
@@ -587,7 +589,7 @@ class _There:
 
 def _launching(device, stream, *inputs):
     """Device and stream of a call, as a context with the raw stream pointer."""
-    if stream is None and torch.cuda.current_device() == device.index:
+    if stream is None and _current_device() == device.index:
         return _Here(device.index)
     return _There(device, stream, inputs)
 
@@ -847,19 +849,24 @@ def gate_bwd(o: torch.Tensor, gate: torch.Tensor, norm_weight: torch.Tensor, eps
 
 def _rows_of(x: torch.Tensor, name: str):
     """(device, rows, width) of a contiguous device tensor [..., width]."""
-    dev = _on_gpu(x, name)
-    if x.dim() < 1 or not x.is_contiguous():
+    if not x.is_cuda or not x.is_contiguous() or x.dim() < 1:
         raise ValueError(f"{name} must be a contiguous device tensor [..., K]")
     K = x.shape[-1]
-    return dev, (x.numel() // K if K else 0), K
+    return x.device, (x.numel() // K if K else 0), K
 
 
-def _weight_of(weight: torch.Tensor, x: torch.Tensor, K: int, name: str) -> int:
+def _weight_of(weight: torch.Tensor, x: torch.Tensor, dev, K: int, name: str) -> int:
     """Rows of a weight [N, K] in x's dtype, on x's device."""
-    if weight.dim() != 2:
-        raise ValueError(f"{name} must be [N, K]")
-    _like(weight, (weight.shape[0], K), x.dtype, x.device, name)
-    return weight.shape[0]
+    shape = weight.shape
+    if len(shape) != 2 or shape[1] != K or weight.dtype is not x.dtype or weight.device != dev or \
+            not weight.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {x.dtype} tensor [N, {K}] on {dev}")
+    return shape[0]
+
+
+def _new(out: Optional[torch.Tensor], shape, like: torch.Tensor) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one of like's dtype and device."""
+    return like.new_empty(shape) if out is None else _out(out, shape, like.dtype, like.device)
 
 
 @functools.lru_cache(maxsize=256)
@@ -887,8 +894,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     dtype (float16 or float32), bias [N] float32; K and N multiples of 8. out
     may be residual."""
     dev, rows, K = _rows_of(x, "x")
-    N = _weight_of(weight, x, K, "weight")
-    shape = x.shape[:-1] + (N,)
+    N = _weight_of(weight, x, dev, K, "weight")
+    shape = (*x.shape[:-1], N)
     if bias is not None:
         _like(bias, (N,), torch.float32, dev, "bias")
     if residual is not None:
@@ -896,8 +903,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     if pre is not None and not return_pre:
         raise ValueError("pre is written with return_pre only")
     with _launching(dev, stream, x, weight, bias, residual, out, pre) as st_ptr:
-        y = _out(out, shape, x.dtype, dev)
-        p = _out(pre, shape, x.dtype, dev) if return_pre else None
+        y = _new(out, shape, x)
+        p = _new(pre, shape, x) if return_pre else None
         st = load().gla_linear(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(residual), _ptr(p),
                                y.data_ptr(), rows, K, N, act, float(alpha), _dtype_code(x), st_ptr)
     _check(st, "gla_linear")
@@ -913,8 +920,8 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, gy: torch.Tensor, act: int
     (not needed for ACT_NONE); the residual's gradient is gy. None for those
     not needed. gx and gweight have x's dtype, gbias is float32."""
     dev, rows, K = _rows_of(x, "x")
-    N = _weight_of(weight, x, K, "weight")
-    shape = x.shape[:-1] + (N,)
+    N = _weight_of(weight, x, dev, K, "weight")
+    shape = (*x.shape[:-1], N)
     _like(gy, shape, x.dtype, dev, "gy")
     if act != ACT_NONE:
         _like(pre, shape, x.dtype, dev, "pre")
@@ -946,17 +953,17 @@ def gated_ff(x: torch.Tensor, gate_weight: torch.Tensor, up_weight: torch.Tensor
     return_parts, the two products for gated_ff_bwd (written to `parts` if
     given). x [..., K], weights [F, K], h, a, u [..., F] in one dtype."""
     dev, rows, K = _rows_of(x, "x")
-    F = _weight_of(gate_weight, x, K, "gate_weight")
-    _like(up_weight, gate_weight.shape, x.dtype, dev, "up_weight")
+    F = _weight_of(gate_weight, x, dev, K, "gate_weight")
+    if _weight_of(up_weight, x, dev, K, "up_weight") != F:
+        raise ValueError(f"up_weight must be [{F}, {K}] as gate_weight is")
     if parts is not None and (not return_parts or len(parts) != 2):
         raise ValueError("parts must be two tensors (a, u), written with return_parts only")
-    shape = x.shape[:-1] + (F,)
+    shape = (*x.shape[:-1], F)
     with _launching(dev, stream, x, gate_weight, up_weight, out, *(parts or ())) as st_ptr:
-        h = _out(out, shape, x.dtype, dev)
+        h = _new(out, shape, x)
         a = u = None
         if return_parts:
-            a = _out(parts[0] if parts else None, shape, x.dtype, dev)
-            u = _out(parts[1] if parts else None, shape, x.dtype, dev)
+            a, u = (_new(t, shape, x) for t in parts or (None, None))
         st = load().gla_gated_ff(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(), _ptr(a),
                                  _ptr(u), h.data_ptr(), rows, K, F, act, _dtype_code(x), st_ptr)
     _check(st, "gla_gated_ff")
@@ -972,9 +979,10 @@ def gated_ff_bwd(x: torch.Tensor, gate_weight: torch.Tensor, up_weight: torch.Te
     """(gx, ggate_weight, gup_weight) of gated_ff from gh = dL/dh and the
     forward's a, u; None for those not needed. All in x's dtype."""
     dev, rows, K = _rows_of(x, "x")
-    F = _weight_of(gate_weight, x, K, "gate_weight")
-    _like(up_weight, gate_weight.shape, x.dtype, dev, "up_weight")
-    _alike(x.shape[:-1] + (F,), x.dtype, dev, "a u gh", a, u, gh)
+    F = _weight_of(gate_weight, x, dev, K, "gate_weight")
+    if _weight_of(up_weight, x, dev, K, "up_weight") != F:
+        raise ValueError(f"up_weight must be [{F}, {K}] as gate_weight is")
+    _alike((*x.shape[:-1], F), x.dtype, dev, "a u gh", a, u, gh)
     if gweights is not None and len(gweights) != 2:
         raise ValueError("gweights must be two tensors (ggate_weight, gup_weight)")
     with _launching(dev, stream, x, gate_weight, up_weight, a, u, gh, gx, workspace,
