@@ -452,8 +452,11 @@ int gla_gate_bwd(const void* o, const void* gate, const float* norm_weight,
  * [N][K] in the input dtype (as a linear layer keeps it), y [rows][N]. K and N
  * are multiples of 8, at most 65536 (GLA_E_UNSUPPORTED otherwise, and for K 0
  * where there are outputs); any number of rows up to 2^31. Sums are float, over
- * half operands or, for GLA_F32, over whole float ones; every output is rounded
- * once. Any finite values: an output beyond the half range is +-Inf in GLA_F16.
+ * half operands or, for GLA_F32, over operands of 24 bits (three bfloat16 terms
+ * each, but for forward calls of up to 64 rows); every output is rounded once.
+ * Any finite values, float ones up to bfloat16's largest, 3.38e38: what lies
+ * beyond it, Inf among them, makes the sums that it enters NaN or Inf. An output
+ * beyond the half range is +-Inf in GLA_F16.
  * An empty problem (no row or no output) returns GLA_OK and writes nothing.
  *
  * Activations, of z in float: silu z / (1 + exp(-z)), gelu z Phi(z) with Phi

@@ -6,12 +6,17 @@
 // bytes of every row (64 halves, 32 floats) into LDS by buffer loads that write
 // LDS directly; a load past the operand's end gives zero. While a step is
 // multiplied the next ones are in flight (kStages buffers, one barrier a step).
-// Half operands go through the 16x16x32 product, float ones through 16x16x4,
-// which keeps them whole; sums are float.
+// Half operands go through the 16x16x32 product as they are, float ones as three
+// bf16 terms (24 bits), of whose products six are kept (the rest is below 2^-24
+// of the largest): 96 cycles of the matrix cores for what the float instruction
+// needs 256 for. Splitting them on every read costs about as many cycles of the
+// vector units again: 20,000 x 768 x 768 190 -> 143 us, 12,000 x 520 x 1,000 125 ->
+// 97, the error against 64 bits halved. Sums are float.
 #pragma once
 
 #include <type_traits>
 
+#include "gla_terms.h"
 #include "gla_tile.h"
 
 namespace gla {
@@ -61,11 +66,11 @@ struct Operand {
   static __device__ __forceinline__ int twist(int row) {
     if (!kCol) return row & 7;
     if (sizeof(T) == 2) return (2 * (row & 3) | (row & 8)) & (kPerRow - 1);
-    return (row & 4) & (kPerRow - 1);
+    return (row >> 1) & 4 & (kPerRow - 1);
   }
 
-  // 16 bytes of contraction for row r0 + lane % 16: elements
-  // 4 kUnit ks + kUnit q + 0..kUnit-1 with q = lane / 16 (both operands alike)
+  // Eight elements of the contraction for row r0 + lane % 16: 32 ks + 8 q + 0..7
+  // with q = lane / 16.
   static __device__ __forceinline__ void read(const char* lds, int r0, int ks, half8& x) {
     const int i = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
     if constexpr (!kCol) {
@@ -82,19 +87,26 @@ struct Operand {
       x = half8{h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
     }
   }
-  static __device__ __forceinline__ void read(const char* lds, int r0, int ks, floatx4& x) {
+  static __device__ __forceinline__ void read(const char* lds, int r0, int, terms::Split8<3>& x) {
     const int i = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
+    float y[8];
     if constexpr (!kCol) {
       const int row = r0 + i;
-      x = *reinterpret_cast<const floatx4*>(lds + row * 128 + 16 * ((4 * ks + q) ^ twist(row)));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const floatx4 v = *reinterpret_cast<const floatx4*>(lds + row * 128 + 16 * ((2 * q + h) ^ twist(row)));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[4 * h + c] = v[c];
+      }
     } else {
       const int col = r0 + i;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = 16 * ks + 4 * q + j;
-        x[j] = *reinterpret_cast<const float*>(lds + row * (4 * R) + 16 * ((col >> 2) ^ twist(row)) + 4 * (col & 3));
+      for (int j = 0; j < 8; ++j) {
+        const int row = 8 * q + j;
+        y[j] = *reinterpret_cast<const float*>(lds + row * (4 * R) + 16 * ((col >> 2) ^ twist(row)) + 4 * (col & 3));
       }
     }
+    x = terms::split8<3>(y);
   }
 
   // How thread `tid` of NT, of wave w, loads its units of a step.
@@ -128,6 +140,9 @@ struct Operand {
 };
 
 __device__ __forceinline__ floatx4 product(half8 a, half8 b, floatx4 c) { return mfma16x16x32(a, b, c); }
+__device__ __forceinline__ floatx4 product(const terms::Split8<3>& a, const terms::Split8<3>& b, floatx4 c) {
+  return terms::mm<3>(a, b, c);
+}
 __device__ __forceinline__ floatx4 product(floatx4 a, floatx4 b, floatx4 c) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
@@ -354,7 +369,7 @@ __device__ __forceinline__ void gemm_tile(const Args& g, int id, int count, char
   using OB = Operand<T, BN, kColB>;
   using LA = typename OA::template Loader<NT>;
   using LB = typename OB::template Loader<NT>;
-  using Frag = typename std::conditional<sizeof(T) == 2, half8, floatx4>::type;
+  using Frag = typename std::conditional<sizeof(T) == 2, half8, terms::Split8<3>>::type;
   constexpr int kStep = Num<T>::kStep, kStageBytes = OA::kBytes + OB::kBytes;
   static_assert(!kDual || !kColB, "both sides of a gated product lie along the contraction");
   constexpr int kInFlight = LA::kLoads + LB::kLoads;
@@ -420,7 +435,7 @@ __device__ __forceinline__ void gemm_tile(const Args& g, int id, int count, char
     const char* sa = smem + stage * kStageBytes;
     const char* sb = sa + OA::kBytes;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
+    for (int ks = 0; ks < kStep / 32; ++ks) {
       Frag fa[MI], fb[NI];
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi) OA::read(sa, (wm * MI + mi) * 16, ks, fa[mi]);
@@ -499,9 +514,9 @@ __global__ __launch_bounds__((kTileThreads<T, kTile, kEpi == kGated>)) void gemm
 
 // What a launch costs, in us. A step (128 bytes of every row) costs a CU about
 // 0.28, the meeting of the waves and the latency of LDS, and 1.3 for each 256 x
-// 256 half outputs (7 for float ones, whose matrix instructions do a sixteenth of
-// the work in as much time); a tile starts and ends in 2 and 5 for as many
-// outputs, and groups of waves add their sums up. Within 20% of what was measured
+// 256 half outputs (7 for float ones, whose values every wave splits into terms,
+// 5.5 with 128 x 128, which split each fewer times); a tile starts and ends in 2
+// and 5 for as many outputs, and groups of waves add their sums up. Within 20% of what was measured
 // over 100 to 25,600 rows of 100 to 4,096 values. Half, 25,600 x 2,048 x 768 with
 // 320, 256, 192 and 128 rows of 256 columns: 77, 107, 90 and 106 (0.94, 1.17, 1.57
 // and 2.34 rounds of the CUs); 1,600 x 768 x 768 with 128 x 128 12.7, 64 x 64 8.5,
@@ -514,7 +529,7 @@ inline long tile_count(const TileShape& s, long M, long N) { return ((M + s.m - 
 // One round of tiles, `on` workgroups on every CU.
 template <typename T>
 float round_cost(const TileShape& s, long steps, long on) {
-  const float area = s.m * s.n / 65536.f, per_step = sizeof(T) == 2 ? 1.3f : 7.f;
+  const float area = s.m * s.n / 65536.f, per_step = sizeof(T) == 2 ? 1.3f : s.m == 128 ? 5.5f : 7.f;
   return (steps + s.groups - 1) / s.groups * (0.28f + per_step * area * on * s.groups) + 2.f + 5.f * area * on +
          (s.groups - 1) * (0.25f + 8.f * area);
 }
