@@ -453,7 +453,7 @@ int gla_gate_bwd(const void* o, const void* gate, const float* norm_weight,
  * are multiples of 8, at most 65536 (GLA_E_UNSUPPORTED otherwise, and for K 0
  * where there are outputs); any number of rows up to 2^31. Sums are float, over
  * half operands or, for GLA_F32, over operands of 24 bits (three bfloat16 terms
- * each, but for forward calls of up to 64 rows); every output is rounded once.
+ * each, but for forward calls of few rows); every output is rounded once.
  * Any finite values, float ones up to bfloat16's largest, 3.38e38: what lies
  * beyond it, Inf among them, makes the sums that it enters NaN or Inf. An output
  * beyond the half range is +-Inf in GLA_F16.
@@ -470,9 +470,9 @@ enum { GLA_ACT_NONE = 0, GLA_ACT_SILU = 1, GLA_ACT_GELU = 2, GLA_ACT_LOGSIGMOID 
  *   y = alpha * act(x W^T + bias) + residual.
  * bias: float [N], 16-byte aligned, or NULL; residual: [rows][N] in the input
  * dtype or NULL; pre: [rows][N] takes x W^T + bias for the gradient, or NULL.
- * y may be residual itself; nothing else may overlap. Up to 64 rows (the new
- * tokens of as many sequences) run in a form of their own, which reads the
- * weight once. */
+ * y may be residual itself; nothing else may overlap. Few rows (the new tokens
+ * of up to 16 sequences; of up to 8 to 64 in gla_gated_ff) run in a form of
+ * their own, which reads the weight once. */
 int gla_linear(const void* x, const void* weight, const float* bias,
                const void* residual, void* pre, void* y, int64_t rows, int K,
                int N, int act, float alpha, int dtype, void* stream);

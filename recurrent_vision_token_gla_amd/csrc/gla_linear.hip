@@ -8,90 +8,104 @@
 namespace gla {
 namespace gemm {
 
-// Up to 16 MI rows. A workgroup takes 16 columns (gated: 16 of both weights);
-// its eight waves take steps of the contraction in turn, straight from memory
-// into the operands of the matrix cores: lane i, q holds row i and the 32 bytes
-// 32 q .. of the step's 128, whole lines of a weight row by four lanes. The
-// waves' sums meet in LDS.
+// Up to 16 MI rows. A workgroup takes 16 columns of the matrix cores' tile (gated:
+// eight of either weight, so that a small F still occupies the CUs: 37 rows x 768
+// x 2,048 with 16 of both 6.8 us, with eight 5.9); its eight waves take steps of the
+// contraction in turn, straight from memory into the operands of the matrix cores:
+// lane i, q holds row i and the 32 bytes 32 q .. of the step's 128, whole lines of a
+// weight row by four lanes. The waves' sums meet in LDS. Bound by the latency of
+// one load, the exchange and the launch where the weights are small (one row x 768
+// x 3,840: 3.7 us), by the weights' way from memory where they are large (one row x
+// 4,096 x 11,264, gated, 185 MB: 34.6 us, 5.3 TB/s).
 constexpr int kSkinnyWaves = 8;
 
 template <typename T, int MI, bool kDual>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const Args g) {
-  constexpr int kUnit = Num<T>::kUnit, kStep = Num<T>::kStep, ND = kDual ? 2 : 1;
+  constexpr int kUnit = Num<T>::kUnit, kStep = Num<T>::kStep, kCols = kDual ? 8 : 16;
   using Frag = typename std::conditional<sizeof(T) == 2, half8, floatx4>::type;
-  __shared__ __attribute__((aligned(16))) float red[kSkinnyWaves][ND][16 * MI][16];
+  __shared__ __attribute__((aligned(16))) float red[kSkinnyWaves][16 * MI][16];
   const int i = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3, w = wave();
-  const long n0 = 16L * blockIdx.x, n = min(n0 + i, g.N - 1);
-  const T* pw[2] = {static_cast<const T*>(g.b[0]) + n * g.ldb, static_cast<const T*>(g.b[ND - 1]) + n * g.ldb};
+  const long n0 = (long)kCols * blockIdx.x, n = min(n0 + i % kCols, g.N - 1);
+  const T* pw = static_cast<const T*>(g.b[kDual ? i >> 3 : 0]) + n * g.ldb;
   const T* px[MI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) px[mi] = static_cast<const T*>(g.a[0]) + min(16L * mi + i, g.M - 1) * g.lda;
-  floatx4 acc[ND][MI];
+  floatx4 acc[MI];
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) acc[d][mi] = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (int mi = 0; mi < MI; ++mi) acc[mi] = floatx4{0.f, 0.f, 0.f, 0.f};
   const int steps = (int)g.steps;
   // two steps a round, all of their loads in flight; beyond the contraction's
   // end they read its last elements, which then count as zero
   for (int s = w; s < steps; s += 2 * kSkinnyWaves) {
-    Frag fw[ND][4], fx[MI][4];
+    Frag fw[4], fx[MI][4];
     bool in[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const long k = (long)(s + (u >> 1) * kSkinnyWaves) * kStep + (2 * q + (u & 1)) * kUnit;
       const long at = min(k, g.K - kUnit);
       in[u] = k < g.K;
-#pragma unroll
-      for (int d = 0; d < ND; ++d) fw[d][u] = *reinterpret_cast<const Frag*>(pw[d] + at);
+      fw[u] = *reinterpret_cast<const Frag*>(pw + at);
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi) fx[mi][u] = *reinterpret_cast<const Frag*>(px[mi] + at);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi) {
-        const Frag x = in[u] ? fx[mi][u] : Frag{};
-#pragma unroll
-        for (int d = 0; d < ND; ++d) acc[d][mi] = product(in[u] ? fw[d][u] : Frag{}, x, acc[d][mi]);
-      }
+      for (int mi = 0; mi < MI; ++mi)
+        acc[mi] = product(in[u] ? fw[u] : Frag{}, in[u] ? fx[mi][u] : Frag{}, acc[mi]);
   }
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) *reinterpret_cast<floatx4*>(&red[w][d][16 * mi + i][4 * q]) = acc[d][mi];
+  for (int mi = 0; mi < MI; ++mi) *reinterpret_cast<floatx4*>(&red[w][16 * mi + i][4 * q]) = acc[mi];
   __syncthreads();
-  for (int t = threadIdx.x; t < 64 * MI; t += 64 * kSkinnyWaves) {
-    const int r = t >> 2, c = 4 * (t & 3);
-    const long nn = n0 + c;
-    if (r >= g.M || nn >= g.N) continue;
-    float x[ND][4];
+  const int r = threadIdx.x / (kCols / 4), c = 4 * (threadIdx.x % (kCols / 4));
+  const long nn = n0 + c;
+  if (r >= g.M || r >= 16 * MI || nn >= g.N) return;
+  float x[kDual ? 2 : 1][4];
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      floatx4 y = {0.f, 0.f, 0.f, 0.f};
+  for (int d = 0; d < (kDual ? 2 : 1); ++d) {
+    floatx4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int v = 0; v < kSkinnyWaves; ++v) y += *reinterpret_cast<const floatx4*>(&red[v][d][r][c]);
+    for (int v = 0; v < kSkinnyWaves; ++v) y += *reinterpret_cast<const floatx4*>(&red[v][r][8 * d + c]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[d][e] = y[e];
-    }
-    if constexpr (kDual) finish_gated<T>(g, r, nn, x[0], x[1]);
-    else finish<T>(g, 0, r, nn, x[0]);
+    for (int e = 0; e < 4; ++e) x[d][e] = y[e];
   }
+  if constexpr (kDual) finish_gated<T>(g, r, nn, x[0], x[1]);
+  else finish<T>(g, 0, r, nn, x[0]);
 }
 
-template <typename T, bool kDual>
+template <typename T, int MI, bool kDual>
 hipError_t skinny(const Args& g, hipStream_t s) {
-  const dim3 grid((unsigned)((g.N + 15) / 16)), block(64 * kSkinnyWaves);
-  if (g.M <= 16) hipLaunchKernelGGL((skinny_kernel<T, 1, kDual>), grid, block, 0, s, g);
-  else if (g.M <= 32) hipLaunchKernelGGL((skinny_kernel<T, 2, kDual>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((skinny_kernel<T, 4, kDual>), grid, block, 0, s, g);
+  constexpr int kCols = kDual ? 8 : 16;
+  hipLaunchKernelGGL((skinny_kernel<T, MI, kDual>), dim3((unsigned)((g.N + kCols - 1) / kCols)),
+                     dim3(64 * kSkinnyWaves), 0, s, g);
   return hipGetLastError();
+}
+
+// Rows up to which skinny_kernel is taken. us, it against the tiles: linear, 16
+// rows x 768 x 768 3.7 and 4.0, 24 rows 4.4 and 4.3, 64 rows 6.8 and 4.3. Gated, up
+// to one workgroup a CU: 32 rows x 768 x 2,048 5.6 and 5.6, x 2,048 x 768 8.4 and
+// 10.5, 40 rows x 768 x 2,048 6.4 and 5.5; above: 8 rows x 1,024 x 8,192 8.9 and 9.3,
+// 16 rows 10.3 and 7.9. Gated float, whose tiles cost more: 64 rows x 768 x 2,048
+// 14.9 and 16.8; 16 rows x 1,024 x 8,192 22.2 and 23.1, 24 rows 26.5 and 23.6.
+template <typename T, bool kDual>
+long skinny_rows(long N) {
+  if (!kDual) return 16;
+  return (N <= 8 * kCus ? 32 : 8) * (sizeof(T) == 4 ? 2 : 1);
 }
 
 template <typename T, int kEpi>
 hipError_t forward(const Args& g, hipStream_t s) {
   constexpr bool kDual = kEpi == kGated;
-  if (g.M <= 64) return skinny<T, kDual>(g, s);
+  if (g.M <= skinny_rows<T, kDual>(g.N)) {
+    if constexpr (kDual) {
+      if constexpr (sizeof(T) == 4) {
+        if (g.M > 48) return skinny<T, 4, kDual>(g, s);
+        if (g.M > 32) return skinny<T, 3, kDual>(g, s);
+      }
+      if (g.M > 16) return skinny<T, 2, kDual>(g, s);
+    }
+    return skinny<T, 1, kDual>(g, s);
+  }
   return launch_product<T, false, false, kEpi>(g, best_tile<T, false, kEpi>(g.M, kDual ? 2 * g.N : g.N, 1, g.steps), s);
 }
 

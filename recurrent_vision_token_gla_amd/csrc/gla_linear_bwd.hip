@@ -42,15 +42,11 @@ __global__ __launch_bounds__(256) void slope_kernel(const T* __restrict__ pre, c
 #pragma unroll
   for (int c = 0; c < 8; ++c) s[threadIdx.x][c] = sum[c];
   __syncthreads();
-  if (ty == 0 && n < N) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      float y = 0.f;
-      for (int t = 0; t < per; ++t) y += s[tx + (t << shift)][c];
-      sum[c] = alpha * y;
-    }
-    tile::store_f8(part + (long)blockIdx.y * N + n, sum);
-  }
+  const long col = ((8L * blockIdx.x) << shift) + threadIdx.x;  // one column a thread
+  if (threadIdx.x >= 8 << shift || col >= N) return;
+  float y = 0.f;
+  for (int t = 0; t < per; ++t) y += s[(threadIdx.x >> 3) + (t << shift)][threadIdx.x & 7];
+  part[(long)blockIdx.y * N + col] = alpha * y;
 }
 
 // ga = gh u act'(a), gu = gh act(a), eight values a thread.
