@@ -455,8 +455,9 @@ int gla_gate_bwd(const void* o, const void* gate, const float* norm_weight,
  * half operands or, for GLA_F32, over operands of 24 bits (three bfloat16 terms
  * each, but for forward calls of few rows); every output is rounded once.
  * Any finite values, float ones up to bfloat16's largest, 3.38e38: what lies
- * beyond it, Inf among them, makes the sums that it enters NaN or Inf. An output
- * beyond the half range is +-Inf in GLA_F16.
+ * beyond it, Inf among them, makes the sums that it enters NaN or Inf. Float
+ * operands below 2^-110 are kept to 2^-134. An output beyond the half range is
+ * +-Inf in GLA_F16.
  * An empty problem (no row or no output) returns GLA_OK and writes nothing.
  *
  * Activations, of z in float: silu z / (1 + exp(-z)), gelu z Phi(z) with Phi
