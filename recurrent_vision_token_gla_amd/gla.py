@@ -9,6 +9,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import math
 import os
 import weakref
 from typing import Optional, Sequence, Union
@@ -852,7 +853,7 @@ def _rows_of(x: torch.Tensor, name: str):
     if not x.is_cuda or not x.is_contiguous() or x.dim() < 1:
         raise ValueError(f"{name} must be a contiguous device tensor [..., K]")
     K = x.shape[-1]
-    return x.device, (x.numel() // K if K else 0), K
+    return x.device, (x.numel() // K if K else math.prod(x.shape[:-1])), K
 
 
 def _weight_of(weight: torch.Tensor, x: torch.Tensor, dev, K: int, name: str) -> int:

@@ -317,3 +317,67 @@ def test_gradients_refuse_a_prepared_workspace():
     for call in calls:
         call()
     torch.cuda.synchronize()
+
+
+def test_rows_without_values_are_refused():
+    """A contraction of nothing has outputs, which no call writes; without outputs
+    there is nothing to do."""
+    x, w = torch.empty(3, 0, device="cuda").half(), torch.empty(24, 0, device="cuda").half()
+    gy = torch.zeros(3, 24, device="cuda").half()
+    for call in (lambda: gla.linear(x, w), lambda: gla.gated_ff(x, w, w), lambda: gla.linear_bwd(x, w, gy),
+                 lambda: gla.gated_ff_bwd(x, w, w, gy, gy, gy)):
+        with pytest.raises(gla.GLAError) as e:
+            call()
+        assert e.value.status == gla.E_UNSUPPORTED
+    assert gla.linear(x, w[:0]).shape == (3, 0)
+    y, s = gla.gated_add_rmsnorm(x, x, torch.empty(0, device="cuda"), EPS)
+    assert y.shape == s.shape == (3, 0)
+
+
+def test_many_rows_and_offsets_beyond_32_bits():
+    """More rows than one launch takes, outputs of more than 4 GiB. Values are
+    whole and small, so that every sum is exact in float."""
+    rows, K, N = (1 << 22) + 17, 8, 520
+    torch.manual_seed(9)
+    whole = lambda *shape: torch.randint(-1, 2, shape, device="cuda", dtype=torch.int8).half()
+    x, w = whole(rows, K), whole(N, K)
+    y = gla.linear(x, w)
+    h, a, u = gla.gated_ff(x, w, w, act=gla.ACT_NONE, return_parts=True)
+    torch.cuda.synchronize()
+    some = torch.cat([torch.arange(70), torch.arange((1 << 22) - 40, rows), torch.arange(1 << 21, (1 << 21) + 70)]).cuda()
+    want = x[some].float() @ w.float().t()
+    for got, t in ((y, want), (a, want), (u, want), (h, want * want)):
+        assert torch.equal(got[some].float(), t)
+    del y, a, u
+    gy = h.clamp_(-1, 1)
+    gx, gw, gb = gla.linear_bwd(x, w, gy)
+    torch.cuda.synchronize()
+    assert torch.equal(gx[some].float(), gy[some].float() @ w.float())
+    gW, gB = torch.zeros(N, K, device="cuda"), torch.zeros(N, device="cuda")
+    for r in range(0, rows, 1 << 19):
+        g = gy[r:r + (1 << 19)].float()
+        gW += g.t() @ x[r:r + (1 << 19)].float()
+        gB += g.sum(0)
+    assert gW.abs().max() < 1 << 24 and gB.abs().max() < 1 << 24
+    assert torch.equal(gw, gW.half()) and torch.equal(gb, gB)
+    del x, h, gy, gx
+    torch.cuda.empty_cache()
+
+
+def test_norms_with_offsets_beyond_32_bits():
+    rows, F, G = (1 << 21) + 2, 1032, 2
+    torch.manual_seed(10)
+    x, res = (torch.randn(rows, F, device="cuda", dtype=torch.float16) for _ in range(2))
+    w, gate = torch.ones(F, device="cuda"), torch.randn(G, F, device="cuda").half()
+    y, s = gla.gated_add_rmsnorm(x, res, w, EPS, gate=gate)
+    gx, gres, _, _, ggate, _ = gla.gated_add_rmsnorm_bwd(x, s, w, EPS, res, gate=gate)
+    torch.cuda.synchronize()
+    for r in (slice(0, 50), slice(rows // 2 - 50, rows // 2), slice(rows // 2, rows // 2 + 50), slice(rows - 50, rows)):
+        g = gate[r.start * G // rows][None].contiguous()
+        part = gla.gated_add_rmsnorm(x[r], res[r], w, EPS, gate=g)
+        back = gla.gated_add_rmsnorm_bwd(x[r], part[1], w, EPS, res[r], gate=g)
+        torch.cuda.synchronize()
+        for got, want in zip((y, s, gx, gres), (*part, *back[:2])):
+            assert torch.equal(got[r], want)
+    del x, res, y, s, gx, gres, got
+    torch.cuda.empty_cache()
