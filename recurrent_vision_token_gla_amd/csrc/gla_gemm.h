@@ -321,14 +321,14 @@ struct Place {
 // workgroups that a CU holds at once, and groups of such waves in a workgroup,
 // which take a part of the steps each and add their sums up at the end (few
 // tiles, a long contraction).
-enum Tile { k320x256, k256x256, k192x256, k128x256, k128x128, k64x64, k64x64by2, k64x64by4,
+enum Tile { k320x256, k256x256, k192x256, k128x256, k128x128, k128x128by2, k64x64, k64x64by2, k64x64by4,
             k32x32by4, k32x32by8, kTiles };
 struct TileShape {
   int m, n, wm, wn, stages, per_cu, groups;
 };
 constexpr TileShape kTileShapes[kTiles] = {
     {320, 256, 4, 4, 2, 1, 1}, {256, 256, 4, 4, 2, 1, 1}, {192, 256, 4, 4, 2, 1, 1}, {128, 256, 4, 4, 2, 1, 1},
-    {128, 128, 2, 2, 2, 2, 1}, {64, 64, 2, 2, 4, 2, 1},   {64, 64, 2, 2, 4, 1, 2},   {64, 64, 2, 2, 2, 1, 4},
+    {128, 128, 2, 2, 2, 2, 1}, {128, 128, 2, 2, 2, 1, 2}, {64, 64, 2, 2, 4, 2, 1},   {64, 64, 2, 2, 4, 1, 2},   {64, 64, 2, 2, 2, 1, 4},
     {32, 32, 1, 1, 2, 2, 4},   {32, 32, 1, 1, 2, 1, 8}};
 constexpr TileShape tile_shape(int tile, bool is_float, bool gated) {
   TileShape s = kTileShapes[tile];
@@ -514,14 +514,18 @@ __global__ __launch_bounds__((kTileThreads<T, kTile, kEpi == kGated>)) void gemm
 
 // What a launch costs, in us. A step (128 bytes of every row) costs a CU about
 // 0.28, the meeting of the waves and the latency of LDS, and 1.3 for each 256 x
-// 256 half outputs (7 for float ones, whose values every wave splits into terms,
-// 5.5 with 128 x 128, which split each fewer times); a tile starts and ends in 2
-// and 5 for as many outputs, and groups of waves add their sums up. Within 20% of what was measured
-// over 100 to 25,600 rows of 100 to 4,096 values. Half, 25,600 x 2,048 x 768 with
-// 320, 256, 192 and 128 rows of 256 columns: 77, 107, 90 and 106 (0.94, 1.17, 1.57
-// and 2.34 rounds of the CUs); 1,600 x 768 x 768 with 128 x 128 12.7, 64 x 64 8.5,
-// by two groups 11.3; 130 x 768 x 768 11.8, 6.4, 6.1, and with 32 x 32 by four
-// groups 5.0.
+// 256 half outputs; one wave alone on its SIMD (128 x 128, one workgroup on a CU)
+// takes 1.6 times that. Float ones cost 7, as every wave splits its values into
+// terms, and 5.5 with 128 x 128, which split each fewer times (4.6 by two groups,
+// of which one splits while the other multiplies). A tile starts and ends in 2 and
+// 5 for as many outputs, and groups of waves add their sums up. Within 20% of what
+// was measured over 100 to 25,600 rows of 100 to 4,096 values. Half, 25,600 x 2,048
+// x 768 with 320, 256, 192 and 128 rows of 256 columns: 77, 107, 90 and 106 (0.94,
+// 1.17, 1.57 and 2.34 rounds of the CUs); 4,000 x 1,024 x 1,024 with 128 x 128 16.1,
+// by two groups 14.5, 64 x 64 17.3; 1,600 x 768 x 768 13.0, 11.7, 8.2; 130 x 768 x
+// 768 with 128 x 128 11.8, 64 x 64 6.4, 32 x 32 by four groups 5.0. Float, 4,000 x
+// 1,024 x 1,024 with 128 x 128 56.5, by two groups 50.5, 64 x 64 64.6; 1,600 x 768 x
+// 768 43.0, 36.5, 29.3, with 32 x 32 by four groups 24.7.
 constexpr int kCus = 256;
 
 inline long tile_count(const TileShape& s, long M, long N) { return ((M + s.m - 1) / s.m) * ((N + s.n - 1) / s.n); }
@@ -529,7 +533,9 @@ inline long tile_count(const TileShape& s, long M, long N) { return ((M + s.m - 
 // One round of tiles, `on` workgroups on every CU.
 template <typename T>
 float round_cost(const TileShape& s, long steps, long on) {
-  const float area = s.m * s.n / 65536.f, per_step = sizeof(T) == 2 ? 1.3f : s.m == 128 ? 5.5f : 7.f;
+  const float area = s.m * s.n / 65536.f;
+  const bool square = s.m == 128 && s.n == 128, alone = square && s.groups == 1 && on == 1;
+  const float per_step = sizeof(T) == 2 ? (alone ? 2.1f : 1.3f) : !square ? 7.f : s.groups == 1 ? 5.5f : 4.6f;
   return (steps + s.groups - 1) / s.groups * (0.28f + per_step * area * on * s.groups) + 2.f + 5.f * area * on +
          (s.groups - 1) * (0.25f + 8.f * area);
 }
