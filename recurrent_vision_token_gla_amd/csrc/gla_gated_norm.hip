@@ -1,7 +1,9 @@
 // Norms after and before a block with its gate and residual scale,
 //   p = x / sqrt(mean(x^2) + eps) * post,  s = residual + scale gate p,
 //   y = s / sqrt(mean(s^2) + eps) * w,
-// and their gradient. A few flops per byte: memory bounds them. A team of TPR
+// and their gradient. A few flops per byte: memory bounds them (4 x 6,400 x 768 half
+// with gates: 27.4 us, 5.7 TB/s; the gradient 44.0, 5.4 TB/s, and 5.7 for the join of
+// its sums; 1,600 x 768 5.5 us, a launch's and two loads' latency). A team of TPR
 // threads holds a row in registers, VPT groups of eight columns a thread, from
 // its loads to its stores, and walks rows, so that the weights are read once.
 // Statistics, weight gradients and the gate's gradient are summed in float in a
@@ -363,9 +365,8 @@ __global__ __launch_bounds__(1024) void gated_norm_join_kernel(
 // How the gradient's rows are shared out: teams that own groups once there are
 // enough of them, else chunks of each group's rows, in as many workgroups as the
 // CUs hold at once (25,600 x 768 half: 58.6 us with 512, 70.7 with 1,024). Up to
-// eight groups the last
-// launch takes side by side (four of 6,400 rows of 768: 5.4 us instead of 9.1 for
-// two launches).
+// eight groups the last launch takes side by side (four of 6,400 rows of 768: 5.4
+// us instead of 9.1 for two launches).
 constexpr long kMaxParts2 = 512, kMaxAtOnce = 8;
 int teams(int F) { return F <= 64 ? 32 : F <= 256 ? 16 : F <= 512 ? 8 : F <= 1024 ? 4 : 1; }
 struct GroupPlan {

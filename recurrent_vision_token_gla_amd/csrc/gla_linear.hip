@@ -15,7 +15,7 @@ namespace gemm {
 // lane i, q holds row i and the 32 bytes 32 q .. of the step's 128, whole lines of a
 // weight row by four lanes. The waves' sums meet in LDS. Bound by the latency of
 // one load, the exchange and the launch where the weights are small (one row x 768
-// x 3,840: 3.7 us), by the weights' way from memory where they are large (one row x
+// x 3,840: 4.0 us), by the weights' way from memory where they are large (one row x
 // 4,096 x 11,264, gated, 185 MB: 34.6 us, 5.3 TB/s).
 constexpr int kSkinnyWaves = 8;
 

