@@ -520,26 +520,30 @@ __global__ __launch_bounds__((kTileThreads<T, kTile, kEpi == kGated>)) void gemm
 // 256 half outputs; one wave alone on its SIMD (128 x 128, one workgroup on a CU)
 // takes 1.6 times that. Float ones cost 7, as every wave splits its values into
 // terms, and 5.5 with 128 x 128, which split each fewer times (4.6 by two groups,
-// of which one splits while the other multiplies). A tile starts and ends in 2 and
-// 5 for as many outputs, and groups of waves add their sums up. Within 20% of what
+// of which one splits while the other multiplies). Four or more groups that read
+// both half operands turned need 0.4 more a step. A tile starts and ends in 2 and 5
+// for as many outputs, and groups of waves add their sums up. Within 20% of what
 // was measured over 100 to 25,600 rows of 100 to 4,096 values. Half, 25,600 x 2,048
 // x 768 with 320, 256, 192 and 128 rows of 256 columns: 77, 107, 90 and 106 (0.94,
 // 1.17, 1.57 and 2.34 rounds of the CUs); 4,000 x 1,024 x 1,024 with 128 x 128 16.1,
 // by two groups 14.5, 64 x 64 17.3; 1,600 x 768 x 768 13.0, 11.7, 8.2; 130 x 768 x
 // 768 with 128 x 128 11.8, 64 x 64 6.4, 32 x 32 by four groups 5.0. Float, 4,000 x
 // 1,024 x 1,024 with 128 x 128 56.5, by two groups 50.5, 64 x 64 64.6; 1,600 x 768 x
-// 768 43.0, 36.5, 29.3, with 32 x 32 by four groups 24.7.
+// 768 43.0, 36.5, 29.3, with 32 x 32 by four groups 24.7. Weights' gradient, half,
+// 768 x 768 over 1,600 with 64 x 64 10.7, by four groups 11.0, 32 x 32 18.2.
 constexpr int kCus = 256;
 
 inline long tile_count(const TileShape& s, long M, long N) { return ((M + s.m - 1) / s.m) * ((N + s.n - 1) / s.n); }
 
-// One round of tiles, `on` workgroups on every CU.
+// One round of tiles, `on` workgroups on every CU; `turned`: both operands lie
+// down the columns.
 template <typename T>
-float round_cost(const TileShape& s, long steps, long on) {
+float round_cost(const TileShape& s, long steps, long on, bool turned) {
   const float area = s.m * s.n / 65536.f;
   const bool square = s.m == 128 && s.n == 128, alone = square && s.groups == 1 && on == 1;
   const float per_step = sizeof(T) == 2 ? (alone ? 2.1f : 1.3f) : !square ? 7.f : s.groups == 1 ? 5.5f : 4.6f;
-  return (steps + s.groups - 1) / s.groups * (0.28f + per_step * area * on * s.groups) + 2.f + 5.f * area * on +
+  const float meet = sizeof(T) == 2 && turned && s.groups >= 4 ? 0.68f : 0.28f;
+  return (steps + s.groups - 1) / s.groups * (meet + per_step * area * on * s.groups) + 2.f + 5.f * area * on +
          (s.groups - 1) * (0.25f + 8.f * area);
 }
 
@@ -554,8 +558,8 @@ int best_tile(long M, long N, long others, long steps, float* cost = nullptr) {
     const TileShape s = tile_shape(t, sizeof(T) == 4, false);
     const long count = tile_count(s, M, N) * others, slots = (long)kCus * s.per_cu;
     const long whole = count / slots, rest = count % slots;
-    const float c = whole * round_cost<T>(s, steps, s.per_cu) +
-                    (rest ? round_cost<T>(s, steps, (rest + kCus - 1) / kCus) : 0.f);
+    const float c = whole * round_cost<T>(s, steps, s.per_cu, kColA) +
+                    (rest ? round_cost<T>(s, steps, (rest + kCus - 1) / kCus, kColA) : 0.f);
     if (best < 0 || c < least) least = c, best = t;
   }
   if (cost) *cost = least;

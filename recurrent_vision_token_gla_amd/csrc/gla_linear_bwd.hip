@@ -178,7 +178,8 @@ void plan(long rows, int K, int N, int mparts, LinearBwdLayout* l) {
       const long nx = tile_count(a, rows, K), nw = tile_count(a, N, K) * mparts * splits;
       const long slots = (long)kCus * a.per_cu, per = (nx + nw + kCus - 1) / kCus;
       const long on = per < a.per_cu ? per : a.per_cu;
-      const float rx = round_cost<T>(a, steps_x, on), rw = round_cost<T>(a, each, on), longer = rx > rw ? rx : rw;
+      const float rx = round_cost<T>(a, steps_x, on, false), rw = round_cost<T>(a, each, on, true);
+      const float longer = rx > rw ? rx : rw;
       c = join + (nx + nw <= slots ? longer : (nx * rx + nw * rw) / slots + 0.5f * longer);
       if (c < least) least = c, l->tile_w = l->tile_x = p, l->splits = (int)splits, l->each = each, l->pair = true;
     }
