@@ -337,17 +337,17 @@ constexpr TileShape tile_shape(int tile, bool is_float, bool gated) {
   TileShape s = kTileShapes[tile];
   // the matrix instructions bound float: more workgroups instead of more steps in flight
   if (is_float && tile == k64x64) s.stages = 2, s.per_cu = 4;
-  // the gated product needs two column blocks of each weight in a wave
-  if (gated && s.m == 64) s.wm = 4, s.wn = 1;
+  // two column blocks of each weight in a wave, so that a lane stores 16 bytes of halves
+  if (gated && !is_float && s.m == 64) s.wm = 4, s.wn = 1;
   return s;
 }
 // Float tiles gain nothing above 128 x 128; the weights' gradients take no
 // others of 256 columns than 256 x 256 (320 rows need more registers than there
-// are); 32 columns are too few for the gated product.
+// are).
 template <typename T, bool kColA, int kEpi>
 constexpr bool has_tile(int t) {
   if (t < k128x128) return sizeof(T) == 2 && (!kColA || t == k256x256);
-  return t < k32x32by4 || kEpi != kGated;
+  return true;
 }
 
 // Workgroup `id` of `count` of one product, with kTileBytes of LDS.
@@ -476,14 +476,24 @@ __device__ __forceinline__ void gemm_tile(const Args& g, int id, int count, char
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] += sums[(o * MI * NI + mi * NI + ni) * NT + tid];
   }
 
-  // each lane: row lane % 16 of the row blocks, eight columns of each pair of column blocks
+  // each lane: row lane % 16 of the row blocks, eight columns of each pair of column blocks;
+  // gated, four of each block where they are 16 bytes or there is one block of each weight
+  constexpr bool kFour = sizeof(T) == 4 || NI / 2 == 1;
   const int i = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3, c8 = 16 * (q & 1) + 8 * (q >> 1);
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     const long m = m0 + (wm * MI + mi) * 16 + i;
     if constexpr (kDual) {
 #pragma unroll
-      for (int p = 0; p < NI / 4; ++p) {
+      for (int p = 0; p < (kFour ? NI / 2 : 0); ++p) {
+        float x[4], u[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = acc[mi][p][c], u[c] = acc[mi][NI / 2 + p][c];
+        const long n = n0 + (wn * (NI / 2) + p) * 16 + 4 * q;
+        if (m < g.M && n < g.N) finish_gated<T>(g, m, n, x, u);
+      }
+#pragma unroll
+      for (int p = 0; p < (kFour ? 0 : NI / 4); ++p) {
         float x[8], u[8];
         pair8(acc[mi][2 * p], acc[mi][2 * p + 1], x);
         pair8(acc[mi][NI / 2 + 2 * p], acc[mi][NI / 2 + 2 * p + 1], u);

@@ -8,36 +8,31 @@
 namespace gla {
 namespace gemm {
 
-// Up to 16 MI rows. A workgroup takes 16 columns of the matrix cores' tile (gated:
-// eight of either weight, so that a small F still occupies the CUs: 37 rows x 768
-// x 2,048 with 16 of both 6.8 us, with eight 5.9); its eight waves take steps of the
+// Up to 16 rows. A workgroup takes the 16 columns of the matrix cores' tile (gated:
+// eight of either weight, so that a small F still occupies the CUs: 16 rows x 768 x
+// 2,048 with 16 of both 5.1 us, with eight 4.3); its eight waves take steps of the
 // contraction in turn, straight from memory into the operands of the matrix cores:
 // lane i, q holds row i and the 32 bytes 32 q .. of the step's 128, whole lines of a
 // weight row by four lanes. The waves' sums meet in LDS. Bound by the latency of
-// one load, the exchange and the launch where the weights are small (one row x 768
-// x 3,840: 4.0 us), by the weights' way from memory where they are large (one row x
-// 4,096 x 11,264, gated, 185 MB: 34.6 us, 5.3 TB/s).
-constexpr int kSkinnyWaves = 8;
+// one load, the exchange and the launch (one row x 768 x 3,840: 4.0 us; four rows x
+// 8,192 x 1,024: 12.2, 1.4 TB/s, where the tiles take 15.5).
+constexpr int kFewRows = 16, kSkinnyWaves = 8;
 
-template <typename T, int MI, bool kDual>
+template <typename T, bool kDual>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const Args g) {
   constexpr int kUnit = Num<T>::kUnit, kStep = Num<T>::kStep, kCols = kDual ? 8 : 16;
   using Frag = typename std::conditional<sizeof(T) == 2, half8, floatx4>::type;
-  __shared__ __attribute__((aligned(16))) float red[kSkinnyWaves][16 * MI][16];
+  __shared__ __attribute__((aligned(16))) float red[kSkinnyWaves][kFewRows][16];
   const int i = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3, w = wave();
   const long n0 = (long)kCols * blockIdx.x, n = min(n0 + i % kCols, g.N - 1);
   const T* pw = static_cast<const T*>(g.b[kDual ? i >> 3 : 0]) + n * g.ldb;
-  const T* px[MI];
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi) px[mi] = static_cast<const T*>(g.a[0]) + min(16L * mi + i, g.M - 1) * g.lda;
-  floatx4 acc[MI];
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi) acc[mi] = floatx4{0.f, 0.f, 0.f, 0.f};
+  const T* px = static_cast<const T*>(g.a[0]) + min((long)i, g.M - 1) * g.lda;
+  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
   const int steps = (int)g.steps;
   // two steps a round, all of their loads in flight; beyond the contraction's
   // end they read its last elements, which then count as zero
   for (int s = w; s < steps; s += 2 * kSkinnyWaves) {
-    Frag fw[4], fx[MI][4];
+    Frag fw[4], fx[4];
     bool in[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -45,21 +40,16 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const Args g)
       const long at = min(k, g.K - kUnit);
       in[u] = k < g.K;
       fw[u] = *reinterpret_cast<const Frag*>(pw + at);
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) fx[mi][u] = *reinterpret_cast<const Frag*>(px[mi] + at);
+      fx[u] = *reinterpret_cast<const Frag*>(px + at);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
-        acc[mi] = product(in[u] ? fw[u] : Frag{}, in[u] ? fx[mi][u] : Frag{}, acc[mi]);
+    for (int u = 0; u < 4; ++u) acc = product(in[u] ? fw[u] : Frag{}, in[u] ? fx[u] : Frag{}, acc);
   }
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi) *reinterpret_cast<floatx4*>(&red[w][16 * mi + i][4 * q]) = acc[mi];
+  *reinterpret_cast<floatx4*>(&red[w][i][4 * q]) = acc;
   __syncthreads();
   const int r = threadIdx.x / (kCols / 4), c = 4 * (threadIdx.x % (kCols / 4));
   const long nn = n0 + c;
-  if (r >= g.M || r >= 16 * MI || nn >= g.N) return;
+  if (r >= g.M || nn >= g.N) return;
   float x[kDual ? 2 : 1][4];
 #pragma unroll
   for (int d = 0; d < (kDual ? 2 : 1); ++d) {
@@ -73,38 +63,19 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const Args g)
   else finish<T>(g, 0, r, nn, x[0]);
 }
 
-template <typename T, int MI, bool kDual>
-hipError_t skinny(const Args& g, hipStream_t s) {
-  constexpr int kCols = kDual ? 8 : 16;
-  hipLaunchKernelGGL((skinny_kernel<T, MI, kDual>), dim3((unsigned)((g.N + kCols - 1) / kCols)),
-                     dim3(64 * kSkinnyWaves), 0, s, g);
-  return hipGetLastError();
-}
-
-// Rows up to which skinny_kernel is taken. us, it against the tiles: linear, 16
-// rows x 768 x 768 3.7 and 4.0, 24 rows 4.4 and 4.3, 64 rows 6.8 and 4.3. Gated, up
-// to one workgroup a CU: 32 rows x 768 x 2,048 5.6 and 5.6, x 2,048 x 768 8.4 and
-// 10.5, 40 rows x 768 x 2,048 6.4 and 5.5; above: 8 rows x 1,024 x 8,192 8.9 and 9.3,
-// 16 rows 10.3 and 7.9. Gated float, whose tiles cost more: 64 rows x 768 x 2,048
-// 14.9 and 16.8; 16 rows x 1,024 x 8,192 22.2 and 23.1, 24 rows 26.5 and 23.6.
-template <typename T, bool kDual>
-long skinny_rows(long N) {
-  if (!kDual) return 16;
-  return (N <= 8 * kCus ? 32 : 8) * (sizeof(T) == 4 ? 2 : 1);
-}
-
+// skinny_kernel up to 16 rows, gated up to one workgroup a CU besides. us, it against
+// the tiles: linear, 16 rows x 768 x 768 3.7 and 4.0, 24 rows (as two such kernels'
+// work) 4.4 and 4.3, 64 rows 6.8 and 4.3. Gated, 16 rows x 768 x 2,048 4.6 and 4.9, 32
+// rows 5.7 and 5.2; 8 rows x 768 x 4,096 5.7 and 5.7, x 1,024 x 8,192 9.3 and 7.6; float
+// 16 rows x 768 x 2,048 6.8 and 8.4, x 1,024 x 8,192 22.3 and 15.7.
 template <typename T, int kEpi>
 hipError_t forward(const Args& g, hipStream_t s) {
   constexpr bool kDual = kEpi == kGated;
-  if (g.M <= skinny_rows<T, kDual>(g.N)) {
-    if constexpr (kDual) {
-      if constexpr (sizeof(T) == 4) {
-        if (g.M > 48) return skinny<T, 4, kDual>(g, s);
-        if (g.M > 32) return skinny<T, 3, kDual>(g, s);
-      }
-      if (g.M > 16) return skinny<T, 2, kDual>(g, s);
-    }
-    return skinny<T, 1, kDual>(g, s);
+  constexpr int kCols = kDual ? 8 : 16;
+  if (g.M <= kFewRows && (!kDual || g.N <= kCols * kCus)) {
+    hipLaunchKernelGGL((skinny_kernel<T, kDual>), dim3((unsigned)((g.N + kCols - 1) / kCols)), dim3(64 * kSkinnyWaves),
+                       0, s, g);
+    return hipGetLastError();
   }
   return launch_product<T, false, false, kEpi>(g, best_tile<T, false, kEpi>(g.M, kDual ? 2 * g.N : g.N, 1, g.steps), s);
 }
