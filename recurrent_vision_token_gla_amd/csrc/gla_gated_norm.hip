@@ -297,9 +297,9 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_bwd_kernel(
 // Sums of the pairs of rows of part, gw and Q (or sum gate Q), `count` of them in
 // each of `groups` groups (kLast; else in group blockIdx.y): 16 columns and 64
 // rows of threads per workgroup. gate: the sums are Q, of which ggate (if wanted)
-// and gate Q are made. kLast: into the weights' gradients. Else into pair
-// blockIdx.y of `next`.
-template <typename T, bool kLast>
+// and gate Q are made; kEach: as many groups as pairs, each pair one group's whole
+// sum. kLast: into the weights' gradients. Else into pair blockIdx.y of `next`.
+template <typename T, bool kLast, bool kEach>
 __global__ __launch_bounds__(1024) void gated_norm_join_kernel(
     const float* __restrict__ part, float* __restrict__ next, int count, int groups, int F,
     const float* __restrict__ post, const T* __restrict__ gate, const float* __restrict__ scale,
@@ -310,6 +310,7 @@ __global__ __launch_bounds__(1024) void gated_norm_join_kernel(
   // `each` rows of threads to a group, a power of two and at least eight
   const int each = groups == 1 ? 64 : groups == 2 ? 32 : groups <= 4 ? 16 : 8, o = g / each, r = g % each;
   const long group = kLast ? o : blockIdx.y;
+  const float a = post && col < F ? post[col] : 1.f, b = scale && col < F ? scale[col] : 1.f;
   float y[2] = {0.f, 0.f};
   if (col < F && o < groups) {
     const float* from = part + 2 * group * count * F + col;
@@ -319,6 +320,16 @@ __global__ __launch_bounds__(1024) void gated_norm_join_kernel(
       for (int i = 0; i < W; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) x[h][i] = p + each * i < count ? from[(2L * (p + each * i) + h) * F] : 0.f;
+      if constexpr (kEach) {
+        float gates[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) gates[i] = p + each * i < count ? (float)gate[(long)(p + each * i) * F + col] : 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          if (ggp && p + each * i < count) ggp[(long)(p + each * i) * F + col] = (T)(a * b * x[1][i]);
+          x[1][i] *= gates[i];
+        }
+      }
 #pragma unroll
       for (int i = 0; i < W; ++i) y[0] += x[0][i], y[1] += x[1][i];
     }
@@ -335,12 +346,11 @@ __global__ __launch_bounds__(1024) void gated_norm_join_kernel(
     }
   }
   __syncthreads();
-  const float a = post && col < F ? post[col] : 1.f, b = scale && col < F ? scale[col] : 1.f;
   if (r == 0 && o < groups && col < F) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       for (int i = 8; i < each; i += 8) y[h] += s[h][g + i][c];
-    if (gate) {
+    if (!kEach && gate) {
       if (ggp) ggp[group * F + col] = (T)(a * b * y[1]);
       y[1] *= (float)gate[group * F + col];
     }
@@ -362,11 +372,15 @@ __global__ __launch_bounds__(1024) void gated_norm_join_kernel(
   }
 }
 
-// How the gradient's rows are shared out: teams that own groups once there are
-// enough of them, else chunks of each group's rows, in as many workgroups as the
-// CUs hold at once (25,600 x 768 half: 58.6 us with 512, 70.7 with 1,024). Up to
-// eight groups the last launch takes side by side (four of 6,400 rows of 768: 5.4
-// us instead of 9.1 for two launches).
+// How the gradient's rows are shared out: teams that own groups where these are many
+// and short, else chunks of each group's rows, in as many workgroups as the CUs hold
+// at once (25,600 x 768 half: 58.6 us with 512, 70.7 with 1,024) and at least one a
+// group. Up to eight groups the last launch takes side by side (four of 6,400 rows
+// of 768: 5.4 us instead of 9.1 for two launches), and one-chunk groups row by row.
+// A team needs 1.2 to 2.3 us for a row of its group, the last launch 7 for 512
+// groups of chunks. Teams against chunks, half: 600 groups of 1,000 rows of 64
+// 1,140 and 95 us, 512 of 392 of 768 924 and 337, 512 of 8 24.8 and 21.4, of 5 17.1
+// and 19.6; 6,000 of 24 254 and 320, 6,000 of 100 of 64 147 and 139, 9,000 164 and 211.
 constexpr long kMaxParts2 = 512, kMaxAtOnce = 8;
 int teams(int F) { return F <= 64 ? 32 : F <= 256 ? 16 : F <= 512 ? 8 : F <= 1024 ? 4 : 1; }
 struct GroupPlan {
@@ -377,7 +391,7 @@ struct GroupPlan {
 GroupPlan group_plan(long rows, long groups, int F) {
   GroupPlan p;
   const long rpb = teams(F), per = rows / groups;
-  p.own = groups >= kMaxParts2;
+  p.own = groups >= kMaxParts2 && per <= groups / 85;
   p.chunks = 1;
   if (p.own) {
     const long steps = (groups + rpb - 1) / rpb, each = (steps + kMaxParts2 - 1) / kMaxParts2;
@@ -392,6 +406,10 @@ GroupPlan group_plan(long rows, long groups, int F) {
   }
   return p;
 }
+
+// Each workgroup's sums are a whole group's, and there are more groups than the last
+// launch takes side by side.
+bool each_a_group(const GroupPlan& p, long groups) { return !p.own && p.chunks == 1 && groups > kMaxAtOnce; }
 
 template <int TPR, int VPT, typename T>
 hipError_t gated_norm_t(const GatedNormArgs& a, hipStream_t s) {
@@ -427,16 +445,21 @@ hipError_t gated_norm_bwd_t(const GatedNormBwdArgs& a, float* ws, hipStream_t s)
   // the sums of teams that own groups have the gate in them
   int count = p.own ? (int)p.blocks : p.chunks, groups = p.own ? 1 : (int)a.groups;
   bool gated = p.own;
+  if (each_a_group(p, groups)) {
+    hipLaunchKernelGGL((gated_norm_join_kernel<T, true, true>), dim3(cols), dim3(1024), 0, s, part, nullptr, groups, 1,
+                       a.F, a.post, gate, a.scale, ggate, a.gpost, a.gscale, a.gweight);
+    return hipGetLastError();
+  }
   if (groups > kMaxAtOnce) {
     float* next = ws + 2 * p.blocks * a.F;
-    hipLaunchKernelGGL((gated_norm_join_kernel<T, false>), dim3(cols, (unsigned)groups), dim3(1024), 0, s, ws, next,
-                       count, 1, a.F, a.post, gate, a.scale, ggate, nullptr, nullptr, nullptr);
+    hipLaunchKernelGGL((gated_norm_join_kernel<T, false, false>), dim3(cols, (unsigned)groups), dim3(1024), 0, s, ws,
+                       next, count, 1, a.F, a.post, gate, a.scale, ggate, nullptr, nullptr, nullptr);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     part = next, count = groups, groups = 1, gated = true;
   }
-  hipLaunchKernelGGL((gated_norm_join_kernel<T, true>), dim3(cols), dim3(1024), 0, s, part, nullptr, count, groups,
-                     a.F, a.post, gated ? nullptr : gate, a.scale, ggate, a.gpost, a.gscale, a.gweight);
+  hipLaunchKernelGGL((gated_norm_join_kernel<T, true, false>), dim3(cols), dim3(1024), 0, s, part, nullptr, count,
+                     groups, a.F, a.post, gated ? nullptr : gate, a.scale, ggate, a.gpost, a.gscale, a.gweight);
   return hipGetLastError();
 }
 
@@ -462,7 +485,7 @@ hipError_t launch_gated_norm(const GatedNormArgs& a, hipStream_t s) {
 
 size_t gated_norm_bwd_workspace(long rows, long groups, int F) {
   const norm::GroupPlan p = norm::group_plan(rows, groups, F);
-  const long joined = !p.own && groups > norm::kMaxAtOnce ? groups : 0;
+  const long joined = !p.own && p.chunks > 1 && groups > norm::kMaxAtOnce ? groups : 0;
   return (size_t)2 * (p.blocks + joined) * F * sizeof(float);
 }
 

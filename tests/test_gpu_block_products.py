@@ -14,6 +14,7 @@ import torch
 import oracle
 from gpu_util import say, to_dev
 from recurrent_vision_token_gla_amd import gla
+import test_gpu_gated_norm as norms
 from test_gpu_linear import U, act_off, check, expect_linear, half_step, normal, sums
 
 pytestmark = pytest.mark.gpu
@@ -381,3 +382,14 @@ def test_norms_with_offsets_beyond_32_bits():
             assert torch.equal(got[r], want)
     del x, res, y, s, gx, gres, got
     torch.cuda.empty_cache()
+
+
+# groups of a gate's rows around the ways their sums are shared out: a team or a workgroup to a group, one
+# or several workgroups, more groups than the last launch takes side by side
+@pytest.mark.parametrize("G,per,F", [(8, 5, 40), (9, 5, 40), (20, 70, 64), (300, 3, 72), (511, 2, 24), (512, 6, 40),
+                                     (600, 7, 72), (600, 8, 72), (520, 12, 264), (1100, 2, 1032), (9, 300, 64)])
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_norms_with_groups_of_every_number(G, per, F, dtype):
+    norms.test_forward(G, per, F, dtype)
+    for carry in (True, False):
+        norms.test_backward(G, per, F, dtype, carry)
