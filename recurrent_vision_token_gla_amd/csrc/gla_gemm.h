@@ -165,7 +165,8 @@ __device__ __forceinline__ void pair8(floatx4 lo, floatx4 hi, float (&x)[8]) {
 }
 
 // Values of the activations and of their derivatives (codes of gla.h), in
-// float and within 2^-21 of themselves, on the reciprocal and exp2 units.
+// float and within (8 + |z| + z^2) 2^-22 of themselves, on the reciprocal and exp2
+// units (the rounding of exp2's argument grows with it).
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + tile::fexp2(-z * kLog2e));
 }
