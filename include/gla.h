@@ -530,10 +530,11 @@ int gla_gated_ff_bwd(const void* x, const void* gate_weight,
  *   y   = sum / sqrt(mean(sum^2) + eps) * weight.
  * gate: [groups][F] in the input dtype, one row for each of `groups` equal runs
  * of rows (groups = batch size: one for each image; groups = rows: one for each
- * token; groups must divide rows), or NULL (groups is not looked at); scale,
- * post_weight: float [F] or NULL. sum may be NULL. sum and y may each be x or
- * residual themselves (not both the same one) but must not overlap anything
- * otherwise. Squares are summed in float (see gla_add_rmsnorm). */
+ * token; groups must divide rows, and may be 0 where there are none), or NULL
+ * (groups is not looked at); scale, post_weight: float [F] or NULL. sum may be
+ * NULL. sum and y may each be x or residual themselves (not both the same one)
+ * but must not overlap anything otherwise. Squares are summed in float (see
+ * gla_add_rmsnorm). */
 int gla_gated_add_rmsnorm(const void* x, const void* residual,
                           const float* post_weight, const void* gate,
                           int64_t groups, const float* scale,

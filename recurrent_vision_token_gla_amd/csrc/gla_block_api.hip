@@ -26,9 +26,9 @@ int check_product(int64_t rows, int in, int out, int act, int dtype, bool* empty
 
 int check_float_weight(const float* w) { return w && aligned(w, 16) ? GLA_OK : GLA_E_ARG; }
 
-// Groups of a gate's rows: as many rows in each.
+// Groups of a gate's rows: as many rows in each. No rows may have no groups.
 int check_groups(int64_t rows, const void* gate, int64_t* groups) {
-  if (!gate) *groups = 1;
+  if (!gate || (rows == 0 && *groups == 0)) *groups = 1;
   return *groups >= 1 && rows % *groups == 0 ? GLA_OK : GLA_E_ARG;
 }
 

@@ -1020,6 +1020,8 @@ def _gated_norm_args(x, weight, post_weight, gate, scale):
     if gate is not None:
         _like(gate, gate.shape[:-1] + (F,), x.dtype, dev, "gate")
         groups = gate.numel() // F if F else 1
+        if groups == 0 and rows == 0:  # an empty batch
+            groups = 1
         if groups < 1 or rows % groups:
             raise ValueError(f"gate must have one row for each of equal groups of the {rows} rows, got {groups}")
     return dev, rows, F, groups
