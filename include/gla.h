@@ -489,7 +489,8 @@ size_t gla_linear_bwd_workspace_bytes(int64_t rows, int K, int N, int act,
  *   gbias = alpha sum over rows of gp  (float [N], 16-byte aligned);
  * gx and gweight in the input dtype. Each may be NULL: not wanted (then x, or
  * weight, is not looked at). gp is rounded to the input dtype for the products,
- * not for gbias. No output may overlap an input, another output or the
+ * not for gbias (any finite gy of GLA_F16 has a finite one; what lies below 2^-14
+ * loses digits, as such halves do). No output may overlap an input, another output or the
  * workspace. */
 int gla_linear_bwd(const void* x, const void* weight, const void* pre,
                    const void* gy, void* gx, void* gweight, float* gbias,
@@ -511,7 +512,10 @@ size_t gla_gated_ff_bwd_workspace_bytes(int64_t rows, int K, int F, int dtype);
 /* Gradient of gla_gated_ff from gh = dL/dh and the kept a = gate, u = up: with
  * ga = gh u act'(a) and gu = gh act(a),
  *   gx = ga Wg + gu Wu,   ggate_weight = ga^T x,   gup_weight = gu^T x,
- * all in the input dtype; ga and gu are rounded to it for the products. gx may
+ * all in the input dtype; ga and gu are rounded to it for the products (GLA_F16:
+ * where the call's largest finite one is beyond that type, all of them divided
+ * by the power of two that brings it below 2^15, and the sums multiplied by it;
+ * what is then below 2^-14 loses digits). gx may
  * be NULL, and both weights' gradients may be (not one of them: GLA_E_ARG). No
  * output may overlap an input, another output or the workspace. */
 int gla_gated_ff_bwd(const void* x, const void* gate_weight,
