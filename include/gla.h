@@ -457,7 +457,8 @@ int gla_gate_bwd(const void* o, const void* gate, const float* norm_weight,
  * Any finite values, float ones up to bfloat16's largest, 3.38e38: what lies
  * beyond it, Inf among them, makes the sums that it enters NaN or Inf. Float
  * operands below 2^-110 are kept to 2^-134. An output beyond the half range is
- * +-Inf in GLA_F16.
+ * +-Inf in GLA_F16; at a sum kept as +-Inf the gradients take the limits of the
+ * activations' slopes, and of silu and gelu below.
  * An empty problem (no row or no output) returns GLA_OK and writes nothing.
  *
  * Activations, of z in float: silu z / (1 + exp(-z)), gelu z Phi(z) with Phi

@@ -218,7 +218,9 @@ __device__ __forceinline__ void activate(float (&z)[W], int act) {
     for (int c = 0; c < W; ++c) z[c] = fminf(z[c], 0.f) - log_1p(tile::fexp2(-fabsf(z[c]) * kLog2e));
   }
 }
+// At +-Inf, as a kept sum beyond half's range is stored, the limits 1 and 0.
 __device__ __forceinline__ float slope(float z, int act) {
+  z = fabsf(z) == __builtin_inff() ? copysignf(65504.f, z) : z;
   if (act == 1) {
     const float s = sigmoid(z);
     return s * fmaf(z, 1.f - s, 1.f);

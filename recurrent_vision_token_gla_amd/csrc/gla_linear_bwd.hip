@@ -67,6 +67,10 @@ __device__ __forceinline__ void gated_slopes(const T* ap, const T* up, const T* 
   load8(ap, a);
   load8(up, u);
   load8(ghp, g);
+  if (act == 1 || act == 2) {  // zero at -Inf, as a kept product below half's range is stored
+#pragma unroll
+    for (int c = 0; c < 8; ++c) a[c] = a[c] == -__builtin_inff() ? -65504.f : a[c];
+  }
 #pragma unroll
   for (int c = 0; c < 8; ++c) u[c] *= g[c] * slope(a[c], act);
   activate(a, act);

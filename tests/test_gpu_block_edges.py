@@ -1,5 +1,5 @@
 """GPU: the products and norms between a block's mixers at the edges of what they
-take: empty batches, gradients beyond half's range on their way.
+take: empty batches, sums and gradients beyond half's range on their way.
 
 Tolerances are those of test_gpu_linear.py; half values that were divided by 2^p
 before they were rounded are off by 2^(p - 25) below the smallest normal."""
@@ -126,3 +126,52 @@ def test_linear_gradient_at_halfs_largest_values(rows, K, N, kind):
     check("gx", got[0], want[0], off @ W + sums(np.float16, N + 2, A @ W) + half_step(np.float16, want[0]))
     check("gweight", got[1], want[1], off.T @ X + sums(np.float16, rows + 2, A.T @ X) + half_step(np.float16, want[1]))
     check("gbias", got[2], want[2], slope_off.sum(0) + (rows + 4) * U * A.sum(0))
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "logsigmoid"])
+def test_sums_kept_beyond_halfs_range_have_slopes(kind):
+    """pre of +-7e4 to 5e5 among ordinary ones: kept as infinities, behind an
+    output that is finite; the slopes there are the limits."""
+    r = np.random.default_rng(21)
+    rows, K, N = 70, 72, 40
+    x, w = normal(r, np.float16, rows, K), normal(r, np.float16, N, K, s=K ** -0.5)
+    b = np.zeros(N, np.float32)
+    b[:8] = np.linspace(7e4, 5e5, 8) * np.tile([1, -1], 4)
+    gy = normal(r, np.float16, rows, N)
+    dx, dw, db, dgy = to_dev(x, w, b, gy)
+    y, pre = gla.linear(dx, dw, db, act=ACTS[kind], alpha=2.0 ** -6, return_pre=True)
+    got = gla.linear_bwd(dx, dw, dgy, act=ACTS[kind], alpha=2.0 ** -6, pre=pre)
+    torch.cuda.synchronize()
+    assert torch.isfinite(y).all() and torch.isinf(pre[:, :8]).all() and torch.isfinite(pre[:, 8:]).all()
+    z = pre.double().cpu().numpy()
+    z[:, :8] = oracle.linear(x, w, b)[0][:, :8]
+    want = oracle.linear_backward(x, w, z, gy, kind, 2.0 ** -6)
+    gp = gy * oracle.act_slope(z, kind)
+    far = np.isinf(pre.double().cpu().numpy())
+    slope_off = np.where(far, 0, act_off(np.where(far, 0, z)) * np.abs(gy) * 1.13)
+    off = slope_off + half_step(np.float16, gp)
+    A, W, X = np.abs(gp) + off, np.abs(w.astype(np.float64)), np.abs(x.astype(np.float64))
+    c = 2.0 ** -6
+    check("gx", got[0], want[0], c * (off @ W + sums(np.float16, N + 2, A @ W)) + half_step(np.float16, want[0]))
+    check("gweight", got[1], want[1], c * (off.T @ X + sums(np.float16, rows + 2, A.T @ X)) + half_step(np.float16, want[1]))
+    check("gbias", got[2], want[2], c * (slope_off.sum(0) + (rows + 4) * U * A.sum(0)) + 1e-30)
+    nan = pre.clone()
+    nan[3, 5] = float("nan")
+    gx = gla.linear_bwd(dx, dw, dgy, act=ACTS[kind], pre=nan)[0]
+    torch.cuda.synchronize()
+    assert torch.isnan(gx[3]).all() and torch.isfinite(gx[:3]).all()
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_gates_kept_below_halfs_range_pass_nothing(kind):
+    r = np.random.default_rng(22)
+    rows, K, F = 70, 72, 40
+    x, gh = normal(r, np.float16, rows, K), normal(r, np.float16, rows, F)
+    wg, wu = (normal(r, np.float16, F, K, s=K ** -0.5) for _ in range(2))
+    a, u = normal(r, np.float16, rows, F), normal(r, np.float16, rows, F)
+    a[:, ::5] = -np.inf
+    got = gla.gated_ff_bwd(*to_dev(x, wg, wu, a, u, gh), act=ACTS[kind])
+    a[:, ::5] = -60000  # zero there, and as flat
+    want = gla.gated_ff_bwd(*to_dev(x, wg, wu, a, u, gh), act=ACTS[kind])
+    torch.cuda.synchronize()
+    assert all(torch.isfinite(g).all() and torch.equal(g, t) for g, t in zip(got, want))
