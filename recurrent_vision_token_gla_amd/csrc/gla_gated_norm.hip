@@ -161,9 +161,12 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_kernel(
 //   gx = rx (gS f - n mean(gS f n))             (gS f without post),
 //   gw = sum gy m,   Q = sum over a group's rows of gS n:
 //   ggate = scale post Q,  gpost = scale sum gate Q,  gscale = post sum gate Q.
-// mean(gS f n) is put together from sums that do not wait for gS, so that all
-// six sums of a row go over the team at once:
-//   sum gS f n = rx (sum gsum f x + rs sum gy w f x - rs^2 mean(gy w m) sum f x s).
+// mean(gS f n) is put together from sums that do not wait for gS,
+//   sum gS f n = sum gsum f n + rs (sum gy w f n - mean(gy w m) sum f n m),
+// and half rows, whose values are far from float's ends, take them of x and s and
+// put rx and rs in front, so that all six sums of a row go over the team at once.
+// Float rows would leave float's range there (x, s of 1e18 and f of 1e3 have a
+// product of 1e39): their two squares go first.
 // kOwn: a team takes whole groups and writes ggate itself; part[workgroup] holds
 // gw and sum gate Q. Else a workgroup takes rows of one chunk of a group;
 // part[group][chunk] holds gw and Q.
@@ -173,6 +176,7 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_bwd_kernel(
     const T* __restrict__ gate, const float* __restrict__ scale, const float* __restrict__ wp, float eps,
     T* gxp, T* grp, T* __restrict__ ggp, float* __restrict__ part, long groups, long per, int chunks, int F) {
   constexpr int RPB = kTeamThreads<TPR> / TPR, NS = 6;
+  constexpr bool kFirst = sizeof(T) == 4;  // m and n before the other sums
   __shared__ float lds[TPR > 64 ? NS * TPR / 64 : 1];
   __shared__ float join[RPB > 1 ? kTeamThreads<TPR> * VPT * 8 : 1];
   const int t = threadIdx.x % TPR, team = threadIdx.x / TPR, nv = F / 8;
@@ -195,7 +199,7 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_bwd_kernel(
       if (t + TPR * i < nv) load8(gate + group * F + 8 * (t + TPR * i), g[i]);
   };
   auto do_row = [&](long row) {
-    float x[VPT][8], s[VPT][8], gy[VPT][8], gs[VPT][8], z[NS] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float x[VPT][8], s[VPT][8], gy[VPT][8], gs[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int u = t + TPR * i;
@@ -209,30 +213,52 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_bwd_kernel(
         if (gsp) load8(gsp + at, gs[i]);
       }
     }
+    float squares[2] = {0.f, 0.f}, rs = 1.f, rx = 1.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        squares[0] = fmaf(s[i][c], s[i][c], squares[0]);
+        squares[1] = fmaf(x[i][c], x[i][c], squares[1]);
+      }
+    auto roots = [&](float ss, float xx) {
+      rs = __builtin_amdgcn_rsqf(fmaf(ss, over, eps));
+      rx = post ? __builtin_amdgcn_rsqf(fmaf(xx, over, eps)) : 1.f;
+    };
+    if constexpr (kFirst) {
+      team_sums<TPR>(squares, lds);
+      roots(squares[0], squares[1]);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s[i][c] *= rs, x[i][c] *= rx;
+    }
+    float z[kFirst ? 4 : 6] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const float fx = f[i][c] * g[i][c] * x[i][c], gm = gy[i][c] * w[i][c];
-        z[0] = fmaf(s[i][c], s[i][c], z[0]);
-        z[1] = fmaf(x[i][c], x[i][c], z[1]);
-        z[2] = fmaf(gm, s[i][c], z[2]);
-        z[3] = fmaf(gs[i][c], fx, z[3]);
-        z[4] = fmaf(gm, fx, z[4]);
-        z[5] = fmaf(fx, s[i][c], z[5]);
+        z[0] = fmaf(gm, s[i][c], z[0]);
+        z[1] = fmaf(gs[i][c], fx, z[1]);
+        z[2] = fmaf(gm, fx, z[2]);
+        z[3] = fmaf(fx, s[i][c], z[3]);
       }
+    if constexpr (!kFirst) z[4] = squares[0], z[5] = squares[1];
     team_sums<TPR>(z, lds);
-    const float rs = __builtin_amdgcn_rsqf(fmaf(z[0], over, eps));
-    const float rx = post ? __builtin_amdgcn_rsqf(fmaf(z[1], over, eps)) : 1.f;
-    const float dot = z[2] * rs * over;  // mean(gy w m)
-    const float mean = post ? rx * over * fmaf(rs, fmaf(-rs * dot, z[5], z[4]), z[3]) : 0.f;
+    if constexpr (!kFirst) {
+      roots(z[4], z[5]);
+      z[0] *= rs, z[1] *= rx, z[2] *= rx, z[3] *= rx * rs;
+    }
+    const float dot = z[0] * over;  // mean(gy w m)
+    const float mean = post ? over * fmaf(rs, fmaf(-dot, z[3], z[2]), z[1]) : 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int u = t + TPR * i;
       const long at = row * F + 8 * u;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float m = s[i][c] * rs, n = x[i][c] * rx;
+        const float m = kFirst ? s[i][c] : s[i][c] * rs, n = kFirst ? x[i][c] : x[i][c] * rx;
         gw[i][c] = fmaf(gy[i][c], m, gw[i][c]);
         gs[i][c] = fmaf(rs, fmaf(gy[i][c], w[i][c], -m * dot), gs[i][c]);
         q[i][c] = fmaf(gs[i][c], n, q[i][c]);

@@ -1,5 +1,6 @@
 """GPU: the products and norms between a block's mixers at the edges of what they
-take: empty batches, sums and gradients beyond half's range on their way.
+take: empty batches, sums and gradients beyond half's range on their way, rows
+near the ends of float's range.
 
 Tolerances are those of test_gpu_linear.py; half values that were divided by 2^p
 before they were rounded are off by 2^(p - 25) below the smallest normal."""
@@ -8,6 +9,7 @@ import pytest
 import torch
 
 import oracle
+import test_gpu_gated_norm as norms
 from gpu_util import say, to_dev
 from recurrent_vision_token_gla_amd import gla
 from test_gpu_linear import ACTS, U, act_off, check, half_step, normal, sums
@@ -175,3 +177,58 @@ def test_gates_kept_below_halfs_range_pass_nothing(kind):
     want = gla.gated_ff_bwd(*to_dev(x, wg, wu, a, u, gh), act=ACTS[kind])
     torch.cuda.synchronize()
     assert all(torch.isfinite(g).all() and torch.equal(g, t) for g, t in zip(got, want))
+
+
+def norm_gradient_bounds(d, want, eps, gsum=True):
+    """Bounds of test_gpu_gated_norm.py for (gx, gresidual, gweight, gpost, ggate, gscale) of one group a row or
+    one for all, with post, gate and scale. The sums that meet in mean(gS f n) are of the same values, so they are
+    off by as much of their magnitudes."""
+    NU, u = norms.NU, norms.U
+    f64 = lambda a: np.asarray(a, np.float64)
+    X, S, GY, W = f64(d["x"]), f64(d["res"]), f64(d["gy"]), f64(d["w"])
+    G0 = f64(d["gsum"]) if gsum else np.zeros_like(X)
+    mean = lambda a: np.mean(a, axis=-1, keepdims=True)
+    rs, rx = 1 / np.sqrt(mean(S * S) + eps), 1 / np.sqrt(mean(X * X) + eps)
+    m, n, gw = S * rs, X * rx, GY * W
+    rows, F = X.shape
+    per = rows // len(d["gate"])
+    gate = np.repeat(f64(d["gate"]), per, 0)
+    a, b = f64(d["post"]), f64(d["scale"])
+    f = np.abs(a * b * gate)
+    dot = mean(np.abs(gw * m))
+    e = rs * NU * (np.abs(gw) + np.abs(m) * dot) + 2 * u * (np.abs(want[1]) + np.abs(G0))
+    E = NU * mean(np.abs(G0 * f * n) + rs * np.abs(gw * f * n) + rs * dot * np.abs(f * n * m))
+    half = (lambda x: half_step(np.float16, x)) if d["x"].dtype == np.float16 else (lambda x: 2.0 ** -24 * np.abs(x))
+    low = 0 if d["x"].dtype == np.float16 else 2.0 ** -149
+    top = np.abs(want[1]) * f + np.abs(n) * E / NU
+    q = np.abs(n) * e + (rows + 64) * u * np.abs(want[1] * n)
+    fine = lambda x: 2.0 ** -24 * np.abs(x) + low
+    return (rx * (f * e + np.abs(n) * E + 16 * u * top) + half(want[0]) + low, e + half(want[1]) + low,
+            (rows + 48) * u * np.abs(GY * m).sum(0) + fine(want[2]),
+            (q * np.abs(b * gate)).sum(0) + fine(want[3]),
+            (q * np.abs(a * b)).reshape(len(d["gate"]), per, F).sum(1) + half(want[4]) + low,
+            (q * np.abs(a * gate)).sum(0) + fine(want[5]))
+
+
+def hold_norm_gradient(d, eps):
+    x, s, w, post, gate, scale, gy, gs = norms.dev(d, "x", "res", "w", "post", "gate", "scale", "gy", "gsum")
+    got = gla.gated_add_rmsnorm_bwd(x, s, w, eps, gy, post_weight=post, gate=gate, scale=scale, gsum=gs)
+    torch.cuda.synchronize()
+    want = oracle.gated_add_rmsnorm_backward(d["x"], d["res"], d["w"], eps, d["gy"], d["gsum"], d["post"], d["gate"],
+                                             d["scale"])
+    for name, g, t, tol in zip(("gx", "gresidual", "gweight", "gpost", "ggate", "gscale"), got, want,
+                               norm_gradient_bounds(d, want, eps)):
+        check(name, g, t, tol)
+
+
+# x, s, scale, gy and gsum times these: a product of two of them is beyond float's range, or far below its normal
+# values, where mean(x^2) and mean(s^2) are normal floats and every gradient is in range
+@pytest.mark.parametrize("x,s,scale,gy,gsum", [(1e16, 1e16, 1e8, 1, 1e-16), (1e-17, 1e-17, 1, 1e-22, 1e-5),
+                                               (1, 1e15, 1, 1e25, 1e10), (1e15, 1, 1, 1, 1e25), (1e-15, 1, 1, 1e-25, 1e-25)])
+@pytest.mark.parametrize("G,per,F", [(3, 5, 40), (4, 50, 256), (2, 30, 768), (2, 3, 2056), (2, 3, 4104), (2, 3, 8200),
+                                     (600, 1, 72)])
+def test_norms_gradient_of_floats_near_their_ends(x, s, scale, gy, gsum, G, per, F):
+    d = norms.make(G, per, F, np.float32, (1, 1, 1), G + per + F + 5)
+    for name, c in (("x", x), ("res", s), ("scale", scale), ("gy", gy), ("gsum", gsum)):
+        d[name] = d[name] * np.float32(c)
+    hold_norm_gradient(d, 0.0 if min(x, s) < 1 else EPS)
