@@ -76,6 +76,14 @@ struct Raw8<float> {
 template <int TPR>
 constexpr int kTeamThreads = TPR > 256 ? TPR : 256;
 
+// A uniform pointer that the compiler takes for another: what is loaded through it is
+// loaded there, not kept from an earlier load of the same.
+template <typename T>
+__device__ __forceinline__ const T* again(const T* p) {
+  asm volatile("" : "+s"(p));
+  return p;
+}
+
 // sum and y may be x or residual: a thread has read its columns when it writes them.
 template <int TPR, int VPT, typename T>
 __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_kernel(
@@ -83,12 +91,17 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_kernel(
     const float* __restrict__ scale, const float* __restrict__ wp, float eps, T* sp, T* yp, long rows,
     long per, int F) {
   constexpr int RPB = kTeamThreads<TPR> / TPR;
+  // float rows of more than 8,192 columns: the 128 registers of 1,024 threads hold the row and the next one, and
+  // factors and gate are read where they are used, from L2 (2,368 rows of 8,200: 72 us; kept, with 64 registers
+  // spilled, 127)
+  constexpr bool kAgain = TPR == 1024 && sizeof(T) == 4;
+  constexpr int K = kAgain ? 1 : VPT;
   __shared__ float lds[TPR > 64 ? TPR / 64 : 1];
   const int t = threadIdx.x % TPR, nv = F / 8;
   const float over = 1.f / (float)F;
-  float f[VPT][8], w[VPT][8];
+  float f[K][8], w[K][8];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
+  for (int i = 0; i < (kAgain ? 0 : VPT); ++i) {
     const int u = t + TPR * i;
 #pragma unroll
     for (int c = 0; c < 8; ++c) f[i][c] = w[i][c] = 0.f;
@@ -99,7 +112,7 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_kernel(
   }
   const long stride = (long)gridDim.x * RPB;
   long row = (long)blockIdx.x * RPB + threadIdx.x / TPR;
-  Raw8<T> nx[VPT], nr[VPT], ng[VPT];  // the next row
+  Raw8<T> nx[VPT], nr[VPT], ng[K];  // the next row
   auto fetch = [&](long at) {
     const long grow = gate ? at / per : 0;
 #pragma unroll
@@ -108,20 +121,20 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_kernel(
       if (u < nv) {
         nx[i].load(xp + at * F + 8 * u);
         nr[i].load(rp + at * F + 8 * u);
-        if (gate) ng[i].load(gate + grow * F + 8 * u);
+        if (!kAgain && gate) ng[i % K].load(gate + grow * F + 8 * u);
       }
     }
   };
   if (row < rows) fetch(row);
   for (; row < rows; row += stride) {
-    float x[VPT][8], r[VPT][8], g[VPT][8], ss[1] = {0.f};
+    float x[VPT][8], r[VPT][8], g[K][8], ss[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int u = t + TPR * i;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         x[i][c] = u < nv ? nx[i][c] : 0.f, r[i][c] = u < nv ? nr[i][c] : 0.f;
-        g[i][c] = u < nv && gate ? ng[i][c] : 1.f;
+        if (!kAgain) g[i % K][c] = u < nv && gate ? ng[i % K][c] : 1.f;
         ss[0] = fmaf(x[i][c], x[i][c], ss[0]);
       }
     }
@@ -133,12 +146,21 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_kernel(
     }
     ss[0] = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < VPT; ++i) {
+      if constexpr (kAgain) {
+        const int u = t + TPR * i;
+        if (u >= nv) break;
+        factor8(again(post), again(scale), 8 * u, f[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) g[0][c] = 1.f;
+        if (gate) load8(again(gate) + row / per * F + 8 * u, g[0]);
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        x[i][c] = round_to(fmaf(x[i][c] * rx, f[i][c] * g[i][c], r[i][c]), T());
+        x[i][c] = round_to(fmaf(x[i][c] * rx, f[i % K][c] * g[i % K][c], r[i][c]), T());
         ss[0] = fmaf(x[i][c], x[i][c], ss[0]);
       }
+    }
     team_sums<TPR>(ss, lds);
     const float rs = __builtin_amdgcn_rsqf(fmaf(ss[0], over, eps));
 #pragma unroll
@@ -147,8 +169,9 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_kernel(
       if (u < nv) {
         const long at = row * F + 8 * u;
         if (sp) store8(sp + at, x[i]);
+        if constexpr (kAgain) tile::load_f8(again(wp) + 8 * u, w[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[i][c] *= rs * w[i][c];
+        for (int c = 0; c < 8; ++c) x[i][c] *= rs * w[i % K][c];
         store8(yp + at, x[i]);
       }
     }
@@ -181,12 +204,18 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_bwd_kernel(
   __shared__ float join[RPB > 1 ? kTeamThreads<TPR> * VPT * 8 : 1];
   const int t = threadIdx.x % TPR, team = threadIdx.x / TPR, nv = F / 8;
   const float over = 1.f / (float)F;
-  float f[VPT][8], w[VPT][8], gw[VPT][8], q[VPT][8], p[kOwn ? VPT : 1][8], g[VPT][8];
+  // 512 threads have 256 registers each: sum gate Q waits in LDS where it would be spilled (2,368 half rows of
+  // 8,192 columns with a gate each 91 us instead of 100, float ones, of which 8 registers still are, 153 and 160)
+  constexpr bool kPark = kOwn && TPR == 512;
+  __shared__ floatx4 park[kPark ? 2 * VPT * TPR : 1];
+  constexpr int P = kOwn && !kPark ? VPT : 1;
+  float f[VPT][8], w[VPT][8], gw[VPT][8], q[VPT][8], p[P][8], g[VPT][8];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int u = t + TPR * i;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) f[i][c] = w[i][c] = gw[i][c] = q[i][c] = p[kOwn ? i : 0][c] = 0.f, g[i][c] = 1.f;
+    for (int c = 0; c < 8; ++c) f[i][c] = w[i][c] = gw[i][c] = q[i][c] = p[i % P][c] = 0.f, g[i][c] = 1.f;
+    if constexpr (kPark) park[t + TPR * 2 * i] = park[t + TPR * (2 * i + 1)] = floatx4{0.f, 0.f, 0.f, 0.f};
     if (u < nv) {
       factor8(post, scale, 8 * u, f[i]);
       tile::load_f8(wp + 8 * u, w[i]);
@@ -283,9 +312,19 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_bwd_kernel(
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           y[c] = f[i][c] * q[i][c];
-          p[i][c] = fmaf(g[i][c], q[i][c], p[i][c]);
-          q[i][c] = 0.f;
+          if constexpr (!kPark) p[i][c] = fmaf(g[i][c], q[i][c], p[i][c]);
         }
+        if constexpr (kPark) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            floatx4 z = park[t + TPR * (2 * i + h)];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) z[c] = fmaf(g[i][4 * h + c], q[i][4 * h + c], z[c]);
+            park[t + TPR * (2 * i + h)] = z;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) q[i][c] = 0.f;
         if (ggp && t + TPR * i < nv) store8(ggp + group * F + 8 * (t + TPR * i), y);
       }
     }
@@ -316,8 +355,142 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_bwd_kernel(
     }
   };
   write(out, gw);
-  if constexpr (kOwn) write(out + F, p);
+  if constexpr (kPark) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) q[i][c] = park[t + TPR * (2 * i + c / 4)][c % 4];
+  }
+  if constexpr (kOwn && !kPark) write(out + F, p);
   else write(out + F, q);
+}
+
+// The same for rows of more than 8,192 columns, a workgroup of 1,024 threads to a
+// row: their 128 registers do not hold what the kernel above keeps of a column (it
+// spilled 34 to 195 of them: 2,368 half rows of 8,200 columns 230 us, with a gate of
+// every row's own 425; here 97 and 119, 2.4 and 2.6 TB/s, as a CU has one row in
+// flight and two exchanges in it). Up to 8,192 columns the kernel above is faster (62
+// us against 92). The weights' sums wait in LDS, where a
+// thread comes back to its own columns, and the factors are read again, from L2,
+// where they are used; the row is kept as it was loaded. kOwn: every row is a group.
+template <typename T, bool kOwn>
+__global__ __launch_bounds__(1024) void gated_norm_bwd_wide_kernel(
+    const T* xp, const T* sp, const T* gyp, const T* gsp, const float* __restrict__ post,
+    const T* __restrict__ gate, const float* __restrict__ scale, const float* __restrict__ wp, float eps,
+    T* gxp, T* grp, T* __restrict__ ggp, float* __restrict__ part, long groups, long per, int chunks, int F) {
+  constexpr int TPR = 1024, VPT = 2;
+  __shared__ float lds[4 * TPR / 64];
+  // gw, and sum gate Q (kOwn) or Q: the first four columns of every eight, then the others
+  __shared__ floatx4 sums[2][2 * VPT * TPR];
+  const int t = threadIdx.x, nv = F / 8;
+  const float over = 1.f / (float)F;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 2 * VPT; ++i) sums[h][t + TPR * i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  auto add = [&](int h, int u, const float (&y)[8]) {
+    sums[h][u] += floatx4{y[0], y[1], y[2], y[3]};
+    sums[h][VPT * TPR + u] += floatx4{y[4], y[5], y[6], y[7]};
+  };
+  auto factors = [&](long group, int u, float (&f)[8], float (&g)[8]) {
+    factor8(again(post), again(scale), 8 * u, f);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) g[c] = 1.f;
+    if (gate) load8(again(gate) + group * F + 8 * u, g);
+  };
+  auto do_row = [&](long group, long row) {
+    Raw8<T> x[VPT], s[VPT], gy[VPT], gs[VPT];
+    float squares[2] = {0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int u = t + TPR * i;
+      const long at = row * F + 8 * u;
+      x[i] = s[i] = gy[i] = gs[i] = Raw8<T>{};
+      if (u < nv) {
+        x[i].load(xp + at);
+        s[i].load(sp + at);
+        gy[i].load(gyp + at);
+        if (gsp) gs[i].load(gsp + at);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        squares[0] = fmaf(s[i][c], s[i][c], squares[0]);
+        squares[1] = fmaf(x[i][c], x[i][c], squares[1]);
+      }
+    team_sums<TPR>(squares, lds);
+    const float rs = __builtin_amdgcn_rsqf(fmaf(squares[0], over, eps));
+    const float rx = post ? __builtin_amdgcn_rsqf(fmaf(squares[1], over, eps)) : 1.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int u = t + TPR * i;
+      if (u < nv) {
+        float f[8], g[8], w[8];
+        factors(group, u, f, g);
+        tile::load_f8(again(wp) + 8 * u, w);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float m = s[i][c] * rs, fn = f[c] * g[c] * (x[i][c] * rx), gm = gy[i][c] * w[c];
+          z[0] = fmaf(gm, m, z[0]);
+          z[1] = fmaf(gs[i][c], fn, z[1]);
+          z[2] = fmaf(gm, fn, z[2]);
+          z[3] = fmaf(fn, m, z[3]);
+        }
+      }
+    }
+    team_sums<TPR>(z, lds);
+    const float dot = z[0] * over;  // mean(gy w m)
+    const float mean = post ? over * fmaf(rs, fmaf(-dot, z[3], z[2]), z[1]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int u = t + TPR * i;
+      if (u < nv) {
+        const long at = row * F + 8 * u;
+        float y[8], r[8], f[8], g[8];
+        tile::load_f8(again(wp) + 8 * u, r);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float m = s[i][c] * rs;
+          y[c] = gy[i][c] * m;
+          r[c] = fmaf(rs, fmaf(gy[i][c], r[c], -m * dot), gs[i][c]);
+        }
+        add(0, u, y);
+        store8(grp + at, r);
+        factors(group, u, f, g);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float n = x[i][c] * rx;
+          y[c] = rx * fmaf(r[c], f[c] * g[c], -n * mean);
+          r[c] *= n;
+        }
+        store8(gxp + at, y);
+        if constexpr (kOwn) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) f[c] *= r[c], r[c] *= g[c];
+          if (ggp) store8(ggp + at, f);
+        }
+        add(1, u, r);
+      }
+    }
+  };
+  if constexpr (kOwn) {
+    for (long row = blockIdx.x; row < groups; row += gridDim.x) do_row(row, row);
+  } else {
+    const long group = blockIdx.x / chunks;
+    for (long r = blockIdx.x % chunks; r < per; r += chunks) do_row(group, group * per + r);
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int u = t + TPR * i;
+    if (u >= nv) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      floatx4* to = reinterpret_cast<floatx4*>(part + (2L * blockIdx.x + h) * F + 8 * u);
+      to[0] = sums[h][u], to[1] = sums[h][VPT * TPR + u];
+    }
+  }
 }
 
 // Sums of the pairs of rows of part, gw and Q (or sum gate Q), `count` of them in
@@ -417,7 +590,7 @@ struct GroupPlan {
 GroupPlan group_plan(long rows, long groups, int F) {
   GroupPlan p;
   const long rpb = teams(F), per = rows / groups;
-  p.own = groups >= kMaxParts2 && per <= groups / 85;
+  p.own = groups >= kMaxParts2 && (F <= 8192 ? per <= groups / 85 : per == 1);
   p.chunks = 1;
   if (p.own) {
     const long steps = (groups + rpb - 1) / rpb, each = (steps + kMaxParts2 - 1) / kMaxParts2;
@@ -456,7 +629,10 @@ template <int TPR, int VPT, typename T>
 hipError_t gated_norm_bwd_t(const GatedNormBwdArgs& a, float* ws, hipStream_t s) {
   const GroupPlan p = group_plan(a.rows, a.groups, a.F);
   const long per = a.rows / a.groups;
-  auto kernel = p.own ? gated_norm_bwd_kernel<TPR, VPT, T, true> : gated_norm_bwd_kernel<TPR, VPT, T, false>;
+  auto kernel = [&] {
+    if constexpr (TPR * VPT > 1024) return p.own ? gated_norm_bwd_wide_kernel<T, true> : gated_norm_bwd_wide_kernel<T, false>;
+    else return p.own ? gated_norm_bwd_kernel<TPR, VPT, T, true> : gated_norm_bwd_kernel<TPR, VPT, T, false>;
+  }();
   const T* gate = static_cast<const T*>(a.gate);
   T* ggate = static_cast<T*>(a.ggate);
   hipLaunchKernelGGL(kernel, dim3((unsigned)p.blocks), dim3(kTeamThreads<TPR>), 0, s,

@@ -1,6 +1,6 @@
 """GPU: the products and norms between a block's mixers at the edges of what they
 take: empty batches, sums and gradients beyond half's range on their way, rows
-near the ends of float's range.
+near the ends of float's range, wide rows with many groups.
 
 Tolerances are those of test_gpu_linear.py; half values that were divided by 2^p
 before they were rounded are off by 2^(p - 25) below the smallest normal."""
@@ -232,3 +232,27 @@ def test_norms_gradient_of_floats_near_their_ends(x, s, scale, gy, gsum, G, per,
     for name, c in (("x", x), ("res", s), ("scale", scale), ("gy", gy), ("gsum", gsum)):
         d[name] = d[name] * np.float32(c)
     hold_norm_gradient(d, 0.0 if min(x, s) < 1 else EPS)
+
+
+# rows of every width that has a kernel of its own, with a gate of every row's own, of two rows', and chunks of a group
+@pytest.mark.parametrize("G,per,F", [(520, 1, 4104), (512, 2, 4104), (515, 1, 8192), (520, 1, 8200), (512, 2, 8200),
+                                     (514, 1, 16384), (3, 200, 8200), (1, 600, 16384)])
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_norms_of_wide_rows_with_many_groups(G, per, F, dtype):
+    d = norms.make(G, per, F, dtype, (1, 1, 1), G + per + F + 6)
+    hold_norm_gradient(d, EPS)
+    y, s = norms.run(d)
+    torch.cuda.synchronize()
+    _, _, whole = oracle.gated_add_rmsnorm(d["x"], d["res"], d["w"], EPS, d["post"], d["gate"], d["scale"])
+    add = np.abs(whole - d["res"].astype(np.float64))
+    check("s", s, whole, norms.NU * add + 4 * norms.U * (np.abs(d["res"]) + np.abs(whole)) + norms.half_step(dtype, whole))
+    want, _ = oracle.add_rmsnorm(s.cpu().numpy(), None, d["w"], EPS)
+    check("y", y, want, norms.NU * np.abs(want) + norms.half_step(dtype, want))
+    alone = gla.gated_add_rmsnorm_bwd(*norms.dev(d, "x", "res", "w"), EPS, *norms.dev(d, "gy"))
+    torch.cuda.synchronize()
+    plain = dict(d, post=np.ones(F, np.float32), gate=np.ones((1, F), dtype), scale=np.ones(F, np.float32))
+    want = oracle.gated_add_rmsnorm_backward(d["x"], d["res"], d["w"], EPS, d["gy"])
+    tol = norm_gradient_bounds(plain, want[:3] + (want[2],) * 3, EPS, gsum=False)
+    for name, k in (("gresidual alone", 1), ("gweight alone", 2)):
+        check(name, alone[k], want[k], tol[k])
+    check("gx alone", alone[0], want[0], tol[1])  # the same values
