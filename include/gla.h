@@ -473,8 +473,8 @@ enum { GLA_ACT_NONE = 0, GLA_ACT_SILU = 1, GLA_ACT_GELU = 2, GLA_ACT_LOGSIGMOID 
  * bias: float [N], 16-byte aligned, or NULL; residual: [rows][N] in the input
  * dtype or NULL; pre: [rows][N] takes x W^T + bias for the gradient, or NULL.
  * y may be residual itself; nothing else may overlap. Up to 16 rows (the new
- * tokens of as many sequences) run in a form of their own, which reads the
- * weight once. */
+ * tokens of as many sequences) of up to 4,096 outputs, or four of up to 8,192,
+ * run in a form of their own, which reads the weight once. */
 int gla_linear(const void* x, const void* weight, const float* bias,
                const void* residual, void* pre, void* y, int64_t rows, int K,
                int N, int act, float alpha, int dtype, void* stream);

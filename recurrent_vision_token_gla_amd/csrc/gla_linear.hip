@@ -63,16 +63,22 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const Args g)
   else finish<T>(g, 0, r, nn, x[0]);
 }
 
-// skinny_kernel up to 16 rows, gated up to one workgroup a CU besides. us, it against
-// the tiles: linear, 16 rows x 768 x 768 3.7 and 4.0, 24 rows (as two such kernels'
-// work) 4.4 and 4.3, 64 rows 6.8 and 4.3. Gated, 16 rows x 768 x 2,048 4.6 and 4.9, 32
-// rows 5.7 and 5.2; 8 rows x 768 x 4,096 5.7 and 5.7, x 1,024 x 8,192 9.3 and 7.6; float
-// 16 rows x 768 x 2,048 6.8 and 8.4, x 1,024 x 8,192 22.3 and 15.7.
+// skinny_kernel up to 16 rows, and no more workgroups than CUs, or twice as many for up
+// to four rows: more of them wait for their weights one after the other, where the
+// tiles, of 32 to 256 columns, read ahead. us, it against the tiles, half: linear of one
+// row x 768 x 4,096 4.2 and 5.2, 16 rows 4.7 and 5.3; x 8,192 5.6 and 6.5, 4 rows 6.1 and
+// 6.5, 16 rows 7.3 and 6.6; x 16,384 8.3 and 7.7, 16 rows 11.7 and 7.8; x 65,536 23 and 24,
+// 16 rows 37 and 24; one row x 2,048 x 16,384 17.0 and 15.0; 24 rows x 768 x 768 (as two
+// such kernels' work) 4.4 and 4.3, 64 rows 6.8 and 4.3. Float, one row x 2,048 x 8,192 17.4
+// and 17.6, 16 rows 22.8 and 18.6, 16 rows x 768 x 65,536 75 and 49. Gated, one row x 2,048
+// x 4,096 9.9 and 12.2, 16 rows 12.7 and 12.3, x 8,192 15.8 and 14.8, 16 rows 22 and 15; 16
+// rows x 768 x 2,048 5.0 and 5.2, 32 rows 5.7 and 5.2; float one row x 768 x 4,096 9.7 and
+// 10.2, 16 rows 12.2 and 10.2.
 template <typename T, int kEpi>
 hipError_t forward(const Args& g, hipStream_t s) {
   constexpr bool kDual = kEpi == kGated;
   constexpr int kCols = kDual ? 8 : 16;
-  if (g.M <= kFewRows && (!kDual || g.N <= kCols * kCus)) {
+  if (g.M <= kFewRows && g.N <= kCols * kCus * (g.M <= 4 ? 2 : 1)) {
     hipLaunchKernelGGL((skinny_kernel<T, kDual>), dim3((unsigned)((g.N + kCols - 1) / kCols)), dim3(64 * kSkinnyWaves),
                        0, s, g);
     return hipGetLastError();

@@ -1,6 +1,7 @@
 """GPU: the products and norms between a block's mixers at the edges of what they
 take: empty batches, sums and gradients beyond half's range on their way, rows
-near the ends of float's range, wide rows with many groups.
+near the ends of float's range, wide rows with many groups, the borders of the
+form for few rows.
 
 Tolerances are those of test_gpu_linear.py; half values that were divided by 2^p
 before they were rounded are off by 2^(p - 25) below the smallest normal."""
@@ -12,7 +13,7 @@ import oracle
 import test_gpu_gated_norm as norms
 from gpu_util import say, to_dev
 from recurrent_vision_token_gla_amd import gla
-from test_gpu_linear import ACTS, U, act_off, check, half_step, normal, sums
+from test_gpu_linear import ACTS, U, act_off, check, expect_linear, half_step, normal, sums
 
 pytestmark = pytest.mark.gpu
 EPS = 1e-6
@@ -256,3 +257,28 @@ def test_norms_of_wide_rows_with_many_groups(G, per, F, dtype):
     for name, k in (("gresidual alone", 1), ("gweight alone", 2)):
         check(name, alone[k], want[k], tol[k])
     check("gx alone", alone[0], want[0], tol[1])  # the same values
+
+
+@pytest.mark.parametrize("rows", [1, 4, 5, 16, 17])
+@pytest.mark.parametrize("N", [2056, 4096, 4104, 8192, 8200, 16392])
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_few_rows_with_many_outputs(rows, N, dtype):
+    K = 136
+    r = np.random.default_rng(rows + N + 7)
+    x, w, v = normal(r, dtype, rows, K), normal(r, dtype, N, K, s=K ** -0.5), normal(r, dtype, N, K, s=K ** -0.5)
+    b, res = normal(r, np.float32, N), normal(r, dtype, rows, N)
+    dx, dw, dv, db, dres = to_dev(x, w, v, b, res)
+    y, ty, pre, tpre = expect_linear(x, w, b, "silu", 0.5, res, dtype)
+    got, gpre = gla.linear(dx, dw, db, act=gla.ACT_SILU, alpha=0.5, residual=dres, return_pre=True)
+    h, a, u = gla.gated_ff(dx, dw, dv, return_parts=True)
+    torch.cuda.synchronize()
+    check("linear", got, y, ty)
+    check("pre", gpre, pre, tpre)
+    X = np.abs(x.astype(np.float64))
+    oa, ou = (sums(dtype, K, X @ np.abs(m.astype(np.float64)).T) for m in (w, v))
+    rh, ra, ru = oracle.gated_ff(x, w, v, "silu")
+    act = np.abs(oracle.act(ra, "silu"))
+    check("a", a, ra, oa + half_step(dtype, ra))
+    check("u", u, ru, ou + half_step(dtype, ru))
+    check("h", h, rh, (1.13 * oa + act_off(ra) * act) * (np.abs(ru) + ou) + act * ou + 2 * U * np.abs(rh) +
+          half_step(dtype, rh))
