@@ -164,9 +164,12 @@ __device__ __forceinline__ void pair8(floatx4 lo, floatx4 hi, float (&x)[8]) {
   }
 }
 
-// Values of the activations and of their derivatives (codes of gla.h), in
-// float and within (8 + |z| + z^2) 2^-22 of themselves, on the reciprocal and exp2
-// units (the rounding of exp2's argument grows with it).
+// Values of the activations and of their derivatives (codes of gla.h), in float, on
+// the reciprocal and exp2 units (the rounding of exp2's argument grows with it): the
+// values within (8 + |z| + z^2) 2^-22 of themselves, the derivatives within as much
+// of the magnitudes of the two terms that they are sums of (s and z s (1 - s), Phi(z)
+// and z phi(z); they cancel where silu' and gelu' cross zero). What a sigmoid or a
+// bell below 2^-126 makes counts as zero.
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + tile::fexp2(-z * kLog2e));
 }
@@ -175,7 +178,7 @@ __device__ __forceinline__ float bell(float z) { return tile::fexp2(z * z * (-0.
 // The normal distribution's integral up to z, erfc(-z / sqrt 2) / 2: for x >= 0
 // erfc(x) exp(x^2) (1 + x / 2) is smooth in t = 1 / (1 + x / 2), and this
 // polynomial in t, a least-squares fit weighted to even out its relative error,
-// is within 5e-8 of it on 0.14 <= t <= 1 (beyond, x > 12, exp(-x^2) is zero in
+// is within 5.5e-8 of it on 0.14 <= t <= 1 (beyond, x > 12, exp(-x^2) is zero in
 // float). The lower tail keeps its digits.
 __device__ __forceinline__ float normal_below(float z) {
   const float x = fabsf(z) * 0.70710678118654752f, t = __builtin_amdgcn_rcpf(fmaf(0.5f, x, 1.f));

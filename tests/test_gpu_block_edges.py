@@ -1,7 +1,7 @@
 """GPU: the products and norms between a block's mixers at the edges of what they
 take: empty batches, sums and gradients beyond half's range on their way, rows
 near the ends of float's range, wide rows with many groups, the borders of the
-form for few rows.
+form for few rows, slopes far out and where they cross zero.
 
 Tolerances are those of test_gpu_linear.py; half values that were divided by 2^p
 before they were rounded are off by 2^(p - 25) below the smallest normal."""
@@ -282,3 +282,26 @@ def test_few_rows_with_many_outputs(rows, N, dtype):
     check("u", u, ru, ou + half_step(dtype, ru))
     check("h", h, rh, (1.13 * oa + act_off(ra) * act) * (np.abs(ru) + ou) + act * ou + 2 * U * np.abs(rh) +
           half_step(dtype, rh))
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "logsigmoid"])
+def test_slopes_over_their_range(kind):
+    """The bias's gradient of one row with gy 1 is the slope in float: from -100 to
+    100, close to where silu' and gelu' cross zero, next to 0 and at float's ends,
+    to the bound of the two terms that it is the sum of. A sigmoid or a bell below
+    2^-126 counts as zero, and at |z| <= 128 makes up to 2^-119."""
+    z = np.concatenate([np.linspace(-100, 100, 8001), np.linspace(-1.2785, -1.2784, 500), np.linspace(-0.752, -0.7517, 500),
+                        np.logspace(-30, -1, 400), -np.logspace(-30, -1, 400), [1e4, -1e4, 3e38, -3e38]])
+    z = z[len(z) % 8:].astype(np.float32)
+    N = len(z)
+    zeros = torch.zeros(N, 8, device="cuda")
+    gb = gla.linear_bwd(zeros[:1], zeros, torch.ones(1, N, device="cuda"), act=ACTS[kind], pre=to_dev(z[None])[0],
+                        need_x=False, need_weight=False)[2]
+    torch.cuda.synchronize()
+    x = z.astype(np.float64)
+    want = oracle.act_slope(x, kind)
+    s = np.exp(-np.logaddexp(0, -x))
+    phi = np.exp(-np.minimum(np.abs(x), 1e3) ** 2 / 2) / np.sqrt(2 * np.pi)
+    terms = {"silu": s + np.abs(x) * s * np.exp(-np.logaddexp(0, x)), "gelu": np.abs(want - x * phi) + np.abs(x) * phi,
+             "logsigmoid": want}[kind]
+    check(kind, gb, want, act_off(np.minimum(np.abs(x), 128)) * terms + 2.0 ** -24 * np.abs(want) + 2.0 ** -119)
