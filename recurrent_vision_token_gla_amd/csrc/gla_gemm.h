@@ -351,7 +351,7 @@ constexpr TileShape tile_shape(int tile, bool is_float, bool gated) {
 // Float tiles gain nothing above 128 x 128; the weights' gradients take no
 // others of 256 columns than 256 x 256 (320 rows need more registers than there
 // are).
-template <typename T, bool kColA, int kEpi>
+template <typename T, bool kColA>
 constexpr bool has_tile(int t) {
   if (t < k128x128) return sizeof(T) == 2 && (!kColA || t == k256x256);
   return true;
@@ -576,12 +576,12 @@ float round_cost(const TileShape& s, long steps, long on, bool turned) {
 
 // M x N outputs, `others` such products at once, `steps` steps each: the best
 // tile, and what it costs in *cost.
-template <typename T, bool kColA, int kEpi>
+template <typename T, bool kColA>
 int best_tile(long M, long N, long others, long steps, float* cost = nullptr) {
   int best = -1;
   float least = 0.f;
   for (int t = 0; t < kTiles; ++t) {
-    if (!has_tile<T, kColA, kEpi>(t)) continue;
+    if (!has_tile<T, kColA>(t)) continue;
     const TileShape s = tile_shape(t, sizeof(T) == 4, false);
     const long count = tile_count(s, M, N) * others, slots = (long)kCus * s.per_cu;
     const long whole = count / slots, rest = count % slots;
@@ -609,7 +609,7 @@ hipError_t launch_product(const Args& g, int tile, hipStream_t s) {
   if constexpr (kTile == kTiles) {
     return hipErrorInvalidValue;
   } else {
-    if constexpr (has_tile<T, kColA, kEpi>(kTile))
+    if constexpr (has_tile<T, kColA>(kTile))
       if (tile == kTile) return launch_tiles<T, kTile, kColA, kColB, kEpi>(g, s);
     return launch_product<T, kColA, kColB, kEpi, kTile + 1>(g, tile, s);
   }

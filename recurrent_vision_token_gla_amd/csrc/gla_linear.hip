@@ -83,7 +83,7 @@ hipError_t forward(const Args& g, hipStream_t s) {
                        0, s, g);
     return hipGetLastError();
   }
-  return launch_product<T, false, false, kEpi>(g, best_tile<T, false, kEpi>(g.M, kDual ? 2 * g.N : g.N, 1, g.steps), s);
+  return launch_product<T, false, false, kEpi>(g, best_tile<T, false>(g.M, kDual ? 2 * g.N : g.N, 1, g.steps), s);
 }
 
 // Any number of rows: at most 2^22 per launch, so that the grid's numbers fit 32

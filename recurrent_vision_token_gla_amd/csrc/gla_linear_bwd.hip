@@ -241,14 +241,14 @@ template <typename T>
 void plan(long rows, int K, int N, int mparts, LinearBwdLayout* l) {
   const long step = Num<T>::kStep, steps = (rows + step - 1) / step, steps_x = mparts * ((N + step - 1) / step);
   float x, least = 0.f;
-  l->tile_x = best_tile<T, false, kLinear>(rows < 1L << 22 ? rows : 1L << 22, K, 1, steps_x, &x);
+  l->tile_x = best_tile<T, false>(rows < 1L << 22 ? rows : 1L << 22, K, 1, steps_x, &x);
   l->steps = steps;
   for (long s : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32}) {
     if (s > 1 && steps < 4 * s) break;
     const long each = (steps + s - 1) / s, splits = (steps + each - 1) / each;
     const float join = splits > 1 ? 4.f + 2e-6f * splits * mparts * N * K : 0.f;
     float w;
-    const int t = best_tile<T, true, kLinear>(N, K, mparts * splits, each, &w);
+    const int t = best_tile<T, true>(N, K, mparts * splits, each, &w);
     float c = w + join + x + 3.f;
     if (least == 0.f || c < least) least = c, l->tile_w = t, l->splits = (int)splits, l->each = each, l->pair = false;
     for (int p = k128x128; rows <= 1L << 20 && p < kTiles; ++p) {
@@ -261,7 +261,7 @@ void plan(long rows, int K, int N, int mparts, LinearBwdLayout* l) {
       c = join + (nx + nw <= slots ? longer : (nx * rx + nw * rw) / slots + 0.5f * longer);
       if (c < least) least = c, l->tile_w = l->tile_x = p, l->splits = (int)splits, l->each = each, l->pair = true;
     }
-    if (!l->pair) l->tile_x = best_tile<T, false, kLinear>(rows < 1L << 22 ? rows : 1L << 22, K, 1, steps_x);
+    if (!l->pair) l->tile_x = best_tile<T, false>(rows < 1L << 22 ? rows : 1L << 22, K, 1, steps_x);
   }
 }
 
