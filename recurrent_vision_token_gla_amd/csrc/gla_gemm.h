@@ -593,6 +593,13 @@ int best_tile(long M, long N, long others, long steps, float* cost = nullptr) {
   return best;
 }
 
+// Rows of a forward product per launch: at most 2^22, and 2^31 outputs. A tile has
+// at most a thread for each of its outputs (the gated one of 32 columns, 16 of each
+// weight, by eight groups), and a launch may have less than 2^32 threads.
+inline long rows_at_once(long N) {
+  return (1L << 31) / (N > 512 ? N : 512);
+}
+
 // One product on tiles of the given kind.
 template <typename T, int kTile, bool kColA, bool kColB, int kEpi>
 hipError_t launch_tiles(Args g, hipStream_t s) {

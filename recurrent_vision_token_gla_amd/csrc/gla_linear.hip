@@ -86,11 +86,10 @@ hipError_t forward(const Args& g, hipStream_t s) {
   return launch_product<T, false, false, kEpi>(g, best_tile<T, false>(g.M, kDual ? 2 * g.N : g.N, 1, g.steps), s);
 }
 
-// Any number of rows: at most 2^22 per launch, so that the grid's numbers fit 32
-// bits.
+// Any number of rows, rows_at_once of them per launch.
 template <int kEpi>
 hipError_t products(const Args& all, int dtype, hipStream_t s) {
-  constexpr long most = 1L << 22;
+  const long most = rows_at_once(all.N);
   const long es = dtype == 0 ? 2 : 4;
   auto on = [&](auto* p, long rows, long width) {
     return p ? (decltype(p))((uintptr_t)p + (size_t)(rows * width * es)) : p;
