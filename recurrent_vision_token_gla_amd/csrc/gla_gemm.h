@@ -593,6 +593,29 @@ int best_tile(long M, long N, long others, long steps, float* cost = nullptr) {
   return best;
 }
 
+// The tile of a forward product, or kTiles: skinny_kernel (gla_linear.hip), which takes
+// up to 16 rows and 16 columns a workgroup (gated: eight of either weight). It runs for up
+// to 16 rows where there are no more workgroups than CUs, or twice as many for up
+// to four rows: more of them wait for their weights one after the other, where the
+// tiles, of 32 to 256 columns, read ahead. us, it against the tiles, half: linear of one
+// row x 768 x 4,096 4.2 and 5.2, 16 rows 4.7 and 5.3; x 8,192 5.6 and 6.5, 4 rows 6.1 and
+// 6.5, 16 rows 7.3 and 6.6; x 16,384 8.3 and 7.7, 16 rows 11.7 and 7.8; x 65,536 23 and 24,
+// 16 rows 37 and 24; one row x 2,048 x 16,384 17.0 and 15.0; 24 rows x 768 x 768 (as two
+// such kernels' work) 4.4 and 4.3, 64 rows 6.8 and 4.3. Float, one row x 2,048 x 8,192 17.4
+// and 17.6, 16 rows 22.8 and 18.6, 16 rows x 768 x 65,536 75 and 49. Gated, one row x 2,048
+// x 4,096 9.9 and 12.2, 16 rows 12.7 and 12.3, x 8,192 15.8 and 14.8, 16 rows 22 and 15; 16
+// rows x 768 x 2,048 5.0 and 5.2, 32 rows 5.7 and 5.2; float one row x 768 x 4,096 9.7 and
+// 10.2, 16 rows 12.2 and 10.2.
+constexpr int kFewRows = 16;
+template <bool kDual>
+constexpr int kFewCols = kDual ? 8 : 16;
+template <typename T, int kEpi>
+int forward_tile(long M, long N, long steps) {
+  constexpr bool kDual = kEpi == kGated;
+  if (M <= kFewRows && N <= kFewCols<kDual> * kCus * (M <= 4 ? 2 : 1)) return kTiles;
+  return best_tile<T, false>(M, kDual ? 2 * N : N, 1, steps);
+}
+
 // Rows of a forward product per launch: at most 2^22, and 2^31 outputs. A tile has
 // at most a thread for each of its outputs (the gated one of 32 columns, 16 of each
 // weight, by eight groups), and a launch may have less than 2^32 threads.

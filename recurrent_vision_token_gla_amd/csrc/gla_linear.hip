@@ -16,11 +16,11 @@ namespace gemm {
 // weight row by four lanes. The waves' sums meet in LDS. Bound by the latency of
 // one load, the exchange and the launch (one row x 768 x 3,840: 4.0 us; four rows x
 // 8,192 x 1,024: 12.2, 1.4 TB/s, where the tiles take 15.5).
-constexpr int kFewRows = 16, kSkinnyWaves = 8;
+constexpr int kSkinnyWaves = 8;
 
 template <typename T, bool kDual>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const Args g) {
-  constexpr int kUnit = Num<T>::kUnit, kStep = Num<T>::kStep, kCols = kDual ? 8 : 16;
+  constexpr int kUnit = Num<T>::kUnit, kStep = Num<T>::kStep, kCols = kFewCols<kDual>;
   using Frag = typename std::conditional<sizeof(T) == 2, half8, floatx4>::type;
   __shared__ __attribute__((aligned(16))) float red[kSkinnyWaves][kFewRows][16];
   const int i = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3, w = wave();
@@ -63,27 +63,17 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const Args g)
   else finish<T>(g, 0, r, nn, x[0]);
 }
 
-// skinny_kernel up to 16 rows, and no more workgroups than CUs, or twice as many for up
-// to four rows: more of them wait for their weights one after the other, where the
-// tiles, of 32 to 256 columns, read ahead. us, it against the tiles, half: linear of one
-// row x 768 x 4,096 4.2 and 5.2, 16 rows 4.7 and 5.3; x 8,192 5.6 and 6.5, 4 rows 6.1 and
-// 6.5, 16 rows 7.3 and 6.6; x 16,384 8.3 and 7.7, 16 rows 11.7 and 7.8; x 65,536 23 and 24,
-// 16 rows 37 and 24; one row x 2,048 x 16,384 17.0 and 15.0; 24 rows x 768 x 768 (as two
-// such kernels' work) 4.4 and 4.3, 64 rows 6.8 and 4.3. Float, one row x 2,048 x 8,192 17.4
-// and 17.6, 16 rows 22.8 and 18.6, 16 rows x 768 x 65,536 75 and 49. Gated, one row x 2,048
-// x 4,096 9.9 and 12.2, 16 rows 12.7 and 12.3, x 8,192 15.8 and 14.8, 16 rows 22 and 15; 16
-// rows x 768 x 2,048 5.0 and 5.2, 32 rows 5.7 and 5.2; float one row x 768 x 4,096 9.7 and
-// 10.2, 16 rows 12.2 and 10.2.
+// The form for few rows, or the tiles.
 template <typename T, int kEpi>
 hipError_t forward(const Args& g, hipStream_t s) {
   constexpr bool kDual = kEpi == kGated;
-  constexpr int kCols = kDual ? 8 : 16;
-  if (g.M <= kFewRows && g.N <= kCols * kCus * (g.M <= 4 ? 2 : 1)) {
-    hipLaunchKernelGGL((skinny_kernel<T, kDual>), dim3((unsigned)((g.N + kCols - 1) / kCols)), dim3(64 * kSkinnyWaves),
-                       0, s, g);
+  const int tile = forward_tile<T, kEpi>(g.M, g.N, g.steps);
+  if (tile == kTiles) {
+    hipLaunchKernelGGL((skinny_kernel<T, kDual>), dim3((unsigned)((g.N + kFewCols<kDual> - 1) / kFewCols<kDual>)),
+                       dim3(64 * kSkinnyWaves), 0, s, g);
     return hipGetLastError();
   }
-  return launch_product<T, false, false, kEpi>(g, best_tile<T, false>(g.M, kDual ? 2 * g.N : g.N, 1, g.steps), s);
+  return launch_product<T, false, false, kEpi>(g, tile, s);
 }
 
 // Any number of rows, rows_at_once of them per launch.

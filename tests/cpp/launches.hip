@@ -15,7 +15,9 @@ void look(long rows, long K, long N) {
   const long es = sizeof(T), steps = (K * es + 127) / 128;
   if ((double)es * ((double)rows * (K + N) + (kDual ? 2 : 1) * (double)N * K) > 300e9) return;
   const long most = rows_at_once(N), M = rows < most ? rows : most;
-  const TileShape s = tile_shape(best_tile<T, false>(M, kDual ? 2 * N : N, 1, steps), es == 4, kDual);
+  const int tile = forward_tile<T, kEpi>(M, N, steps);
+  if (tile == kTiles) return;  // up to 16 rows: 512 threads for eight or 16 of up to 65,536 columns
+  const TileShape s = tile_shape(tile, es == 4, kDual);
   const long columns = kDual ? s.n / 2 : s.n, tiles = ((M + s.m - 1) / s.m) * ((N + columns - 1) / columns);
   const long threads = tiles * 64 * s.groups * s.wm * s.wn;
   if (M < 1 || M > 1L << 22 || threads >= 1L << 32)
