@@ -90,3 +90,13 @@ def test_gated_backward(dtype, rows, K, N):
     same("gx", gx, ga @ wg.double() + gu @ wu.double())
     same("ggate_weight", gwg, ga.t() @ x.double())
     same("gup_weight", gwu, gu.t() @ x.double())
+
+
+@pytest.mark.parametrize("rows,K,N", [(1, 65536, 8), (1, 8, 65536), (5, 65536, 16), (16, 8, 65536), (17, 65536, 40),
+                                      (40, 16, 65536), (300, 65536, 24), (300, 24, 65536)])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_the_widest_rows(dtype, rows, K, N):
+    test_linear(dtype, rows, K, N)
+    test_gated(dtype, rows, min(K, 4096), N)
+    test_linear_backward(dtype, rows, K, N)
+    test_gated_backward(dtype, rows, K, N)
