@@ -372,15 +372,17 @@ __global__ __launch_bounds__(kTeamThreads<TPR>) void gated_norm_bwd_kernel(
 // flight and two exchanges in it). Up to 8,192 columns the kernel above is faster (62
 // us against 92). The weights' sums wait in LDS, where a
 // thread comes back to its own columns, and the factors are read again, from L2,
-// where they are used; the row is kept as it was loaded. kOwn: every row is a group.
-template <typename T, bool kOwn>
+// where they are used; the row is kept as it was loaded. kRows: every row is a group,
+// or a workgroup takes whole groups of rows, or rows of one chunk of a group.
+enum WideRows { kEachAGroup, kGroups, kChunks };
+template <typename T, WideRows kRows>
 __global__ __launch_bounds__(1024) void gated_norm_bwd_wide_kernel(
     const T* xp, const T* sp, const T* gyp, const T* gsp, const float* __restrict__ post,
     const T* __restrict__ gate, const float* __restrict__ scale, const float* __restrict__ wp, float eps,
     T* gxp, T* grp, T* __restrict__ ggp, float* __restrict__ part, long groups, long per, int chunks, int F) {
   constexpr int TPR = 1024, VPT = 2;
   __shared__ float lds[4 * TPR / 64];
-  // gw, and sum gate Q (kOwn) or Q: the first four columns of every eight, then the others
+  // gw, and sum gate Q (kChunks: Q): the first four columns of every eight, then the others
   __shared__ floatx4 sums[2][2 * VPT * TPR];
   const int t = threadIdx.x, nv = F / 8;
   const float over = 1.f / (float)F;
@@ -398,21 +400,30 @@ __global__ __launch_bounds__(1024) void gated_norm_bwd_wide_kernel(
     for (int c = 0; c < 8; ++c) g[c] = 1.f;
     if (gate) load8(again(gate) + group * F + 8 * u, g);
   };
+  // the group's sums take the registers of float rows' gsum, which is read again as the factors are
+  constexpr bool kTwice = kRows == kGroups && sizeof(T) == 4;
+  float q[kRows == kGroups ? VPT : 1][8];
   auto do_row = [&](long group, long row) {
-    Raw8<T> x[VPT], s[VPT], gy[VPT], gs[VPT];
+    Raw8<T> x[VPT], s[VPT], gy[VPT], kept[kTwice ? 1 : VPT];
     float squares[2] = {0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int u = t + TPR * i;
       const long at = row * F + 8 * u;
-      x[i] = s[i] = gy[i] = gs[i] = Raw8<T>{};
+      x[i] = s[i] = gy[i] = kept[kTwice ? 0 : i] = Raw8<T>{};
       if (u < nv) {
         x[i].load(xp + at);
         s[i].load(sp + at);
         gy[i].load(gyp + at);
-        if (gsp) gs[i].load(gsp + at);
+        if (!kTwice && gsp) kept[kTwice ? 0 : i].load(gsp + at);
       }
     }
+    auto carried = [&](int i, long at) {
+      Raw8<T> gs = {};
+      if constexpr (!kTwice) gs = kept[i];
+      else if (gsp) gs.load(again(gsp) + at);
+      return gs;
+    };
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -430,11 +441,12 @@ __global__ __launch_bounds__(1024) void gated_norm_bwd_wide_kernel(
         float f[8], g[8], w[8];
         factors(group, u, f, g);
         tile::load_f8(again(wp) + 8 * u, w);
+        const Raw8<T> gs = carried(i, row * F + 8 * u);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float m = s[i][c] * rs, fn = f[c] * g[c] * (x[i][c] * rx), gm = gy[i][c] * w[c];
           z[0] = fmaf(gm, m, z[0]);
-          z[1] = fmaf(gs[i][c], fn, z[1]);
+          z[1] = fmaf(gs[c], fn, z[1]);
           z[2] = fmaf(gm, fn, z[2]);
           z[3] = fmaf(fn, m, z[3]);
         }
@@ -450,11 +462,12 @@ __global__ __launch_bounds__(1024) void gated_norm_bwd_wide_kernel(
         const long at = row * F + 8 * u;
         float y[8], r[8], f[8], g[8];
         tile::load_f8(again(wp) + 8 * u, r);
+        const Raw8<T> gs = carried(i, at);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float m = s[i][c] * rs;
           y[c] = gy[i][c] * m;
-          r[c] = fmaf(rs, fmaf(gy[i][c], r[c], -m * dot), gs[i][c]);
+          r[c] = fmaf(rs, fmaf(gy[i][c], r[c], -m * dot), gs[c]);
         }
         add(0, u, y);
         store8(grp + at, r);
@@ -464,19 +477,40 @@ __global__ __launch_bounds__(1024) void gated_norm_bwd_wide_kernel(
           const float n = x[i][c] * rx;
           y[c] = rx * fmaf(r[c], f[c] * g[c], -n * mean);
           r[c] *= n;
+          if constexpr (kRows == kGroups) q[i][c] += r[c];
         }
         store8(gxp + at, y);
-        if constexpr (kOwn) {
+        if constexpr (kRows == kEachAGroup) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) f[c] *= r[c], r[c] *= g[c];
           if (ggp) store8(ggp + at, f);
         }
-        add(1, u, r);
+        if constexpr (kRows != kGroups) add(1, u, r);
       }
     }
   };
-  if constexpr (kOwn) {
+  if constexpr (kRows == kEachAGroup) {
     for (long row = blockIdx.x; row < groups; row += gridDim.x) do_row(row, row);
+  } else if constexpr (kRows == kGroups) {
+    for (long group = blockIdx.x; group < groups; group += gridDim.x) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) q[i][c] = 0.f;
+      for (long r = 0; r < per; ++r) do_row(group, group * per + r);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int u = t + TPR * i;
+        if (u < nv) {
+          float f[8], g[8];
+          factors(group, u, f, g);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) f[c] *= q[i][c], g[c] *= q[i][c];
+          if (ggp) store8(ggp + group * F + 8 * u, f);
+          add(1, u, g);
+        }
+      }
+    }
   } else {
     const long group = blockIdx.x / chunks;
     for (long r = blockIdx.x % chunks; r < per; r += chunks) do_row(group, group * per + r);
@@ -590,7 +624,7 @@ struct GroupPlan {
 GroupPlan group_plan(long rows, long groups, int F) {
   GroupPlan p;
   const long rpb = teams(F), per = rows / groups;
-  p.own = groups >= kMaxParts2 && (F <= 8192 ? per <= groups / 85 : per == 1);
+  p.own = groups >= kMaxParts2 && per <= groups / 85;
   p.chunks = 1;
   if (p.own) {
     const long steps = (groups + rpb - 1) / rpb, each = (steps + kMaxParts2 - 1) / kMaxParts2;
@@ -630,7 +664,10 @@ hipError_t gated_norm_bwd_t(const GatedNormBwdArgs& a, float* ws, hipStream_t s)
   const GroupPlan p = group_plan(a.rows, a.groups, a.F);
   const long per = a.rows / a.groups;
   auto kernel = [&] {
-    if constexpr (TPR * VPT > 1024) return p.own ? gated_norm_bwd_wide_kernel<T, true> : gated_norm_bwd_wide_kernel<T, false>;
+    if constexpr (TPR * VPT > 1024)
+      return !p.own     ? gated_norm_bwd_wide_kernel<T, kChunks>
+             : per == 1 ? gated_norm_bwd_wide_kernel<T, kEachAGroup>
+                        : gated_norm_bwd_wide_kernel<T, kGroups>;
     else return p.own ? gated_norm_bwd_kernel<TPR, VPT, T, true> : gated_norm_bwd_kernel<TPR, VPT, T, false>;
   }();
   const T* gate = static_cast<const T*>(a.gate);

@@ -305,3 +305,29 @@ def test_slopes_over_their_range(kind):
     terms = {"silu": s + np.abs(x) * s * np.exp(-np.logaddexp(0, x)), "gelu": np.abs(want - x * phi) + np.abs(x) * phi,
              "logsigmoid": want}[kind]
     check(kind, gb, want, act_off(np.minimum(np.abs(x), 128)) * terms + 2.0 ** -24 * np.abs(want) + 2.0 ** -119)
+
+
+@pytest.mark.parametrize("G,per,F", [(3, 4, 8200), (515, 1, 8200), (512, 2, 8200), (513, 1, 4104)])
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_wide_rows_in_place_and_in_their_workspace(G, per, F, dtype):
+    """gx and gresidual in each of the rows that they are made from, in a workspace
+    of exactly the stated size between guards."""
+    d = norms.make(G, per, F, dtype, (1, 1, 1), G + per + F + 8)
+    x, res, w, post, gate, scale, gy, gs = norms.dev(d, "x", "res", "w", "post", "gate", "scale", "gy", "gsum")
+    kw = dict(post_weight=post, gate=gate, scale=scale)
+    y, s = gla.gated_add_rmsnorm(x, res, w, EPS, **kw)
+    x2, r2 = x.clone(), res.clone()
+    gla.gated_add_rmsnorm(x2, r2, w, EPS, out=x2, sum_out=r2, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(y, x2) and torch.equal(s, r2)
+    want = gla.gated_add_rmsnorm_bwd(x, s, w, EPS, gy, gsum=gs, **kw)
+    need = gla.load().gla_gated_add_rmsnorm_bwd_workspace_bytes(G * per, G, F)
+    assert need <= 2 * 4 * F * 1024
+    room = torch.full((need + 8192,), 0xa5, dtype=torch.uint8, device="cuda")
+    for which in range(4):
+        t = [u.clone() for u in (x, s, gy, gs)]
+        got = gla.gated_add_rmsnorm_bwd(t[0], t[1], w, EPS, t[2], gsum=t[3], gx=t[which], gresidual=t[(which + 1) % 4],
+                                        workspace=room[4096:4096 + need], **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert torch.all(room[:4096] == 0xa5) and torch.all(room[4096 + need:] == 0xa5)
