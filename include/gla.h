@@ -513,10 +513,10 @@ size_t gla_gated_ff_bwd_workspace_bytes(int64_t rows, int K, int F, int dtype);
 /* Gradient of gla_gated_ff from gh = dL/dh and the kept a = gate, u = up: with
  * ga = gh u act'(a) and gu = gh act(a),
  *   gx = ga Wg + gu Wu,   ggate_weight = ga^T x,   gup_weight = gu^T x,
- * all in the input dtype; ga and gu are rounded to it for the products (GLA_F16:
- * where the call's largest finite one is beyond that type, all of them divided
- * by the power of two that brings it below 2^15, and the sums multiplied by it;
- * what is then below 2^-14 loses digits). gx may
+ * all in the input dtype; ga and gu are rounded to it for the products. (GLA_F16:
+ * one beyond 65504, gh u act'(a) of large gh and u, is +-Inf and makes its row of
+ * gx and its row of the weight's gradient Inf or NaN; below 2^-14 they lose
+ * digits, as such halves do.) gx may
  * be NULL, and both weights' gradients may be (not one of them: GLA_E_ARG). No
  * output may overlap an input, another output or the workspace. */
 int gla_gated_ff_bwd(const void* x, const void* gate_weight,

@@ -248,7 +248,6 @@ struct Args {
   const float* bias;
   const void* residual;
   float alpha;
-  const float* rescale;  // half gradients: what the sums are multiplied by, in memory, or nullptr
   int act;
   void *gate_out, *up_out;  // the gated product's two sides, or nullptr
 };
@@ -481,16 +480,6 @@ __device__ __forceinline__ void gemm_tile(const Args& g, int id, int count, char
       for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] += sums[(o * MI * NI + mi * NI + ni) * NT + tid];
-  }
-
-  if constexpr (sizeof(T) == 2 && kColB) {
-    const float f = g.rescale ? tile::uniform(*g.rescale) : 1.f;
-    if (f != 1.f) {
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni) acc[mi][ni] *= f;
-    }
   }
 
   // each lane: row lane % 16 of the row blocks, eight columns of each pair of column blocks;

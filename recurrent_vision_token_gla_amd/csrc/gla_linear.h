@@ -38,7 +38,6 @@ hipError_t launch_gated(const GatedArgs& a, hipStream_t s);
 struct LinearBwdLayout {
   size_t g[2];     // gradients behind the activation, [rows][N] each
   size_t colsum;   // float [parts][N]
-  size_t top;      // half gated gradients: what g was divided by, and from the fifth float on each workgroup's largest
   size_t partial;  // float [splits][parts of the weights][N][K]
   size_t total;
   int tile_x, tile_w, splits;

@@ -3,12 +3,17 @@
 //   gx = alpha gp W,   gW = alpha gp^T x,   gbias = alpha sum over rows of gp:
 // one pass forms gp (and the column sums) and two products follow, whose
 // operands lie down the columns where the forward's lie along the contraction.
-// gp is kept in the input type between them, as gy itself is; sums are float.
+// gp is kept in the input type between them, as gy itself is; sums are float. Half, the
+// rounding of every gp by up to 2^-11 adds to that of the outputs: 2.9e-4 of the largest
+// value against 64 bits, 2.1e-4 without. A second term for what it leaves would double
+// both products (25,600 x 768 x 2,048 gated: 323 of 390 us), and dividing values beyond
+// half's range by a power of two takes either a launch more for every call (17.3 -> 19.9
+// us for 421 x 384 x 1,032) and digits of all other rows, or a look at every step of the
+// products (5 to 20% more).
 #include "gla_linear.h"
 
 #include "gla_colsum.h"
 #include "gla_gemm.h"
-#include "gla_rows.h"
 
 namespace gla {
 namespace gemm {
@@ -59,91 +64,26 @@ __global__ __launch_bounds__(256) void slope_kernel(const T* __restrict__ pre, c
   part[(long)blockIdx.y * N + col] = alpha * y;
 }
 
-// ga = gh u act'(a) in u, gu = gh act(a) in a, of eight values.
-template <typename T>
-__device__ __forceinline__ void gated_slopes(const T* ap, const T* up, const T* ghp, int act, float (&a)[8],
-                                             float (&u)[8]) {
-  float g[8];
-  load8(ap, a);
-  load8(up, u);
-  load8(ghp, g);
-  if (act == 1 || act == 2) {  // zero at -Inf, as a kept product below half's range is stored
-#pragma unroll
-    for (int c = 0; c < 8; ++c) a[c] = a[c] == -__builtin_inff() ? -65504.f : a[c];
-  }
-#pragma unroll
-  for (int c = 0; c < 8; ++c) u[c] *= g[c] * slope(a[c], act);
-  activate(a, act);
-#pragma unroll
-  for (int c = 0; c < 8; ++c) a[c] *= g[c];
-}
-
-// The largest of a workgroup's 256 values, on every thread.
-__device__ __forceinline__ float largest(float x) {
-  __shared__ float lds[4];
-  return norm::row_reduce<256, true>(x, lds);
-}
-
-// Both, eight values a thread, and, half, the largest of the workgroup's finite
-// ones (top[4 + workgroup]). Bound by memory: 25,600 x 2,048 half 92 us, 525 MB at 5.7 TB/s.
+// ga = gh u act'(a), gu = gh act(a), eight values a thread. Bound by memory: 25,600 x
+// 2,048 half 92 us, 525 MB at 5.7 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void gated_slope_kernel(const T* __restrict__ ap, const T* __restrict__ up,
                                                           const T* __restrict__ ghp, T* __restrict__ gap,
-                                                          T* __restrict__ gup, float* __restrict__ top, int act,
-                                                          long groups) {
-  float most = 0.f;
+                                                          T* __restrict__ gup, int act, long groups) {
   for (long t = 256L * blockIdx.x + threadIdx.x; t < groups; t += 256L * gridDim.x) {
-    float a[8], u[8];
-    gated_slopes(ap + 8 * t, up + 8 * t, ghp + 8 * t, act, a, u);
-    store8(gap + 8 * t, u);
-    store8(gup + 8 * t, a);
-    if constexpr (sizeof(T) == 2) {
-      float x = 0.f;
+    float a[8], u[8], g[8];
+    load8(ap + 8 * t, a);
+    load8(up + 8 * t, u);
+    load8(ghp + 8 * t, g);
+    if (act == 1 || act == 2) {  // zero at -Inf, as a kept product below half's range is stored
 #pragma unroll
-      for (int c = 0; c < 8; ++c) x = fmaxf(x, fmaxf(fabsf(u[c]), fabsf(a[c])));  // NaN does not count
-      if (x == __builtin_inff()) {  // nor does Inf
-        x = 0.f;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          for (float y : {fabsf(u[c]), fabsf(a[c])}) x = y > x && y < __builtin_inff() ? y : x;
-      }
-      most = fmaxf(most, x);
+      for (int c = 0; c < 8; ++c) a[c] = a[c] == -__builtin_inff() ? -65504.f : a[c];
     }
-  }
-  if constexpr (sizeof(T) == 2) {
-    most = largest(most);
-    if (threadIdx.x == 0) top[4 + blockIdx.x] = most;
-  }
-}
-
-// gh u act'(a) of finite halves reaches 2^32, and the sums that it enters may be in
-// half's range all the same. Where one of the `parts` workgroups above met such a
-// value, both products are formed again, divided by the power of two that brings
-// the largest below 2^15; top[0] is that power (1 otherwise). The check alone, with
-// which a call is done nearly always, is a launch: the gradient of 421 x 384 x 1,032
-// takes 19.9 us instead of 17.3, of 25,600 x 768 x 2,048 1% more.
-template <typename T>
-__global__ __launch_bounds__(256) void gated_rescale_kernel(const T* __restrict__ ap, const T* __restrict__ up,
-                                                            const T* __restrict__ ghp, T* __restrict__ gap,
-                                                            T* __restrict__ gup, float* __restrict__ top, int parts,
-                                                            int act, long groups) {
-  float most = 0.f;
-  for (int p = 4 * threadIdx.x; p < parts; p += 1024) {
-    const floatx4 x = *reinterpret_cast<const floatx4*>(top + 4 + p);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) most = p + c < parts ? fmaxf(most, x[c]) : most;
-  }
-  most = largest(most);
-  const bool fits = most < 65520.f;  // rounds to a half
-  const int power = fits ? 0 : (int)(__float_as_uint(most) >> 23) - 127 - 14;
-  if (blockIdx.x == 0 && threadIdx.x == 0) top[0] = __uint_as_float((unsigned)(127 + power) << 23);
-  if (fits) return;
-  const float down = __uint_as_float((unsigned)(127 - power) << 23);
-  for (long t = 256L * blockIdx.x + threadIdx.x; t < groups; t += 256L * gridDim.x) {
-    float a[8], u[8];
-    gated_slopes(ap + 8 * t, up + 8 * t, ghp + 8 * t, act, a, u);
+    for (int c = 0; c < 8; ++c) u[c] *= g[c] * slope(a[c], act);
+    activate(a, act);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) u[c] *= down, a[c] *= down;
+    for (int c = 0; c < 8; ++c) a[c] *= g[c];
     store8(gap + 8 * t, u);
     store8(gup + 8 * t, a);
   }
@@ -341,8 +281,6 @@ SlopePlan slope_plan(long rows, int N) {
   return p;
 }
 
-unsigned gated_slope_parts(long rows, int F) { return spread((rows * F / 8 + 255) / 256); }
-
 size_t pad(size_t n) { return (n + 255) & ~(size_t)255; }
 
 LinearBwdLayout layout(long rows, int K, int N, int dtype, int sides, bool sums, int mparts) {
@@ -355,8 +293,6 @@ LinearBwdLayout layout(long rows, int K, int N, int dtype, int sides, bool sums,
   }
   l.colsum = at;
   if (sums) at += pad((size_t)slope_plan(rows, N).parts * N * sizeof(float));
-  l.top = at;
-  if (sides == 2 && dtype == 0) at += pad((8 + (size_t)gated_slope_parts(rows, N)) * sizeof(float));
   l.partial = at;
   if (dtype == 0) plan<half_t>(rows, K, N, mparts, &l);
   else plan<float>(rows, K, N, mparts, &l);
@@ -390,24 +326,15 @@ hipError_t linear_bwd_t(const LinearBwdArgs& a, const LinearBwdLayout& l, char* 
 template <typename T>
 hipError_t gated_bwd_t(const GatedBwdArgs& a, const LinearBwdLayout& l, char* ws, hipStream_t s) {
   T *ga = reinterpret_cast<T*>(ws + l.g[0]), *gu = reinterpret_cast<T*>(ws + l.g[1]);
-  const T *gate = static_cast<const T*>(a.gate), *up = static_cast<const T*>(a.up);
-  const T* gh = static_cast<const T*>(a.gh);
-  float* top = sizeof(T) == 2 ? reinterpret_cast<float*>(ws + l.top) : nullptr;
   const long groups = a.rows * a.F / 8;
-  const unsigned parts = gated_slope_parts(a.rows, a.F);
-  hipLaunchKernelGGL((gated_slope_kernel<T>), dim3(parts), dim3(256), 0, s, gate, up, gh, ga, gu, top, a.act, groups);
-  hipError_t e = hipGetLastError();
+  hipLaunchKernelGGL((gated_slope_kernel<T>), dim3(spread((groups + 255) / 256)), dim3(256), 0, s,
+                     static_cast<const T*>(a.gate), static_cast<const T*>(a.up),
+                     static_cast<const T*>(a.gh), ga, gu, a.act, groups);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if constexpr (sizeof(T) == 2) {
-    hipLaunchKernelGGL((gated_rescale_kernel<T>), dim3(parts < 256 ? parts : 256), dim3(256), 0, s, gate, up, gh, ga, gu,
-                       top, (int)parts, a.act, groups);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  Args x = input_gradient<T>(ga, gu, a.gate_weight, a.up_weight, a.rows, a.F, a.K, 2, 1.f, a.gx);
-  Args w = weight_gradient<T>(ga, gu, a.x, a.rows, a.K, a.F, 2, 1.f, a.ggate_weight, a.gup_weight, l, ws);
-  x.rescale = w.rescale = top;
-  return launch_products<T>(x, w, Sums{}, l, s);
+  return launch_products<T>(
+      input_gradient<T>(ga, gu, a.gate_weight, a.up_weight, a.rows, a.F, a.K, 2, 1.f, a.gx),
+      weight_gradient<T>(ga, gu, a.x, a.rows, a.K, a.F, 2, 1.f, a.ggate_weight, a.gup_weight, l, ws), Sums{}, l, s);
 }
 
 }  // namespace gemm
