@@ -12,7 +12,7 @@ using namespace gla::api;
 namespace {
 
 // Rows, widths and codes of a product with `in` values in and `out` values out
-// a row. Widths are examined where rows and outputs exist.
+// a row; `in` may be 0 where there are no rows or no outputs.
 int check_product(int64_t rows, int in, int out, int act, int dtype, bool* empty) {
   if (rows < 0 || in < 0 || out < 0) return GLA_E_ARG;
   if (dtype != GLA_F16 && dtype != GLA_F32) return GLA_E_ARG;

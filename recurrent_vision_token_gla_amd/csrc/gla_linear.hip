@@ -15,7 +15,7 @@ namespace gemm {
 // lane i, q holds row i and the 32 bytes 32 q .. of the step's 128, whole lines of a
 // weight row by four lanes. The waves' sums meet in LDS. Bound by the latency of
 // one load, the exchange and the launch (one row x 768 x 3,840: 4.0 us; four rows x
-// 8,192 x 1,024: 12.2, 1.4 TB/s, where the tiles take 15.5).
+// 8,192 x 1,024: 13.1, 1.3 TB/s, where the tiles take 21.2).
 constexpr int kSkinnyWaves = 8;
 
 template <typename T, bool kDual>
