@@ -223,7 +223,8 @@ def test_norms_gradient_of_floats_near_their_ends(x, s, scale, gy, gsum, G, per,
 
 # rows of every width that has a kernel of its own, with a gate of every row's own, of two rows', and chunks of a group
 @pytest.mark.parametrize("G,per,F", [(520, 1, 4104), (512, 2, 4104), (515, 1, 8192), (520, 1, 8200), (512, 2, 8200),
-                                     (514, 1, 16384), (3, 200, 8200), (1, 600, 16384)])
+                                     (514, 1, 16384), (3, 200, 8200), (1, 600, 16384), (20, 3, 8200),
+                                     (300, 1, 8200)])
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])
 def test_norms_of_wide_rows_with_many_groups(G, per, F, dtype):
     d = norms.make(G, per, F, dtype, (1, 1, 1), G + per + F + 6)
